@@ -573,6 +573,161 @@ typedef struct {
 csa2_status csa2_linear(const csa2_linear_args* a, void* stream);
 
 /* ------------------------------------------------------------------------------------
+ * Paged 8-bit cache of a grouped-query attention layer.  (The pages describe no such layer: it
+ * is what a model serves next to its CSA2 layers, with the same forms - FP8 rows kept after
+ * RoPE, a sink logit, a sliding window, records written by slot.)
+ *
+ * A sequence's tokens lie in pages of `page_size` tokens, page table[b, j] holding tokens
+ * j * page_size .. of sequence b.  Keys and values are OCP E4M3 codes [n_pages, kv_heads,
+ * page_size, head_dim] with one fp32 scale per (page, kv head): value = code * scale.
+ * Query / key / value rows of all sequences lie one after the other: sequence b's new tokens are
+ * rows row_start[b] .. row_start[b+1]-1, the last ones of its kv_len[b] tokens.
+ * Every call works on device lengths: nothing is read back, and a captured call follows them.
+ * ------------------------------------------------------------------------------------ */
+typedef enum csa2_type { CSA2_T_BF16 = 0, CSA2_T_F16 = 1, CSA2_T_F32 = 2 } csa2_type;
+
+/* csa2_page_plan - page tables and slot maps from request lengths.
+ *
+ * Sequence b has ctx_len[b] tokens in the cache and gets new_len[b] more (negative lengths count
+ * as 0).  The pages that these need are taken from free_pages in order, sequence after sequence:
+ *   table[b, j] for ceil(ctx / page) <= j < ceil((ctx + new) / page); the other entries stay
+ *   row_start[b] = new tokens of the sequences before b,  kv_len[b] = ctx + new
+ *   n_taken[0]   = pages needed: free_pages[n_taken ..] remain
+ * and for row r of sequence b (0 <= r < row_start[n_seq])
+ *   seq_of_row[r] = b,  pos[r] = ctx_len[b] + r - row_start[b],
+ *   slot[r]       = table[b, pos / page] * page + pos % page       (csa2_write_records' dst_row)
+ * Rows behind the last sequence get -1 in all three.  Where free_pages or table_cols do not
+ * suffice, the missing entries and slots are -1; where rows exceed max_rows, the rest are left
+ * out; both, and a negative entry among a sequence's cached pages, are reported as
+ * CSA2_EDEVICE_INDEX through dev_status.  Running a plan again on its own table repeats it. */
+typedef struct {
+  const int32_t* ctx_len;     /* [n_seq] */
+  const int32_t* new_len;     /* [n_seq] (sums below 2^31) */
+  int32_t n_seq;              /* 0 .. 8192 */
+  int32_t page_size;          /* 1 .. 65536 */
+  int32_t* table;             /* in / out [n_seq, table_cols] */
+  int32_t table_cols;         /* >= 1 */
+  const int32_t* free_pages;  /* [n_free]; may be NULL with n_free 0 */
+  int32_t n_free;
+  int32_t max_rows;           /* >= 0 */
+  int32_t* row_start;         /* out [n_seq + 1] */
+  int32_t* kv_len;            /* out [n_seq] */
+  int32_t* seq_of_row;        /* out [max_rows], 16-byte aligned */
+  int64_t* pos;               /* out [max_rows], 16-byte aligned */
+  int64_t* slot;              /* out [max_rows], 16-byte aligned */
+  int32_t* n_taken;           /* out [1] */
+  int32_t* dev_status;        /* optional */
+} csa2_page_plan_args;
+csa2_status csa2_page_plan(const csa2_page_plan_args* a, void* stream);
+
+/* csa2_rope_axes - rotary positions with several axes (time, height, width of images and video;
+ * one axis for text).
+ *
+ * Pair i (0 <= i < rot_dim / 2) of every head turns by pos[axis_of_pair[i], t] * theta^(-2i/rot_dim):
+ *   (u, v) -> (u cos - v sin, u sin + v cos),
+ * pairs (2i, 2i+1) or, with half_pairs, (i, i + rot_dim/2), counted from dim rot_first.  `inverse`
+ * turns back, which is also the gradient with respect to x.  The other dims are copied.  Angles
+ * are formed modulo a turn in 64-bit fixed point (any position), the rotation in fp32. */
+#define CSA2_ROPE_AXES_MAX_PAIRS 128
+typedef struct {
+  int32_t n_tokens;           /* >= 0 */
+  int32_t n_heads;            /* >= 1 */
+  int32_t head_dim;           /* multiple of 8, <= 4096 */
+  int32_t dtype;              /* csa2_type of x and out */
+  const void* x;              /* element (t, h, d) at t * x_row + h * x_head + d */
+  int64_t x_row, x_head;      /* strides in elements, multiples of 16 bytes */
+  void* out;                  /* likewise; may be x itself with the same strides */
+  int64_t out_row, out_head;
+  const int64_t* pos;         /* [n_axes, n_tokens] */
+  int32_t n_axes;             /* 1 .. 16 */
+  int32_t rot_first;          /* multiple of 8 */
+  int32_t rot_dim;            /* multiple of 16, <= 256, rot_first + rot_dim <= head_dim */
+  int32_t half_pairs;
+  int32_t inverse;
+  float theta;                /* > 0 */
+  uint8_t axis_of_pair[CSA2_ROPE_AXES_MAX_PAIRS];  /* on the host */
+} csa2_rope_axes_args;
+csa2_status csa2_rope_axes(const csa2_rope_axes_args* a, void* stream);
+
+/* csa2_write_pages - appends key and value rows to the cache.
+ *
+ * For every page and head that gets new rows, of K and of V each:
+ *   need  = the smallest 2^e, -100 <= e <= 119, with |x| <= 448 * 2^e for its new finite values
+ *   scale = need; where the page holds older tokens of the sequence, the larger of the page's
+ *           scale and need, and the older codes are rounded again to a scale that grew
+ *   code  = E4M3(x / scale), nearest even; infinities saturate, a NaN makes the scale NaN
+ *           (csa2_paged_attn then gives NaN to rows that see the page's tokens)
+ * What the page's other slots hold is left.  Rows outside [0, row_start[n_seq]) and rows of
+ * sequences outside [0, n_seq) are left out; a page outside [0, n_pages) is skipped and reported.
+ * No page may belong to two sequences that get rows in the call.  Calling it again on the same
+ * rows writes the same. */
+typedef struct {
+  int32_t n_rows;             /* rows of k and v (>= 0) */
+  int32_t n_seq;
+  int32_t kv_heads;           /* 1 .. 65535 */
+  int32_t head_dim;           /* 64 or 128 */
+  int32_t page_size;          /* 16, 32, 64 or 128 */
+  int32_t n_pages;
+  int32_t table_cols;
+  int32_t dtype;              /* csa2_type of k and v */
+  const void* k;              /* element (r, h, d) at r * k_row + h * k_head + d */
+  int64_t k_row, k_head;      /* strides in elements, multiples of 16 bytes */
+  const void* v;
+  int64_t v_row, v_head;
+  const int32_t* row_start;   /* [n_seq + 1] */
+  const int32_t* kv_len;      /* [n_seq] tokens with the new ones */
+  const int32_t* seq_of_row;  /* [n_rows] */
+  const int32_t* table;       /* [n_seq, table_cols] */
+  uint8_t* k_codes;           /* [n_pages, kv_heads, page_size, head_dim] */
+  uint8_t* v_codes;
+  float* k_scale;             /* [n_pages, kv_heads] */
+  float* v_scale;
+  int32_t* dev_status;        /* optional */
+} csa2_write_pages_args;
+csa2_status csa2_write_pages(const csa2_write_pages_args* a, void* stream);
+
+/* csa2_paged_attn - attention of the new tokens' queries over the cache.
+ *
+ * Row r of sequence b, at position p = kv_len[b] - row_start[b+1] + r, head h of kv head h / G
+ * (G = heads / kv_heads):
+ *   z_j = softmax_scale * q . k_j  for tokens j <= p, and j > p - window where window > 0
+ *   out = sum_j exp(z_j) v_j / (sum_j exp(z_j) + exp(sink[h]))
+ * A row without such a token is 0.  Rows outside [0, row_start[n_seq]) of q and out are left.
+ * A table entry outside [0, n_pages) hides its tokens and is reported; kv_len beyond the table
+ * counts as its end.  Codes 0x7f and 0xff (E4M3's NaN, which csa2_write_pages does not write)
+ * must not occur among a sequence's tokens; scales are >= 0 or NaN. */
+typedef struct {
+  int32_t n_rows;             /* rows of q and out (>= 0) */
+  int32_t n_seq;
+  int32_t heads;              /* a multiple of kv_heads */
+  int32_t kv_heads;
+  int32_t head_dim;           /* 64 or 128 */
+  int32_t page_size;          /* 16, 32, 64 or 128 */
+  int32_t n_pages;
+  int32_t table_cols;
+  int32_t q_dtype;            /* CSA2_T_BF16 or CSA2_T_F16 */
+  int32_t out_dtype;          /* csa2_type */
+  const void* q;              /* element (r, h, d) at r * q_row + h * q_head + d */
+  int64_t q_row, q_head;      /* strides in elements, multiples of 16 bytes */
+  const int32_t* row_start;   /* [n_seq + 1] ascending */
+  const int32_t* kv_len;      /* [n_seq] */
+  const int32_t* table;       /* [n_seq, table_cols] */
+  const uint8_t* k_codes;
+  const uint8_t* v_codes;
+  const float* k_scale;
+  const float* v_scale;
+  float softmax_scale;
+  int32_t window;             /* 0: none */
+  const float* sink;          /* [heads] or NULL */
+  void* out;                  /* [n_rows, heads, head_dim] */
+  void* workspace;            /* csa2_paged_attn_workspace_size bytes, any contents */
+  size_t workspace_bytes;
+  int32_t* dev_status;        /* optional */
+} csa2_paged_attn_args;
+size_t csa2_paged_attn_workspace_size(const csa2_paged_attn_args* a);
+csa2_status csa2_paged_attn(const csa2_paged_attn_args* a, void* stream);
+
+/* ------------------------------------------------------------------------------------
  * Utilities
  * ------------------------------------------------------------------------------------ */
 const char* csa2_status_string(csa2_status s);

@@ -31,3 +31,4 @@ from .csa2 import *  # noqa: F401,F403
 from .writer import *  # noqa: F401,F403
 from .compressor import *  # noqa: F401,F403
 from .projections import *  # noqa: F401,F403
+from . import paged  # noqa: F401

@@ -622,3 +622,8 @@ def expand_mxfp4(codes, exps):
     a.codes, a.exps, a.out = _ptr(codes), _ptr(exps), _ptr(out)
     _check(_expand(C.byref(a), _stream()), "csa2_expand_mxfp4")
     return out
+
+
+# ------------------------------------------------------------------ paged 8-bit cache
+from .paged import (PageCache, PagedAttn, PagePlan, PageWriter, RopeAxes, page_plan, paged_attn, rope_axes,  # noqa: E402
+                    write_pages)

@@ -1,0 +1,97 @@
+// Parameters and launchers of the paged 8-bit cache's kernels (page plan, rotary positions with
+// several axes, page writer, paged attention); the host side is paged_api.cu.
+#pragma once
+
+#include <cstdint>
+#include <cuda_runtime.h>
+
+#include "../../include/csa2.h"
+
+namespace csa2 {
+
+struct PagePlanParams {
+  const int32_t* ctx_len;
+  const int32_t* new_len;
+  int n_seq;
+  int page_size;
+  int32_t* table;
+  int table_cols;
+  const int32_t* free_pages;
+  int n_free;
+  int max_rows;
+  int32_t* row_start;
+  int32_t* kv_len;
+  int32_t* seq_of_row;
+  int64_t* pos;
+  int64_t* slot;
+  int32_t* n_taken;
+  int32_t* dev_status;
+};
+cudaError_t launch_page_plan(const PagePlanParams& p, cudaStream_t stream);
+
+struct RopeAxesParams {
+  const void* x;
+  void* out;
+  long long x_row, x_head, out_row, out_head;  // strides in elements
+  int n_tokens, n_heads, head_dim;
+  int rot_first, rot_dim;
+  int copy_rest;                               // the dims outside the rotary range are copied to out
+  const int64_t* pos;                          // [n_axes, n_tokens]
+  uint64_t turns[CSA2_ROPE_AXES_MAX_PAIRS];    // frequency of a pair in turns per position, times 2^64
+  uint8_t axis[CSA2_ROPE_AXES_MAX_PAIRS];
+};
+cudaError_t launch_rope_axes(const RopeAxesParams& p, int dtype, bool half_pairs, bool inverse, cudaStream_t stream);
+
+struct PageWriteParams {
+  const void* x[2];                 // k, v
+  long long x_row[2], x_head[2];    // strides in elements
+  uint8_t* codes[2];                // [n_pages, kv_heads, page, dim]
+  float* scale[2];                  // [n_pages, kv_heads]
+  int n_rows, n_seq, kv_heads, page_shift;
+  int n_pages, table_cols;
+  const int32_t* row_start;
+  const int32_t* kv_len;
+  const int32_t* seq_of_row;
+  const int32_t* table;
+  int chunk;                        // rows a block looks at
+  int32_t* dev_status;
+};
+cudaError_t launch_page_write(const PageWriteParams& p, int dtype, int head_dim, cudaStream_t stream);
+
+// What a block of the split attention leaves open: the item whose last unit it computed lies
+// beyond its range.  end < 0: nothing is open.
+struct PagedOpen {
+  long long end;                    // one past the item's last unit
+  int row0;                         // first row of the tile within the sequence's rows x heads
+  int n;                            // its rows
+  int first_row;                    // the sequence's first query row
+  int kv_head;
+};
+
+struct PagedAttnParams {
+  const void* q;
+  long long q_row, q_head;          // strides in elements
+  int n_rows, n_seq, kv_heads, group;
+  const int32_t* row_start;
+  const int32_t* kv_len;
+  const int32_t* table;
+  int table_cols, n_pages, page_shift;
+  const uint8_t* k;
+  const uint8_t* v;
+  const float* k_scale;
+  const float* v_scale;
+  float scale_log2;                 // softmax_scale * log2(e)
+  int window;                       // 0: none
+  const float* sink;
+  void* out;                        // [n_rows, kv_heads * group, dim]
+  int out_dtype;
+  float* part_o;                    // [2 * blocks, 16, dim]
+  float* part_ml;                   // [2 * blocks, 16, 2]
+  PagedOpen* open;                  // [blocks]
+  long long* units;                 // [1] all units of the call
+  int32_t* dev_status;
+};
+cudaError_t launch_paged_attn(const PagedAttnParams& p, int q_dtype, int head_dim, bool rows8, int blocks,
+                              cudaStream_t stream);
+
+}  // namespace csa2

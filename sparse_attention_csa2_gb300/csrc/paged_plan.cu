@@ -1,0 +1,274 @@
+// Page plan (block tables and slot maps from request lengths) and rotary positions with several
+// axes.
+#include "common.cuh"
+#include "paged.h"
+
+namespace csa2 {
+namespace {
+
+// ----------------------------------------------------------------------------- page plan
+// Two exclusive sums over the sequences, of the new rows and of the pages these need, then one
+// lookup per row: its sequence (the last whose first row is at or before it), position and slot.
+//
+// Every block forms both sums for itself in shared memory (a few KB of lengths, read from L2) and
+// then takes its share of the rows and pages, so that one launch does it all: a scan in a kernel of
+// its own would add a launch to a call that takes a few microseconds at the sizes of a decode step.
+// Bound by that latency below some 10^5 rows and by the 20 bytes written per row above.
+constexpr int kPlanThreads = 512;
+constexpr int kPlanRows = 4;  // consecutive rows of a thread: one search, 16-byte stores
+
+__device__ __forceinline__ int pages_of(int tokens, int page) { return (int)(((unsigned)tokens + page - 1) / (unsigned)page); }
+
+__global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const PagePlanParams p) {
+  extern __shared__ int sums[];  // [n_seq + 1] first rows, [n_seq + 1] first new pages
+  int* row0 = sums;
+  int* page0 = sums + p.n_seq + 1;
+  __shared__ int warp_tmp[kPlanThreads / 32];
+  const int tid = threadIdx.x;
+  // a thread sums a run of sequences, the block scans the threads' sums
+  const int run = (p.n_seq + kPlanThreads - 1) / kPlanThreads;
+  const int b0 = min(tid * run, p.n_seq), b1 = min(b0 + run, p.n_seq);
+  int rows = 0, need = 0;
+  for (int b = b0; b < b1; ++b) {
+    const int c = max(p.ctx_len[b], 0), n = max(p.new_len[b], 0);
+    row0[b] = rows;
+    page0[b] = need;
+    rows += n;
+    need += pages_of(c + n, p.page_size) - pages_of(c, p.page_size);
+  }
+  int total_rows, total_need;
+  const int first_row = block_excl_scan<kPlanThreads>(rows, warp_tmp, &total_rows);
+  const int first_need = block_excl_scan<kPlanThreads>(need, warp_tmp, &total_need);
+  for (int b = b0; b < b1; ++b) {
+    row0[b] += first_row;
+    page0[b] += first_need;
+  }
+  if (tid == 0) row0[p.n_seq] = total_rows, page0[p.n_seq] = total_need;
+  __syncthreads();
+
+  bool bad = false;
+  const int at = blockIdx.x * kPlanThreads + tid, all = gridDim.x * kPlanThreads;
+  for (int b = at; b <= p.n_seq; b += all) {
+    p.row_start[b] = row0[b];
+    if (b < p.n_seq) {
+      const int c = max(p.ctx_len[b], 0), kv = c + row0[b + 1] - row0[b];
+      p.kv_len[b] = kv;
+      bad |= pages_of(kv, p.page_size) > p.table_cols;
+    }
+  }
+  if (at == 0) {
+    p.n_taken[0] = total_need;
+    bad |= total_need > p.n_free || total_rows > p.max_rows;
+  }
+  // the new pages' table entries
+  for (int f = at; f < total_need; f += all) {
+    int lo = 0, hi = p.n_seq;  // page0[lo] <= f < page0[hi]
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (page0[mid] <= f) lo = mid; else hi = mid;
+    }
+    const int col = pages_of(max(p.ctx_len[lo], 0), p.page_size) + f - page0[lo];
+    if (col < p.table_cols) p.table[(long long)lo * p.table_cols + col] = f < p.n_free ? p.free_pages[f] : -1;
+  }
+  // rows
+  for (int r = at * kPlanRows; r < p.max_rows; r += all * kPlanRows) {
+    int lo = 0, hi = p.n_seq;
+    if (r < total_rows)
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (row0[mid] <= r) lo = mid; else hi = mid;
+      }
+    int seq[kPlanRows];
+    int64_t pos[kPlanRows], slot[kPlanRows];
+    int b = lo, known = -1, c = 0, held = 0;
+#pragma unroll
+    for (int k = 0; k < kPlanRows; ++k) {
+      seq[k] = -1, pos[k] = -1, slot[k] = -1;
+      if (r + k >= total_rows) continue;
+      while (row0[b + 1] <= r + k) ++b;  // empty sequences too
+      if (b != known) {
+        c = max(p.ctx_len[b], 0);
+        held = pages_of(c, p.page_size);
+        known = b;
+      }
+      const int at_pos = c + r + k - row0[b];
+      const int col = at_pos / p.page_size;
+      int page = -1;
+      if (col < p.table_cols) {
+        const int f = page0[b] + col - held;
+        page = col < held ? p.table[(long long)b * p.table_cols + col] : f < p.n_free ? p.free_pages[f] : -1;
+      }
+      seq[k] = b;
+      pos[k] = at_pos;
+      slot[k] = page < 0 ? -1 : (int64_t)page * p.page_size + at_pos % p.page_size;
+      bad |= page < 0;
+    }
+    if (r + kPlanRows <= p.max_rows) {
+      *reinterpret_cast<int4*>(p.seq_of_row + r) = make_int4(seq[0], seq[1], seq[2], seq[3]);
+      longlong2* pp = reinterpret_cast<longlong2*>(p.pos + r);
+      longlong2* ps = reinterpret_cast<longlong2*>(p.slot + r);
+      pp[0] = make_longlong2(pos[0], pos[1]), pp[1] = make_longlong2(pos[2], pos[3]);
+      ps[0] = make_longlong2(slot[0], slot[1]), ps[1] = make_longlong2(slot[2], slot[3]);
+    } else {
+#pragma unroll
+      for (int k = 0; k < kPlanRows; ++k)
+        if (r + k < p.max_rows) p.seq_of_row[r + k] = seq[k], p.pos[r + k] = pos[k], p.slot[r + k] = slot[k];
+    }
+  }
+  if (bad && p.dev_status) atomicExch(p.dev_status, (int)CSA2_EDEVICE_INDEX);
+}
+
+// ----------------------------------------------------------------------------- rotary axes
+// y = R(angle) x for each pair of a head's rotary dims, angle = pos[axis] * theta^(-2i/R).  The
+// inverse turns by -angle, which is also the gradient: R is orthogonal.
+//
+// The angle is formed in turns as a 64-bit fixed-point product, position times frequency modulo one
+// turn: exact but for the frequency's own rounding to 2^-64 (53 bits of it significant), so that
+// positions of any size keep their full accuracy with one integer multiplication and no reduction.
+//
+// A thread owns one 16-byte piece of a token's head (for half-split pairs: the two pieces of
+// partners) and walks the heads with it, so that its angles' sines are formed once and stay in
+// registers.  Bound by memory: every element read and written once.
+template <typename T>
+struct Vec;
+template <>
+struct Vec<__nv_bfloat16> {
+  static constexpr int N = 8;
+  static __device__ __forceinline__ void get(uint4 u, float (&f)[8]) {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) f[2 * k] = bf16_lo(w[k]), f[2 * k + 1] = bf16_hi(w[k]);
+  }
+  static __device__ __forceinline__ uint4 put(const float (&f)[8]) {
+    return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
+  }
+};
+template <>
+struct Vec<__half> {
+  static constexpr int N = 8;
+  static __device__ __forceinline__ void get(uint4 u, float (&f)[8]) {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&w[k]));
+      f[2 * k] = v.x, f[2 * k + 1] = v.y;
+    }
+  }
+  static __device__ __forceinline__ uint4 put(const float (&f)[8]) {
+    return make_uint4(pack_f16x2(f[0], f[1]), pack_f16x2(f[2], f[3]), pack_f16x2(f[4], f[5]), pack_f16x2(f[6], f[7]));
+  }
+};
+template <>
+struct Vec<float> {
+  static constexpr int N = 4;
+  static __device__ __forceinline__ void get(uint4 u, float (&f)[4]) {
+    f[0] = __uint_as_float(u.x), f[1] = __uint_as_float(u.y), f[2] = __uint_as_float(u.z), f[3] = __uint_as_float(u.w);
+  }
+  static __device__ __forceinline__ uint4 put(const float (&f)[4]) {
+    return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
+  }
+};
+
+// Sine and cosine of pair i's angle at a position.
+__device__ __forceinline__ void turn(const RopeAxesParams& p, int i, int token, float& c, float& s) {
+  const int64_t at = __ldg(p.pos + (long long)p.axis[i] * p.n_tokens + token);
+  const int32_t frac = (int32_t)(((uint64_t)at * p.turns[i] + 0x80000000ull) >> 32);  // of a turn, nearest 2^-32
+  sincospif((float)frac * 4.656612873077393e-10f, &s, &c);                            // 2^-31: half turns
+}
+
+template <typename T, bool HALF, bool INV>
+__global__ void __launch_bounds__(256) rope_axes_kernel(const __grid_constant__ RopeAxesParams p, int pieces,
+                                                        int turned, int heads_per) {
+  constexpr int N = Vec<T>::N;
+  constexpr int NP = HALF ? N : N / 2;  // pairs of a piece
+  const long long u = (long long)blockIdx.x * blockDim.x + threadIdx.x;
+  const int token = (int)(u / pieces), piece = (int)(u - (long long)token * pieces);
+  if (token >= p.n_tokens) return;
+  const int h0 = blockIdx.y * heads_per, h1 = min(h0 + heads_per, p.n_heads);
+  const T* src = static_cast<const T*>(p.x) + token * p.x_row + h0 * p.x_head;
+  T* dst = static_cast<T*>(p.out) + token * p.out_row + h0 * p.out_head;
+  if (piece >= turned) {  // dims outside the rotary range
+    int d = (piece - turned) * N;
+    if (d >= p.rot_first) d += p.rot_dim;
+#pragma unroll 4
+    for (int h = h0; h < h1; ++h, src += p.x_head, dst += p.out_head)
+      *reinterpret_cast<uint4*>(dst + d) = *reinterpret_cast<const uint4*>(src + d);
+    return;
+  }
+  float c[NP], s[NP];
+#pragma unroll
+  for (int k = 0; k < NP; ++k) {
+    turn(p, piece * NP + k, token, c[k], s[k]);
+    if (INV) s[k] = -s[k];
+  }
+  const int d0 = p.rot_first + piece * N, d1 = d0 + p.rot_dim / 2;
+#pragma unroll 4
+  for (int h = h0; h < h1; ++h, src += p.x_head, dst += p.out_head) {
+    float a[N];
+    const uint4 ua = *reinterpret_cast<const uint4*>(src + d0);
+    if constexpr (HALF) {
+      const uint4 ub = *reinterpret_cast<const uint4*>(src + d1);
+      float b[N], x[N], y[N];
+      Vec<T>::get(ua, a);
+      Vec<T>::get(ub, b);
+#pragma unroll
+      for (int k = 0; k < N; ++k) x[k] = a[k] * c[k] - b[k] * s[k], y[k] = a[k] * s[k] + b[k] * c[k];
+      *reinterpret_cast<uint4*>(dst + d0) = Vec<T>::put(x);
+      *reinterpret_cast<uint4*>(dst + d1) = Vec<T>::put(y);
+    } else {
+      float x[N];
+      Vec<T>::get(ua, a);
+#pragma unroll
+      for (int k = 0; k < NP; ++k) {
+        x[2 * k] = a[2 * k] * c[k] - a[2 * k + 1] * s[k];
+        x[2 * k + 1] = a[2 * k] * s[k] + a[2 * k + 1] * c[k];
+      }
+      *reinterpret_cast<uint4*>(dst + d0) = Vec<T>::put(x);
+    }
+  }
+}
+
+template <typename T>
+cudaError_t rope_launch(const RopeAxesParams& p, bool half, bool inv, cudaStream_t stream) {
+  constexpr int N = Vec<T>::N;
+  const int turned = half ? p.rot_dim / 2 / N : p.rot_dim / N;
+  const int pieces = turned + (p.copy_rest ? (p.head_dim - p.rot_dim) / N : 0);
+  const long long threads = (long long)p.n_tokens * pieces;
+  const int blocks = (int)((threads + 255) / 256);
+  // heads split over blocks until some four blocks per SM are there
+  int per = p.n_heads;
+  while (per > 1 && (long long)blocks * ((p.n_heads + per - 1) / per) < 608) per = (per + 1) / 2;
+  const dim3 grid(blocks, (p.n_heads + per - 1) / per);
+  if (half) {
+    if (inv) rope_axes_kernel<T, true, true><<<grid, 256, 0, stream>>>(p, pieces, turned, per);
+    else rope_axes_kernel<T, true, false><<<grid, 256, 0, stream>>>(p, pieces, turned, per);
+  } else {
+    if (inv) rope_axes_kernel<T, false, true><<<grid, 256, 0, stream>>>(p, pieces, turned, per);
+    else rope_axes_kernel<T, false, false><<<grid, 256, 0, stream>>>(p, pieces, turned, per);
+  }
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_page_plan(const PagePlanParams& p, cudaStream_t stream) {
+  const int smem = 2 * (p.n_seq + 1) * (int)sizeof(int);
+  if (smem > 40 * 1024) {
+    const cudaError_t e = cudaFuncSetAttribute(page_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+  }
+  const long long per = (long long)kPlanThreads * kPlanRows;
+  long long blocks = (p.max_rows + per - 1) / per;
+  if (blocks > 152) blocks = 152;
+  if (blocks < 1) blocks = 1;
+  page_plan_kernel<<<(int)blocks, kPlanThreads, smem, stream>>>(p);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_rope_axes(const RopeAxesParams& p, int dtype, bool half_pairs, bool inverse, cudaStream_t stream) {
+  if (dtype == CSA2_T_BF16) return rope_launch<__nv_bfloat16>(p, half_pairs, inverse, stream);
+  if (dtype == CSA2_T_F16) return rope_launch<__half>(p, half_pairs, inverse, stream);
+  return rope_launch<float>(p, half_pairs, inverse, stream);
+}
+
+}  // namespace csa2
