@@ -14,18 +14,22 @@
 // sums, and a second kernel joins the pieces in order.
 //
 // Within a block each of the four warps streams its own 32 tokens of a unit through a ring in shared
-// memory (cp.async, two stages of K and of V; no block barrier until the tile's end) and keeps its own
-// running maximum, sum and output.
+// memory (TMA copies of 16 tokens of a page, two stages of K and of V; no block barrier until the
+// tile's end) and keeps its own running maximum, sum and output.
 //
-// Arithmetic.  K stays in its 8 bits: a query row, scaled by a power of two, is split into E4M3 pieces
-// (two hold a bf16's 8 bits, three an fp16's 11, below 2^-9 of a row maximum in [224, 448]), and the
-// scores are the sum of the pieces' E4M3 products in fp32: mma.m16n8k32 runs at twice the rate per
-// instruction of the fp16 form with twice its depth, and no conversion is needed.  V is converted to
-// fp16 (exact), weights are fp16 of exp2(z - max + 15), at most 2^15, so that weights down to 2^-29
-// of the largest keep 11 bits.  A page's V scale enters the weight relative to the largest seen.
-// Maxima, sums and outputs are fp32.
+// Arithmetic.  Tokens are the MMAs' rows and query rows their columns, eight to a column block, so that
+// the few query rows of a decode step fill the tensor cores' shape.  K stays in its 8 bits: a query
+// row, scaled by a power of two to a maximum in [224, 448), is split into E4M3 pieces (two hold a
+// bf16's 8 bits, three an fp16's 11, to 2^-10 absolute), and the scores are the sum of the pieces'
+// E4M3 products in fp32: mma.m16n8k32 runs at twice the fp16 form's rate per instruction with twice
+// its depth, and no conversion is needed.  V is converted to fp16 (exact), weights are fp16 of
+// exp2(z - max + 15), at most 2^15, so that weights down to 2^-29 of the largest keep 11 bits.  A
+// page's V scale enters the weight relative to the largest seen.  Maxima, sums and outputs are fp32.
+#include <cudaTypedefs.h>
+
 #include "common.cuh"
 #include "paged.h"
+#include "tc05.cuh"
 
 namespace csa2 {
 namespace {
@@ -76,7 +80,7 @@ __device__ __forceinline__ void store_row(const PagedAttnParams& p, int row, int
 struct Seq {
   int first, rows;     // its first query row; query rows x heads of a group
   int ctx, kv;         // position of its first query row; cached tokens
-  int lo, blocks;      // first token any row sees (down to a multiple of 16); units of a tile
+  int lo, blocks;      // first token any row sees, down to a step within its page; units of a tile
   int tiles;           // tiles of a kv head
   long long units;
 };
@@ -91,31 +95,63 @@ __device__ __forceinline__ Seq seq_of(const PagedAttnParams& p, int b) {
   s.ctx = kv - (r1 - r0);
   s.kv = (int)min((long long)kv, cap);
   s.rows = n * p.group;
-  s.lo = p.window > 0 ? max(s.ctx - p.window + 1, 0) & ~15 : 0;
+  s.lo = p.window > 0 ? max(s.ctx - p.window + 1, 0) & (p.page_shift == 4 ? ~15 : ~31) : 0;
   s.blocks = max((max(s.kv - s.lo, 0) + kUnit - 1) / kUnit, 1);
   s.tiles = (s.rows + NR - 1) / NR;
   s.units = (long long)s.tiles * p.kv_heads * s.blocks;
   return s;
 }
 
+// Byte offset of a 16-byte chunk of a row in a stage as the copies lay it out (rows of D bytes,
+// TMA's 128-byte or 64-byte swizzle): the lanes of a phase then meet different banks.
 template <int D>
-__device__ __forceinline__ int phys(int row, int chunk) {  // byte offset of a 16-byte chunk in a stage
-  // D = 128: chunk ^ row, so that the 8 lanes of a phase (two rows of K, four of V) meet 8 banks groups
-  return D == 128 ? row * 128 + ((chunk ^ (row & 7)) << 4) : row * 64 + (chunk << 4);
+__device__ __forceinline__ int phys(int row, int chunk) {
+  return row * D + ((D == 128 ? chunk ^ (row & 7) : chunk ^ ((row >> 1) & 3)) << 4);
+}
+__device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* tm, int x, int y, int z, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];\n" ::"r"(
+          smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(tm)), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
+      : "memory");
+}
+// 8x8 matrix of 16-bit values over a warp, transposed.
+__device__ __forceinline__ uint32_t transpose8(uint32_t v) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;\n" : "=r"(r) : "r"(v));
+  return r;
+}
+// The four codes of a register (low byte first) as two pairs of f16.
+__device__ __forceinline__ void f16_pairs(uint32_t v, uint32_t& lo, uint32_t& hi) {
+  asm("{\n .reg .b16 a, b;\n mov.b32 {a, b}, %2;\n cvt.rn.f16x2.e4m3x2 %0, a;\n cvt.rn.f16x2.e4m3x2 %1, b;\n}\n"
+      : "=r"(lo), "=r"(hi)
+      : "r"(v));
 }
 
-template <int D, int NR, int PIECES, bool F16>
-__global__ void __launch_bounds__(kWarps * 32, 3) paged_attn_kernel(const PagedAttnParams p) {
+struct CopyMaps {
+  CUtensorMap k, v;
+};
+
+template <int D, int NB, int PIECES, bool F16>
+__global__ void __launch_bounds__(kWarps * 32, NB == 1 ? 3 : 2)
+    paged_attn_kernel(const PagedAttnParams p, const __grid_constant__ CopyMaps maps) {
+  constexpr int NR = 8 * NB;            // query rows of a tile
   constexpr int KS = D / 32;            // MMA steps of a score
-  constexpr int NT = D / 8;             // MMA columns of an output
+  constexpr int MT = D / 16;            // MMA rows of an output, in sixteens
   constexpr int kStage = kTok * D;      // bytes of K (or V) of a step
-  constexpr bool FULL = NR == 16;       // rows 8 .. 15 in use
-  extern __shared__ __align__(128) uint8_t smem[];
+  constexpr int kHalf = kStage / 2;     // of 16 tokens: a copy
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   __shared__ __align__(16) float scales[kWarps][2][4];
-  __shared__ float ml[kWarps][16][3];
+  __shared__ __align__(8) uint64_t full[kWarps][4];  // K0 K1 V0 V1
+  __shared__ float ml[kWarps][NR][3];
   __shared__ long long scan_warp[kWarps];
   __shared__ long long place[2];        // sequence, its first unit
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, c = lane & 3;
+  if (tid == 0) {
+    for (int i = 0; i < kWarps * 4; ++i) tc05::mbar_init(&full[0][0] + i, 1);
+    tc05::fence_barrier_init();
+  }
 
   // ---- this block's piece of the line of units
   long long u, u_end;
@@ -164,8 +200,9 @@ __global__ void __launch_bounds__(kWarps * 32, 3) paged_attn_kernel(const PagedA
     b_first = place[1];
   }
   uint8_t* ring = smem + warp * 4 * kStage;  // K0 K1 V0 V1
+  uint32_t phases = 0;                       // bit of each barrier of `full`: parity of its next completion
   long long open_end = -1;
-  bool bad = false;
+  bool bad = false, dead = false;
 
   while (u < u_end) {
     const Seq s = seq_of<NR>(p, b);
@@ -179,38 +216,41 @@ __global__ void __launch_bounds__(kWarps * 32, 3) paged_attn_kernel(const PagedA
     const int head = (int)(item / s.tiles), tile = (int)(item - (long long)head * s.tiles);
     const int seg = (int)min((long long)(s.blocks - blk0), u_end - u);
     const int row0 = tile * NR, n = min(NR, s.rows - row0);
-    const int pos_last = s.ctx + (row0 + n - 1) / p.group;
+    const int pos_first = s.ctx + row0 / p.group, pos_last = s.ctx + (row0 + n - 1) / p.group;
     const int t_begin = s.lo + blk0 * kUnit;
     const int t_end = min(min(t_begin + seg * kUnit, s.kv), pos_last + 1);
-    // the two rows of this thread: their positions and their first token
-    const int ra = min(g, n - 1), rb = min(g + 8, n - 1);
-    const int pos_a = s.ctx + (row0 + ra) / p.group, pos_b = s.ctx + (row0 + rb) / p.group;
-    const int pos_first = s.ctx + row0 / p.group;
-    const int lo_a = p.window > 0 ? pos_a - p.window + 1 : 0, lo_b = p.window > 0 ? pos_b - p.window + 1 : 0;
     const int lo_last = p.window > 0 ? pos_last - p.window + 1 : 0;
 
-    // ---- loads: page ids one step ahead of the copies, copies one step ahead of their use
+    // ---- loads: page ids one step ahead of the copies, copies up to two steps ahead of their use
     const int32_t* trow = p.table + (long long)b * p.table_cols;
+    const int page_mask = (1 << p.page_shift) - 1;
     auto page_id = [&](int tok) -> int {  // -1: no such token, -2: a bad entry
       if (tok >= t_end) return -1;
       const int id = __ldg(trow + (tok >> p.page_shift));
       return (unsigned)id < (unsigned)p.n_pages ? id : -2;
     };
-    const int page_mask = (1 << p.page_shift) - 1;
-    auto copy = [&](const uint8_t* codes, uint8_t* to, int tok, int id0, int id1) {
-      const long long o0 = id0 < 0 ? 0 : ((((long long)id0 * p.kv_heads + head) << p.page_shift) + (tok & page_mask)) * D;
-      const long long o1 = id1 < 0 ? 0 : ((((long long)id1 * p.kv_heads + head) << p.page_shift) + ((tok + 16) & page_mask)) * D;
+    auto second_id = [&](int tok, int id0) -> int {  // pages of 32 tokens and more hold a whole step
+      return p.page_shift == 4 ? page_id(tok + 16) : id0;
+    };
+    auto copy = [&](const CUtensorMap* map, int which, int tok, int id0, int id1) {
+      uint8_t* to = ring + which * kStage;
+      uint64_t* bar = &full[warp][which];
+      if (id0 < 0 || id1 < 0) {  // a half without a page reads as zeros
 #pragma unroll
-      for (int i = 0; i < kStage / 512; ++i) {
-        const int chunk = i * 32 + lane, row = chunk / (D / 16), ch = chunk % (D / 16);
-        const bool second = i >= kStage / 1024;
-        const bool ok = (second ? id1 : id0) >= 0 && tok + row < t_end;
-        cp_async16(to + phys<D>(row, ch), codes + (second ? o1 : o0) + (ok ? (row & 15) * D + ch * 16 : 0), ok);
+        for (int i = 0; i < kStage / 512; ++i)
+          if ((i < kHalf / 512 ? id0 : id1) < 0) reinterpret_cast<uint4*>(to + 512 * i)[lane] = make_uint4(0, 0, 0, 0);
+        asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
+        __syncwarp();
+      }
+      if (lane == 0) {
+        tc05::mbar_expect_tx(bar, (id0 >= 0 ? kHalf : 0) + (id1 >= 0 ? kHalf : 0));
+        if (id0 >= 0) tma_load_3d(to, map, 0, tok & page_mask, id0 * p.kv_heads + head, bar);
+        if (id1 >= 0) tma_load_3d(to + kHalf, map, 0, (tok + 16) & page_mask, id1 * p.kv_heads + head, bar);
       }
     };
     auto copy_k = [&](int slot, int tok, int id0, int id1) {
       if (tok < t_end) {
-        copy(p.k, ring + slot * kStage, tok, id0, id1);
+        copy(&maps.k, slot, tok, id0, id1);
         if (lane < 4) {
           const int id = lane & 1 ? id1 : id0;
           const float* sc = lane < 2 ? p.k_scale : p.v_scale;
@@ -220,28 +260,32 @@ __global__ void __launch_bounds__(kWarps * 32, 3) paged_attn_kernel(const PagedA
       cp_async_commit();
     };
     auto copy_v = [&](int slot, int tok, int id0, int id1) {
-      if (tok < t_end) copy(p.v, ring + (2 + slot) * kStage, tok, id0, id1);
-      cp_async_commit();
+      if (tok < t_end) copy(&maps.v, 2 + slot, tok, id0, id1);
+    };
+    auto arrived = [&](int which) {
+      if (!dead && !tc05::mbar_wait(&full[warp][which], (phases >> which) & 1)) dead = true;
+      phases ^= 1u << which;
+      __syncwarp();
     };
     int tok = t_begin + warp * kTok;
-    int ida0 = page_id(tok), ida1 = page_id(tok + 16);
-    int idb0 = page_id(tok + kUnit), idb1 = page_id(tok + kUnit + 16);
+    int ida0 = page_id(tok), ida1 = second_id(tok, ida0);
+    int idb0 = page_id(tok + kUnit), idb1 = second_id(tok + kUnit, idb0);
     copy_k(0, tok, ida0, ida1);
     copy_v(0, tok, ida0, ida1);
     copy_k(1, tok + kUnit, idb0, idb1);
     copy_v(1, tok + kUnit, idb0, idb1);
 
-    // ---- the query rows as E4M3 pieces: this thread's dims are D/4 * c .. of rows g and g + 8
-    uint32_t qa[PIECES][KS][4];
-    float f_a, f_b;  // score in log2 units = f * sum of products * k_scale
+    // ---- the query rows as E4M3 pieces: this thread's dims are D/4 * c .. of rows 8 nb + g
+    uint32_t qb[NB][PIECES][KS][2];
+    float f[NB][2];   // rows 8 nb + 2c, + 1: score in log2 units = f * sum of products * k_scale
+    int pos[NB][2];   // their positions
 #pragma unroll
-    for (int half = 0; half < 2; ++half) {
+    for (int nb = 0; nb < NB; ++nb) {
       float x[D / 4];
-      const int r = g + 8 * half;
-      const bool has = r < n && (FULL || half == 0);
+      const int r = 8 * nb + g;
       float amax = 0.f;
       bool odd = false;
-      if (has) {
+      if (r < n) {
         const int rr = row0 + r, i = rr / p.group;
         const uint16_t* src = static_cast<const uint16_t*>(p.q) + (long long)(s.first + i) * p.q_row +
                               (long long)(head * p.group + rr - i * p.group) * p.q_head + D / 4 * c;
@@ -265,14 +309,13 @@ __global__ void __launch_bounds__(kWarps * 32, 3) paged_attn_kernel(const PagedA
       }
       amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
       amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-      odd = odd || __shfl_xor_sync(0xffffffffu, (int)odd, 1);
-      odd = odd || __shfl_xor_sync(0xffffffffu, (int)odd, 2);
+      odd = (__ballot_sync(0xffffffffu, odd) >> (4 * g) & 15u) != 0;
       // 2^e with amax / 2^e in [224, 448): e = exponent of amax - 8 (1.75 * 2^8 = 448), or one more
       const uint32_t ua = __float_as_uint(amax);
       int e = (int)(ua >> 23) - 127 - 8 + ((ua & 0x7fffffu) >= 0x600000u ? 1 : 0);
       e = min(max(e, -110), 119);
       const float down = __uint_as_float((uint32_t)(127 - e) << 23), up = __uint_as_float((uint32_t)(127 + e) << 23);
-      (half ? f_b : f_a) = odd ? __uint_as_float(0x7fc00000u) : p.scale_log2 * up;  // a NaN or infinity: the row is NaN
+      const float factor = odd ? __uint_as_float(0x7fc00000u) : p.scale_log2 * up;  // a NaN or infinity: the row is NaN
 #pragma unroll
       for (int k = 0; k < D / 4; ++k) x[k] = odd ? 0.f : x[k] * down;
 #pragma unroll
@@ -282,44 +325,61 @@ __global__ void __launch_bounds__(kWarps * 32, 3) paged_attn_kernel(const PagedA
 #pragma unroll
           for (int j = 0; j < 2; ++j) {  // words of 4 dims: j = 0 the MMA's k 4c .. , j = 1 its k 16 + 4c ..
             float* y = x + 8 * ks + 4 * j;
-            const uint32_t w0 = e4m3_pair(y[0], y[1]), w1 = e4m3_pair(y[2], y[3]);
-            qa[m][ks][2 * j + half] = w0 | w1 << 16;
+            const uint32_t w = e4m3_pair(y[0], y[1]) | e4m3_pair(y[2], y[3]) << 16;
+            qb[nb][m][ks][j] = w;
             if (m + 1 < PIECES) {
-              const uint32_t h0 = e4m3x2_to_f16x2((uint16_t)w0), h1 = e4m3x2_to_f16x2((uint16_t)w1);
+              uint32_t h0, h1;
+              f16_pairs(w, h0, h1);
               const float2 v0 = __half22float2(*reinterpret_cast<const __half2*>(&h0));
               const float2 v1 = __half22float2(*reinterpret_cast<const __half2*>(&h1));
               y[0] -= v0.x, y[1] -= v0.y, y[2] -= v1.x, y[3] -= v1.y;  // exact
             }
           }
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        f[nb][j] = __shfl_sync(0xffffffffu, factor, 4 * (2 * c + j));
+        pos[nb][j] = s.ctx + (row0 + min(8 * nb + 2 * c + j, n - 1)) / p.group;
+      }
     }
 
-    float acc[NT][4];
+    float acc[MT][NB][4];
 #pragma unroll
-    for (int i = 0; i < NT; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
-    float m_a = -INFINITY, m_b = -INFINITY, l_a = 0.f, l_b = 0.f, vref = 0.f, vinv = 0.f;
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb) acc[i][nb][0] = acc[i][nb][1] = acc[i][nb][2] = acc[i][nb][3] = 0.f;
+    float m[NB][2], l[NB][2], vref = 0.f, vinv = 0.f;
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) m[nb][0] = m[nb][1] = -INFINITY, l[nb][0] = l[nb][1] = 0.f;
 
-    for (int slot = 0; tok < t_end; tok += kUnit, slot ^= 1) {
-      const int idc0 = page_id(tok + 2 * kUnit), idc1 = page_id(tok + 2 * kUnit + 16);
+    for (int slot = 0; tok < t_end && !dead; tok += kUnit, slot ^= 1) {
+      const int idc0 = page_id(tok + 2 * kUnit), idc1 = second_id(tok + 2 * kUnit, idc0);
       bad |= ida0 == -2 || ida1 == -2;
-      cp_async_wait<3>();
-      __syncwarp();
-      // ---- scores of 32 tokens: S[4][4], token 8t + (column)
-      float S[4][4];
+      cp_async_wait<1>();
+      arrived(slot);
+      // ---- scores of 32 tokens: S[half][rows of 8][..], tokens 16 half + g (0, 1) and + 8 (2, 3), rows 2c, 2c + 1
+      float S[2][NB][4];
       const uint8_t* kt = ring + slot * kStage;
 #pragma unroll
-      for (int t = 0; t < 4; ++t) {
-        uint32_t w[2 * KS];
-        const int row = 8 * t + g;
+      for (int h = 0; h < 2; ++h) {
+        uint32_t wa[2 * KS], wb[2 * KS];
 #pragma unroll
-        for (int h = 0; h < D / 64; ++h) {
-          const uint4 v = *reinterpret_cast<const uint4*>(kt + phys<D>(row, D / 64 * c + h));
-          w[4 * h] = v.x, w[4 * h + 1] = v.y, w[4 * h + 2] = v.z, w[4 * h + 3] = v.w;
+        for (int k = 0; k < D / 64; ++k) {
+          const uint4 v = *reinterpret_cast<const uint4*>(kt + phys<D>(16 * h + g, D / 64 * c + k));
+          const uint4 x = *reinterpret_cast<const uint4*>(kt + phys<D>(16 * h + 8 + g, D / 64 * c + k));
+          wa[4 * k] = v.x, wa[4 * k + 1] = v.y, wa[4 * k + 2] = v.z, wa[4 * k + 3] = v.w;
+          wb[4 * k] = x.x, wb[4 * k + 1] = x.y, wb[4 * k + 2] = x.z, wb[4 * k + 3] = x.w;
         }
-        S[t][0] = S[t][1] = S[t][2] = S[t][3] = 0.f;
 #pragma unroll
-        for (int m = 0; m < PIECES; ++m)
+        for (int nb = 0; nb < NB; ++nb) {
+          S[h][nb][0] = S[h][nb][1] = S[h][nb][2] = S[h][nb][3] = 0.f;
 #pragma unroll
-          for (int ks = 0; ks < KS; ++ks) mma_e4m3(S[t], qa[m][ks], w[2 * ks], w[2 * ks + 1]);
+          for (int q = 0; q < PIECES; ++q)
+#pragma unroll
+            for (int ks = 0; ks < KS; ++ks) {
+              const uint32_t a[4] = {wa[2 * ks], wb[2 * ks], wa[2 * ks + 1], wb[2 * ks + 1]};
+              mma_e4m3(S[h][nb], a, qb[nb][q][ks][0], qb[nb][q][ks][1]);
+            }
+        }
       }
       const float4 sc = *reinterpret_cast<const float4*>(scales[warp][slot]);  // k scales, v scales
       __syncwarp();
@@ -328,73 +388,87 @@ __global__ void __launch_bounds__(kWarps * 32, 3) paged_attn_kernel(const PagedA
       // a NaN in either scale marks the page: its visible tokens give NaN
       const float k0 = sc.x + 0.f * sc.z, k1 = sc.y + 0.f * sc.w;
       const bool whole = tok + kTok - 1 <= min(pos_first, t_end - 1) && tok >= lo_last && ida0 >= 0 && ida1 >= 0;
+      bool grows = false;
 #pragma unroll
-      for (int t = 0; t < 4; ++t) {
-        const float ks = t < 2 ? k0 : k1;
-        S[t][0] *= f_a * ks, S[t][1] *= f_a * ks;
-        if (FULL) S[t][2] *= f_b * ks, S[t][3] *= f_b * ks;
+      for (int nb = 0; nb < NB; ++nb) {
+        const float fa0 = f[nb][0] * k0, fb0 = f[nb][1] * k0, fa1 = f[nb][0] * k1, fb1 = f[nb][1] * k1;
+        S[0][nb][0] *= fa0, S[0][nb][1] *= fb0, S[0][nb][2] *= fa0, S[0][nb][3] *= fb0;
+        S[1][nb][0] *= fa1, S[1][nb][1] *= fb1, S[1][nb][2] *= fa1, S[1][nb][3] *= fb1;
       }
       if (!whole) {
 #pragma unroll
-        for (int t = 0; t < 4; ++t)
+        for (int h = 0; h < 2; ++h)
 #pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            const int at = tok + 8 * t + 2 * c + j;
-            const bool there = (t < 2 ? ida0 : ida1) >= 0 && at < t_end;
-            if (!(there && at <= pos_a && at >= lo_a)) S[t][j] = -INFINITY;
-            if (FULL && !(there && at <= pos_b && at >= lo_b)) S[t][2 + j] = -INFINITY;
+          for (int j = 0; j < 4; ++j) {
+            const int at = tok + 16 * h + 8 * (j >> 1) + g;
+            const bool there = (h ? ida1 : ida0) >= 0 && at < t_end;
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb) {
+              const int ps = pos[nb][j & 1];
+              if (!(there && at <= ps && (p.window == 0 || at > ps - p.window))) S[h][nb][j] = -INFINITY;
+            }
           }
       }
-      float x_a = m_a, x_b = m_b;
+      float top[NB][2];
 #pragma unroll
-      for (int t = 0; t < 4; ++t) {
-        x_a = fmaxf(x_a, fmaxf(S[t][0], S[t][1]));
-        if (FULL) x_b = fmaxf(x_b, fmaxf(S[t][2], S[t][3]));
-      }
-      x_a = fmaxf(x_a, __shfl_xor_sync(0xffffffffu, x_a, 1));
-      x_a = fmaxf(x_a, __shfl_xor_sync(0xffffffffu, x_a, 2));
-      if (FULL) {
-        x_b = fmaxf(x_b, __shfl_xor_sync(0xffffffffu, x_b, 1));
-        x_b = fmaxf(x_b, __shfl_xor_sync(0xffffffffu, x_b, 2));
-      }
-      float v0 = sc.z, v1 = sc.w;
-      if (!(v0 > 0.f)) v0 = 0.f;
-      if (!(v1 > 0.f)) v1 = 0.f;
-      const float vnew = fmaxf(vref, fmaxf(v0, v1));
-      if (__any_sync(0xffffffffu, x_a > m_a || (FULL && x_b > m_b) || vnew > vref)) {
+      for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          top[nb][j] = fmaxf(fmaxf(S[0][nb][j], S[0][nb][2 + j]), fmaxf(S[1][nb][j], S[1][nb][2 + j]));
+          grows |= top[nb][j] > m[nb][j];
+        }
+      const float v0 = sc.z > 0.f ? sc.z : 0.f, v1 = sc.w > 0.f ? sc.w : 0.f;
+      grows |= fmaxf(v0, v1) > vref;
+      if (__any_sync(0xffffffffu, grows)) {  // a new maximum, of a row or of the V scales: what is there moves to it
+        const float vnew = fmaxf(vref, fmaxf(v0, v1));
         if (vnew > vref) vinv = __fdiv_rn(1.f, vnew);
         const float vf = vref * vinv;
-        const float e_a = m_a == -INFINITY ? 0.f : ex2(m_a - x_a), e_b = FULL && m_b > -INFINITY ? ex2(m_b - x_b) : 0.f;
-        l_a *= e_a, l_b *= e_b;
-        const float o_a = e_a * vf, o_b = e_b * vf;
+        vref = vnew;
 #pragma unroll
-        for (int i = 0; i < NT; ++i) {
-          acc[i][0] *= o_a, acc[i][1] *= o_a;
-          if (FULL) acc[i][2] *= o_b, acc[i][3] *= o_b;
-        }
-        m_a = x_a, m_b = x_b, vref = vnew;
-      }
-      const float c0 = v0 * vinv, c1 = v1 * vinv;
-      const float s_a = m_a == -INFINITY ? 0.f : kLift - m_a, s_b = m_b == -INFINITY ? 0.f : kLift - m_b;
-      uint32_t pw[4][2];
+        for (int nb = 0; nb < NB; ++nb) {
+          float o[2];
 #pragma unroll
-      for (int t = 0; t < 4; ++t) {
-        const float cv = t < 2 ? c0 : c1;
-        const float p0 = ex2(S[t][0] + s_a), p1 = ex2(S[t][1] + s_a);
-        l_a += p0 + p1;
-        pw[t][0] = pack_f16x2(p0 * cv, p1 * cv);
-        if (FULL) {
-          const float p2 = ex2(S[t][2] + s_b), p3 = ex2(S[t][3] + s_b);
-          l_b += p2 + p3;
-          pw[t][1] = pack_f16x2(p2 * cv, p3 * cv);
-        } else {
-          pw[t][1] = 0u;
+          for (int j = 0; j < 2; ++j) {
+            float x = fmaxf(top[nb][j], m[nb][j]);
+            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+            const float e = m[nb][j] == -INFINITY ? 0.f : ex2(m[nb][j] - x);
+            l[nb][j] *= e;
+            o[j] = e * vf;
+            m[nb][j] = x;
+          }
+#pragma unroll
+          for (int i = 0; i < MT; ++i)
+            acc[i][nb][0] *= o[0], acc[i][nb][1] *= o[1], acc[i][nb][2] *= o[0], acc[i][nb][3] *= o[1];
         }
       }
-      // ---- outputs: two steps of 16 tokens; this thread's tokens 2c, 2c + 1, 2c + 8, 2c + 9, dims D/8 * g ..
-      cp_async_wait<3>();
-      __syncwarp();
-      const uint8_t* vt = ring + (2 + slot) * kStage;
+      uint32_t pw[2][NB][2];
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb) {
+        const float s0 = m[nb][0] == -INFINITY ? 0.f : kLift - m[nb][0], s1 = m[nb][1] == -INFINITY ? 0.f : kLift - m[nb][1];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const float cv = (h ? v1 : v0) * vinv;
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const float p0 = ex2(S[h][nb][2 * j] + s0), p1 = ex2(S[h][nb][2 * j + 1] + s1);
+            l[nb][0] += p0, l[nb][1] += p1;
+            pw[h][nb][j] = transpose8(pack_f16x2(p0 * cv, p1 * cv));
+          }
+        }
+      }
+      // ---- outputs: this thread's tokens 2c, 2c + 1, 2c + 8, 2c + 9 of each half, dims D/8 * g ..
+      arrived(2 + slot);
+      uint8_t* vt = ring + (2 + slot) * kStage;
+      if (tok + kTok > t_end) {  // slots behind the last token may hold anything: 0 * NaN is not 0
+        if (tok + lane >= t_end) {
+#pragma unroll
+          for (int k = 0; k < D / 16; ++k) *reinterpret_cast<uint4*>(vt + lane * D + 16 * k) = make_uint4(0, 0, 0, 0);
+        }
+        asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
+        __syncwarp();
+      }
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         constexpr int W = D / 32;  // words of D/8 dims
@@ -406,21 +480,18 @@ __global__ void __launch_bounds__(kWarps * 32, 3) paged_attn_kernel(const PagedA
             const uint4 v = *reinterpret_cast<const uint4*>(vt + phys<D>(row, g));
             w[j][0] = v.x, w[j][1] = v.y, w[j][2] = v.z, w[j][3] = v.w;
           } else {
-            const uint2 v = *reinterpret_cast<const uint2*>(vt + row * 64 + 8 * g);
+            const uint2 v = *reinterpret_cast<const uint2*>(vt + phys<D>(row, g >> 1) + 8 * (g & 1));
             w[j][0] = v.x, w[j][1] = v.y;
           }
         }
 #pragma unroll
-        for (int k = 0; k < W; ++k) {
-          const uint32_t lo0 = __byte_perm(w[0][k], w[1][k], 0x5140), hi0 = __byte_perm(w[0][k], w[1][k], 0x7362);
-          const uint32_t lo1 = __byte_perm(w[2][k], w[3][k], 0x5140), hi1 = __byte_perm(w[2][k], w[3][k], 0x7362);
+        for (int i = 0; i < MT; ++i) {  // dims D/8 * g + 2i, + 1
+          const int k = i >> 1, sel = i & 1 ? 0x7362 : 0x5140;
+          uint32_t a0, a1, a2, a3;
+          f16_pairs(__byte_perm(w[0][k], w[1][k], sel), a0, a1);
+          f16_pairs(__byte_perm(w[2][k], w[3][k], sel), a2, a3);
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const uint32_t b0 = j < 2 ? lo0 : hi0, b1 = j < 2 ? lo1 : hi1;
-            mma_f16(acc[4 * k + j], pw[2 * h][0], pw[2 * h][1], pw[2 * h + 1][0], pw[2 * h + 1][1],
-                    e4m3x2_to_f16x2((uint16_t)(j & 1 ? b0 >> 16 : b0 & 0xffffu)),
-                    e4m3x2_to_f16x2((uint16_t)(j & 1 ? b1 >> 16 : b1 & 0xffffu)));
-          }
+          for (int nb = 0; nb < NB; ++nb) mma_f16(acc[i][nb], a0, a1, a2, a3, pw[h][nb][0], pw[h][nb][1]);
         }
       }
       __syncwarp();
@@ -430,28 +501,34 @@ __global__ void __launch_bounds__(kWarps * 32, 3) paged_attn_kernel(const PagedA
     cp_async_wait<0>();
 
     // ---- the four warps' sums joined
-    l_a += __shfl_xor_sync(0xffffffffu, l_a, 1);
-    l_a += __shfl_xor_sync(0xffffffffu, l_a, 2);
-    if (FULL) {
-      l_b += __shfl_xor_sync(0xffffffffu, l_b, 1);
-      l_b += __shfl_xor_sync(0xffffffffu, l_b, 2);
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        l[nb][j] += __shfl_xor_sync(0xffffffffu, l[nb][j], 4);
+        l[nb][j] += __shfl_xor_sync(0xffffffffu, l[nb][j], 8);
+        l[nb][j] += __shfl_xor_sync(0xffffffffu, l[nb][j], 16);
+      }
+    if (__syncthreads_or(dead)) {  // a copy never came: nothing of this block's is in flight any more that will
+      if (tid == 0) {
+        if (p.dev_status) atomicExch(p.dev_status, (int)CSA2_ETIMEOUT);
+        p.open[blockIdx.x].end = -1;
+      }
+      return;
     }
-    __syncthreads();  // every warp has left its ring
     float* part = reinterpret_cast<float*>(smem);  // [warp][NR][D]
-    {
-      float* to = part + (warp * NR + g) * D + D / 4 * c;
 #pragma unroll
-      for (int k = 0; k < 2; ++k)
+    for (int nb = 0; nb < NB; ++nb) {
 #pragma unroll
-        for (int i = 0; i < NT; i += 4) {
-          *reinterpret_cast<float4*>(to + k * NT + i) = make_float4(acc[i][k], acc[i + 1][k], acc[i + 2][k], acc[i + 3][k]);
-          if (FULL)
-            *reinterpret_cast<float4*>(to + 8 * D + k * NT + i) =
-                make_float4(acc[i][2 + k], acc[i + 1][2 + k], acc[i + 2][2 + k], acc[i + 3][2 + k]);
+      for (int j = 0; j < 2; ++j) {
+        float* to = part + (warp * NR + 8 * nb + 2 * c + j) * D + D / 8 * g;
+#pragma unroll
+        for (int i = 0; i < MT; i += 2)
+          *reinterpret_cast<float4*>(to + 2 * i) = make_float4(acc[i][nb][j], acc[i][nb][2 + j], acc[i + 1][nb][j], acc[i + 1][nb][2 + j]);
+        if (g == 0) {
+          float* to_ml = ml[warp][8 * nb + 2 * c + j];
+          to_ml[0] = m[nb][j], to_ml[1] = l[nb][j], to_ml[2] = vref;
         }
-      if (c == 0) {
-        ml[warp][g][0] = m_a, ml[warp][g][1] = l_a, ml[warp][g][2] = vref;
-        if (FULL) ml[warp][g + 8][0] = m_b, ml[warp][g + 8][1] = l_b, ml[warp][g + 8][2] = vref;
       }
     }
     __syncthreads();
@@ -467,10 +544,10 @@ __global__ void __launch_bounds__(kWarps * 32, 3) paged_attn_kernel(const PagedA
       for (int w = 0; w < kWarps; ++w) {
         const float mw = ml[w][r][0];
         if (mw == -INFINITY && ml[w][r][1] == 0.f) continue;  // a warp that saw nothing (not one whose sum is NaN)
-        const float e = mw == -INFINITY ? 1.f : ex2(mw - M), f = e * ml[w][r][2];
+        const float e = mw == -INFINITY ? 1.f : ex2(mw - M), fw = e * ml[w][r][2];
         const float4 a = *reinterpret_cast<const float4*>(part + (w * NR + r) * D + d);
         L += ml[w][r][1] * e;
-        o.x += a.x * f, o.y += a.y * f, o.z += a.z * f, o.w += a.w * f;
+        o.x += a.x * fw, o.y += a.y * fw, o.z += a.z * fw, o.w += a.w * fw;
       }
       if (starts && ends) {
         const int rr = row0 + r, tokn = rr / p.group, hq = head * p.group + rr - tokn * p.group;
@@ -485,6 +562,7 @@ __global__ void __launch_bounds__(kWarps * 32, 3) paged_attn_kernel(const PagedA
       o.row0 = row0, o.n = n, o.first_row = s.first, o.kv_head = head;
     }
     open_end = starts && !ends ? u - blk0 + s.blocks : -1;
+    asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
     __syncthreads();  // the sums are read before the ring is filled again
     u += seg;
     if (u == b_first + s.units) {
@@ -529,13 +607,41 @@ __global__ void __launch_bounds__(128) paged_join_kernel(const PagedAttnParams p
   }
 }
 
-template <int D, int NR, int PIECES, bool F16>
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      f = nullptr;
+    return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
+  }();
+  return fn;
+}
+
+// Codes as [pages x heads, page, dim]; a copy takes 16 tokens of a page.
+bool make_map(CUtensorMap* map, const uint8_t* codes, const PagedAttnParams& p, int dim) {
+  if (p.n_pages == 0 || p.table_cols == 0) return true;  // no page is ever read
+  const PFN_cuTensorMapEncodeTiled_v12000 fn = encode_fn();
+  if (fn == nullptr) return false;
+  const cuuint64_t page = 1ull << p.page_shift;
+  const cuuint64_t dims[3] = {(cuuint64_t)dim, page, (cuuint64_t)p.n_pages * p.kv_heads};
+  const cuuint64_t strides[2] = {(cuuint64_t)dim, dim * page};
+  const cuuint32_t box[3] = {(cuuint32_t)dim, 16, 1}, one[3] = {1, 1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<uint8_t*>(codes), dims, strides, box, one,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, dim == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D, int NB, int PIECES, bool F16>
 cudaError_t launch(const PagedAttnParams& p, int blocks, cudaStream_t stream) {
-  constexpr int smem = kWarps * 4 * kTok * D;
-  static_assert(smem >= kWarps * NR * D * 4, "the joined sums fit the ring");
-  cudaError_t e = cudaFuncSetAttribute(paged_attn_kernel<D, NR, PIECES, F16>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  constexpr int smem = kWarps * 4 * kTok * D + 1024;
+  static_assert(smem - 1024 >= kWarps * 8 * NB * D * 4, "the joined sums fit the ring");
+  CopyMaps maps{};
+  if (!make_map(&maps.k, p.k, p, D) || !make_map(&maps.v, p.v, p, D)) return cudaErrorNotSupported;
+  cudaError_t e = cudaFuncSetAttribute(paged_attn_kernel<D, NB, PIECES, F16>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  paged_attn_kernel<D, NR, PIECES, F16><<<blocks, kWarps * 32, smem, stream>>>(p);
+  paged_attn_kernel<D, NB, PIECES, F16><<<blocks, kWarps * 32, smem, stream>>>(p, maps);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
@@ -556,11 +662,11 @@ cudaError_t launch_paged_attn(const PagedAttnParams& p, int q_dtype, int head_di
                               cudaStream_t stream) {
   const bool f16 = q_dtype == CSA2_T_F16;
   if (head_dim == 128) {
-    if (f16) return rows8 ? launch<128, 8, 3, true>(p, blocks, stream) : launch<128, 16, 3, true>(p, blocks, stream);
-    return rows8 ? launch<128, 8, 2, false>(p, blocks, stream) : launch<128, 16, 2, false>(p, blocks, stream);
+    if (f16) return rows8 ? launch<128, 1, 3, true>(p, blocks, stream) : launch<128, 2, 3, true>(p, blocks, stream);
+    return rows8 ? launch<128, 1, 2, false>(p, blocks, stream) : launch<128, 2, 2, false>(p, blocks, stream);
   }
-  if (f16) return rows8 ? launch<64, 8, 3, true>(p, blocks, stream) : launch<64, 16, 3, true>(p, blocks, stream);
-  return rows8 ? launch<64, 8, 2, false>(p, blocks, stream) : launch<64, 16, 2, false>(p, blocks, stream);
+  if (f16) return rows8 ? launch<64, 1, 3, true>(p, blocks, stream) : launch<64, 2, 3, true>(p, blocks, stream);
+  return rows8 ? launch<64, 1, 2, false>(p, blocks, stream) : launch<64, 2, 2, false>(p, blocks, stream);
 }
 
 }  // namespace csa2
