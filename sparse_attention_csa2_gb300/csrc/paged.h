@@ -58,10 +58,10 @@ struct PageWriteParams {
 };
 cudaError_t launch_page_write(const PageWriteParams& p, int dtype, int head_dim, cudaStream_t stream);
 
-// What a block of the split attention leaves open: the item whose last unit it computed lies
-// beyond its range.  end < 0: nothing is open.
+// What a block of the split attention leaves open: a tile whose last unit lies beyond its range, in so
+// many pieces (its own and one of each block after it); 0: nothing is open.
 struct PagedOpen {
-  long long end;                    // one past the item's last unit
+  int pieces;
   int row0;                         // first row of the tile within the sequence's rows x heads
   int n;                            // its rows
   int first_row;                    // the sequence's first query row
@@ -88,7 +88,6 @@ struct PagedAttnParams {
   float* part_o;                    // [2 * blocks, 16, dim]
   float* part_ml;                   // [2 * blocks, 16, 2]
   PagedOpen* open;                  // [blocks]
-  long long* units;                 // [1] all units of the call
   int32_t* dev_status;
 };
 cudaError_t launch_paged_attn(const PagedAttnParams& p, int q_dtype, int head_dim, bool rows8, int blocks,

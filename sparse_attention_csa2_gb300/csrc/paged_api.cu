@@ -24,7 +24,7 @@ int page_shift(int32_t page) { return page == 16 ? 4 : page == 32 ? 5 : page == 
 struct AttnPlan {
   bool rows8;
   int blocks;
-  size_t part_o, part_ml, open, units, bytes;
+  size_t part_o, part_ml, open, bytes;
 };
 AttnPlan attn_plan(const csa2_paged_attn_args* a) {
   AttnPlan pl{};
@@ -42,7 +42,6 @@ AttnPlan attn_plan(const csa2_paged_attn_args* a) {
   pl.part_o = at, at += align_up(slots * a->head_dim * 4);
   pl.part_ml = at, at += align_up(slots * 8);
   pl.open = at, at += align_up((size_t)pl.blocks * sizeof(PagedOpen));
-  pl.units = at, at += align_up(8);
   pl.bytes = at;
   return pl;
 }
@@ -187,7 +186,6 @@ csa2_status csa2_paged_attn(const csa2_paged_attn_args* a, void* stream) {
   p.part_o = reinterpret_cast<float*>(ws + pl.part_o);
   p.part_ml = reinterpret_cast<float*>(ws + pl.part_ml);
   p.open = reinterpret_cast<PagedOpen*>(ws + pl.open);
-  p.units = reinterpret_cast<long long*>(ws + pl.units);
   p.dev_status = a->dev_status;
   return cuda_status(launch_paged_attn(p, a->q_dtype, a->head_dim, pl.rows8, pl.blocks, static_cast<cudaStream_t>(stream)));
 }

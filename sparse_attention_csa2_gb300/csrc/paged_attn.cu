@@ -14,8 +14,8 @@
 // sums, and a second kernel joins the pieces in order.
 //
 // Within a block each of the four warps streams its own 32 tokens of a unit through a ring in shared
-// memory (TMA copies of 16 tokens of a page, two stages of K and of V; no block barrier until the
-// tile's end) and keeps its own running maximum, sum and output.
+// memory (TMA copies of 16 tokens of a page, two stages of K and of V, four at dim 64; no block barrier
+// until the tile's end) and keeps its own running maximum, sum and output.
 //
 // Arithmetic.  Tokens are the MMAs' rows and query rows their columns, eight to a column block, so that
 // the few query rows of a decode step fill the tensor cores' shape.  K stays in its 8 bits: a query
@@ -128,34 +128,42 @@ __device__ __forceinline__ void f16_pairs(uint32_t v, uint32_t& lo, uint32_t& hi
       : "r"(v));
 }
 
+// Stages of the ring: 64 KB a block.
+template <int D>
+constexpr int kStages = 256 / D;
+
 struct CopyMaps {
   CUtensorMap k, v;
 };
 
 template <int D, int NB, int PIECES, bool F16>
-__global__ void __launch_bounds__(kWarps * 32, NB == 1 ? 3 : 2)
+__global__ void __launch_bounds__(kWarps * 32, 3)
     paged_attn_kernel(const PagedAttnParams p, const __grid_constant__ CopyMaps maps) {
   constexpr int NR = 8 * NB;            // query rows of a tile
   constexpr int KS = D / 32;            // MMA steps of a score
   constexpr int MT = D / 16;            // MMA rows of an output, in sixteens
   constexpr int kStage = kTok * D;      // bytes of K (or V) of a step
   constexpr int kHalf = kStage / 2;     // of 16 tokens: a copy
+  constexpr int ST = kStages<D>;
+  constexpr bool QS = NB > 1;           // the query pieces lie in shared memory: two column blocks of them
+                                        // and of outputs do not fit the registers of three blocks per SM
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-  __shared__ __align__(16) float scales[kWarps][2][4];
-  __shared__ __align__(8) uint64_t full[kWarps][4];  // K0 K1 V0 V1
+  __shared__ __align__(16) float scales[kWarps][ST][4];
+  __shared__ __align__(8) uint64_t full[kWarps][2 * ST];  // K stages, V stages
+  __shared__ __align__(16) uint2 qs[QS ? NB * PIECES * KS * 32 : 1];
   __shared__ float ml[kWarps][NR][3];
   __shared__ long long scan_warp[kWarps];
   __shared__ long long place[2];        // sequence, its first unit
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, c = lane & 3;
   if (tid == 0) {
-    for (int i = 0; i < kWarps * 4; ++i) tc05::mbar_init(&full[0][0] + i, 1);
+    for (int i = 0; i < kWarps * 2 * ST; ++i) tc05::mbar_init(&full[0][0] + i, 1);
     tc05::fence_barrier_init();
   }
 
   // ---- this block's piece of the line of units
-  long long u, u_end;
-  int b;
+  long long u, u_end, all;
+  int b, used;
   long long b_first;
   {
     const int run = (p.n_seq + kWarps * 32 - 1) / (kWarps * 32);
@@ -177,9 +185,10 @@ __global__ void __launch_bounds__(kWarps * 32, NB == 1 ? 3 : 2)
       total += scan_warp[w];
     }
     before += x - mine;
-    u = total * blockIdx.x / gridDim.x;
-    u_end = total * (blockIdx.x + 1) / gridDim.x;
-    if (blockIdx.x == 0 && tid == 0) p.units[0] = total;
+    used = (int)min((long long)gridDim.x, total);  // blocks with work: every one of them has some
+    u = (int)blockIdx.x < used ? total * blockIdx.x / used : 0;
+    u_end = (int)blockIdx.x < used ? total * (blockIdx.x + 1) / used : 0;
+    all = total;
     if (u < u_end && before <= u && u < before + mine) {
       long long at = before;
       int i = q0;
@@ -193,15 +202,15 @@ __global__ void __launch_bounds__(kWarps * 32, NB == 1 ? 3 : 2)
     }
     __syncthreads();
     if (u >= u_end) {
-      if (tid == 0) p.open[blockIdx.x].end = -1;
+      if (tid == 0) p.open[blockIdx.x].pieces = 0;
       return;
     }
     b = (int)place[0];
     b_first = place[1];
   }
-  uint8_t* ring = smem + warp * 4 * kStage;  // K0 K1 V0 V1
+  uint8_t* ring = smem + warp * 2 * ST * kStage;  // K stages, V stages
   uint32_t phases = 0;                       // bit of each barrier of `full`: parity of its next completion
-  long long open_end = -1;
+  int pieces = 0;                            // of the tile that this block leaves open
   bool bad = false, dead = false;
 
   while (u < u_end) {
@@ -260,7 +269,7 @@ __global__ void __launch_bounds__(kWarps * 32, NB == 1 ? 3 : 2)
       cp_async_commit();
     };
     auto copy_v = [&](int slot, int tok, int id0, int id1) {
-      if (tok < t_end) copy(&maps.v, 2 + slot, tok, id0, id1);
+      if (tok < t_end) copy(&maps.v, ST + slot, tok, id0, id1);
     };
     auto arrived = [&](int which) {
       if (!dead && !tc05::mbar_wait(&full[warp][which], (phases >> which) & 1)) dead = true;
@@ -268,15 +277,25 @@ __global__ void __launch_bounds__(kWarps * 32, NB == 1 ? 3 : 2)
       __syncwarp();
     };
     int tok = t_begin + warp * kTok;
-    int ida0 = page_id(tok), ida1 = second_id(tok, ida0);
-    int idb0 = page_id(tok + kUnit), idb1 = second_id(tok + kUnit, idb0);
-    copy_k(0, tok, ida0, ida1);
-    copy_v(0, tok, ida0, ida1);
-    copy_k(1, tok + kUnit, idb0, idb1);
-    copy_v(1, tok + kUnit, idb0, idb1);
+    uint32_t okay = 0;  // two bits a stage: its halves have pages
+    auto note = [&](int slot, int id0, int id1) {
+      okay = (okay & ~(3u << 2 * slot)) | (uint32_t)((id0 >= 0) | (id1 >= 0) << 1) << 2 * slot;
+      bad |= id0 == -2 || id1 == -2;
+    };
+    {
+      int id0[ST], id1[ST];
+#pragma unroll
+      for (int i = 0; i < ST; ++i) id0[i] = page_id(tok + i * kUnit), id1[i] = second_id(tok + i * kUnit, id0[i]);
+#pragma unroll
+      for (int i = 0; i < ST; ++i) {
+        note(i, id0[i], id1[i]);
+        copy_k(i, tok + i * kUnit, id0[i], id1[i]);
+        copy_v(i, tok + i * kUnit, id0[i], id1[i]);
+      }
+    }
 
     // ---- the query rows as E4M3 pieces: this thread's dims are D/4 * c .. of rows 8 nb + g
-    uint32_t qb[NB][PIECES][KS][2];
+    uint32_t qb[QS ? 1 : NB][PIECES][KS][2];
     float f[NB][2];   // rows 8 nb + 2c, + 1: score in log2 units = f * sum of products * k_scale
     int pos[NB][2];   // their positions
 #pragma unroll
@@ -326,7 +345,11 @@ __global__ void __launch_bounds__(kWarps * 32, NB == 1 ? 3 : 2)
           for (int j = 0; j < 2; ++j) {  // words of 4 dims: j = 0 the MMA's k 4c .. , j = 1 its k 16 + 4c ..
             float* y = x + 8 * ks + 4 * j;
             const uint32_t w = e4m3_pair(y[0], y[1]) | e4m3_pair(y[2], y[3]) << 16;
-            qb[nb][m][ks][j] = w;
+            if (QS) {
+              if (warp == nb % kWarps) reinterpret_cast<uint32_t*>(qs + ((nb * PIECES + m) * KS + ks) * 32 + lane)[j] = w;
+            } else {
+              qb[nb][m][ks][j] = w;
+            }
             if (m + 1 < PIECES) {
               uint32_t h0, h1;
               f16_pairs(w, h0, h1);
@@ -342,6 +365,8 @@ __global__ void __launch_bounds__(kWarps * 32, NB == 1 ? 3 : 2)
       }
     }
 
+    if (QS) __syncthreads();
+
     float acc[MT][NB][4];
 #pragma unroll
     for (int i = 0; i < MT; ++i)
@@ -351,10 +376,11 @@ __global__ void __launch_bounds__(kWarps * 32, NB == 1 ? 3 : 2)
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) m[nb][0] = m[nb][1] = -INFINITY, l[nb][0] = l[nb][1] = 0.f;
 
-    for (int slot = 0; tok < t_end && !dead; tok += kUnit, slot ^= 1) {
-      const int idc0 = page_id(tok + 2 * kUnit), idc1 = second_id(tok + 2 * kUnit, idc0);
-      bad |= ida0 == -2 || ida1 == -2;
-      cp_async_wait<1>();
+    for (int slot = 0; tok < t_end && !dead; tok += kUnit, slot = slot + 1 == ST ? 0 : slot + 1) {
+      const int next = tok + ST * kUnit;
+      const int idc0 = page_id(next), idc1 = second_id(next, idc0);
+      const bool ok0 = okay >> 2 * slot & 1, ok1 = okay >> 2 * slot & 2;
+      cp_async_wait<ST - 1>();
       arrived(slot);
       // ---- scores of 32 tokens: S[half][rows of 8][..], tokens 16 half + g (0, 1) and + 8 (2, 3), rows 2c, 2c + 1
       float S[2][NB][4];
@@ -377,17 +403,21 @@ __global__ void __launch_bounds__(kWarps * 32, NB == 1 ? 3 : 2)
 #pragma unroll
             for (int ks = 0; ks < KS; ++ks) {
               const uint32_t a[4] = {wa[2 * ks], wb[2 * ks], wa[2 * ks + 1], wb[2 * ks + 1]};
-              mma_e4m3(S[h][nb], a, qb[nb][q][ks][0], qb[nb][q][ks][1]);
+              uint2 b2;
+              if (QS) b2 = qs[((nb * PIECES + q) * KS + ks) * 32 + lane];
+              else b2 = make_uint2(qb[nb][q][ks][0], qb[nb][q][ks][1]);
+              mma_e4m3(S[h][nb], a, b2.x, b2.y);
             }
         }
       }
       const float4 sc = *reinterpret_cast<const float4*>(scales[warp][slot]);  // k scales, v scales
       __syncwarp();
-      copy_k(slot, tok + 2 * kUnit, idc0, idc1);
+      note(slot, idc0, idc1);
+      copy_k(slot, next, idc0, idc1);
 
       // a NaN in either scale marks the page: its visible tokens give NaN
       const float k0 = sc.x + 0.f * sc.z, k1 = sc.y + 0.f * sc.w;
-      const bool whole = tok + kTok - 1 <= min(pos_first, t_end - 1) && tok >= lo_last && ida0 >= 0 && ida1 >= 0;
+      const bool whole = tok + kTok - 1 <= min(pos_first, t_end - 1) && tok >= lo_last && ok0 && ok1;
       bool grows = false;
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb) {
@@ -401,7 +431,7 @@ __global__ void __launch_bounds__(kWarps * 32, NB == 1 ? 3 : 2)
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             const int at = tok + 16 * h + 8 * (j >> 1) + g;
-            const bool there = (h ? ida1 : ida0) >= 0 && at < t_end;
+            const bool there = (h ? ok1 : ok0) && at < t_end;
 #pragma unroll
             for (int nb = 0; nb < NB; ++nb) {
               const int ps = pos[nb][j & 1];
@@ -459,8 +489,8 @@ __global__ void __launch_bounds__(kWarps * 32, NB == 1 ? 3 : 2)
         }
       }
       // ---- outputs: this thread's tokens 2c, 2c + 1, 2c + 8, 2c + 9 of each half, dims D/8 * g ..
-      arrived(2 + slot);
-      uint8_t* vt = ring + (2 + slot) * kStage;
+      arrived(ST + slot);
+      uint8_t* vt = ring + (ST + slot) * kStage;
       if (tok + kTok > t_end) {  // slots behind the last token may hold anything: 0 * NaN is not 0
         if (tok + lane >= t_end) {
 #pragma unroll
@@ -495,8 +525,7 @@ __global__ void __launch_bounds__(kWarps * 32, NB == 1 ? 3 : 2)
         }
       }
       __syncwarp();
-      copy_v(slot, tok + 2 * kUnit, idc0, idc1);
-      ida0 = idb0, ida1 = idb1, idb0 = idc0, idb1 = idc1;
+      copy_v(slot, next, idc0, idc1);
     }
     cp_async_wait<0>();
 
@@ -512,7 +541,7 @@ __global__ void __launch_bounds__(kWarps * 32, NB == 1 ? 3 : 2)
     if (__syncthreads_or(dead)) {  // a copy never came: nothing of this block's is in flight any more that will
       if (tid == 0) {
         if (p.dev_status) atomicExch(p.dev_status, (int)CSA2_ETIMEOUT);
-        p.open[blockIdx.x].end = -1;
+        p.open[blockIdx.x].pieces = 0;
       }
       return;
     }
@@ -561,7 +590,8 @@ __global__ void __launch_bounds__(kWarps * 32, NB == 1 ? 3 : 2)
       PagedOpen& o = p.open[blockIdx.x];
       o.row0 = row0, o.n = n, o.first_row = s.first, o.kv_head = head;
     }
-    open_end = starts && !ends ? u - blk0 + s.blocks : -1;
+    // the block of the tile's last unit w: the largest x with all * x / used <= w
+    pieces = starts && !ends ? (int)(((u + s.blocks) * used - 1) / all) - (int)blockIdx.x + 1 : 0;
     asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
     __syncthreads();  // the sums are read before the ring is filled again
     u += seg;
@@ -570,41 +600,73 @@ __global__ void __launch_bounds__(kWarps * 32, NB == 1 ? 3 : 2)
       ++b;
     }
   }
-  if (tid == 0) p.open[blockIdx.x].end = open_end;
+  if (tid == 0) p.open[blockIdx.x].pieces = pieces;
   if (bad && p.dev_status && lane == 0) atomicExch(p.dev_status, (int)CSA2_EDEVICE_INDEX);
 }
 
 // Joins the pieces of the tile that block x of the attention left open: its own sums and those of the
-// blocks after it up to the tile's end, in that order.  blockIdx.y takes every gridDim.y-th row.
+// blocks after it up to the tile's end.  A block takes a row: its warps take the pieces in turn (every
+// load independent of the others), then are summed in order.
+constexpr int kJoinWarps = 4;
 template <int D>
-__global__ void __launch_bounds__(128) paged_join_kernel(const PagedAttnParams p) {
+__global__ void __launch_bounds__(kJoinWarps * 32) paged_join_kernel(const PagedAttnParams p) {
+  __shared__ float weight[kJoinWarps][32];
+  __shared__ float4 sum[kJoinWarps][D / 4];
+  __shared__ float2 stat[kJoinWarps];
   asm volatile("griddepcontrol.wait;\n" ::: "memory");
   const PagedOpen o = p.open[blockIdx.x];
-  if (o.end < 0) return;
-  const long long total = p.units[0];
-  int last = blockIdx.x + 1;  // blocks blockIdx.x + 1 .. last - 1 computed the rest
-  while (last < (int)gridDim.x && total * last / gridDim.x < o.end) ++last;
-  constexpr int L4 = D / 4, ROWS = 128 / L4;
-  const int d = threadIdx.x % L4 * 4;
-  for (int r = threadIdx.x / L4 + ROWS * blockIdx.y; r < o.n; r += ROWS * gridDim.y) {
-    float M = -INFINITY, L = 0.f;
-    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int x = blockIdx.x; x < last; ++x) {
-      const int slot = 2 * x + (x == (int)blockIdx.x ? 1 : 0);
-      const long long at = (long long)slot * 16 + r;
-      if (total * x / gridDim.x == total * (x + 1) / gridDim.x) continue;  // a block without units wrote nothing
-      const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + at * 2);
-      const float4 v = *reinterpret_cast<const float4*>(p.part_o + at * D + d);
-      if (ml.x == -INFINITY && ml.y == 0.f) continue;
-      const float m = fmaxf(M, ml.x);
-      const float e0 = M == -INFINITY ? 1.f : ex2(M - m), e1 = ml.x == -INFINITY ? 1.f : ex2(ml.x - m);
-      a.x = a.x * e0 + v.x * e1, a.y = a.y * e0 + v.y * e1, a.z = a.z * e0 + v.z * e1, a.w = a.w * e0 + v.w * e1;
-      L = L * e0 + ml.y * e1;
-      M = m;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  constexpr int L4 = D / 4, SUB = 32 / L4;  // lanes of a piece, pieces of a warp's load
+  const int r = blockIdx.y;
+  if (o.pieces == 0 || r >= o.n) return;
+  const float* part = p.part_o + (2LL * blockIdx.x * 16 + r) * D + lane % L4 * 4;  // a piece further: 32 rows further
+  const float* part_ml = p.part_ml + (2LL * blockIdx.x * 16 + r) * 2;
+  auto at = [](int i) { return i == 0 ? 16 : 32 * i; };  // row of piece i: the first block's second slot, then first slots
+  float M = -INFINITY, L = 0.f;
+  float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int i0 = 0; i0 < o.pieces; i0 += 32 * kJoinWarps) {  // a round: pieces i0 + warp, + 4, ..
+    const int mine = i0 + lane * kJoinWarps + warp;
+    const float2 ml = mine < o.pieces ? *reinterpret_cast<const float2*>(part_ml + 2 * at(mine)) : make_float2(-INFINITY, 0.f);
+    const float m = fmaxf(M, warp_max(ml.x));
+    const float old = M == -INFINITY ? 1.f : ex2(M - m);
+    const float w = ml.x == -INFINITY ? (ml.y == 0.f ? 0.f : 1.f) : ex2(ml.x - m);
+    weight[warp][lane] = w;
+    __syncwarp();
+    L = L * old + warp_sum(ml.y * w);
+    a.x *= old, a.y *= old, a.z *= old, a.w *= old;
+    M = m;
+    const int n = min(32, (o.pieces - i0 - warp + kJoinWarps - 1) / kJoinWarps);
+#pragma unroll 8
+    for (int i = lane / L4; i < n; i += SUB) {
+      const float f = weight[warp][i];
+      const float4 v = *reinterpret_cast<const float4*>(part + (long long)at(i0 + i * kJoinWarps + warp) * D);
+      a.x += v.x * f, a.y += v.y * f, a.z += v.z * f, a.w += v.w * f;
     }
-    const int rr = o.row0 + r, tokn = rr / p.group, hq = o.kv_head * p.group + rr - tokn * p.group;
-    store_row<D>(p, o.first_row + tokn, hq, d, a, M, L);
+    __syncwarp();
   }
+  if (SUB == 2) {
+    a.x += __shfl_xor_sync(0xffffffffu, a.x, 16), a.y += __shfl_xor_sync(0xffffffffu, a.y, 16);
+    a.z += __shfl_xor_sync(0xffffffffu, a.z, 16), a.w += __shfl_xor_sync(0xffffffffu, a.w, 16);
+  }
+  if (lane < L4) sum[warp][lane] = a;
+  if (lane == 0) stat[warp] = make_float2(M, L);
+  __syncthreads();
+  if (threadIdx.x >= L4) return;
+  float T = -INFINITY, N = 0.f;
+  float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+  for (int w = 0; w < kJoinWarps; ++w) T = fmaxf(T, stat[w].x);
+#pragma unroll
+  for (int w = 0; w < kJoinWarps; ++w) {
+    const float2 ml = stat[w];
+    if (ml.x == -INFINITY && ml.y == 0.f) continue;
+    const float f = ml.x == -INFINITY ? 1.f : ex2(ml.x - T);
+    const float4 v = sum[w][threadIdx.x];
+    N += ml.y * f;
+    t.x += v.x * f, t.y += v.y * f, t.z += v.z * f, t.w += v.w * f;
+  }
+  const int rr = o.row0 + r, tokn = rr / p.group, hq = o.kv_head * p.group + rr - tokn * p.group;
+  store_row<D>(p, o.first_row + tokn, hq, threadIdx.x * 4, t, T, N);
 }
 
 PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
@@ -635,7 +697,7 @@ bool make_map(CUtensorMap* map, const uint8_t* codes, const PagedAttnParams& p, 
 
 template <int D, int NB, int PIECES, bool F16>
 cudaError_t launch(const PagedAttnParams& p, int blocks, cudaStream_t stream) {
-  constexpr int smem = kWarps * 4 * kTok * D + 1024;
+  constexpr int smem = kWarps * 2 * kStages<D> * kTok * D + 1024;
   static_assert(smem - 1024 >= kWarps * 8 * NB * D * 4, "the joined sums fit the ring");
   CopyMaps maps{};
   if (!make_map(&maps.k, p.k, p, D) || !make_map(&maps.v, p.v, p, D)) return cudaErrorNotSupported;
@@ -645,8 +707,8 @@ cudaError_t launch(const PagedAttnParams& p, int blocks, cudaStream_t stream) {
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(blocks, 4);
-  cfg.blockDim = dim3(128);
+  cfg.gridDim = dim3(blocks, 8 * NB);
+  cfg.blockDim = dim3(kJoinWarps * 32);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
