@@ -23,8 +23,9 @@
 // bf16's 8 bits, three an fp16's 11, to 2^-10 absolute), and the scores are the sum of the pieces'
 // E4M3 products in fp32: mma.m16n8k32 runs at twice the fp16 form's rate per instruction with twice
 // its depth, and no conversion is needed.  V is converted to fp16 (exact), weights are fp16 of
-// exp2(z - max + 15), at most 2^15, so that weights down to 2^-29 of the largest keep 11 bits.  A
-// page's V scale enters the weight relative to the largest seen.  Maxima, sums and outputs are fp32.
+// exp2(z - max + 11), where the maximum follows a larger score only when that exceeds it by 2^4:
+// weights are at most 2^15, those down to 2^-21 of the largest keep 11 bits, and the output is rarely
+// rescaled.  A page's V scale enters the weight relative to the largest seen.  Maxima, sums and outputs are fp32.
 #include <cudaTypedefs.h>
 
 #include "common.cuh"
@@ -37,7 +38,8 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kTok = 32;                // tokens of a warp's step
 constexpr int kUnit = kWarps * kTok;    // tokens of a unit
-constexpr float kLift = 15.f;           // weights are held times 2^15
+constexpr float kLift = 11.f;           // weights are held times 2^11,
+constexpr float kSlack = 4.f;           // relative to a maximum that may be 2^4 too small
 constexpr float kLog2e = 1.4426950408889634f;
 
 __device__ __forceinline__ float ex2(float x) {
@@ -445,7 +447,7 @@ __global__ void __launch_bounds__(kWarps * 32, 3)
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
           top[nb][j] = fmaxf(fmaxf(S[0][nb][j], S[0][nb][2 + j]), fmaxf(S[1][nb][j], S[1][nb][2 + j]));
-          grows |= top[nb][j] > m[nb][j];
+          grows |= top[nb][j] > m[nb][j] + kSlack;
         }
       const float v0 = sc.z > 0.f ? sc.z : 0.f, v1 = sc.w > 0.f ? sc.w : 0.f;
       grows |= fmaxf(v0, v1) > vref;
