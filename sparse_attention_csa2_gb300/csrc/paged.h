@@ -85,12 +85,18 @@ struct PagedAttnParams {
   const float* sink;
   void* out;                        // [n_rows, kv_heads * group, dim]
   int out_dtype;
-  float* part_o;                    // [2 * blocks, 16, dim]
-  float* part_ml;                   // [2 * blocks, 16, 2]
+  float* part_o;                    // [2 * blocks, rows of a tile, dim]: a block's first tile where it began before
+  float* part_ml;                   // [.., 2] the block, its last where it goes on behind it
   PagedOpen* open;                  // [blocks]
   int32_t* dev_status;
 };
+// Few query rows per (sequence, kv head): tiles of 8 or 16.
 cudaError_t launch_paged_attn(const PagedAttnParams& p, int q_dtype, int head_dim, bool rows8, int blocks,
                               cudaStream_t stream);
+
+// Many: tiles of 256.
+cudaError_t launch_paged_wide(const PagedAttnParams& p, int q_dtype, int head_dim, int blocks, cudaStream_t stream);
+// The open tiles' pieces; both launch it.
+cudaError_t launch_paged_join(const PagedAttnParams& p, int head_dim, int rows, int blocks, cudaStream_t stream);
 
 }  // namespace csa2

@@ -19,26 +19,27 @@ int type_size(int32_t t) { return t == CSA2_T_F32 ? 4 : 2; }
 bool stride_ok(int64_t row, int64_t head, int32_t t) { return row % (16 / type_size(t)) == 0 && head % (16 / type_size(t)) == 0; }
 int page_shift(int32_t page) { return page == 16 ? 4 : page == 32 ? 5 : page == 64 ? 6 : page == 128 ? 7 : 0; }
 
-// Blocks of the split attention: three per SM, and no more than there can be units (a tile has at
-// most the table's tokens, a sequence one tile more than its rows fill).
+// Which kernel, and its workspace.  Up to 16 query rows per sequence and kv head in the mean take the
+// split attention, three blocks per SM; more take tiles of 256, one block per SM.  No more blocks than
+// there can be units of 128 tokens (a tile has at most the table's, a sequence one tile more than its
+// rows fill).
 struct AttnPlan {
-  bool rows8;
+  int rows;  // of a tile: 8, 16 or 256
   int blocks;
   size_t part_o, part_ml, open, bytes;
 };
 AttnPlan attn_plan(const csa2_paged_attn_args* a) {
   AttnPlan pl{};
   const long long group = a->heads / a->kv_heads;
-  pl.rows8 = group <= 8 && (long long)a->n_rows <= a->n_seq;
-  const int nr = pl.rows8 ? 8 : 16;
-  const long long tiles = ((long long)a->n_rows * group + nr - 1) / nr + a->n_seq;
-  const long long blocks = ((long long)a->table_cols * a->page_size + 127) / 128;
-  const long long most = 3LL * device_sm_count();
-  const double units = (double)tiles * a->kv_heads * (blocks < 1 ? 1 : blocks);
-  pl.blocks = units < (double)most ? (int)units : (int)most;
-  if (pl.blocks < 1) pl.blocks = 1;
+  const bool wide = a->n_rows * group > 16LL * a->n_seq && a->n_seq <= 16384;
+  pl.rows = wide ? 256 : group <= 8 && a->n_rows <= a->n_seq ? 8 : 16;
+  const long long tiles = ((long long)a->n_rows * group + pl.rows - 1) / pl.rows + a->n_seq;
+  const long long units = ((long long)a->table_cols * a->page_size + 127) / 128 + 1;
+  const long long most = (wide ? 1 : 3) * device_sm_count();
+  const double all = (double)tiles * a->kv_heads * units;
+  pl.blocks = all < (double)most ? (int)all : (int)most;
   size_t at = 0;
-  const size_t slots = 2 * (size_t)pl.blocks * 16;
+  const size_t slots = 2 * (size_t)pl.blocks * pl.rows;
   pl.part_o = at, at += align_up(slots * a->head_dim * 4);
   pl.part_ml = at, at += align_up(slots * 8);
   pl.open = at, at += align_up((size_t)pl.blocks * sizeof(PagedOpen));
@@ -187,7 +188,9 @@ csa2_status csa2_paged_attn(const csa2_paged_attn_args* a, void* stream) {
   p.part_ml = reinterpret_cast<float*>(ws + pl.part_ml);
   p.open = reinterpret_cast<PagedOpen*>(ws + pl.open);
   p.dev_status = a->dev_status;
-  return cuda_status(launch_paged_attn(p, a->q_dtype, a->head_dim, pl.rows8, pl.blocks, static_cast<cudaStream_t>(stream)));
+  cudaStream_t on = static_cast<cudaStream_t>(stream);
+  return cuda_status(pl.rows == 256 ? launch_paged_wide(p, a->q_dtype, a->head_dim, pl.blocks, on)
+                                    : launch_paged_attn(p, a->q_dtype, a->head_dim, pl.rows == 8, pl.blocks, on));
 }
 
 }  // extern "C"

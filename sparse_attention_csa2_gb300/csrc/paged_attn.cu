@@ -30,6 +30,7 @@
 
 #include "common.cuh"
 #include "paged.h"
+#include "paged_dev.cuh"
 #include "tc05.cuh"
 
 namespace csa2 {
@@ -38,15 +39,6 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kTok = 32;                // tokens of a warp's step
 constexpr int kUnit = kWarps * kTok;    // tokens of a unit
-constexpr float kLift = 11.f;           // weights are held times 2^11,
-constexpr float kSlack = 4.f;           // relative to a maximum that may be 2^4 too small
-constexpr float kLog2e = 1.4426950408889634f;
-
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
-  return y;
-}
 __device__ __forceinline__ void mma_e4m3(float* c, const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm volatile(
       "mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
@@ -60,46 +52,17 @@ __device__ __forceinline__ uint32_t e4m3_pair(float lo, float hi) {
   return r;
 }
 
-// Four values of an output row: sums o relative to maximum M (log2 units) over the row's denominator.
-// A row that saw no key is 0.
-template <int D>
-__device__ __forceinline__ void store_row(const PagedAttnParams& p, int row, int head, int d, float4 o, float M, float L) {
-  float den = L;
-  if (p.sink != nullptr && M > -INFINITY) den += ex2(p.sink[head] * kLog2e - M + kLift);
-  const float inv = L == 0.f ? 0.f : __fdividef(1.f, den);
-  const long long at = ((long long)row * (p.kv_heads * p.group) + head) * D + d;
-  o.x *= inv, o.y *= inv, o.z *= inv, o.w *= inv;
-  if (p.out_dtype == CSA2_T_F32) {
-    *reinterpret_cast<float4*>(static_cast<float*>(p.out) + at) = o;
-  } else {
-    const bool h = p.out_dtype == CSA2_T_F16;
-    const uint2 u = h ? make_uint2(pack_f16x2(o.x, o.y), pack_f16x2(o.z, o.w)) : make_uint2(pack_bf16x2(o.x, o.y), pack_bf16x2(o.z, o.w));
-    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + at) = u;
-  }
-}
-
-// The rows and units of one sequence.
-struct Seq {
-  int first, rows;     // its first query row; query rows x heads of a group
-  int ctx, kv;         // position of its first query row; cached tokens
+// A sequence with its units.
+struct Seq : PagedSeq {
   int lo, blocks;      // first token any row sees, down to a step within its page; units of a tile
-  int tiles;           // tiles of a kv head
   long long units;
 };
 template <int NR>
 __device__ __forceinline__ Seq seq_of(const PagedAttnParams& p, int b) {
   Seq s;
-  const int r0 = p.row_start[b], r1 = p.row_start[b + 1];
-  s.first = min(max(r0, 0), p.n_rows);
-  const int n = max(min(r1, p.n_rows) - s.first, 0);
-  const long long cap = (long long)p.table_cols << p.page_shift;
-  const int kv = max(p.kv_len[b], 0);
-  s.ctx = kv - (r1 - r0);
-  s.kv = (int)min((long long)kv, cap);
-  s.rows = n * p.group;
+  static_cast<PagedSeq&>(s) = paged_seq<NR>(p, b);
   s.lo = p.window > 0 ? max(s.ctx - p.window + 1, 0) & (p.page_shift == 4 ? ~15 : ~31) : 0;
   s.blocks = max((max(s.kv - s.lo, 0) + kUnit - 1) / kUnit, 1);
-  s.tiles = (s.rows + NR - 1) / NR;
   s.units = (long long)s.tiles * p.kv_heads * s.blocks;
   return s;
 }
@@ -123,13 +86,6 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t v) {
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;\n" : "=r"(r) : "r"(v));
   return r;
 }
-// The four codes of a register (low byte first) as two pairs of f16.
-__device__ __forceinline__ void f16_pairs(uint32_t v, uint32_t& lo, uint32_t& hi) {
-  asm("{\n .reg .b16 a, b;\n mov.b32 {a, b}, %2;\n cvt.rn.f16x2.e4m3x2 %0, a;\n cvt.rn.f16x2.e4m3x2 %1, b;\n}\n"
-      : "=r"(lo), "=r"(hi)
-      : "r"(v));
-}
-
 // Stages of the ring: 64 KB a block.
 template <int D>
 constexpr int kStages = 256 / D;
@@ -447,7 +403,7 @@ __global__ void __launch_bounds__(kWarps * 32, 3)
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
           top[nb][j] = fmaxf(fmaxf(S[0][nb][j], S[0][nb][2 + j]), fmaxf(S[1][nb][j], S[1][nb][2 + j]));
-          grows |= top[nb][j] > m[nb][j] + kSlack;
+          grows |= top[nb][j] > m[nb][j] + kPagedSlack;
         }
       const float v0 = sc.z > 0.f ? sc.z : 0.f, v1 = sc.w > 0.f ? sc.w : 0.f;
       grows |= fmaxf(v0, v1) > vref;
@@ -478,7 +434,7 @@ __global__ void __launch_bounds__(kWarps * 32, 3)
       uint32_t pw[2][NB][2];
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb) {
-        const float s0 = m[nb][0] == -INFINITY ? 0.f : kLift - m[nb][0], s1 = m[nb][1] == -INFINITY ? 0.f : kLift - m[nb][1];
+        const float s0 = m[nb][0] == -INFINITY ? 0.f : kPagedLift - m[nb][0], s1 = m[nb][1] == -INFINITY ? 0.f : kPagedLift - m[nb][1];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           const float cv = (h ? v1 : v0) * vinv;
@@ -582,10 +538,10 @@ __global__ void __launch_bounds__(kWarps * 32, 3)
       }
       if (starts && ends) {
         const int rr = row0 + r, tokn = rr / p.group, hq = head * p.group + rr - tokn * p.group;
-        store_row<D>(p, s.first + tokn, hq, d, o, M, L);
+        paged_store<D>(p, s.first + tokn, hq, d, o, M, L);
       } else {
-        *reinterpret_cast<float4*>(p.part_o + ((long long)slot_of * 16 + r) * D + d) = o;
-        if (d == 0) *reinterpret_cast<float2*>(p.part_ml + ((long long)slot_of * 16 + r) * 2) = make_float2(M, L);
+        *reinterpret_cast<float4*>(p.part_o + ((long long)slot_of * NR + r) * D + d) = o;
+        if (d == 0) *reinterpret_cast<float2*>(p.part_ml + ((long long)slot_of * NR + r) * 2) = make_float2(M, L);
       }
     }
     if (starts && !ends && tid == 0) {
@@ -604,71 +560,6 @@ __global__ void __launch_bounds__(kWarps * 32, 3)
   }
   if (tid == 0) p.open[blockIdx.x].pieces = pieces;
   if (bad && p.dev_status && lane == 0) atomicExch(p.dev_status, (int)CSA2_EDEVICE_INDEX);
-}
-
-// Joins the pieces of the tile that block x of the attention left open: its own sums and those of the
-// blocks after it up to the tile's end.  A block takes a row: its warps take the pieces in turn (every
-// load independent of the others), then are summed in order.
-constexpr int kJoinWarps = 4;
-template <int D>
-__global__ void __launch_bounds__(kJoinWarps * 32) paged_join_kernel(const PagedAttnParams p) {
-  __shared__ float weight[kJoinWarps][32];
-  __shared__ float4 sum[kJoinWarps][D / 4];
-  __shared__ float2 stat[kJoinWarps];
-  asm volatile("griddepcontrol.wait;\n" ::: "memory");
-  const PagedOpen o = p.open[blockIdx.x];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  constexpr int L4 = D / 4, SUB = 32 / L4;  // lanes of a piece, pieces of a warp's load
-  const int r = blockIdx.y;
-  if (o.pieces == 0 || r >= o.n) return;
-  const float* part = p.part_o + (2LL * blockIdx.x * 16 + r) * D + lane % L4 * 4;  // a piece further: 32 rows further
-  const float* part_ml = p.part_ml + (2LL * blockIdx.x * 16 + r) * 2;
-  auto at = [](int i) { return i == 0 ? 16 : 32 * i; };  // row of piece i: the first block's second slot, then first slots
-  float M = -INFINITY, L = 0.f;
-  float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int i0 = 0; i0 < o.pieces; i0 += 32 * kJoinWarps) {  // a round: pieces i0 + warp, + 4, ..
-    const int mine = i0 + lane * kJoinWarps + warp;
-    const float2 ml = mine < o.pieces ? *reinterpret_cast<const float2*>(part_ml + 2 * at(mine)) : make_float2(-INFINITY, 0.f);
-    const float m = fmaxf(M, warp_max(ml.x));
-    const float old = M == -INFINITY ? 1.f : ex2(M - m);
-    const float w = ml.x == -INFINITY ? (ml.y == 0.f ? 0.f : 1.f) : ex2(ml.x - m);
-    weight[warp][lane] = w;
-    __syncwarp();
-    L = L * old + warp_sum(ml.y * w);
-    a.x *= old, a.y *= old, a.z *= old, a.w *= old;
-    M = m;
-    const int n = min(32, (o.pieces - i0 - warp + kJoinWarps - 1) / kJoinWarps);
-#pragma unroll 8
-    for (int i = lane / L4; i < n; i += SUB) {
-      const float f = weight[warp][i];
-      const float4 v = *reinterpret_cast<const float4*>(part + (long long)at(i0 + i * kJoinWarps + warp) * D);
-      a.x += v.x * f, a.y += v.y * f, a.z += v.z * f, a.w += v.w * f;
-    }
-    __syncwarp();
-  }
-  if (SUB == 2) {
-    a.x += __shfl_xor_sync(0xffffffffu, a.x, 16), a.y += __shfl_xor_sync(0xffffffffu, a.y, 16);
-    a.z += __shfl_xor_sync(0xffffffffu, a.z, 16), a.w += __shfl_xor_sync(0xffffffffu, a.w, 16);
-  }
-  if (lane < L4) sum[warp][lane] = a;
-  if (lane == 0) stat[warp] = make_float2(M, L);
-  __syncthreads();
-  if (threadIdx.x >= L4) return;
-  float T = -INFINITY, N = 0.f;
-  float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-  for (int w = 0; w < kJoinWarps; ++w) T = fmaxf(T, stat[w].x);
-#pragma unroll
-  for (int w = 0; w < kJoinWarps; ++w) {
-    const float2 ml = stat[w];
-    if (ml.x == -INFINITY && ml.y == 0.f) continue;
-    const float f = ml.x == -INFINITY ? 1.f : ex2(ml.x - T);
-    const float4 v = sum[w][threadIdx.x];
-    N += ml.y * f;
-    t.x += v.x * f, t.y += v.y * f, t.z += v.z * f, t.w += v.w * f;
-  }
-  const int rr = o.row0 + r, tokn = rr / p.group, hq = o.kv_head * p.group + rr - tokn * p.group;
-  store_row<D>(p, o.first_row + tokn, hq, threadIdx.x * 4, t, T, N);
 }
 
 PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
@@ -707,17 +598,7 @@ cudaError_t launch(const PagedAttnParams& p, int blocks, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   paged_attn_kernel<D, NB, PIECES, F16><<<blocks, kWarps * 32, smem, stream>>>(p, maps);
   e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(blocks, 8 * NB);
-  cfg.blockDim = dim3(kJoinWarps * 32);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, paged_join_kernel<D>, p);
+  return e != cudaSuccess ? e : launch_paged_join(p, D, 8 * NB, blocks, stream);
 }
 
 }  // namespace

@@ -1,0 +1,66 @@
+// What the two forms of the paged attention and their join share.
+#pragma once
+
+#include "common.cuh"
+#include "paged.h"
+
+namespace csa2 {
+
+constexpr float kPagedLift = 11.f;   // weights are held times 2^11,
+constexpr float kPagedSlack = 4.f;   // relative to a maximum that may be 2^4 too small
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// The four codes of a register (low byte first) as two pairs of f16.
+__device__ __forceinline__ void f16_pairs(uint32_t v, uint32_t& lo, uint32_t& hi) {
+  asm("{\n .reg .b16 a, b;\n mov.b32 {a, b}, %2;\n cvt.rn.f16x2.e4m3x2 %0, a;\n cvt.rn.f16x2.e4m3x2 %1, b;\n}\n"
+      : "=r"(lo), "=r"(hi)
+      : "r"(v));
+}
+
+// Four values of an output row: sums o relative to maximum M (log2 units) over the row's denominator.
+// A row that saw no key is 0.
+template <int D>
+__device__ __forceinline__ void paged_store(const PagedAttnParams& p, int row, int head, int d, float4 o, float M, float L) {
+  float den = L;
+  if (p.sink != nullptr && M > -INFINITY) den += ex2(p.sink[head] * 1.4426950408889634f - M + kPagedLift);
+  const float inv = L == 0.f ? 0.f : __fdividef(1.f, den);
+  const long long at = ((long long)row * (p.kv_heads * p.group) + head) * D + d;
+  o.x *= inv, o.y *= inv, o.z *= inv, o.w *= inv;
+  if (p.out_dtype == CSA2_T_F32) {
+    *reinterpret_cast<float4*>(static_cast<float*>(p.out) + at) = o;
+  } else {
+    const bool h = p.out_dtype == CSA2_T_F16;
+    const uint2 u = h ? make_uint2(pack_f16x2(o.x, o.y), pack_f16x2(o.z, o.w)) : make_uint2(pack_bf16x2(o.x, o.y), pack_bf16x2(o.z, o.w));
+    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + at) = u;
+  }
+}
+
+// The query rows and tokens of one sequence.
+struct PagedSeq {
+  int index;
+  int first, rows;     // its first query row; query rows x heads of a group
+  int ctx, kv;         // position of its first query row; cached tokens
+  int tiles;           // tiles of a kv head
+};
+template <int NR>
+__device__ __forceinline__ PagedSeq paged_seq(const PagedAttnParams& p, int b) {
+  PagedSeq s;
+  const int r0 = p.row_start[b], r1 = p.row_start[b + 1];
+  s.index = b;
+  s.first = min(max(r0, 0), p.n_rows);
+  const int n = max(min(r1, p.n_rows) - s.first, 0);
+  const long long cap = (long long)p.table_cols << p.page_shift;
+  const int kv = max(p.kv_len[b], 0);
+  s.ctx = kv - (r1 - r0);
+  s.kv = (int)min((long long)kv, cap);
+  s.rows = n * p.group;
+  s.tiles = (s.rows + NR - 1) / NR;
+  return s;
+}
+
+}  // namespace csa2

@@ -1,0 +1,96 @@
+// Joins what the blocks of the paged attention left open.
+#include "common.cuh"
+#include "paged.h"
+#include "paged_dev.cuh"
+
+namespace csa2 {
+namespace {
+
+// Joins the pieces of the tile that block x of the attention left open: its own sums and those of the
+// blocks after it up to the tile's end.  A block takes a row: its warps take the pieces in turn (every
+// load independent of the others), then are summed in order.
+constexpr int kJoinWarps = 4;
+template <int D, int ROWS>
+__global__ void __launch_bounds__(kJoinWarps * 32) paged_join_kernel(const PagedAttnParams p) {
+  __shared__ float weight[kJoinWarps][32];
+  __shared__ float4 sum[kJoinWarps][D / 4];
+  __shared__ float2 stat[kJoinWarps];
+  asm volatile("griddepcontrol.wait;\n" ::: "memory");
+  const PagedOpen o = p.open[blockIdx.x];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  constexpr int L4 = D / 4, SUB = 32 / L4;  // lanes of a piece, pieces of a warp's load
+  const int r = blockIdx.y;
+  if (o.pieces == 0 || r >= o.n) return;
+  const float* part = p.part_o + (2LL * blockIdx.x * ROWS + r) * D + lane % L4 * 4;  // a piece further: 2 * ROWS rows further
+  const float* part_ml = p.part_ml + (2LL * blockIdx.x * ROWS + r) * 2;
+  auto at = [](int i) { return i == 0 ? ROWS : 2 * ROWS * i; };  // row of piece i: the first block's second slot, then first slots
+  float M = -INFINITY, L = 0.f;
+  float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int i0 = 0; i0 < o.pieces; i0 += 32 * kJoinWarps) {  // a round: pieces i0 + warp, + 4, ..
+    const int mine = i0 + lane * kJoinWarps + warp;
+    const float2 ml = mine < o.pieces ? *reinterpret_cast<const float2*>(part_ml + 2 * at(mine)) : make_float2(-INFINITY, 0.f);
+    const float m = fmaxf(M, warp_max(ml.x));
+    const float old = M == -INFINITY ? 1.f : ex2(M - m);
+    const float w = ml.x == -INFINITY ? (ml.y == 0.f ? 0.f : 1.f) : ex2(ml.x - m);
+    weight[warp][lane] = w;
+    __syncwarp();
+    L = L * old + warp_sum(ml.y * w);
+    a.x *= old, a.y *= old, a.z *= old, a.w *= old;
+    M = m;
+    const int n = min(32, (o.pieces - i0 - warp + kJoinWarps - 1) / kJoinWarps);
+#pragma unroll 8
+    for (int i = lane / L4; i < n; i += SUB) {
+      const float f = weight[warp][i];
+      const float4 v = *reinterpret_cast<const float4*>(part + (long long)at(i0 + i * kJoinWarps + warp) * D);
+      a.x += v.x * f, a.y += v.y * f, a.z += v.z * f, a.w += v.w * f;
+    }
+    __syncwarp();
+  }
+  if (SUB == 2) {
+    a.x += __shfl_xor_sync(0xffffffffu, a.x, 16), a.y += __shfl_xor_sync(0xffffffffu, a.y, 16);
+    a.z += __shfl_xor_sync(0xffffffffu, a.z, 16), a.w += __shfl_xor_sync(0xffffffffu, a.w, 16);
+  }
+  if (lane < L4) sum[warp][lane] = a;
+  if (lane == 0) stat[warp] = make_float2(M, L);
+  __syncthreads();
+  if (threadIdx.x >= L4) return;
+  float T = -INFINITY, N = 0.f;
+  float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+  for (int w = 0; w < kJoinWarps; ++w) T = fmaxf(T, stat[w].x);
+#pragma unroll
+  for (int w = 0; w < kJoinWarps; ++w) {
+    const float2 ml = stat[w];
+    if (ml.x == -INFINITY && ml.y == 0.f) continue;
+    const float f = ml.x == -INFINITY ? 1.f : ex2(ml.x - T);
+    const float4 v = sum[w][threadIdx.x];
+    N += ml.y * f;
+    t.x += v.x * f, t.y += v.y * f, t.z += v.z * f, t.w += v.w * f;
+  }
+  const int rr = o.row0 + r, tokn = rr / p.group, hq = o.kv_head * p.group + rr - tokn * p.group;
+  paged_store<D>(p, o.first_row + tokn, hq, threadIdx.x * 4, t, T, N);
+}
+
+template <int D, int ROWS>
+cudaError_t join(const PagedAttnParams& p, int blocks, cudaStream_t stream) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(blocks, ROWS);
+  cfg.blockDim = dim3(kJoinWarps * 32);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, paged_join_kernel<D, ROWS>, p);
+}
+
+}  // namespace
+
+cudaError_t launch_paged_join(const PagedAttnParams& p, int head_dim, int rows, int blocks, cudaStream_t stream) {
+  if (head_dim == 128)
+    return rows == 8 ? join<128, 8>(p, blocks, stream) : rows == 16 ? join<128, 16>(p, blocks, stream) : join<128, 256>(p, blocks, stream);
+  return rows == 8 ? join<64, 8>(p, blocks, stream) : rows == 16 ? join<64, 16>(p, blocks, stream) : join<64, 256>(p, blocks, stream);
+}
+
+}  // namespace csa2

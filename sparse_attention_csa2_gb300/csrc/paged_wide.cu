@@ -1,0 +1,601 @@
+// Attention over a paged cache of E4M3 codes, many query rows per key-value head (prompts, chunks,
+// long drafts): tiles of 256 query rows on the tensor cores' 5th generation form.
+//
+// The same sums as the split attention (paged_attn.cu).  Bound by the tensor cores: 4 * dim
+// operations per row, head and token, half of them scores (Q K^T) and half outputs (P V).
+//
+// A block holds a tile of 256 rows (tokens x heads of a group) as two of 128 and walks its cached
+// tokens 128 at a time:
+//   4 warps   codes of K and V from the pages to fp16 tiles in shared memory (exact), two stages;
+//             both row tiles use what they convert, so that the conversion costs an eighth of the
+//             block's issue slots
+//   1 thread  tcgen05.mma: S_t = Q_t K^T into tensor memory, O_t += P_t V with P_t read from tensor
+//             memory, in an order that computes one row tile's products during the other's softmax
+//   2 x 4 warps  softmax, a row per thread: maximum, weights as fp16 over the scores' own columns,
+//             sum; the output is rescaled only where a score exceeds the running maximum by 2^4
+//
+// fp16 holds every E4M3 value; a bf16 query row is scaled by a power of two into fp16's range.  K's
+// page scale multiplies the fp32 scores, V's enters the fp16 value relative to the largest seen
+// (exact for powers of two).  Weights as in the split attention: at most 2^15, 11 bits down to 2^-21
+// of the largest.
+//
+// Work is split as there: the units (128 tokens of a tile) of the call form one line, of which each
+// block (one per SM) takes an equal piece; open tiles leave partial sums that a second kernel joins.
+#include "common.cuh"
+#include "paged.h"
+#include "paged_dev.cuh"
+#include "tc05.cuh"
+
+namespace csa2 {
+namespace {
+
+constexpr int kRows = 256;
+constexpr int kTile = 128;              // tokens of a unit
+constexpr int kThreads = 13 * 32;       // softmax 0 .. 7, conversion 8 .. 11, products 12
+
+__device__ __forceinline__ uint32_t idesc_f16(int m, int n, bool b_mn_major) {
+  return (1u << 4) | (b_mn_major ? 1u << 16 : 0u) | (uint32_t)(n >> 3) << 17 | (uint32_t)(m >> 4) << 24;
+}
+// Descriptor of an operand in the 128-byte swizzle with explicit leading and stride offsets.
+__device__ __forceinline__ uint64_t sw128_desc_lbo(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
+  return (uint64_t)((saddr & 0x3ffffu) >> 4) | (uint64_t)(lbo >> 4) << 16 | (uint64_t)(sbo >> 4) << 32 | 1ull << 46 | 2ull << 61;
+}
+// D[tmem] (+)= A[tmem] * B[smem], kind::f16.
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(acc)
+      : "memory");
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;\n"
+      : "=l"(reinterpret_cast<uint64_t&>(d))
+      : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)), "l"(reinterpret_cast<uint64_t&>(c)));
+  return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("add.rn.f32x2 %0, %1, %2;\n"
+      : "=l"(reinterpret_cast<uint64_t&>(d))
+      : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)));
+  return d;
+}
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
+  const __half2 r = __hmul2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+
+// What the conversion tells the softmax about 128 tokens.
+struct TileInfo {
+  float k_scale[8];   // of each 16 tokens
+  float v_factor;     // what the outputs so far are to be multiplied by: the V reference grew
+  float v_ref;
+  uint32_t flags;     // bits 0-7: 16 tokens have a page; 8-15: their scales say NaN
+};
+
+struct Tile {
+  int row0, n, pos_first, pos_last, lo, hi, blocks;
+};
+__device__ __forceinline__ Tile tile_of(const PagedAttnParams& p, const PagedSeq& s, int t) {
+  Tile g;
+  g.row0 = t * kRows;
+  g.n = min(kRows, s.rows - g.row0);
+  g.pos_first = s.ctx + g.row0 / p.group;
+  g.pos_last = s.ctx + (g.row0 + g.n - 1) / p.group;
+  g.hi = min(s.kv, g.pos_last + 1);
+  g.lo = p.window > 0 ? max(g.pos_first - p.window + 1, 0) & ~15 : 0;
+  g.blocks = max((max(g.hi - g.lo, 0) + kTile - 1) / kTile, 1);
+  return g;
+}
+
+// A place on the line of units: sequence, tile, head, block of the tile.
+struct Place {
+  int b, t, h, blk;
+};
+struct Segment {
+  PagedSeq s;
+  Tile g;
+  int h, blk, n;      // its blocks blk .. blk + n - 1
+};
+// The block's segments one after the other; every role walks them for itself.
+struct Walk {
+  const PagedAttnParams& p;
+  Place at;
+  long long u, u_end;
+  __device__ __forceinline__ bool next(Segment& x) {
+    if (u >= u_end) return false;
+    for (;;) {
+      x.s = paged_seq<kRows>(p, at.b);
+      if (at.t < x.s.tiles) break;
+      ++at.b, at.t = at.h = at.blk = 0;
+    }
+    x.g = tile_of(p, x.s, at.t);
+    x.h = at.h, x.blk = at.blk;
+    x.n = (int)min((long long)(x.g.blocks - at.blk), u_end - u);
+    u += x.n;
+    at.blk += x.n;
+    if (at.blk == x.g.blocks) {
+      at.blk = 0;
+      if (++at.h == p.kv_heads) at.h = 0, ++at.t;
+    }
+    return true;
+  }
+};
+
+struct Shared {
+  uint64_t k_full[2], k_free[2], v_full[2], v_free[2], s_full[2], p_ready[2], o_full[2], q_full[2];
+  uint64_t info_full[4];
+  TileInfo info[4];
+  uint32_t tmem;
+  Place place;
+  long long scan[kThreads / 32];
+};
+
+template <int D, bool F16>
+__global__ void __launch_bounds__(kThreads, 1) paged_wide_kernel(const PagedAttnParams p) {
+  constexpr int kPanel = 128 * 128;            // 128 rows of 64 fp16
+  constexpr int kPanels = D / 64;
+  constexpr int kTileBytes = kPanels * kPanel; // a tile of Q, K or V
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ Shared sh;
+  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  uint8_t* q_tiles = smem;
+  uint8_t* k_tiles = smem + 2 * kTileBytes;
+  uint8_t* v_tiles = smem + 4 * kTileBytes;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (warp == 12) tc05::tmem_alloc(&sh.tmem, 512);
+  if (tid == 0) {
+    for (int i = 0; i < 2; ++i) {
+      tc05::mbar_init(&sh.k_full[i], 128), tc05::mbar_init(&sh.k_free[i], 1);
+      tc05::mbar_init(&sh.v_full[i], 128), tc05::mbar_init(&sh.v_free[i], 1);
+      tc05::mbar_init(&sh.s_full[i], 1), tc05::mbar_init(&sh.p_ready[i], 128);
+      tc05::mbar_init(&sh.o_full[i], 1), tc05::mbar_init(&sh.q_full[i], 128);
+    }
+    for (int i = 0; i < 4; ++i) tc05::mbar_init(&sh.info_full[i], 1);
+    tc05::fence_barrier_init();
+  }
+
+  // ---- this block's piece of the line: tiles of the sequences before each (in the space of K's tiles),
+  // then units of the tiles before each thread's run of tiles
+  long long all, u, u_end;
+  int used;
+  {
+    int* tiles_before = reinterpret_cast<int*>(k_tiles);  // [n_seq + 1]
+    auto scan = [&](long long v, long long& total) {       // exclusive sum over the block's threads
+      long long x = v;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+      }
+      if (lane == 31) sh.scan[warp] = x;
+      __syncthreads();
+      long long before = 0;
+      total = 0;
+      for (int w = 0; w < kThreads / 32; ++w) {
+        if (w < warp) before += sh.scan[w];
+        total += sh.scan[w];
+      }
+      __syncthreads();
+      return before + x - v;
+    };
+    const int run = (p.n_seq + kThreads - 1) / kThreads;
+    const int q0 = min(tid * run, p.n_seq), q1 = min(q0 + run, p.n_seq);
+    int mine = 0;
+    for (int b = q0; b < q1; ++b) mine += paged_seq<kRows>(p, b).tiles;
+    long long n_tiles;
+    int before = (int)scan(mine, n_tiles);
+    for (int b = q0; b < q1; ++b) tiles_before[b] = before, before += paged_seq<kRows>(p, b).tiles;
+    if (tid == 0) tiles_before[p.n_seq] = (int)n_tiles;
+    __syncthreads();
+    const int trun = (int)((n_tiles + kThreads - 1) / kThreads);
+    const int t0 = min(tid * trun, (int)n_tiles), t1 = min(t0 + trun, (int)n_tiles);
+    int lo = 0, hi = p.n_seq;  // the sequence of tile t0: the last with tiles_before <= t0 that has tiles
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (tiles_before[mid] <= t0) lo = mid; else hi = mid;
+    }
+    auto walk = [&](auto&& visit) {
+      int b = lo;
+      PagedSeq s = paged_seq<kRows>(p, b);
+      for (int t = t0; t < t1; ++t) {
+        while (t >= tiles_before[b + 1]) s = paged_seq<kRows>(p, ++b);
+        visit(b, t - tiles_before[b], (long long)tile_of(p, s, t - tiles_before[b]).blocks * p.kv_heads);
+      }
+    };
+    long long units = 0;
+    walk([&](int, int, long long n) { units += n; });
+    long long first = scan(units, all);
+    used = (int)min((long long)gridDim.x, all);
+    u = (int)blockIdx.x < used ? all * blockIdx.x / used : 0;
+    u_end = (int)blockIdx.x < used ? all * (blockIdx.x + 1) / used : 0;
+    if (u < u_end && first <= u && u < first + units) {
+      walk([&](int b, int t, long long n) {
+        if (first <= u && u < first + n) {
+          const int blocks = (int)(n / p.kv_heads), in = (int)(u - first);
+          sh.place = {b, t, in / blocks, in % blocks};
+        }
+        first += n;
+      });
+    }
+    tc05::fence_before();
+    __syncthreads();
+    tc05::fence_after();
+  }
+  const uint32_t tmem = sh.tmem;
+  Walk walk{p, sh.place, u, u_end};
+  Segment x;
+  int pieces = 0;
+  bool dead = false, bad = false;
+  auto wait = [&](uint64_t* bar, uint32_t parity) {
+    if (!dead && !tc05::mbar_wait(bar, parity)) dead = true;
+    if (warp < 12) dead = __any_sync(0xffffffffu, dead);
+  };
+
+  if (u >= u_end) {
+    // nothing to do
+  } else if (warp < 8) {
+    // ------------------------------------------------------------------ softmax: a row per thread
+    const int t = warp >> 2, row = (warp & 3) * 32 + lane;  // row of the tile of 128
+    const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+    const uint32_t s_cols = lanes + 128 * t, o_cols = lanes + 256 + D * t;
+    uint8_t* q_row = q_tiles + t * kTileBytes + row * 128;
+    uint32_t turn = 0, done = 0;  // uses of s_full, of o_full
+    uint32_t count = 0;           // units of the block
+    while (walk.next(x) && !dead) {
+      const int r = 128 * t + row;
+      if (128 * t >= x.g.n) {  // no rows in this half: its products are not computed
+        count += x.n;
+        continue;
+      }
+      const bool has = r < x.g.n;
+      const int rr = x.g.row0 + min(r, x.g.n - 1), i = rr / p.group;
+      const int pos = x.s.ctx + i;
+      // the query row to fp16, scaled to a maximum in [2^13, 2^14); a negative softmax scale turns its sign
+      float f;
+      {
+        const uint16_t* src = static_cast<const uint16_t*>(p.q) + (long long)(x.s.first + i) * p.q_row +
+                              (long long)(x.h * p.group + rr - i * p.group) * p.q_head;
+        float amax = 0.f;
+        bool odd = false;
+#pragma unroll
+        for (int c = 0; c < D / 8; ++c) {
+          const uint4 v4 = has ? *reinterpret_cast<const uint4*>(src + 8 * c) : make_uint4(0, 0, 0, 0);
+          const uint32_t w[4] = {v4.x, v4.y, v4.z, v4.w};
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float2 v = F16 ? __half22float2(*reinterpret_cast<const __half2*>(&w[k])) : make_float2(bf16_lo(w[k]), bf16_hi(w[k]));
+            odd |= !(fabsf(v.x) < INFINITY) || !(fabsf(v.y) < INFINITY);
+            amax = fmaxf(amax, fmaxf(fabsf(v.x), fabsf(v.y)));
+          }
+        }
+        int e = (int)(__float_as_uint(amax) >> 23) - 127 - 13;
+        e = min(max(e, -110), 119);
+        float down = __uint_as_float((uint32_t)(127 - e) << 23);
+        const float up = __uint_as_float((uint32_t)(127 + e) << 23);
+        f = odd ? __uint_as_float(0x7fc00000u) : fabsf(p.scale_log2) * up;
+        if (odd) down = 0.f;
+        if (p.scale_log2 < 0.f) down = -down;
+#pragma unroll
+        for (int c = 0; c < D / 8; ++c) {
+          const uint4 v4 = has ? *reinterpret_cast<const uint4*>(src + 8 * c) : make_uint4(0, 0, 0, 0);
+          const uint32_t w[4] = {v4.x, v4.y, v4.z, v4.w};
+          uint32_t o[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float2 v = F16 ? __half22float2(*reinterpret_cast<const __half2*>(&w[k])) : make_float2(bf16_lo(w[k]), bf16_hi(w[k]));
+            o[k] = odd ? 0u : pack_f16x2(v.x * down, v.y * down);
+          }
+          *reinterpret_cast<uint4*>(q_row + (c >> 3) * kPanel + (((c & 7) ^ (row & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+        }
+        asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
+        tc05::mbar_arrive(&sh.q_full[t]);
+      }
+      float m = -INFINITY, v_ref = 0.f;
+      float2 l2 = make_float2(0.f, 0.f);
+      const int see_hi = min(pos + 1, x.g.hi), see_lo = p.window > 0 ? pos - p.window + 1 : 0;
+      for (int j = 0; j < x.n && !dead; ++j, ++count, ++turn) {
+        wait(&sh.s_full[t], turn & 1);
+        if (dead) break;
+        wait(&sh.info_full[count & 3], count >> 2 & 1);
+        if (dead) break;
+        tc05::fence_after();
+        const TileInfo& info = sh.info[count & 3];
+        const int tok = x.g.lo + (x.blk + j) * kTile;
+        const int hi = see_hi - tok, lo = see_lo - tok;  // the row sees columns lo .. hi - 1
+        const uint32_t flags = info.flags;
+        const bool whole = __all_sync(0xffffffffu, hi >= kTile && lo <= 0) && flags == 0xffu;
+        float2 ks[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) ks[c] = make_float2(f * info.k_scale[2 * c], f * info.k_scale[2 * c + 1]);
+        // maximum
+        float top = -INFINITY;
+        uint32_t v[32];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          tc05::tmem_ld32(s_cols + 32 * c, v);
+          tc05::tmem_ld_wait();
+          if (!whole) {
+#pragma unroll
+            for (int k = 0; k < 32; ++k) {
+              const int col = 32 * c + k;
+              const bool sees = col < hi && col >= lo && (flags >> (col >> 4) & 1);
+              if (!sees) v[k] = 0xff800000u;
+            }
+          }
+          float a = __uint_as_float(v[0]), b = __uint_as_float(v[16]);
+#pragma unroll
+          for (int k = 1; k < 16; ++k) a = fmaxf(a, __uint_as_float(v[k])), b = fmaxf(b, __uint_as_float(v[16 + k]));
+          // a column that is not seen stays -inf whatever its scale
+          if (a > -INFINITY) top = fmaxf(top, a * ks[c].x);
+          if (b > -INFINITY) top = fmaxf(top, b * ks[c].y);
+        }
+        v_ref = info.v_ref;
+        const float v_factor = info.v_factor;
+        const bool grows = top > m + kPagedSlack;
+        if (__any_sync(0xffffffffu, grows) || v_factor != 1.f) {
+          const float to = grows ? top : m;
+          const float e = m == -INFINITY ? 0.f : to == m ? 1.f : ex2(m - to);
+          l2.x *= e, l2.y *= e;
+          m = to;
+          if (j > 0) {
+            const float o = e * v_factor;
+#pragma unroll
+            for (int c = 0; c < D / 32; ++c) {
+              tc05::tmem_ld32(o_cols + 32 * c, v);
+              tc05::tmem_ld_wait();
+#pragma unroll
+              for (int k = 0; k < 32; ++k) v[k] = __float_as_uint(__uint_as_float(v[k]) * o);
+              tc05::tmem_st32(o_cols + 32 * c, v);
+            }
+          }
+        }
+        // weights, over the score columns that have been read
+        const float off = m == -INFINITY ? 0.f : kPagedLift - m;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          tc05::tmem_ld32(s_cols + 32 * c, v);
+          tc05::tmem_ld_wait();
+          uint32_t w[16];
+#pragma unroll
+          for (int k = 0; k < 16; ++k) {
+            const float s = k < 8 ? ks[c].x : ks[c].y;
+            float2 z = fma2(make_float2(__uint_as_float(v[2 * k]), __uint_as_float(v[2 * k + 1])), make_float2(s, s), make_float2(off, off));
+            if (!whole) {
+              const int col = 32 * c + 2 * k;
+              const bool page = flags >> (col >> 4) & 1, nan = flags >> (8 + (col >> 4)) & 1;
+              if (nan) z.x = z.y = __uint_as_float(0x7fc00000u);
+              if (!(page && col < hi && col >= lo)) z.x = -INFINITY;
+              if (!(page && col + 1 < hi && col + 1 >= lo)) z.y = -INFINITY;
+            }
+            const float2 e = make_float2(ex2(z.x), ex2(z.y));
+            l2 = add2(l2, e);
+            w[k] = pack_f16x2(e.x, e.y);
+          }
+          tc05::tmem_st16(s_cols + 16 * c, w);
+        }
+        tc05::tmem_st_wait();
+        tc05::fence_before();
+        tc05::mbar_arrive(&sh.p_ready[t]);
+      }
+      // ---- the row's output, or its partial sums
+      wait(&sh.o_full[t], done & 1);
+      ++done;
+      if (dead) break;
+      tc05::fence_after();
+      const bool starts = x.blk == 0, ends = x.blk + x.n == x.g.blocks;
+      const float L = l2.x + l2.y;
+      const long long slot = (2LL * blockIdx.x + (starts ? 1 : 0)) * kRows + r;
+#pragma unroll
+      for (int c = 0; c < D / 32; ++c) {
+        uint32_t v[32];
+        tc05::tmem_ld32(o_cols + 32 * c, v);
+        tc05::tmem_ld_wait();
+#pragma unroll
+        for (int k = 0; k < 32; k += 4) {
+          if (!has) break;
+          const float4 o = make_float4(__uint_as_float(v[k]) * v_ref, __uint_as_float(v[k + 1]) * v_ref,
+                                       __uint_as_float(v[k + 2]) * v_ref, __uint_as_float(v[k + 3]) * v_ref);
+          if (starts && ends) paged_store<D>(p, x.s.first + i, x.h * p.group + rr - i * p.group, 32 * c + k, o, m, L);
+          else *reinterpret_cast<float4*>(p.part_o + slot * D + 32 * c + k) = o;
+        }
+      }
+      if (has && !(starts && ends)) *reinterpret_cast<float2*>(p.part_ml + slot * 2) = make_float2(m, L);
+      tc05::fence_before();
+    }
+  } else if (warp < 12) {
+    // ------------------------------------------------------------------ codes to fp16 tiles
+    const int gt = tid - 256;                    // thread of the group
+    const int row_in = gt >> 3, ch = gt & 7;     // D = 128: row of 16, 16-byte piece of codes
+    constexpr int LD = kTile * D / (128 * 16);   // pieces of a thread: 8, or 4 at dim 64
+    constexpr int RPL = 2048 / D;                // rows of a load of the group: 16, or 32
+    uint32_t count = 0;
+    while (walk.next(x) && !dead) {
+      const int32_t* trow = p.table + (long long)x.s.index * p.table_cols;
+      const int mask = (1 << p.page_shift) - 1;
+      float v_ref = 0.f;
+      // lane l < 8 knows the page of tokens 16 l .. of a tile and its scales
+      auto ids = [&](int j) {
+        const int tok = x.g.lo + (x.blk + j) * kTile + 16 * (lane & 7);
+        if (j >= x.n || tok >= x.g.hi) return -1;
+        const int id = __ldg(trow + (tok >> p.page_shift));
+        return (unsigned)id < (unsigned)p.n_pages ? id : -2;
+      };
+      uint4 rk[LD], rv[LD];
+      auto load = [&](const uint8_t* codes, uint4 (&r)[LD], int j, int id) {
+        const int tok0 = x.g.lo + (x.blk + j) * kTile;
+#pragma unroll
+        for (int i = 0; i < LD; ++i) {
+          const int row = D == 128 ? i * RPL + row_in : i * RPL + (gt >> 2), c16 = D == 128 ? ch : gt & 3;
+          const int pg = __shfl_sync(0xffffffffu, id, row >> 4), tok = tok0 + row;
+          r[i] = make_uint4(0, 0, 0, 0);
+          if (pg >= 0 && tok < x.g.hi)
+            r[i] = __ldg(reinterpret_cast<const uint4*>(codes + (((((long long)pg * p.kv_heads + x.h) << p.page_shift) + (tok & mask)) * D) + 16 * c16));
+        }
+      };
+      auto store = [&](uint8_t* tile, const uint4 (&r)[LD], uint32_t ratio, bool scaled) {
+#pragma unroll
+        for (int i = 0; i < LD; ++i) {
+          const int row = D == 128 ? i * RPL + row_in : i * RPL + (gt >> 2), c16 = D == 128 ? ch : gt & 3;
+          const uint32_t w[4] = {r[i].x, r[i].y, r[i].z, r[i].w};
+          uint32_t h[8];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) f16_pairs(w[k], h[2 * k], h[2 * k + 1]);
+          if (scaled) {
+            const uint32_t s = __shfl_sync(0xffffffffu, ratio, row >> 4);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) h[k] = mul_f16x2(h[k], s);
+          }
+          // fp16 pieces 2 c16 and 2 c16 + 1 of the row's panel; the second panel's lanes store them in the
+          // other order, so that a phase's eight lanes meet all banks
+          uint8_t* to = tile + (c16 >> 2) * kPanel + row * 128;
+          const int a = 2 * (c16 & 3), sw = c16 >> 2;
+          const uint4 h0 = make_uint4(h[0], h[1], h[2], h[3]), h1 = make_uint4(h[4], h[5], h[6], h[7]);
+          *reinterpret_cast<uint4*>(to + (((a + sw) ^ (row & 7)) << 4)) = sw ? h1 : h0;
+          *reinterpret_cast<uint4*>(to + (((a + 1 - sw) ^ (row & 7)) << 4)) = sw ? h0 : h1;
+        }
+        asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
+      };
+      int id = ids(0), id_next = ids(1);
+      load(p.k, rk, 0, id);
+      load(p.v, rv, 0, id);
+      auto scale = [&](const float* s, int pg) { return pg >= 0 ? __ldg(s + (long long)pg * p.kv_heads + x.h) : 0.f; };
+      float sk = scale(p.k_scale, id), sv = scale(p.v_scale, id);
+      for (int j = 0; j < x.n && !dead; ++j, ++count) {
+        const int stage = count & 1;
+        const uint32_t parity = (count >> 1 & 1) ^ 1;
+        bad |= id == -2;
+        const uint32_t pages = __ballot_sync(0xffffffffu, id != -2) & 0xffu;
+        const uint32_t nans = __ballot_sync(0xffffffffu, sk != sk || sv != sv) & 0xffu;
+        float vm = sv > 0.f ? sv : 0.f;
+        const float sv_here = vm;
+        vm = fmaxf(vm, __shfl_xor_sync(0xffffffffu, vm, 1));
+        vm = fmaxf(vm, __shfl_xor_sync(0xffffffffu, vm, 2));
+        vm = fmaxf(vm, __shfl_xor_sync(0xffffffffu, vm, 4));
+        const float v_new = fmaxf(v_ref, vm);
+        const float v_inv = v_new > 0.f ? __fdiv_rn(1.f, v_new) : 0.f;
+        const float rf = sv_here * v_inv;
+        const uint32_t ratio = pack_f16x2(rf, rf);
+        wait(&sh.k_free[stage], parity);
+        if (gt < 8) {
+          TileInfo& info = sh.info[count & 3];
+          info.k_scale[gt] = sk == sk ? sk : 0.f;
+          if (gt == 0) {
+            info.v_factor = v_new > v_ref ? v_ref * v_inv : 1.f;
+            info.v_ref = v_new;
+            info.flags = pages | nans << 8;
+          }
+        }
+        __syncwarp();
+        if (gt == 0) tc05::mbar_arrive(&sh.info_full[count & 3]);
+        v_ref = v_new;
+        store(k_tiles + stage * kTileBytes, rk, 0u, false);
+        tc05::mbar_arrive(&sh.k_full[stage]);
+        const int id_far = ids(j + 2);
+        if (j + 1 < x.n) load(p.k, rk, j + 1, id_next);
+        wait(&sh.v_free[stage], parity);
+        store(v_tiles + stage * kTileBytes, rv, ratio, __any_sync(0xffffffffu, rf != 1.f));
+        tc05::mbar_arrive(&sh.v_full[stage]);
+        if (j + 1 < x.n) {
+          load(p.v, rv, j + 1, id_next);
+          sk = scale(p.k_scale, id_next), sv = scale(p.v_scale, id_next);
+        }
+        id = id_next, id_next = id_far;
+      }
+    }
+  } else if (lane == 0) {
+    // ------------------------------------------------------------------ products
+    const uint32_t q_u = smem_u32(q_tiles), k_u = smem_u32(k_tiles), v_u = smem_u32(v_tiles);
+    const uint32_t id_s = idesc_f16(128, 128, false), id_o = idesc_f16(128, D, true);
+    uint32_t count = 0, segs[2] = {0, 0}, turns[2] = {0, 0};
+    auto scores = [&](int t, int stage) {
+#pragma unroll
+      for (int k = 0; k < D / 16; ++k) {
+        const uint32_t at = (k >> 2) * kPanel + (k & 3) * 32;
+        tc05::mma_bf16(tmem + 128 * t, tc05::sw128_desc(q_u + t * kTileBytes + at), tc05::sw128_desc(k_u + stage * kTileBytes + at),
+                       id_s, k > 0);
+      }
+    };
+    auto outputs = [&](int t, int stage, bool acc) {
+#pragma unroll
+      for (int k = 0; k < kTile / 16; ++k)
+        mma_ts(tmem + 256 + D * t, tmem + 128 * t + 8 * k, sw128_desc_lbo(v_u + stage * kTileBytes + 2048 * k, kPanel, 1024), id_o,
+               acc || k > 0);
+    };
+    while (walk.next(x) && !dead) {
+      const int halves = x.g.n > 128 ? 2 : 1;
+      for (int t = 0; t < halves; ++t) {
+        wait(&sh.q_full[t], segs[t] & 1);
+        ++segs[t];
+      }
+      wait(&sh.k_full[count & 1], count >> 1 & 1);
+      tc05::fence_after();
+      for (int t = 0; t < halves && !dead; ++t) {
+        scores(t, count & 1);
+        tc05::mma_commit(&sh.s_full[t]);
+      }
+      tc05::mma_commit(&sh.k_free[count & 1]);
+      for (int j = 0; j < x.n && !dead; ++j, ++count) {
+        const int stage = count & 1, next = stage ^ 1;
+        const bool more = j + 1 < x.n;
+        wait(&sh.v_full[stage], count >> 1 & 1);
+        for (int t = 0; t < halves && !dead; ++t) {
+          wait(&sh.p_ready[t], turns[t] & 1);
+          ++turns[t];
+          if (dead) break;
+          tc05::fence_after();
+          outputs(t, stage, j > 0);
+          if (t == halves - 1) tc05::mma_commit(&sh.v_free[stage]);
+          if (more) {
+            if (t == 0) wait(&sh.k_full[next], (count + 1) >> 1 & 1);
+            if (dead) break;
+            tc05::fence_after();
+            scores(t, next);
+            tc05::mma_commit(&sh.s_full[t]);
+            if (t == halves - 1) tc05::mma_commit(&sh.k_free[next]);
+          } else {
+            tc05::mma_commit(&sh.o_full[t]);
+          }
+        }
+      }
+    }
+  }
+  if (dead && p.dev_status) atomicExch(p.dev_status, (int)CSA2_ETIMEOUT);
+  if (bad && p.dev_status) atomicExch(p.dev_status, (int)CSA2_EDEVICE_INDEX);
+  // the tile that stays open at the end
+  if (tid == 0 && u < u_end) {
+    Walk last{p, sh.place, u, u_end};
+    while (last.next(x)) {
+    }
+    if (x.blk == 0 && x.n < x.g.blocks) {
+      pieces = (int)(((u_end - x.n + x.g.blocks) * used - 1) / all) - (int)blockIdx.x + 1;
+      PagedOpen& o = p.open[blockIdx.x];
+      o.row0 = x.g.row0, o.n = x.g.n, o.first_row = x.s.first, o.kv_head = x.h;
+    }
+  }
+  __syncwarp();
+  const int any_dead = __syncthreads_or(dead);
+  if (tid == 0) p.open[blockIdx.x].pieces = any_dead ? 0 : pieces;
+  if (warp == 12) tc05::tmem_dealloc(tmem, 512);
+}
+
+template <int D, bool F16>
+cudaError_t launch(const PagedAttnParams& p, int blocks, cudaStream_t stream) {
+  constexpr int smem = 6 * 128 * D * 2 + 1024;
+  const cudaError_t e = cudaFuncSetAttribute(paged_wide_kernel<D, F16>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  paged_wide_kernel<D, F16><<<blocks, kThreads, smem, stream>>>(p);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_paged_wide(const PagedAttnParams& p, int q_dtype, int head_dim, int blocks, cudaStream_t stream) {
+  const bool f16 = q_dtype == CSA2_T_F16;
+  const cudaError_t e = head_dim == 128 ? (f16 ? launch<128, true>(p, blocks, stream) : launch<128, false>(p, blocks, stream))
+                                        : (f16 ? launch<64, true>(p, blocks, stream) : launch<64, false>(p, blocks, stream));
+  return e != cudaSuccess ? e : launch_paged_join(p, head_dim, kRows, blocks, stream);
+}
+
+}  // namespace csa2
