@@ -31,7 +31,13 @@ namespace {
 
 constexpr int kRows = 256;
 constexpr int kTile = 128;              // tokens of a unit
-constexpr int kThreads = 13 * 32;       // softmax 0 .. 7, conversion 8 .. 11, products 12
+constexpr int kThreads = 16 * 32;       // warps: softmax 0 .. 7, conversion 8 .. 11, products 12 (13 .. 15 idle)
+// Registers of a thread of each part, from 128 at launch: 2 * 160 + 120 + 72 = 4 * 128.
+constexpr int kSoftmaxRegs = 160, kConvertRegs = 120, kProductRegs = 72;
+template <int N>
+__device__ __forceinline__ void more_registers() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(N)); }
+template <int N>
+__device__ __forceinline__ void fewer_registers() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(N)); }
 
 __device__ __forceinline__ uint32_t idesc_f16(int m, int n, bool b_mn_major) {
   return (1u << 4) | (b_mn_major ? 1u << 16 : 0u) | (uint32_t)(n >> 3) << 17 | (uint32_t)(m >> 4) << 24;
@@ -233,9 +239,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_wide_kernel(const PagedAttn
     if (warp < 12) dead = __any_sync(0xffffffffu, dead);
   };
 
-  if (u >= u_end) {
-    // nothing to do
-  } else if (warp < 8) {
+  if (warp < 8) {
+    more_registers<kSoftmaxRegs>();
     // ------------------------------------------------------------------ softmax: a row per thread
     const int t = warp >> 2, row = (warp & 3) * 32 + lane;  // row of the tile of 128
     const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
@@ -259,7 +264,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_wide_kernel(const PagedAttn
                               (long long)(x.h * p.group + rr - i * p.group) * p.q_head;
         float amax = 0.f;
         bool odd = false;
-#pragma unroll
+#pragma unroll 4
         for (int c = 0; c < D / 8; ++c) {
           const uint4 v4 = has ? *reinterpret_cast<const uint4*>(src + 8 * c) : make_uint4(0, 0, 0, 0);
           const uint32_t w[4] = {v4.x, v4.y, v4.z, v4.w};
@@ -277,7 +282,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_wide_kernel(const PagedAttn
         f = odd ? __uint_as_float(0x7fc00000u) : fabsf(p.scale_log2) * up;
         if (odd) down = 0.f;
         if (p.scale_log2 < 0.f) down = -down;
-#pragma unroll
+#pragma unroll 4
         for (int c = 0; c < D / 8; ++c) {
           const uint4 v4 = has ? *reinterpret_cast<const uint4*>(src + 8 * c) : make_uint4(0, 0, 0, 0);
           const uint32_t w[4] = {v4.x, v4.y, v4.z, v4.w};
@@ -306,30 +311,38 @@ __global__ void __launch_bounds__(kThreads, 1) paged_wide_kernel(const PagedAttn
         const int hi = see_hi - tok, lo = see_lo - tok;  // the row sees columns lo .. hi - 1
         const uint32_t flags = info.flags;
         const bool whole = __all_sync(0xffffffffu, hi >= kTile && lo <= 0) && flags == 0xffu;
-        float2 ks[4];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) ks[c] = make_float2(f * info.k_scale[2 * c], f * info.k_scale[2 * c + 1]);
-        // maximum
         float top = -INFINITY;
-        uint32_t v[32];
+        if (whole) {
+          uint32_t va[32], vb[32];
+          tc05::tmem_ld32(s_cols, va);
+          auto most = [&](const uint32_t (&v)[32], int c) {
+            float a = __uint_as_float(v[0]), b = __uint_as_float(v[16]);
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          tc05::tmem_ld32(s_cols + 32 * c, v);
+            for (int k = 1; k < 16; ++k) a = fmaxf(a, __uint_as_float(v[k])), b = fmaxf(b, __uint_as_float(v[16 + k]));
+            top = fmaxf(top, fmaxf(a * (f * info.k_scale[2 * c]), b * (f * info.k_scale[2 * c + 1])));
+          };
           tc05::tmem_ld_wait();
-          if (!whole) {
+          tc05::tmem_ld32(s_cols + 32, vb);
+          most(va, 0);
+          tc05::tmem_ld_wait();
+          tc05::tmem_ld32(s_cols + 64, va);
+          most(vb, 1);
+          tc05::tmem_ld_wait();
+          tc05::tmem_ld32(s_cols + 96, vb);
+          most(va, 2);
+          tc05::tmem_ld_wait();
+          most(vb, 3);
+        } else {
+#pragma unroll 1
+          for (int c = 0; c < 8; ++c) {  // 16 columns, of one page
+            uint32_t v[16];
+            tc05::tmem_ld16(s_cols + 16 * c, v);
+            tc05::tmem_ld_wait();
+            float a = -INFINITY;
 #pragma unroll
-            for (int k = 0; k < 32; ++k) {
-              const int col = 32 * c + k;
-              const bool sees = col < hi && col >= lo && (flags >> (col >> 4) & 1);
-              if (!sees) v[k] = 0xff800000u;
-            }
+            for (int k = 0; k < 16; ++k) a = 16 * c + k < hi && 16 * c + k >= lo ? fmaxf(a, __uint_as_float(v[k])) : a;
+            if ((flags >> c & 1) && a > -INFINITY) top = fmaxf(top, a * (f * info.k_scale[c]));
           }
-          float a = __uint_as_float(v[0]), b = __uint_as_float(v[16]);
-#pragma unroll
-          for (int k = 1; k < 16; ++k) a = fmaxf(a, __uint_as_float(v[k])), b = fmaxf(b, __uint_as_float(v[16 + k]));
-          // a column that is not seen stays -inf whatever its scale
-          if (a > -INFINITY) top = fmaxf(top, a * ks[c].x);
-          if (b > -INFINITY) top = fmaxf(top, b * ks[c].y);
         }
         v_ref = info.v_ref;
         const float v_factor = info.v_factor;
@@ -341,8 +354,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_wide_kernel(const PagedAttn
           m = to;
           if (j > 0) {
             const float o = e * v_factor;
-#pragma unroll
+#pragma unroll 1
             for (int c = 0; c < D / 32; ++c) {
+              uint32_t v[32];
               tc05::tmem_ld32(o_cols + 32 * c, v);
               tc05::tmem_ld_wait();
 #pragma unroll
@@ -353,27 +367,52 @@ __global__ void __launch_bounds__(kThreads, 1) paged_wide_kernel(const PagedAttn
         }
         // weights, over the score columns that have been read
         const float off = m == -INFINITY ? 0.f : kPagedLift - m;
+        const float2 off2 = make_float2(off, off);
+        if (whole) {
+          uint32_t va[32], vb[32];
+          tc05::tmem_ld32(s_cols, va);
+          auto weigh = [&](const uint32_t (&v)[32], int c) {
+            uint32_t w[16];
+            const float k0 = f * info.k_scale[2 * c], k1 = f * info.k_scale[2 * c + 1];
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          tc05::tmem_ld32(s_cols + 32 * c, v);
-          tc05::tmem_ld_wait();
-          uint32_t w[16];
-#pragma unroll
-          for (int k = 0; k < 16; ++k) {
-            const float s = k < 8 ? ks[c].x : ks[c].y;
-            float2 z = fma2(make_float2(__uint_as_float(v[2 * k]), __uint_as_float(v[2 * k + 1])), make_float2(s, s), make_float2(off, off));
-            if (!whole) {
-              const int col = 32 * c + 2 * k;
-              const bool page = flags >> (col >> 4) & 1, nan = flags >> (8 + (col >> 4)) & 1;
-              if (nan) z.x = z.y = __uint_as_float(0x7fc00000u);
-              if (!(page && col < hi && col >= lo)) z.x = -INFINITY;
-              if (!(page && col + 1 < hi && col + 1 >= lo)) z.y = -INFINITY;
+            for (int k = 0; k < 16; ++k) {
+              const float ks = k < 8 ? k0 : k1;
+              const float2 z = fma2(make_float2(__uint_as_float(v[2 * k]), __uint_as_float(v[2 * k + 1])), make_float2(ks, ks), off2);
+              const float2 e = make_float2(ex2(z.x), ex2(z.y));
+              l2 = add2(l2, e);
+              w[k] = pack_f16x2(e.x, e.y);
             }
-            const float2 e = make_float2(ex2(z.x), ex2(z.y));
-            l2 = add2(l2, e);
-            w[k] = pack_f16x2(e.x, e.y);
+            tc05::tmem_st16(s_cols + 16 * c, w);
+          };
+          tc05::tmem_ld_wait();
+          tc05::tmem_ld32(s_cols + 32, vb);
+          weigh(va, 0);
+          tc05::tmem_ld_wait();
+          tc05::tmem_ld32(s_cols + 64, va);
+          weigh(vb, 1);
+          tc05::tmem_ld_wait();
+          tc05::tmem_ld32(s_cols + 96, vb);
+          weigh(va, 2);
+          tc05::tmem_ld_wait();
+          weigh(vb, 3);
+        } else {
+#pragma unroll 1
+          for (int c = 0; c < 8; ++c) {
+            uint32_t v[16], w[8];
+            tc05::tmem_ld16(s_cols + 16 * c, v);
+            tc05::tmem_ld_wait();
+            const float ks = flags >> (8 + c) & 1 ? __uint_as_float(0x7fc00000u) : f * info.k_scale[c];
+            const bool page = flags >> c & 1;
+#pragma unroll
+            for (int k = 0; k < 16; ++k) {
+              const bool sees = page && 16 * c + k < hi && 16 * c + k >= lo;
+              v[k] = __float_as_uint(sees ? ex2(fmaf(__uint_as_float(v[k]), ks, off)) : 0.f);
+              l2.x += __uint_as_float(v[k]);
+            }
+#pragma unroll
+            for (int k = 0; k < 8; ++k) w[k] = pack_f16x2(__uint_as_float(v[2 * k]), __uint_as_float(v[2 * k + 1]));
+            tc05::tmem_st8(s_cols + 8 * c, w);
           }
-          tc05::tmem_st16(s_cols + 16 * c, w);
         }
         tc05::tmem_st_wait();
         tc05::fence_before();
@@ -387,7 +426,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_wide_kernel(const PagedAttn
       const bool starts = x.blk == 0, ends = x.blk + x.n == x.g.blocks;
       const float L = l2.x + l2.y;
       const long long slot = (2LL * blockIdx.x + (starts ? 1 : 0)) * kRows + r;
-#pragma unroll
+#pragma unroll 1
       for (int c = 0; c < D / 32; ++c) {
         uint32_t v[32];
         tc05::tmem_ld32(o_cols + 32 * c, v);
@@ -405,6 +444,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_wide_kernel(const PagedAttn
       tc05::fence_before();
     }
   } else if (warp < 12) {
+    fewer_registers<kConvertRegs>();
     // ------------------------------------------------------------------ codes to fp16 tiles
     const int gt = tid - 256;                    // thread of the group
     const int row_in = gt >> 3, ch = gt & 7;     // D = 128: row of 16, 16-byte piece of codes
@@ -423,15 +463,19 @@ __global__ void __launch_bounds__(kThreads, 1) paged_wide_kernel(const PagedAttn
         return (unsigned)id < (unsigned)p.n_pages ? id : -2;
       };
       uint4 rk[LD], rv[LD];
-      auto load = [&](const uint8_t* codes, uint4 (&r)[LD], int j, int id) {
-        const int tok0 = x.g.lo + (x.blk + j) * kTile;
+      // and the place of their codes
+      auto place = [&](int j, int id) {
+        const int tok = x.g.lo + (x.blk + j) * kTile + 16 * (lane & 7);
+        return id < 0 ? -1LL : ((((long long)id * p.kv_heads + x.h) << p.page_shift) + (tok & mask)) * D;
+      };
+      auto load = [&](const uint8_t* codes, uint4 (&r)[LD], int j, long long at) {
+        const int left = x.g.hi - x.g.lo - (x.blk + j) * kTile;  // tokens of the tile that are there
 #pragma unroll
         for (int i = 0; i < LD; ++i) {
           const int row = D == 128 ? i * RPL + row_in : i * RPL + (gt >> 2), c16 = D == 128 ? ch : gt & 3;
-          const int pg = __shfl_sync(0xffffffffu, id, row >> 4), tok = tok0 + row;
+          const long long from = __shfl_sync(0xffffffffu, at, row >> 4);
           r[i] = make_uint4(0, 0, 0, 0);
-          if (pg >= 0 && tok < x.g.hi)
-            r[i] = __ldg(reinterpret_cast<const uint4*>(codes + (((((long long)pg * p.kv_heads + x.h) << p.page_shift) + (tok & mask)) * D) + 16 * c16));
+          if (from >= 0 && row < left) r[i] = __ldg(reinterpret_cast<const uint4*>(codes + from + (row & 15) * D + 16 * c16));
         }
       };
       auto store = [&](uint8_t* tile, const uint4 (&r)[LD], uint32_t ratio, bool scaled) {
@@ -458,8 +502,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_wide_kernel(const PagedAttn
         asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
       };
       int id = ids(0), id_next = ids(1);
-      load(p.k, rk, 0, id);
-      load(p.v, rv, 0, id);
+      load(p.k, rk, 0, place(0, id));
+      load(p.v, rv, 0, place(0, id));
       auto scale = [&](const float* s, int pg) { return pg >= 0 ? __ldg(s + (long long)pg * p.kv_heads + x.h) : 0.f; };
       float sk = scale(p.k_scale, id), sv = scale(p.v_scale, id);
       for (int j = 0; j < x.n && !dead; ++j, ++count) {
@@ -493,35 +537,39 @@ __global__ void __launch_bounds__(kThreads, 1) paged_wide_kernel(const PagedAttn
         store(k_tiles + stage * kTileBytes, rk, 0u, false);
         tc05::mbar_arrive(&sh.k_full[stage]);
         const int id_far = ids(j + 2);
-        if (j + 1 < x.n) load(p.k, rk, j + 1, id_next);
+        const long long at_next = place(j + 1, id_next);
+        if (j + 1 < x.n) load(p.k, rk, j + 1, at_next);
         wait(&sh.v_free[stage], parity);
         store(v_tiles + stage * kTileBytes, rv, ratio, __any_sync(0xffffffffu, rf != 1.f));
         tc05::mbar_arrive(&sh.v_full[stage]);
         if (j + 1 < x.n) {
-          load(p.v, rv, j + 1, id_next);
+          load(p.v, rv, j + 1, at_next);
           sk = scale(p.k_scale, id_next), sv = scale(p.v_scale, id_next);
         }
         id = id_next, id_next = id_far;
       }
     }
-  } else if (lane == 0) {
+  } else {
+    fewer_registers<kProductRegs>();
+    if (warp == 12 && lane == 0) {
     // ------------------------------------------------------------------ products
     const uint32_t q_u = smem_u32(q_tiles), k_u = smem_u32(k_tiles), v_u = smem_u32(v_tiles);
     const uint32_t id_s = idesc_f16(128, 128, false), id_o = idesc_f16(128, D, true);
     uint32_t count = 0, segs[2] = {0, 0}, turns[2] = {0, 0};
+    const uint64_t q_d = tc05::sw128_desc(q_u), k_d = tc05::sw128_desc(k_u), v_d = sw128_desc_lbo(v_u, kPanel, 1024);
     auto scores = [&](int t, int stage) {
+      const uint64_t a = tc05::desc_adv(q_d, t * kTileBytes), b = tc05::desc_adv(k_d, stage * kTileBytes);
 #pragma unroll
       for (int k = 0; k < D / 16; ++k) {
         const uint32_t at = (k >> 2) * kPanel + (k & 3) * 32;
-        tc05::mma_bf16(tmem + 128 * t, tc05::sw128_desc(q_u + t * kTileBytes + at), tc05::sw128_desc(k_u + stage * kTileBytes + at),
-                       id_s, k > 0);
+        tc05::mma_bf16(tmem + 128 * t, tc05::desc_adv(a, at), tc05::desc_adv(b, at), id_s, k > 0);  // of kind::f16
       }
     };
     auto outputs = [&](int t, int stage, bool acc) {
+      const uint64_t b = tc05::desc_adv(v_d, stage * kTileBytes);
 #pragma unroll
       for (int k = 0; k < kTile / 16; ++k)
-        mma_ts(tmem + 256 + D * t, tmem + 128 * t + 8 * k, sw128_desc_lbo(v_u + stage * kTileBytes + 2048 * k, kPanel, 1024), id_o,
-               acc || k > 0);
+        mma_ts(tmem + 256 + D * t, tmem + 128 * t + 8 * k, tc05::desc_adv(b, 2048 * k), id_o, acc || k > 0);
     };
     while (walk.next(x) && !dead) {
       const int halves = x.g.n > 128 ? 2 : 1;
@@ -559,6 +607,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_wide_kernel(const PagedAttn
           }
         }
       }
+    }
     }
   }
   if (dead && p.dev_status) atomicExch(p.dev_status, (int)CSA2_ETIMEOUT);
