@@ -32,8 +32,8 @@ namespace {
 constexpr int kRows = 256;
 constexpr int kTile = 128;              // tokens of a unit
 constexpr int kThreads = 16 * 32;       // warps: softmax 0 .. 7, conversion 8 .. 11, products 12 (13 .. 15 idle)
-// Registers of a thread of each part, from 128 at launch: 2 * 160 + 120 + 72 = 4 * 128.
-constexpr int kSoftmaxRegs = 160, kConvertRegs = 120, kProductRegs = 72;
+// Registers of a thread of each part, from 128 at launch: 2 * 184 + 88 + 56 = 4 * 128.
+constexpr int kSoftmaxRegs = 184, kConvertRegs = 88, kProductRegs = 56;
 template <int N>
 __device__ __forceinline__ void more_registers() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(N)); }
 template <int N>
@@ -42,15 +42,22 @@ __device__ __forceinline__ void fewer_registers() { asm volatile("setmaxnreg.dec
 __device__ __forceinline__ uint32_t idesc_f16(int m, int n, bool b_mn_major) {
   return (1u << 4) | (b_mn_major ? 1u << 16 : 0u) | (uint32_t)(n >> 3) << 17 | (uint32_t)(m >> 4) << 24;
 }
-// Descriptor of an operand in the 128-byte swizzle with explicit leading and stride offsets.
-__device__ __forceinline__ uint64_t sw128_desc_lbo(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
-  return (uint64_t)((saddr & 0x3ffffu) >> 4) | (uint64_t)(lbo >> 4) << 16 | (uint64_t)(sbo >> 4) << 32 | 1ull << 46 | 2ull << 61;
+// Shared-memory descriptors in the 128-byte swizzle, groups of 8 rows 1,024 bytes apart, in two halves: the
+// lower holds address >> 4 and leading offset >> 4 << 16, the upper is the same for all.
+__device__ __forceinline__ uint32_t desc_lo(uint32_t saddr, uint32_t lbo) { return (saddr & 0x3ffffu) >> 4 | (lbo >> 4) << 16; }
+constexpr uint32_t kDescHi = (1024u >> 4) | 1u << 14 | 2u << 29;
+// D[tmem] (+)= A[smem] * B[smem], kind::f16; descriptors by their lower halves.
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n .reg .pred p;\n .reg .b64 da, db;\n mov.b64 da, {%1, %5};\n mov.b64 db, {%2, %5};\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n}\n" ::"r"(d), "r"(a), "r"(b), "r"(idesc), "r"(acc), "r"(kDescHi)
+      : "memory");
 }
 // D[tmem] (+)= A[tmem] * B[smem], kind::f16.
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t acc) {
   asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"(acc)
+      "{\n .reg .pred p;\n .reg .b64 db;\n mov.b64 db, {%2, %5};\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %3, p;\n}\n" ::"r"(d), "r"(a), "r"(b), "r"(idesc), "r"(acc), "r"(kDescHi)
       : "memory");
 }
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
@@ -311,41 +318,35 @@ __global__ void __launch_bounds__(kThreads, 1) paged_wide_kernel(const PagedAttn
         const int hi = see_hi - tok, lo = see_lo - tok;  // the row sees columns lo .. hi - 1
         const uint32_t flags = info.flags;
         const bool whole = __all_sync(0xffffffffu, hi >= kTile && lo <= 0) && flags == 0xffu;
+        v_ref = info.v_ref;
+        const float v_factor = info.v_factor;
+        // the scores' maximum: of a tile that all rows of the warp see whole from registers, where the
+        // scores then stay; otherwise column by column in tensor memory
         float top = -INFINITY;
+        uint32_t v[4][32];
         if (whole) {
-          uint32_t va[32], vb[32];
-          tc05::tmem_ld32(s_cols, va);
-          auto most = [&](const uint32_t (&v)[32], int c) {
-            float a = __uint_as_float(v[0]), b = __uint_as_float(v[16]);
 #pragma unroll
-            for (int k = 1; k < 16; ++k) a = fmaxf(a, __uint_as_float(v[k])), b = fmaxf(b, __uint_as_float(v[16 + k]));
+          for (int c = 0; c < 4; ++c) tc05::tmem_ld32(s_cols + 32 * c, v[c]);
+          tc05::tmem_ld_wait();
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            float a = __uint_as_float(v[c][0]), b = __uint_as_float(v[c][16]);
+#pragma unroll
+            for (int k = 1; k < 16; ++k) a = fmaxf(a, __uint_as_float(v[c][k])), b = fmaxf(b, __uint_as_float(v[c][16 + k]));
             top = fmaxf(top, fmaxf(a * (f * info.k_scale[2 * c]), b * (f * info.k_scale[2 * c + 1])));
-          };
-          tc05::tmem_ld_wait();
-          tc05::tmem_ld32(s_cols + 32, vb);
-          most(va, 0);
-          tc05::tmem_ld_wait();
-          tc05::tmem_ld32(s_cols + 64, va);
-          most(vb, 1);
-          tc05::tmem_ld_wait();
-          tc05::tmem_ld32(s_cols + 96, vb);
-          most(va, 2);
-          tc05::tmem_ld_wait();
-          most(vb, 3);
+          }
         } else {
 #pragma unroll 1
           for (int c = 0; c < 8; ++c) {  // 16 columns, of one page
-            uint32_t v[16];
-            tc05::tmem_ld16(s_cols + 16 * c, v);
+            uint32_t y[16];
+            tc05::tmem_ld16(s_cols + 16 * c, y);
             tc05::tmem_ld_wait();
             float a = -INFINITY;
 #pragma unroll
-            for (int k = 0; k < 16; ++k) a = 16 * c + k < hi && 16 * c + k >= lo ? fmaxf(a, __uint_as_float(v[k])) : a;
+            for (int k = 0; k < 16; ++k) a = 16 * c + k < hi && 16 * c + k >= lo ? fmaxf(a, __uint_as_float(y[k])) : a;
             if ((flags >> c & 1) && a > -INFINITY) top = fmaxf(top, a * (f * info.k_scale[c]));
           }
         }
-        v_ref = info.v_ref;
-        const float v_factor = info.v_factor;
         const bool grows = top > m + kPagedSlack;
         if (__any_sync(0xffffffffu, grows) || v_factor != 1.f) {
           const float to = grows ? top : m;
@@ -355,62 +356,49 @@ __global__ void __launch_bounds__(kThreads, 1) paged_wide_kernel(const PagedAttn
           if (j > 0) {
             const float o = e * v_factor;
 #pragma unroll 1
-            for (int c = 0; c < D / 32; ++c) {
-              uint32_t v[32];
-              tc05::tmem_ld32(o_cols + 32 * c, v);
+            for (int c = 0; c < D / 16; ++c) {
+              uint32_t y[16];
+              tc05::tmem_ld16(o_cols + 16 * c, y);
               tc05::tmem_ld_wait();
 #pragma unroll
-              for (int k = 0; k < 32; ++k) v[k] = __float_as_uint(__uint_as_float(v[k]) * o);
-              tc05::tmem_st32(o_cols + 32 * c, v);
+              for (int k = 0; k < 16; ++k) y[k] = __float_as_uint(__uint_as_float(y[k]) * o);
+              tc05::tmem_st16(o_cols + 16 * c, y);
             }
           }
         }
-        // weights, over the score columns that have been read
         const float off = m == -INFINITY ? 0.f : kPagedLift - m;
-        const float2 off2 = make_float2(off, off);
         if (whole) {
-          uint32_t va[32], vb[32];
-          tc05::tmem_ld32(s_cols, va);
-          auto weigh = [&](const uint32_t (&v)[32], int c) {
+          const float2 off2 = make_float2(off, off);
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
             uint32_t w[16];
             const float k0 = f * info.k_scale[2 * c], k1 = f * info.k_scale[2 * c + 1];
 #pragma unroll
             for (int k = 0; k < 16; ++k) {
               const float ks = k < 8 ? k0 : k1;
-              const float2 z = fma2(make_float2(__uint_as_float(v[2 * k]), __uint_as_float(v[2 * k + 1])), make_float2(ks, ks), off2);
+              const float2 z = fma2(make_float2(__uint_as_float(v[c][2 * k]), __uint_as_float(v[c][2 * k + 1])), make_float2(ks, ks), off2);
               const float2 e = make_float2(ex2(z.x), ex2(z.y));
               l2 = add2(l2, e);
               w[k] = pack_f16x2(e.x, e.y);
             }
             tc05::tmem_st16(s_cols + 16 * c, w);
-          };
-          tc05::tmem_ld_wait();
-          tc05::tmem_ld32(s_cols + 32, vb);
-          weigh(va, 0);
-          tc05::tmem_ld_wait();
-          tc05::tmem_ld32(s_cols + 64, va);
-          weigh(vb, 1);
-          tc05::tmem_ld_wait();
-          tc05::tmem_ld32(s_cols + 96, vb);
-          weigh(va, 2);
-          tc05::tmem_ld_wait();
-          weigh(vb, 3);
+          }
         } else {
 #pragma unroll 1
           for (int c = 0; c < 8; ++c) {
-            uint32_t v[16], w[8];
-            tc05::tmem_ld16(s_cols + 16 * c, v);
+            uint32_t y[16], w[8];
+            tc05::tmem_ld16(s_cols + 16 * c, y);
             tc05::tmem_ld_wait();
             const float ks = flags >> (8 + c) & 1 ? __uint_as_float(0x7fc00000u) : f * info.k_scale[c];
             const bool page = flags >> c & 1;
 #pragma unroll
             for (int k = 0; k < 16; ++k) {
               const bool sees = page && 16 * c + k < hi && 16 * c + k >= lo;
-              v[k] = __float_as_uint(sees ? ex2(fmaf(__uint_as_float(v[k]), ks, off)) : 0.f);
-              l2.x += __uint_as_float(v[k]);
+              y[k] = __float_as_uint(sees ? ex2(fmaf(__uint_as_float(y[k]), ks, off)) : 0.f);
+              l2.x += __uint_as_float(y[k]);
             }
 #pragma unroll
-            for (int k = 0; k < 8; ++k) w[k] = pack_f16x2(__uint_as_float(v[2 * k]), __uint_as_float(v[2 * k + 1]));
+            for (int k = 0; k < 8; ++k) w[k] = pack_f16x2(__uint_as_float(y[2 * k]), __uint_as_float(y[2 * k + 1]));
             tc05::tmem_st8(s_cols + 8 * c, w);
           }
         }
@@ -447,9 +435,12 @@ __global__ void __launch_bounds__(kThreads, 1) paged_wide_kernel(const PagedAttn
     fewer_registers<kConvertRegs>();
     // ------------------------------------------------------------------ codes to fp16 tiles
     const int gt = tid - 256;                    // thread of the group
-    const int row_in = gt >> 3, ch = gt & 7;     // D = 128: row of 16, 16-byte piece of codes
-    constexpr int LD = kTile * D / (128 * 16);   // pieces of a thread: 8, or 4 at dim 64
-    constexpr int RPL = 2048 / D;                // rows of a load of the group: 16, or 32
+    constexpr int PR = D / 16;                   // 16-byte pieces of a row's codes
+    constexpr int LD = 4;                        // pieces of a thread in a group: 64 rows, or 128 at dim 64
+    constexpr int RPL = 128 / PR;                // rows that the threads' pieces cover at once
+    constexpr int GR = LD * RPL;                 // rows of a group
+    constexpr int GROUPS = kTile / GR;           // groups of a tile
+    const int row_in = gt / PR, c16 = gt % PR;
     uint32_t count = 0;
     while (walk.next(x) && !dead) {
       const int32_t* trow = p.table + (long long)x.s.index * p.table_cols;
@@ -462,26 +453,25 @@ __global__ void __launch_bounds__(kThreads, 1) paged_wide_kernel(const PagedAttn
         const int id = __ldg(trow + (tok >> p.page_shift));
         return (unsigned)id < (unsigned)p.n_pages ? id : -2;
       };
-      uint4 rk[LD], rv[LD];
       // and the place of their codes
       auto place = [&](int j, int id) {
         const int tok = x.g.lo + (x.blk + j) * kTile + 16 * (lane & 7);
         return id < 0 ? -1LL : ((((long long)id * p.kv_heads + x.h) << p.page_shift) + (tok & mask)) * D;
       };
-      auto load = [&](const uint8_t* codes, uint4 (&r)[LD], int j, long long at) {
+      auto load = [&](uint4 (&r)[LD], const uint8_t* codes, int group, int j, long long at) {
         const int left = x.g.hi - x.g.lo - (x.blk + j) * kTile;  // tokens of the tile that are there
 #pragma unroll
         for (int i = 0; i < LD; ++i) {
-          const int row = D == 128 ? i * RPL + row_in : i * RPL + (gt >> 2), c16 = D == 128 ? ch : gt & 3;
+          const int row = group * GR + i * RPL + row_in;
           const long long from = __shfl_sync(0xffffffffu, at, row >> 4);
           r[i] = make_uint4(0, 0, 0, 0);
           if (from >= 0 && row < left) r[i] = __ldg(reinterpret_cast<const uint4*>(codes + from + (row & 15) * D + 16 * c16));
         }
       };
-      auto store = [&](uint8_t* tile, const uint4 (&r)[LD], uint32_t ratio, bool scaled) {
+      auto store = [&](const uint4 (&r)[LD], uint8_t* tile, int group, uint32_t ratio, bool scaled) {
 #pragma unroll
         for (int i = 0; i < LD; ++i) {
-          const int row = D == 128 ? i * RPL + row_in : i * RPL + (gt >> 2), c16 = D == 128 ? ch : gt & 3;
+          const int row = group * GR + i * RPL + row_in;
           const uint32_t w[4] = {r[i].x, r[i].y, r[i].z, r[i].w};
           uint32_t h[8];
 #pragma unroll
@@ -499,11 +489,18 @@ __global__ void __launch_bounds__(kThreads, 1) paged_wide_kernel(const PagedAttn
           *reinterpret_cast<uint4*>(to + (((a + sw) ^ (row & 7)) << 4)) = sw ? h1 : h0;
           *reinterpret_cast<uint4*>(to + (((a + 1 - sw) ^ (row & 7)) << 4)) = sw ? h0 : h1;
         }
-        asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
       };
       int id = ids(0), id_next = ids(1);
-      load(p.k, rk, 0, place(0, id));
-      load(p.v, rv, 0, place(0, id));
+      // the groups of K, then of V, one tile after the other; two are held, the load two ahead of its use
+      uint4 r[2][LD];
+      long long at = place(0, id);
+      if (GROUPS == 2) {
+        load(r[0], p.k, 0, 0, at);
+        load(r[1], p.k, 1, 0, at);
+      } else {
+        load(r[0], p.k, 0, 0, at);
+        load(r[1], p.v, 0, 0, at);
+      }
       auto scale = [&](const float* s, int pg) { return pg >= 0 ? __ldg(s + (long long)pg * p.kv_heads + x.h) : 0.f; };
       float sk = scale(p.k_scale, id), sv = scale(p.v_scale, id);
       for (int j = 0; j < x.n && !dead; ++j, ++count) {
@@ -534,18 +531,39 @@ __global__ void __launch_bounds__(kThreads, 1) paged_wide_kernel(const PagedAttn
         __syncwarp();
         if (gt == 0) tc05::mbar_arrive(&sh.info_full[count & 3]);
         v_ref = v_new;
-        store(k_tiles + stage * kTileBytes, rk, 0u, false);
-        tc05::mbar_arrive(&sh.k_full[stage]);
-        const int id_far = ids(j + 2);
+        const bool more = j + 1 < x.n;
         const long long at_next = place(j + 1, id_next);
-        if (j + 1 < x.n) load(p.k, rk, j + 1, at_next);
-        wait(&sh.v_free[stage], parity);
-        store(v_tiles + stage * kTileBytes, rv, ratio, __any_sync(0xffffffffu, rf != 1.f));
-        tc05::mbar_arrive(&sh.v_full[stage]);
-        if (j + 1 < x.n) {
-          load(p.v, rv, j + 1, at_next);
-          sk = scale(p.k_scale, id_next), sv = scale(p.v_scale, id_next);
+        const int id_far = ids(j + 2);
+        const bool scaled = __any_sync(0xffffffffu, rf != 1.f);
+        uint8_t* kt = k_tiles + stage * kTileBytes;
+        uint8_t* vt = v_tiles + stage * kTileBytes;
+        auto done = [&](uint64_t* bar) {
+          asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
+          tc05::mbar_arrive(bar);
+        };
+        if (GROUPS == 2) {
+          store(r[0], kt, 0, 0u, false);
+          load(r[0], p.v, 0, j, at);
+          store(r[1], kt, 1, 0u, false);
+          load(r[1], p.v, 1, j, at);
+          done(&sh.k_full[stage]);
+          wait(&sh.v_free[stage], parity);
+          store(r[0], vt, 0, ratio, scaled);
+          if (more) load(r[0], p.k, 0, j + 1, at_next);
+          store(r[1], vt, 1, ratio, scaled);
+          if (more) load(r[1], p.k, 1, j + 1, at_next);
+          done(&sh.v_full[stage]);
+        } else {
+          store(r[0], kt, 0, 0u, false);
+          if (more) load(r[0], p.k, 0, j + 1, at_next);
+          done(&sh.k_full[stage]);
+          wait(&sh.v_free[stage], parity);
+          store(r[1], vt, 0, ratio, scaled);
+          if (more) load(r[1], p.v, 0, j + 1, at_next);
+          done(&sh.v_full[stage]);
         }
+        if (more) sk = scale(p.k_scale, id_next), sv = scale(p.v_scale, id_next);
+        at = at_next;
         id = id_next, id_next = id_far;
       }
     }
@@ -555,27 +573,27 @@ __global__ void __launch_bounds__(kThreads, 1) paged_wide_kernel(const PagedAttn
     // ------------------------------------------------------------------ products
     const uint32_t q_u = smem_u32(q_tiles), k_u = smem_u32(k_tiles), v_u = smem_u32(v_tiles);
     const uint32_t id_s = idesc_f16(128, 128, false), id_o = idesc_f16(128, D, true);
-    uint32_t count = 0, segs[2] = {0, 0}, turns[2] = {0, 0};
-    const uint64_t q_d = tc05::sw128_desc(q_u), k_d = tc05::sw128_desc(k_u), v_d = sw128_desc_lbo(v_u, kPanel, 1024);
+    uint32_t count = 0, segs = 0, turns = 0;  // bits 0, 1: parity of the halves' next use
+    const uint32_t q_d = desc_lo(q_u, 16), k_d = desc_lo(k_u, 16), v_d = desc_lo(v_u, kPanel);
     auto scores = [&](int t, int stage) {
-      const uint64_t a = tc05::desc_adv(q_d, t * kTileBytes), b = tc05::desc_adv(k_d, stage * kTileBytes);
+      const uint32_t a = q_d + t * (kTileBytes >> 4), b = k_d + stage * (kTileBytes >> 4);
 #pragma unroll
       for (int k = 0; k < D / 16; ++k) {
-        const uint32_t at = (k >> 2) * kPanel + (k & 3) * 32;
-        tc05::mma_bf16(tmem + 128 * t, tc05::desc_adv(a, at), tc05::desc_adv(b, at), id_s, k > 0);  // of kind::f16
+        const uint32_t at = ((k >> 2) * kPanel + (k & 3) * 32) >> 4;
+        mma_ss(tmem + 128 * t, a + at, b + at, id_s, k > 0);
       }
     };
     auto outputs = [&](int t, int stage, bool acc) {
-      const uint64_t b = tc05::desc_adv(v_d, stage * kTileBytes);
+      const uint32_t b = v_d + stage * (kTileBytes >> 4);
 #pragma unroll
       for (int k = 0; k < kTile / 16; ++k)
-        mma_ts(tmem + 256 + D * t, tmem + 128 * t + 8 * k, tc05::desc_adv(b, 2048 * k), id_o, acc || k > 0);
+        mma_ts(tmem + 256 + D * t, tmem + 128 * t + 8 * k, b + (2048 * k >> 4), id_o, acc || k > 0);
     };
     while (walk.next(x) && !dead) {
       const int halves = x.g.n > 128 ? 2 : 1;
       for (int t = 0; t < halves; ++t) {
-        wait(&sh.q_full[t], segs[t] & 1);
-        ++segs[t];
+        wait(&sh.q_full[t], segs >> t & 1);
+        segs ^= 1u << t;
       }
       wait(&sh.k_full[count & 1], count >> 1 & 1);
       tc05::fence_after();
@@ -589,8 +607,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_wide_kernel(const PagedAttn
         const bool more = j + 1 < x.n;
         wait(&sh.v_full[stage], count >> 1 & 1);
         for (int t = 0; t < halves && !dead; ++t) {
-          wait(&sh.p_ready[t], turns[t] & 1);
-          ++turns[t];
+          wait(&sh.p_ready[t], turns >> t & 1);
+          turns ^= 1u << t;
           if (dead) break;
           tc05::fence_after();
           outputs(t, stage, j > 0);
