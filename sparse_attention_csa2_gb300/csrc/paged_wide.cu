@@ -15,9 +15,9 @@
 //             sum; the output is rescaled only where a score exceeds the running maximum by 2^4
 //
 // fp16 holds every E4M3 value; a bf16 query row is scaled by a power of two into fp16's range.  K's
-// page scale multiplies the fp32 scores, V's enters the fp16 value relative to the largest seen
-// (exact for powers of two).  Weights as in the split attention: at most 2^15, 11 bits down to 2^-21
-// of the largest.
+// page scale multiplies the fp32 scores, V's (relative to the largest seen) is an addition to the
+// weight's exponent, taken back from each 16 tokens' sum.  Weights as in the split attention: at most
+// 2^15, 11 bits down to 2^-21 of the largest.
 //
 // Work is split as there: the units (128 tokens of a tile) of the call form one line, of which each
 // block (one per SM) takes an equal piece; open tiles leave partial sums that a second kernel joins.
@@ -32,8 +32,8 @@ namespace {
 constexpr int kRows = 256;
 constexpr int kTile = 128;              // tokens of a unit
 constexpr int kThreads = 16 * 32;       // warps: softmax 0 .. 7, conversion 8 .. 11, products 12 (13 .. 15 idle)
-// Registers of a thread of each part, from 128 at launch: 2 * 184 + 88 + 56 = 4 * 128.
-constexpr int kSoftmaxRegs = 184, kConvertRegs = 88, kProductRegs = 56;
+// Registers of a thread of each part, from 128 at launch: 2 * 192 + 72 + 56 = 4 * 128.
+constexpr int kSoftmaxRegs = 192, kConvertRegs = 72, kProductRegs = 56;
 template <int N>
 __device__ __forceinline__ void more_registers() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(N)); }
 template <int N>
@@ -74,14 +74,11 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
       : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)));
   return d;
 }
-__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
-  const __half2 r = __hmul2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
-  return *reinterpret_cast<const uint32_t*>(&r);
-}
-
 // What the conversion tells the softmax about 128 tokens.
 struct TileInfo {
   float k_scale[8];   // of each 16 tokens
+  float v_log[8];     // log2 of their V scale over the reference, at least -100
+  float v_back[8];    // 2^-v_log
   float v_factor;     // what the outputs so far are to be multiplied by: the V reference grew
   float v_ref;
   uint32_t flags;     // bits 0-7: 16 tokens have a page; 8-15: their scales say NaN
@@ -156,6 +153,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_wide_kernel(const PagedAttn
   uint8_t* q_tiles = smem;
   uint8_t* k_tiles = smem + 2 * kTileBytes;
   uint8_t* v_tiles = smem + 4 * kTileBytes;
+  uint8_t* raw = smem + 6 * kTileBytes;        // 32 KB of codes on their way
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (warp == 12) tc05::tmem_alloc(&sh.tmem, 512);
   if (tid == 0) {
@@ -368,18 +366,21 @@ __global__ void __launch_bounds__(kThreads, 1) paged_wide_kernel(const PagedAttn
         }
         const float off = m == -INFINITY ? 0.f : kPagedLift - m;
         if (whole) {
-          const float2 off2 = make_float2(off, off);
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
             uint32_t w[16];
-            const float k0 = f * info.k_scale[2 * c], k1 = f * info.k_scale[2 * c + 1];
 #pragma unroll
-            for (int k = 0; k < 16; ++k) {
-              const float ks = k < 8 ? k0 : k1;
-              const float2 z = fma2(make_float2(__uint_as_float(v[c][2 * k]), __uint_as_float(v[c][2 * k + 1])), make_float2(ks, ks), off2);
-              const float2 e = make_float2(ex2(z.x), ex2(z.y));
-              l2 = add2(l2, e);
-              w[k] = pack_f16x2(e.x, e.y);
+            for (int h = 0; h < 2; ++h) {
+              const float ks = f * info.k_scale[2 * c + h], o = off + info.v_log[2 * c + h], back = info.v_back[2 * c + h];
+              float2 sum = make_float2(0.f, 0.f);
+#pragma unroll
+              for (int k = 8 * h; k < 8 * h + 8; ++k) {
+                const float2 z = fma2(make_float2(__uint_as_float(v[c][2 * k]), __uint_as_float(v[c][2 * k + 1])), make_float2(ks, ks), make_float2(o, o));
+                const float2 e = make_float2(ex2(z.x), ex2(z.y));
+                sum = add2(sum, e);
+                w[k] = pack_f16x2(e.x, e.y);
+              }
+              l2 = fma2(sum, make_float2(back, back), l2);
             }
             tc05::tmem_st16(s_cols + 16 * c, w);
           }
@@ -391,12 +392,15 @@ __global__ void __launch_bounds__(kThreads, 1) paged_wide_kernel(const PagedAttn
             tc05::tmem_ld_wait();
             const float ks = flags >> (8 + c) & 1 ? __uint_as_float(0x7fc00000u) : f * info.k_scale[c];
             const bool page = flags >> c & 1;
+            const float o = off + info.v_log[c];
+            float sum = 0.f;
 #pragma unroll
             for (int k = 0; k < 16; ++k) {
               const bool sees = page && 16 * c + k < hi && 16 * c + k >= lo;
-              y[k] = __float_as_uint(sees ? ex2(fmaf(__uint_as_float(y[k]), ks, off)) : 0.f);
-              l2.x += __uint_as_float(y[k]);
+              y[k] = __float_as_uint(sees ? ex2(fmaf(__uint_as_float(y[k]), ks, o)) : 0.f);
+              sum += __uint_as_float(y[k]);
             }
+            l2.x = fmaf(sum, info.v_back[c], l2.x);
 #pragma unroll
             for (int k = 0; k < 8; ++k) w[k] = pack_f16x2(__uint_as_float(y[2 * k]), __uint_as_float(y[2 * k + 1]));
             tc05::tmem_st8(s_cols + 8 * c, w);
@@ -458,70 +462,76 @@ __global__ void __launch_bounds__(kThreads, 1) paged_wide_kernel(const PagedAttn
         const int tok = x.g.lo + (x.blk + j) * kTile + 16 * (lane & 7);
         return id < 0 ? -1LL : ((((long long)id * p.kv_heads + x.h) << p.page_shift) + (tok & mask)) * D;
       };
-      auto load = [&](uint4 (&r)[LD], const uint8_t* codes, int group, int j, long long at) {
-        const int left = x.g.hi - x.g.lo - (x.blk + j) * kTile;  // tokens of the tile that are there
+      // a group of K's or V's codes into this thread's own slots of the ring; two (four at dim 64) to a tile
+      auto load = [&](int slot, const uint8_t* codes, int group, int j, long long at) {
+        if (j < x.n) {
+          const int left = x.g.hi - x.g.lo - (x.blk + j) * kTile;  // tokens of the tile that are there
 #pragma unroll
-        for (int i = 0; i < LD; ++i) {
-          const int row = group * GR + i * RPL + row_in;
-          const long long from = __shfl_sync(0xffffffffu, at, row >> 4);
-          r[i] = make_uint4(0, 0, 0, 0);
-          if (from >= 0 && row < left) r[i] = __ldg(reinterpret_cast<const uint4*>(codes + from + (row & 15) * D + 16 * c16));
-        }
-      };
-      auto store = [&](const uint4 (&r)[LD], uint8_t* tile, int group, uint32_t ratio, bool scaled) {
-#pragma unroll
-        for (int i = 0; i < LD; ++i) {
-          const int row = group * GR + i * RPL + row_in;
-          const uint32_t w[4] = {r[i].x, r[i].y, r[i].z, r[i].w};
-          uint32_t h[8];
-#pragma unroll
-          for (int k = 0; k < 4; ++k) f16_pairs(w[k], h[2 * k], h[2 * k + 1]);
-          if (scaled) {
-            const uint32_t s = __shfl_sync(0xffffffffu, ratio, row >> 4);
-#pragma unroll
-            for (int k = 0; k < 8; ++k) h[k] = mul_f16x2(h[k], s);
+          for (int i = 0; i < LD; ++i) {
+            const int row = group * GR + i * RPL + row_in;
+            const long long from = __shfl_sync(0xffffffffu, at, row >> 4);
+            const bool ok = from >= 0 && row < left;
+            cp_async16(raw + (slot * LD + i) * 2048 + gt * 16, codes + (ok ? from + (row & 15) * D + 16 * c16 : 0), ok);
           }
+        }
+        cp_async_commit();
+      };
+      auto store = [&](int slot, uint8_t* tile, int group) {
+        cp_async_wait<3>();
+#pragma unroll
+        for (int i = 0; i < LD; ++i) {
+          const int row = group * GR + i * RPL + row_in;
+          const uint4 w = *reinterpret_cast<const uint4*>(raw + (slot * LD + i) * 2048 + gt * 16);
           // fp16 pieces 2 c16 and 2 c16 + 1 of the row's panel; the second panel's lanes store them in the
           // other order, so that a phase's eight lanes meet all banks
-          uint8_t* to = tile + (c16 >> 2) * kPanel + row * 128;
           const int a = 2 * (c16 & 3), sw = c16 >> 2;
-          const uint4 h0 = make_uint4(h[0], h[1], h[2], h[3]), h1 = make_uint4(h[4], h[5], h[6], h[7]);
-          *reinterpret_cast<uint4*>(to + (((a + sw) ^ (row & 7)) << 4)) = sw ? h1 : h0;
-          *reinterpret_cast<uint4*>(to + (((a + 1 - sw) ^ (row & 7)) << 4)) = sw ? h0 : h1;
+          uint4 h0, h1;
+          f16_pairs(sw ? w.z : w.x, h0.x, h0.y);
+          f16_pairs(sw ? w.w : w.y, h0.z, h0.w);
+          f16_pairs(sw ? w.x : w.z, h1.x, h1.y);
+          f16_pairs(sw ? w.y : w.w, h1.z, h1.w);
+          uint8_t* to = tile + (c16 >> 2) * kPanel + row * 128;
+          *reinterpret_cast<uint4*>(to + (((a + sw) ^ (row & 7)) << 4)) = h0;
+          *reinterpret_cast<uint4*>(to + (((a + 1 - sw) ^ (row & 7)) << 4)) = h1;
         }
       };
-      int id = ids(0), id_next = ids(1);
-      // the groups of K, then of V, one tile after the other; two are held, the load two ahead of its use
-      uint4 r[2][LD];
-      long long at = place(0, id);
-      if (GROUPS == 2) {
-        load(r[0], p.k, 0, 0, at);
-        load(r[1], p.k, 1, 0, at);
-      } else {
-        load(r[0], p.k, 0, 0, at);
-        load(r[1], p.v, 0, 0, at);
-      }
+      auto done = [&](uint64_t* bar) {
+        asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
+        tc05::mbar_arrive(bar);
+      };
       auto scale = [&](const float* s, int pg) { return pg >= 0 ? __ldg(s + (long long)pg * p.kv_heads + x.h) : 0.f; };
-      float sk = scale(p.k_scale, id), sv = scale(p.v_scale, id);
+      constexpr int AHEAD = 2 / GROUPS;  // tiles that a load is ahead of its use
+      int id[AHEAD + 2];                 // page ids of tiles j .. j + AHEAD + 1
+#pragma unroll
+      for (int i = 0; i < AHEAD + 2; ++i) id[i] = ids(i);
+#pragma unroll
+      for (int i = 0; i < AHEAD; ++i) {
+        const long long at = place(i, id[i]);
+#pragma unroll
+        for (int q = 0; q < 2 * GROUPS; ++q) load(i * 2 * GROUPS + q, q < GROUPS ? p.k : p.v, q % GROUPS, i, at);
+      }
+      float sk = scale(p.k_scale, id[0]), sv = scale(p.v_scale, id[0]);
+      int slot = 0;
       for (int j = 0; j < x.n && !dead; ++j, ++count) {
         const int stage = count & 1;
         const uint32_t parity = (count >> 1 & 1) ^ 1;
-        bad |= id == -2;
-        const uint32_t pages = __ballot_sync(0xffffffffu, id != -2) & 0xffu;
+        bad |= id[0] == -2;
+        const uint32_t pages = __ballot_sync(0xffffffffu, id[0] != -2) & 0xffu;
         const uint32_t nans = __ballot_sync(0xffffffffu, sk != sk || sv != sv) & 0xffu;
-        float vm = sv > 0.f ? sv : 0.f;
-        const float sv_here = vm;
+        const float sv_here = sv > 0.f ? sv : 0.f;
+        float vm = sv_here;
         vm = fmaxf(vm, __shfl_xor_sync(0xffffffffu, vm, 1));
         vm = fmaxf(vm, __shfl_xor_sync(0xffffffffu, vm, 2));
         vm = fmaxf(vm, __shfl_xor_sync(0xffffffffu, vm, 4));
         const float v_new = fmaxf(v_ref, vm);
         const float v_inv = v_new > 0.f ? __fdiv_rn(1.f, v_new) : 0.f;
-        const float rf = sv_here * v_inv;
-        const uint32_t ratio = pack_f16x2(rf, rf);
         wait(&sh.k_free[stage], parity);
         if (gt < 8) {
           TileInfo& info = sh.info[count & 3];
+          const float ratio = fmaxf(sv_here * v_inv, 7.888609e-31f);  // 2^-100
           info.k_scale[gt] = sk == sk ? sk : 0.f;
+          info.v_log[gt] = log2f(ratio);
+          info.v_back[gt] = __fdiv_rn(1.f, ratio);
           if (gt == 0) {
             info.v_factor = v_new > v_ref ? v_ref * v_inv : 1.f;
             info.v_ref = v_new;
@@ -531,41 +541,26 @@ __global__ void __launch_bounds__(kThreads, 1) paged_wide_kernel(const PagedAttn
         __syncwarp();
         if (gt == 0) tc05::mbar_arrive(&sh.info_full[count & 3]);
         v_ref = v_new;
-        const bool more = j + 1 < x.n;
-        const long long at_next = place(j + 1, id_next);
-        const int id_far = ids(j + 2);
-        const bool scaled = __any_sync(0xffffffffu, rf != 1.f);
-        uint8_t* kt = k_tiles + stage * kTileBytes;
-        uint8_t* vt = v_tiles + stage * kTileBytes;
-        auto done = [&](uint64_t* bar) {
-          asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
-          tc05::mbar_arrive(bar);
-        };
-        if (GROUPS == 2) {
-          store(r[0], kt, 0, 0u, false);
-          load(r[0], p.v, 0, j, at);
-          store(r[1], kt, 1, 0u, false);
-          load(r[1], p.v, 1, j, at);
-          done(&sh.k_full[stage]);
-          wait(&sh.v_free[stage], parity);
-          store(r[0], vt, 0, ratio, scaled);
-          if (more) load(r[0], p.k, 0, j + 1, at_next);
-          store(r[1], vt, 1, ratio, scaled);
-          if (more) load(r[1], p.k, 1, j + 1, at_next);
-          done(&sh.v_full[stage]);
-        } else {
-          store(r[0], kt, 0, 0u, false);
-          if (more) load(r[0], p.k, 0, j + 1, at_next);
-          done(&sh.k_full[stage]);
-          wait(&sh.v_free[stage], parity);
-          store(r[1], vt, 0, ratio, scaled);
-          if (more) load(r[1], p.v, 0, j + 1, at_next);
-          done(&sh.v_full[stage]);
+        const long long at = place(j + AHEAD, id[AHEAD]);
+        const int id_far = ids(j + AHEAD + 2);
+        sk = scale(p.k_scale, id[1]), sv = scale(p.v_scale, id[1]);
+        uint8_t* tiles[2] = {k_tiles + stage * kTileBytes, v_tiles + stage * kTileBytes};
+#pragma unroll
+        for (int kv = 0; kv < 2; ++kv) {
+          if (kv == 1) wait(&sh.v_free[stage], parity);
+#pragma unroll
+          for (int q = 0; q < GROUPS; ++q) {
+            store(slot, tiles[kv], q);
+            load(slot, kv ? p.v : p.k, q, j + AHEAD, at);
+            slot = (slot + 1) & 3;
+          }
+          done(kv ? &sh.v_full[stage] : &sh.k_full[stage]);
         }
-        if (more) sk = scale(p.k_scale, id_next), sv = scale(p.v_scale, id_next);
-        at = at_next;
-        id = id_next, id_next = id_far;
+#pragma unroll
+        for (int i = 0; i < AHEAD + 1; ++i) id[i] = id[i + 1];
+        id[AHEAD + 1] = id_far;
       }
+      cp_async_wait<0>();
     }
   } else {
     fewer_registers<kProductRegs>();
@@ -649,7 +644,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_wide_kernel(const PagedAttn
 
 template <int D, bool F16>
 cudaError_t launch(const PagedAttnParams& p, int blocks, cudaStream_t stream) {
-  constexpr int smem = 6 * 128 * D * 2 + 1024;
+  constexpr int smem = 6 * 128 * D * 2 + 32768 + 1024;
   const cudaError_t e = cudaFuncSetAttribute(paged_wide_kernel<D, F16>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   paged_wide_kernel<D, F16><<<blocks, kThreads, smem, stream>>>(p);
