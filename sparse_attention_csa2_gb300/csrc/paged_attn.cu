@@ -39,6 +39,8 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kTok = 32;                // tokens of a warp's step
 constexpr int kUnit = kWarps * kTok;    // tokens of a unit
+constexpr int kLead = 4;                // units that a tile's beginning and end take: each tile lies on the line
+                                        // behind so many empty ones
 __device__ __forceinline__ void mma_e4m3(float* c, const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm volatile(
       "mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
@@ -63,7 +65,7 @@ __device__ __forceinline__ Seq seq_of(const PagedAttnParams& p, int b) {
   static_cast<PagedSeq&>(s) = paged_seq<NR>(p, b);
   s.lo = p.window > 0 ? max(s.ctx - p.window + 1, 0) & (p.page_shift == 4 ? ~15 : ~31) : 0;
   s.blocks = max((max(s.kv - s.lo, 0) + kUnit - 1) / kUnit, 1);
-  s.units = (long long)s.tiles * p.kv_heads * s.blocks;
+  s.units = (long long)s.tiles * p.kv_heads * (s.blocks + kLead);
   return s;
 }
 
@@ -178,10 +180,15 @@ __global__ void __launch_bounds__(kWarps * 32, 3)
       continue;
     }
     const long long in_seq = u - b_first;
-    const long long item = in_seq / s.blocks;
-    const int blk0 = (int)(in_seq - item * s.blocks);
+    const long long item = in_seq / (s.blocks + kLead);
+    const int from = (int)(in_seq - item * (s.blocks + kLead)) - kLead;  // place in the tile; below 0 the empty units
+    const int run = (int)min((long long)(s.blocks - from), u_end - u);
+    const int blk0 = max(from, 0), seg = from + run - blk0;
+    if (seg <= 0) {
+      u += run;
+      continue;
+    }
     const int head = (int)(item / s.tiles), tile = (int)(item - (long long)head * s.tiles);
-    const int seg = (int)min((long long)(s.blocks - blk0), u_end - u);
     const int row0 = tile * NR, n = min(NR, s.rows - row0);
     const int pos_first = s.ctx + row0 / p.group, pos_last = s.ctx + (row0 + n - 1) / p.group;
     const int t_begin = s.lo + blk0 * kUnit;
@@ -549,10 +556,10 @@ __global__ void __launch_bounds__(kWarps * 32, 3)
       o.row0 = row0, o.n = n, o.first_row = s.first, o.kv_head = head;
     }
     // the block of the tile's last unit w: the largest x with all * x / used <= w
-    pieces = starts && !ends ? (int)(((u + s.blocks) * used - 1) / all) - (int)blockIdx.x + 1 : 0;
+    pieces = starts && !ends ? (int)(((u - from + s.blocks) * used - 1) / all) - (int)blockIdx.x + 1 : 0;
     asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
     __syncthreads();  // the sums are read before the ring is filled again
-    u += seg;
+    u += run;
     if (u == b_first + s.units) {
       b_first = u;
       ++b;
