@@ -1,6 +1,7 @@
 // C ABI of the paged 8-bit cache (include/csa2.h): validation and launches of the page plan, the
 // rotary axes, the page writer and the paged attention.
 #include <cmath>
+#include <cstring>
 
 #include "kernels.h"
 #include "paged.h"
@@ -18,6 +19,23 @@ bool type_ok(int32_t t) { return t >= CSA2_T_BF16 && t <= CSA2_T_F32; }
 int type_size(int32_t t) { return t == CSA2_T_F32 ? 4 : 2; }
 bool stride_ok(int64_t row, int64_t head, int32_t t) { return row % (16 / type_size(t)) == 0 && head % (16 / type_size(t)) == 0; }
 int page_shift(int32_t page) { return page == 16 ? 4 : page == 32 ? 5 : page == 64 ? 6 : page == 128 ? 7 : 0; }
+
+// Turns per position of each pair, times 2^64, whole turns left out: theta^(-2i/R) / (2 pi).  A model calls with
+// one theta and R, so the thread's last table is kept (64 powers take longer than a launch).
+const uint64_t* rope_turns(float theta, int rot_dim) {
+  thread_local float last_theta = 0.f;
+  thread_local int last_dim = 0;
+  thread_local uint64_t turns[CSA2_ROPE_AXES_MAX_PAIRS];
+  if (theta != last_theta || rot_dim != last_dim) {
+    for (int i = 0; i < rot_dim / 2; ++i) {
+      double t = std::pow((double)theta, -2.0 * i / (double)rot_dim) / 6.283185307179586476925286766559;
+      t -= std::floor(t);
+      turns[i] = (uint64_t)std::ldexp(t, 64);
+    }
+    last_theta = theta, last_dim = rot_dim;
+  }
+  return turns;
+}
 
 // Which kernel, and its workspace.  Up to 16 query rows per sequence and kv head in the mean take the
 // split attention, three blocks per SM; more take tiles of 256, one block per SM.  No more blocks than
@@ -116,12 +134,8 @@ csa2_status csa2_rope_axes(const csa2_rope_axes_args* a, void* stream) {
   p.rot_first = a->rot_first, p.rot_dim = a->rot_dim;
   p.copy_rest = a->x != a->out;
   p.pos = a->pos;
-  for (int i = 0; i < a->rot_dim / 2; ++i) {
-    double t = std::pow((double)a->theta, -2.0 * i / (double)a->rot_dim) / 6.283185307179586476925286766559;
-    t -= std::floor(t);  // whole turns per position change nothing
-    p.turns[i] = (uint64_t)std::ldexp(t, 64);
-    p.axis[i] = a->axis_of_pair[i];
-  }
+  std::memcpy(p.turns, rope_turns(a->theta, a->rot_dim), a->rot_dim / 2 * sizeof(uint64_t));
+  std::memcpy(p.axis, a->axis_of_pair, a->rot_dim / 2);
   return cuda_status(launch_rope_axes(p, a->dtype, a->half_pairs != 0, a->inverse != 0, static_cast<cudaStream_t>(stream)));
 }
 
@@ -148,8 +162,9 @@ csa2_status csa2_write_pages(const csa2_write_pages_args* a, void* stream) {
   p.page_shift = page_shift(a->page_size);
   p.n_pages = a->n_pages, p.table_cols = a->table_cols;
   p.row_start = a->row_start, p.kv_len = a->kv_len, p.seq_of_row = a->seq_of_row, p.table = a->table;
-  // a page of rows per block where sequences bring pages, four rows where they bring a token or two
-  p.chunk = a->n_rows >= 4LL * a->n_seq ? a->page_size : 4;
+  // 64 rows (or a page of 128) per block where sequences bring pages: eight tasks of 16 rows, or two of 64,
+  // for its eight warps; four rows where they bring a token or two
+  p.chunk = a->n_rows >= 4LL * a->n_seq ? (a->page_size > 64 ? a->page_size : 64) : 4;
   p.dev_status = a->dev_status;
   return cuda_status(launch_page_write(p, a->dtype, a->head_dim, static_cast<cudaStream_t>(stream)));
 }

@@ -601,7 +601,7 @@ cudaError_t launch(const PagedAttnParams& p, int blocks, cudaStream_t stream) {
   static_assert(smem - 1024 >= kWarps * 8 * NB * D * 4, "the joined sums fit the ring");
   CopyMaps maps{};
   if (!make_map(&maps.k, p.k, p, D) || !make_map(&maps.v, p.v, p, D)) return cudaErrorNotSupported;
-  cudaError_t e = cudaFuncSetAttribute(paged_attn_kernel<D, NB, PIECES, F16>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  cudaError_t e = allow_smem<paged_attn_kernel<D, NB, PIECES, F16>>(smem);
   if (e != cudaSuccess) return e;
   paged_attn_kernel<D, NB, PIECES, F16><<<blocks, kWarps * 32, smem, stream>>>(p, maps);
   e = cudaGetLastError();

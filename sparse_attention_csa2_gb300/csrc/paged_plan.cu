@@ -192,7 +192,7 @@ __global__ void __launch_bounds__(256) rope_axes_kernel(const __grid_constant__ 
     if (d >= p.rot_first) d += p.rot_dim;
 #pragma unroll 4
     for (int h = h0; h < h1; ++h, src += p.x_head, dst += p.out_head)
-      *reinterpret_cast<uint4*>(dst + d) = *reinterpret_cast<const uint4*>(src + d);
+      __stcs(reinterpret_cast<uint4*>(dst + d), __ldcs(reinterpret_cast<const uint4*>(src + d)));
     return;
   }
   float c[NP], s[NP];
@@ -205,16 +205,16 @@ __global__ void __launch_bounds__(256) rope_axes_kernel(const __grid_constant__ 
 #pragma unroll 4
   for (int h = h0; h < h1; ++h, src += p.x_head, dst += p.out_head) {
     float a[N];
-    const uint4 ua = *reinterpret_cast<const uint4*>(src + d0);
+    const uint4 ua = __ldcs(reinterpret_cast<const uint4*>(src + d0));
     if constexpr (HALF) {
-      const uint4 ub = *reinterpret_cast<const uint4*>(src + d1);
+      const uint4 ub = __ldcs(reinterpret_cast<const uint4*>(src + d1));
       float b[N], x[N], y[N];
       Vec<T>::get(ua, a);
       Vec<T>::get(ub, b);
 #pragma unroll
       for (int k = 0; k < N; ++k) x[k] = a[k] * c[k] - b[k] * s[k], y[k] = a[k] * s[k] + b[k] * c[k];
-      *reinterpret_cast<uint4*>(dst + d0) = Vec<T>::put(x);
-      *reinterpret_cast<uint4*>(dst + d1) = Vec<T>::put(y);
+      __stcs(reinterpret_cast<uint4*>(dst + d0), Vec<T>::put(x));
+      __stcs(reinterpret_cast<uint4*>(dst + d1), Vec<T>::put(y));
     } else {
       float x[N];
       Vec<T>::get(ua, a);
@@ -223,7 +223,7 @@ __global__ void __launch_bounds__(256) rope_axes_kernel(const __grid_constant__ 
         x[2 * k] = a[2 * k] * c[k] - a[2 * k + 1] * s[k];
         x[2 * k + 1] = a[2 * k] * s[k] + a[2 * k + 1] * c[k];
       }
-      *reinterpret_cast<uint4*>(dst + d0) = Vec<T>::put(x);
+      __stcs(reinterpret_cast<uint4*>(dst + d0), Vec<T>::put(x));
     }
   }
 }
@@ -235,8 +235,10 @@ cudaError_t rope_launch(const RopeAxesParams& p, bool half, bool inv, cudaStream
   const int pieces = turned + (p.copy_rest ? (p.head_dim - p.rot_dim) / N : 0);
   const long long threads = (long long)p.n_tokens * pieces;
   const int blocks = (int)((threads + 255) / 256);
-  // heads split over blocks until some four blocks per SM are there
+  // heads split over blocks until some sixteen blocks per SM are there, so that their ends even out; below
+  // four heads a thread only for the sake of four blocks per SM, since each forms its sines anew
   int per = p.n_heads;
+  while (per > 4 && (long long)blocks * ((p.n_heads + per - 1) / per) < 2432) per = (per + 1) / 2;
   while (per > 1 && (long long)blocks * ((p.n_heads + per - 1) / per) < 608) per = (per + 1) / 2;
   const dim3 grid(blocks, (p.n_heads + per - 1) / per);
   if (half) {
@@ -254,7 +256,7 @@ cudaError_t rope_launch(const RopeAxesParams& p, bool half, bool inv, cudaStream
 cudaError_t launch_page_plan(const PagePlanParams& p, cudaStream_t stream) {
   const int smem = 2 * (p.n_seq + 1) * (int)sizeof(int);
   if (smem > 40 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(page_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    const cudaError_t e = allow_smem<page_plan_kernel>(2 * (8192 + 1) * (int)sizeof(int));
     if (e != cudaSuccess) return e;
   }
   const long long per = (long long)kPlanThreads * kPlanRows;

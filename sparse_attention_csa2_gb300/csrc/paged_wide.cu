@@ -645,7 +645,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_wide_kernel(const PagedAttn
 template <int D, bool F16>
 cudaError_t launch(const PagedAttnParams& p, int blocks, cudaStream_t stream) {
   constexpr int smem = 6 * 128 * D * 2 + 32768 + 1024;
-  const cudaError_t e = cudaFuncSetAttribute(paged_wide_kernel<D, F16>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  const cudaError_t e = allow_smem<paged_wide_kernel<D, F16>>(smem);
   if (e != cudaSuccess) return e;
   paged_wide_kernel<D, F16><<<blocks, kThreads, smem, stream>>>(p);
   return cudaGetLastError();

@@ -13,7 +13,8 @@
 // or a sequence, and spreads these tasks over its eight warps: eight tasks of a warp in a decode step
 // (a row each), two of four warps for a whole page.  The rows are read once into registers (up to 8
 // pieces a thread; what a long page has beyond is read again from L2), reduced to the largest
-// magnitude, and written as codes.  Bound by memory: 2 (or 4) bytes read and one written per value.
+// magnitude, and written as codes; four blocks per SM keep the loads of some in flight while others
+// reduce and write.  Bound by memory: 2 (or 4) bytes read and one written per value.
 #include "common.cuh"
 #include "paged.h"
 
@@ -21,15 +22,25 @@ namespace csa2 {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kHeldPieces = 8;
+constexpr int kBlocksWanted = 2048;
 constexpr int kExpMin = -100, kExpMax = 119;
 constexpr uint32_t kNaN = 0x7fc00000u;
 
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.u16x2 %0, %1, %2;\n" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
 template <typename T>
-struct In;  // a piece of 16 bytes as floats
+struct In;  // a piece of 16 bytes: as floats, and the largest magnitude of its words
 template <>
 struct In<__nv_bfloat16> {
   static constexpr int N = 8;
+  static constexpr uint32_t kOdd = 0x7f80u;  // magnitudes from here on are infinities and NaN
+  static __device__ __forceinline__ uint32_t most(uint32_t m, uint32_t w) { return max_u16x2(m, w & 0x7fff7fffu); }
+  static __device__ __forceinline__ uint32_t magnitude(uint32_t m) { return max(m & 0xffffu, m >> 16); }
+  static __device__ __forceinline__ float value(uint32_t m) { return __uint_as_float(m << 16); }
   static __device__ __forceinline__ void get(uint4 u, float (&f)[8]) {
     const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
@@ -39,6 +50,10 @@ struct In<__nv_bfloat16> {
 template <>
 struct In<__half> {
   static constexpr int N = 8;
+  static constexpr uint32_t kOdd = 0x7c00u;
+  static __device__ __forceinline__ uint32_t most(uint32_t m, uint32_t w) { return max_u16x2(m, w & 0x7fff7fffu); }
+  static __device__ __forceinline__ uint32_t magnitude(uint32_t m) { return max(m & 0xffffu, m >> 16); }
+  static __device__ __forceinline__ float value(uint32_t m) { return __half2float(__ushort_as_half((unsigned short)m)); }
   static __device__ __forceinline__ void get(uint4 u, float (&f)[8]) {
     const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
@@ -51,6 +66,10 @@ struct In<__half> {
 template <>
 struct In<float> {
   static constexpr int N = 4;
+  static constexpr uint32_t kOdd = 0x7f800000u;
+  static __device__ __forceinline__ uint32_t most(uint32_t m, uint32_t w) { return max(m, w & 0x7fffffffu); }
+  static __device__ __forceinline__ uint32_t magnitude(uint32_t m) { return m; }
+  static __device__ __forceinline__ float value(uint32_t m) { return __uint_as_float(m); }
   static __device__ __forceinline__ void get(uint4 u, float (&f)[4]) {
     f[0] = __uint_as_float(u.x), f[1] = __uint_as_float(u.y), f[2] = __uint_as_float(u.z), f[3] = __uint_as_float(u.w);
   }
@@ -63,6 +82,14 @@ __device__ __forceinline__ uint32_t codes2(float lo, float hi) {
   lo = lo != lo ? 0.f : lo;
   hi = hi != hi ? 0.f : hi;
   asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;\n" : "=h"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d) {  // of finite values
+  uint32_t r;
+  asm("{\n .reg .b16 x, y;\n cvt.rn.satfinite.e4m3x2.f32 x, %2, %1;\n cvt.rn.satfinite.e4m3x2.f32 y, %4, %3;\n"
+      " mov.b32 %0, {x, y};\n}\n"
+      : "=r"(r)
+      : "f"(a), "f"(b), "f"(c), "f"(d));
   return r;
 }
 __device__ __forceinline__ float2 values2(uint32_t codes) {
@@ -82,42 +109,55 @@ __device__ __forceinline__ bool power_of_two(float s) {
   return (u & 0x7fffffu) == 0 && (u >> 23) > 0 && (u >> 23) < 254;  // and 1 / s a normal number
 }
 
-template <typename T, int D>
-__global__ void __launch_bounds__(kThreads) page_write_kernel(const PageWriteParams p) {
+// HELD: pieces of a thread that stay in registers.
+template <typename T, int D, int HELD>
+__global__ void __launch_bounds__(kThreads, HELD == 1 ? 6 : 4) page_write_kernel(const PageWriteParams p) {
   constexpr int N = In<T>::N;
   constexpr int PR = D / N;  // pieces of a row
-  __shared__ int list[128];  // rows that open a task
+  __shared__ int4 list[128];  // rows that open a task: row, rows of the task, place in the page, page
   __shared__ int count;
+  __shared__ uint32_t warp_most[kThreads / 32];
   __shared__ float warp_max_s[kThreads / 32];
   __shared__ int warp_nan_s[kThreads / 32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int head = blockIdx.y;
   const int page = 1 << p.page_shift;
   if (tid == 0) count = 0;
   __syncthreads();
   const int r0 = blockIdx.x * p.chunk;
+  if (HELD == 1) {  // the rows' way from memory overlaps the lookups that say where they go
+    constexpr int LINES = D * (int)sizeof(T) / 128;
+    const int i = tid / LINES, line = tid % LINES, kv = i & 1, r = r0 + (i >> 1);
+    if (i < 2 * p.chunk && r < p.n_rows) {
+      const char* at = reinterpret_cast<const char*>(static_cast<const T*>(p.x[kv]) + (long long)r * p.x_row[kv] +
+                                                     (long long)blockIdx.y * p.x_head[kv]) + 128 * line;
+      asm volatile("prefetch.global.L2 [%0];\n" ::"l"(at));
+    }
+  }
   if (tid < p.chunk && r0 + tid < p.n_rows) {
     const int r = r0 + tid, b = p.seq_of_row[r];
     if ((unsigned)b < (unsigned)p.n_seq) {
       const int first = p.row_start[b], end = p.row_start[b + 1];
-      const int pos = p.kv_len[b] - end + r;
-      if (r >= first && r < end && pos >= 0 && (r == first || pos == 0 || (pos & (page - 1)) == 0)) list[atomicAdd(&count, 1)] = r;
+      const int pos = p.kv_len[b] - end + r, off = pos & (page - 1);
+      if (r >= first && r < end && pos >= 0 && (r == first || pos == 0 || off == 0)) {
+        const int col = pos >> p.page_shift;
+        const int at = atomicAdd(&count, 1);
+        list[at] = make_int4(r, min(page - off, min(end, p.n_rows) - r), off,
+                             col < p.table_cols ? p.table[(long long)b * p.table_cols + col] : -1);
+      }
     }
   }
   __syncthreads();
-  const int tasks = 2 * count;
+  const int tasks = 2 * count;  // of a head
   if (tasks == 0) return;
-  const int wpt = tasks <= 2 ? 4 : tasks <= 4 ? 2 : 1;  // warps of a task
+  // warps of a task: those that hold a page's pieces in registers, or more where the tasks are few
+  const int fit = HELD == 1 ? 1 : max(1, min(8, (PR << p.page_shift) / (32 * HELD)));
+  const int wpt = max(fit, tasks <= 2 ? 4 : tasks <= 4 ? 2 : 1);
   const int group = warp / wpt, groups = kThreads / 32 / wpt;
   const int gt = tid - group * wpt * 32, gn = wpt * 32;  // thread of the group, its threads
+  for (int head = blockIdx.y; head < p.kv_heads; head += gridDim.y)
   for (int task = group; task < tasks; task += groups) {
-    const int r = list[task >> 1], kv = task & 1;
-    const int b = p.seq_of_row[r];
-    const int end = min(p.row_start[b + 1], p.n_rows);
-    const int pos = p.kv_len[b] - p.row_start[b + 1] + r;
-    const int off = pos & (page - 1), col = pos >> p.page_shift;
-    const int n = min(page - off, end - r);
-    const int id = col < p.table_cols ? p.table[(long long)b * p.table_cols + col] : -1;
+    const int4 what = list[task >> 1];
+    const int r = what.x, n = what.y, off = what.z, id = what.w, kv = task & 1;
     if ((unsigned)id >= (unsigned)p.n_pages) {
       if (gt == 0 && p.dev_status) atomicExch(p.dev_status, (int)CSA2_EDEVICE_INDEX);
       continue;  // the whole group
@@ -128,38 +168,53 @@ __global__ void __launch_bounds__(kThreads) page_write_kernel(const PageWritePar
     float* sp = p.scale[kv] + slab;
     const float old = off ? *sp : 0.f;
 
-    uint4 held[kHeldPieces];
-    float amax = 0.f;
-    bool nan = false;
-    const int all = n * PR;
-    auto take = [&](uint4 u) {
-      float f[N];
-      In<T>::get(u, f);
-#pragma unroll
-      for (int k = 0; k < N; ++k) {
-        const float a = fabsf(f[k]);
-        nan |= a != a;
-        amax = fmaxf(amax, a == INFINITY ? 0.f : a);  // infinities saturate and do not move the scale
-      }
+    uint4 held[HELD];
+    // this thread's pieces: column gt % PR of rows gt / PR, + rows_at_once, ..
+    const int row0 = gt / PR, rows_at_once = gn / PR;
+    const T* from = src + row0 * p.x_row[kv] + gt % PR * N;
+    const long long step = rows_at_once * p.x_row[kv];
+    auto piece = [&](const T* at) { return __ldg(reinterpret_cast<const uint4*>(at)); };
+    auto group_sync = [&]() {
+      if (wpt > 1) asm volatile("bar.sync %0, %1;\n" ::"r"(1 + group), "r"(gn) : "memory");
+      else __syncwarp();
     };
 #pragma unroll
-    for (int k = 0; k < kHeldPieces; ++k) {
-      const int i = gt + k * gn;
-      if (i < all) held[k] = *reinterpret_cast<const uint4*>(src + (long long)(i / PR) * p.x_row[kv] + (i % PR) * N);
-    }
+    for (int k = 0; k < HELD; ++k) held[k] = row0 + k * rows_at_once < n ? piece(from + k * step) : make_uint4(0, 0, 0, 0);
+    uint32_t most = 0;
+    auto take = [&](uint4 u) { most = In<T>::most(In<T>::most(In<T>::most(In<T>::most(most, u.x), u.y), u.z), u.w); };
 #pragma unroll
-    for (int k = 0; k < kHeldPieces; ++k)
-      if (gt + k * gn < all) take(held[k]);
-    for (int i = gt + kHeldPieces * gn; i < all; i += gn)
-      take(*reinterpret_cast<const uint4*>(src + (long long)(i / PR) * p.x_row[kv] + (i % PR) * N));
-    amax = warp_max(amax);
-    nan = __any_sync(0xffffffffu, nan);
+    for (int k = 0; k < HELD; ++k) take(held[k]);
+    for (int r1 = row0 + HELD * rows_at_once; r1 < n; r1 += rows_at_once) take(piece(from + (r1 - row0) * p.x_row[kv]));
+    most = __reduce_max_sync(0xffffffffu, In<T>::magnitude(most));
     if (wpt > 1) {
-      if (lane == 0) warp_max_s[warp] = amax, warp_nan_s[warp] = nan;
-      asm volatile("bar.sync %0, %1;\n" ::"r"(1 + group), "r"(gn) : "memory");
-      for (int w = 0; w < wpt; ++w) {
-        amax = fmaxf(amax, warp_max_s[group * wpt + w]);
-        nan |= warp_nan_s[group * wpt + w] != 0;
+      if (lane == 0) warp_most[warp] = most;
+      group_sync();
+      for (int w = 0; w < wpt; ++w) most = max(most, warp_most[group * wpt + w]);
+    }
+    float amax = In<T>::value(most);
+    bool nan = false;
+    const bool odd = most >= In<T>::kOdd;
+    if (odd) {  // infinities do not move the scale, a NaN is told by it: once more, value by value
+      amax = 0.f;
+      for (int r1 = row0; r1 < n; r1 += rows_at_once) {
+        float f[N];
+        In<T>::get(piece(from + (r1 - row0) * p.x_row[kv]), f);
+#pragma unroll
+        for (int k = 0; k < N; ++k) {
+          const float a = fabsf(f[k]);
+          nan |= a != a;
+          amax = fmaxf(amax, a == INFINITY ? 0.f : a);
+        }
+      }
+      amax = warp_max(amax);
+      nan = __any_sync(0xffffffffu, nan);
+      if (wpt > 1) {
+        if (lane == 0) warp_max_s[warp] = amax, warp_nan_s[warp] = nan;
+        group_sync();
+        for (int w = 0; w < wpt; ++w) {
+          amax = fmaxf(amax, warp_max_s[group * wpt + w]);
+          nan |= warp_nan_s[group * wpt + w] != 0;
+        }
       }
     }
     float s = amax > 0.f ? scale_for(amax) : __uint_as_float((uint32_t)(kExpMin + 127) << 23);
@@ -177,35 +232,59 @@ __global__ void __launch_bounds__(kThreads) page_write_kernel(const PageWritePar
       }
     }
     const bool exact = power_of_two(s);
-    const float inv = exact ? __fdiv_rn(1.f, s) : 0.f;
-    auto write = [&](uint4 u, int i) {
-      float f[N];
-      In<T>::get(u, f);
-#pragma unroll
-      for (int k = 0; k < N; ++k) f[k] = exact ? f[k] * inv : __fdiv_rn(f[k], s);
-      uint8_t* to = dst + (long long)(off + i / PR) * D + (i % PR) * N;
-      const uint32_t w0 = codes2(f[0], f[1]) | codes2(f[2], f[3]) << 16;
-      if constexpr (N == 8)
-        *reinterpret_cast<uint2*>(to) = make_uint2(w0, codes2(f[4], f[5]) | codes2(f[6], f[7]) << 16);
-      else
-        *reinterpret_cast<uint32_t*>(to) = w0;
+    const float inv = __uint_as_float(0x7f000000u - __float_as_uint(s));  // of a power of two
+    const bool plain = exact && !odd;  // the usual case: no division, no NaN
+    uint8_t* into = dst + (off + row0) * D + gt % PR * N;
+    auto put = [&](uint8_t* to, const uint32_t (&w)[N / 4]) {
+      if constexpr (N == 8) *reinterpret_cast<uint2*>(to) = make_uint2(w[0], w[1]);
+      else *reinterpret_cast<uint32_t*>(to) = w[0];
     };
+    if (plain) {
+      auto write = [&](uint4 u, uint8_t* to) {
+        float f[N];
+        In<T>::get(u, f);
+        uint32_t w[N / 4];
 #pragma unroll
-    for (int k = 0; k < kHeldPieces; ++k)
-      if (gt + k * gn < all) write(held[k], gt + k * gn);
-    for (int i = gt + kHeldPieces * gn; i < all; i += gn)
-      write(*reinterpret_cast<const uint4*>(src + (long long)(i / PR) * p.x_row[kv] + (i % PR) * N), i);
-    if (wpt > 1) asm volatile("bar.sync %0, %1;\n" ::"r"(1 + group), "r"(gn) : "memory");  // all have read `old`
-    else __syncwarp();
+        for (int k = 0; k < N / 4; ++k) w[k] = codes4(f[4 * k] * inv, f[4 * k + 1] * inv, f[4 * k + 2] * inv, f[4 * k + 3] * inv);
+        put(to, w);
+      };
+#pragma unroll
+      for (int k = 0; k < HELD; ++k)
+        if (row0 + k * rows_at_once < n) write(held[k], into + k * rows_at_once * D);
+      for (int r1 = row0 + HELD * rows_at_once; r1 < n; r1 += rows_at_once)
+        write(piece(from + (r1 - row0) * p.x_row[kv]), into + (r1 - row0) * D);
+    } else {
+#pragma unroll 1
+      for (int r1 = row0; r1 < n; r1 += rows_at_once) {
+        float f[N];
+        In<T>::get(piece(from + (r1 - row0) * p.x_row[kv]), f);
+        uint32_t w[N / 4];
+#pragma unroll
+        for (int k = 0; k < N; ++k) f[k] = __fdiv_rn(f[k], s);
+#pragma unroll
+        for (int k = 0; k < N / 4; ++k) w[k] = codes2(f[4 * k], f[4 * k + 1]) | codes2(f[4 * k + 2], f[4 * k + 3]) << 16;
+        put(into + (r1 - row0) * D, w);
+      }
+    }
+    group_sync();  // all have read `old` and the warps' maxima
     if (gt == 0) *sp = nan ? __uint_as_float(kNaN) : s;
   }
 }
 
 template <typename T>
 cudaError_t write_launch(const PageWriteParams& p, int head_dim, cudaStream_t stream) {
-  const dim3 grid((p.n_rows + p.chunk - 1) / p.chunk, p.kv_heads);
-  if (head_dim == 128) page_write_kernel<T, 128><<<grid, kThreads, 0, stream>>>(p);
-  else page_write_kernel<T, 64><<<grid, kThreads, 0, stream>>>(p);
+  // heads split over blocks until each SM has some blocks one after the other
+  const int chunks = (p.n_rows + p.chunk - 1) / p.chunk;
+  int y = 1;
+  while (y < p.kv_heads && (long long)chunks * y < kBlocksWanted) y = y * 2 < p.kv_heads ? y * 2 : p.kv_heads;
+  const dim3 grid(chunks, y);
+  if (p.chunk > 4) {
+    if (head_dim == 128) page_write_kernel<T, 128, 8><<<grid, kThreads, 0, stream>>>(p);
+    else page_write_kernel<T, 64, 8><<<grid, kThreads, 0, stream>>>(p);
+  } else {  // a row or two to a task
+    if (head_dim == 128) page_write_kernel<T, 128, 1><<<grid, kThreads, 0, stream>>>(p);
+    else page_write_kernel<T, 64, 1><<<grid, kThreads, 0, stream>>>(p);
+  }
   return cudaGetLastError();
 }
 

@@ -65,6 +65,9 @@ _paged_attn_ws = _sig("csa2_paged_attn_workspace_size", [C.POINTER(PagedAttnArgs
 _paged_attn = _sig("csa2_paged_attn", [C.POINTER(PagedAttnArgs), _vp], C.c_int)
 
 
+_raw_stream = torch._C._cuda_getCurrentRawStream  # a device's current stream as a number
+
+
 # ------------------------------------------------------------------ checks
 def _dense(t, name, dtype, shape, device=None):
     """The address of a dense tensor of the given type and shape on the call's device."""
@@ -102,21 +105,27 @@ class _Prepared:
         self._call, self._args, self._device = call, args, device
         self._ref = C.byref(args)
         self._mine, self._keep = mine, keep
-        self._made_on = torch.cuda.current_stream(device).cuda_stream
+        self._index = device.index
+        self._made_on = _raw_stream(self._index)
+        self._alone = torch.cuda.device_count() == 1
 
     def _run(self):
-        if torch.cuda.current_device() != self._device.index:
+        # a decode step is made of such calls of a few microseconds each: no stream objects, no context
+        # managers on the usual way
+        if not self._alone and torch.cuda.current_device() != self._index:
             with torch.cuda.device(self._device):
                 return self._launch()
         return self._launch()
 
     def _launch(self):
-        stream = torch.cuda.current_stream()
-        raw = stream.cuda_stream
+        raw = _raw_stream(self._index)
         if raw != self._made_on:  # outputs and workspace outlive this stream's work when they are freed
+            stream = torch.cuda.current_stream()
             for t in self._mine:
                 t.record_stream(stream)
-        _check(self._call(self._ref, raw), self._name)
+        status = self._call(self._ref, raw)
+        if status:
+            _check(status, self._name)
 
 
 # ------------------------------------------------------------------ page plan
