@@ -87,6 +87,7 @@ struct PagedAttnParams {
   const void* q;
   long long q_row, q_head;          // strides in elements
   int n_rows, n_seq, kv_heads, group;
+  uint64_t group_inv;               // floor(2^64 / group) + 1 (0 for group 1): n / group is the product's upper half
   const int32_t* row_start;
   const int32_t* kv_len;
   const int32_t* table;

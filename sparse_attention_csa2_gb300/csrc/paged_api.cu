@@ -193,6 +193,7 @@ csa2_status csa2_paged_attn(const csa2_paged_attn_args* a, void* stream) {
   PagedAttnParams p{};
   p.q = a->q, p.q_row = a->q_row, p.q_head = a->q_head;
   p.n_rows = a->n_rows, p.n_seq = a->n_seq, p.kv_heads = a->kv_heads, p.group = a->heads / a->kv_heads;
+  p.group_inv = p.group == 1 ? 0 : ~0ull / p.group + 1;
   p.row_start = a->row_start, p.kv_len = a->kv_len, p.table = a->table;
   p.table_cols = a->table_cols, p.n_pages = a->n_pages, p.page_shift = page_shift(a->page_size);
   p.k = a->k_codes, p.v = a->v_codes, p.k_scale = a->k_scale, p.v_scale = a->v_scale;

@@ -146,8 +146,8 @@ __global__ void __launch_bounds__(kWarps * 32, 3)
     }
     before += x - mine;
     used = (int)min((long long)gridDim.x, total);  // blocks with work: every one of them has some
-    u = (int)blockIdx.x < used ? total * blockIdx.x / used : 0;
-    u_end = (int)blockIdx.x < used ? total * (blockIdx.x + 1) / used : 0;
+    u = (int)blockIdx.x < used ? div_rarely_long(total * blockIdx.x, used) : 0;
+    u_end = (int)blockIdx.x < used ? div_rarely_long(total * (blockIdx.x + 1), used) : 0;
     all = total;
     if (u < u_end && before <= u && u < before + mine) {
       long long at = before;
@@ -180,7 +180,7 @@ __global__ void __launch_bounds__(kWarps * 32, 3)
       continue;
     }
     const long long in_seq = u - b_first;
-    const long long item = in_seq / (s.blocks + kLead);
+    const long long item = div_rarely_long(in_seq, s.blocks + kLead);
     const int from = (int)(in_seq - item * (s.blocks + kLead)) - kLead;  // place in the tile; below 0 the empty units
     const int run = (int)min((long long)(s.blocks - from), u_end - u);
     const int blk0 = max(from, 0), seg = from + run - blk0;
@@ -188,9 +188,9 @@ __global__ void __launch_bounds__(kWarps * 32, 3)
       u += run;
       continue;
     }
-    const int head = (int)(item / s.tiles), tile = (int)(item - (long long)head * s.tiles);
+    const int head = (int)div_rarely_long(item, s.tiles), tile = (int)(item - (long long)head * s.tiles);
     const int row0 = tile * NR, n = min(NR, s.rows - row0);
-    const int pos_first = s.ctx + row0 / p.group, pos_last = s.ctx + (row0 + n - 1) / p.group;
+    const int pos_first = s.ctx + by_group(p, row0), pos_last = s.ctx + by_group(p, row0 + n - 1);
     const int t_begin = s.lo + blk0 * kUnit;
     const int t_end = min(min(t_begin + seg * kUnit, s.kv), pos_last + 1);
     const int lo_last = p.window > 0 ? pos_last - p.window + 1 : 0;
@@ -242,6 +242,22 @@ __global__ void __launch_bounds__(kWarps * 32, 3)
       __syncwarp();
     };
     int tok = t_begin + warp * kTok;
+    // the query rows set out first: they and the page ids come together
+    uint4 raw[NB][D / 32];
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) {
+      const int r = 8 * nb + g;
+      if (r < n) {
+        const int rr = row0 + r, i = by_group(p, rr);
+        const uint16_t* src = static_cast<const uint16_t*>(p.q) + (long long)(s.first + i) * p.q_row +
+                              (long long)(head * p.group + rr - i * p.group) * p.q_head + D / 4 * c;
+#pragma unroll
+        for (int k = 0; k < D / 32; ++k) raw[nb][k] = *reinterpret_cast<const uint4*>(src + 8 * k);
+      } else {
+#pragma unroll
+        for (int k = 0; k < D / 32; ++k) raw[nb][k] = make_uint4(0, 0, 0, 0);
+      }
+    }
     uint32_t okay = 0;  // two bits a stage: its halves have pages
     auto note = [&](int slot, int id0, int id1) {
       okay = (okay & ~(3u << 2 * slot)) | (uint32_t)((id0 >= 0) | (id1 >= 0) << 1) << 2 * slot;
@@ -266,30 +282,20 @@ __global__ void __launch_bounds__(kWarps * 32, 3)
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) {
       float x[D / 4];
-      const int r = 8 * nb + g;
       float amax = 0.f;
       bool odd = false;
-      if (r < n) {
-        const int rr = row0 + r, i = rr / p.group;
-        const uint16_t* src = static_cast<const uint16_t*>(p.q) + (long long)(s.first + i) * p.q_row +
-                              (long long)(head * p.group + rr - i * p.group) * p.q_head + D / 4 * c;
 #pragma unroll
-        for (int k = 0; k < D / 32; ++k) {
-          const uint4 w4 = *reinterpret_cast<const uint4*>(src + 8 * k);
-          const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
+      for (int k = 0; k < D / 32; ++k) {
+        const uint32_t w[4] = {raw[nb][k].x, raw[nb][k].y, raw[nb][k].z, raw[nb][k].w};
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            float2 v;
-            if (F16) v = __half22float2(*reinterpret_cast<const __half2*>(&w[j]));
-            else v = make_float2(bf16_lo(w[j]), bf16_hi(w[j]));
-            x[8 * k + 2 * j] = v.x, x[8 * k + 2 * j + 1] = v.y;
-            odd |= !(fabsf(v.x) < INFINITY) || !(fabsf(v.y) < INFINITY);
-            amax = fmaxf(amax, fmaxf(fabsf(v.x), fabsf(v.y)));
-          }
+        for (int j = 0; j < 4; ++j) {
+          float2 v;
+          if (F16) v = __half22float2(*reinterpret_cast<const __half2*>(&w[j]));
+          else v = make_float2(bf16_lo(w[j]), bf16_hi(w[j]));
+          x[8 * k + 2 * j] = v.x, x[8 * k + 2 * j + 1] = v.y;
+          odd |= !(fabsf(v.x) < INFINITY) || !(fabsf(v.y) < INFINITY);
+          amax = fmaxf(amax, fmaxf(fabsf(v.x), fabsf(v.y)));
         }
-      } else {
-#pragma unroll
-        for (int k = 0; k < D / 4; ++k) x[k] = 0.f;
       }
       amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
       amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
@@ -326,7 +332,7 @@ __global__ void __launch_bounds__(kWarps * 32, 3)
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         f[nb][j] = __shfl_sync(0xffffffffu, factor, 4 * (2 * c + j));
-        pos[nb][j] = s.ctx + (row0 + min(8 * nb + 2 * c + j, n - 1)) / p.group;
+        pos[nb][j] = s.ctx + by_group(p, row0 + min(8 * nb + 2 * c + j, n - 1));
       }
     }
 
@@ -544,7 +550,7 @@ __global__ void __launch_bounds__(kWarps * 32, 3)
         o.x += a.x * fw, o.y += a.y * fw, o.z += a.z * fw, o.w += a.w * fw;
       }
       if (starts && ends) {
-        const int rr = row0 + r, tokn = rr / p.group, hq = head * p.group + rr - tokn * p.group;
+        const int rr = row0 + r, tokn = by_group(p, rr), hq = head * p.group + rr - tokn * p.group;
         paged_store<D>(p, s.first + tokn, hq, d, o, M, L);
       } else {
         *reinterpret_cast<float4*>(p.part_o + ((long long)slot_of * NR + r) * D + d) = o;

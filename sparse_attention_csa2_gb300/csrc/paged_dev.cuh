@@ -40,6 +40,15 @@ __device__ __forceinline__ void paged_store(const PagedAttnParams& p, int row, i
   }
 }
 
+// n / group of a row index.  (The inverse is too large by less than one 2^64th, n below 2^31: exact.)
+__device__ __forceinline__ int by_group(const PagedAttnParams& p, int n) {
+  return p.group == 1 ? n : (int)__umul64hi((uint64_t)n, p.group_inv);
+}
+// Division of numbers that rarely need 64 bits.
+__device__ __forceinline__ long long div_rarely_long(long long a, int b) {
+  return (unsigned long long)a >> 32 ? a / b : (long long)((unsigned)a / (unsigned)b);
+}
+
 // The query rows and tokens of one sequence.
 struct PagedSeq {
   int index;

@@ -67,7 +67,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) paged_join_kernel(const Paged
     N += ml.y * f;
     t.x += v.x * f, t.y += v.y * f, t.z += v.z * f, t.w += v.w * f;
   }
-  const int rr = o.row0 + r, tokn = rr / p.group, hq = o.kv_head * p.group + rr - tokn * p.group;
+  const int rr = o.row0 + r, tokn = by_group(p, rr), hq = o.kv_head * p.group + rr - tokn * p.group;
   paged_store<D>(p, o.first_row + tokn, hq, threadIdx.x * 4, t, T, N);
 }
 

@@ -23,7 +23,7 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const PagePlanP
   extern __shared__ int sums[];  // [n_seq + 1] first rows, [n_seq + 1] first new pages
   int* row0 = sums;
   int* page0 = sums + p.n_seq + 1;
-  __shared__ int warp_tmp[kPlanThreads / 32];
+  __shared__ unsigned long long warp_sum_s[kPlanThreads / 32];
   const int tid = threadIdx.x;
   // a thread sums a run of sequences, the block scans the threads' sums
   const int run = (p.n_seq + kPlanThreads - 1) / kPlanThreads;
@@ -36,9 +36,26 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const PagePlanP
     rows += n;
     need += pages_of(c + n, p.page_size) - pages_of(c, p.page_size);
   }
-  int total_rows, total_need;
-  const int first_row = block_excl_scan<kPlanThreads>(rows, warp_tmp, &total_rows);
-  const int first_need = block_excl_scan<kPlanThreads>(need, warp_tmp, &total_need);
+  // both sums in one scan, a half of 64 bits each (both below 2^31: no carry between them)
+  unsigned long long x = (unsigned long long)(unsigned)rows << 32 | (unsigned)need;
+  const unsigned long long own = x;
+  const int lane = tid & 31, warp = tid >> 5;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const unsigned long long y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  if (lane == 31) warp_sum_s[warp] = x;
+  __syncthreads();
+  unsigned long long before = 0, total = 0;
+#pragma unroll
+  for (int w = 0; w < kPlanThreads / 32; ++w) {
+    if (w < warp) before += warp_sum_s[w];
+    total += warp_sum_s[w];
+  }
+  before += x - own;
+  const int total_rows = (int)(total >> 32), total_need = (int)(unsigned)total;
+  const int first_row = (int)(before >> 32), first_need = (int)(unsigned)before;
   for (int b = b0; b < b1; ++b) {
     row0[b] += first_row;
     page0[b] += first_need;

@@ -91,8 +91,8 @@ __device__ __forceinline__ Tile tile_of(const PagedAttnParams& p, const PagedSeq
   Tile g;
   g.row0 = t * kRows;
   g.n = min(kRows, s.rows - g.row0);
-  g.pos_first = s.ctx + g.row0 / p.group;
-  g.pos_last = s.ctx + (g.row0 + g.n - 1) / p.group;
+  g.pos_first = s.ctx + by_group(p, g.row0);
+  g.pos_last = s.ctx + by_group(p, g.row0 + g.n - 1);
   g.hi = min(s.kv, g.pos_last + 1);
   g.lo = p.window > 0 ? max(g.pos_first - p.window + 1, 0) & ~15 : 0;
   g.blocks = max((max(g.hi - g.lo, 0) + kTile - 1) / kTile, 1);
@@ -219,8 +219,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_wide_kernel(const PagedAttn
     walk([&](int, int, long long n) { units += n; });
     long long first = scan(units, all);
     used = (int)min((long long)gridDim.x, all);
-    u = (int)blockIdx.x < used ? all * blockIdx.x / used : 0;
-    u_end = (int)blockIdx.x < used ? all * (blockIdx.x + 1) / used : 0;
+    u = (int)blockIdx.x < used ? div_rarely_long(all * blockIdx.x, used) : 0;
+    u_end = (int)blockIdx.x < used ? div_rarely_long(all * (blockIdx.x + 1), used) : 0;
     if (u < u_end && first <= u && u < first + units) {
       walk([&](int b, int t, long long n) {
         if (first <= u && u < first + n) {
@@ -260,7 +260,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_wide_kernel(const PagedAttn
         continue;
       }
       const bool has = r < x.g.n;
-      const int rr = x.g.row0 + min(r, x.g.n - 1), i = rr / p.group;
+      const int rr = x.g.row0 + min(r, x.g.n - 1), i = by_group(p, rr);
       const int pos = x.s.ctx + i;
       // the query row to fp16, scaled to a maximum in [2^13, 2^14); a negative softmax scale turns its sign
       float f;
