@@ -17,7 +17,7 @@ OUT_DIR = os.path.join(HERE, "_lib")
 LIB = os.path.join(OUT_DIR, "libcsa2.so")
 SOURCES = ["api.cu", "index_scan.cu", "idx_mma.cu", "topk.cu", "attention.cu", "topk_static.cu", "writer.cu", "proj.cu",
            "selftest.cu", "paged_api.cu", "paged_plan.cu", "paged_write.cu", "paged_attn.cu", "paged_wide.cu",
-           "paged_join.cu"]
+           "paged_join.cu", "paged_rows.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2"]
 

@@ -37,23 +37,23 @@ const uint64_t* rope_turns(float theta, int rot_dim) {
   return turns;
 }
 
-// Which kernel, and its workspace.  Up to 16 query rows per sequence and kv head in the mean take the
-// split attention, three blocks per SM; more take tiles of 256, one block per SM.  No more blocks than
-// there can be units of 128 tokens (a tile has at most the table's, a sequence one tile more than its
-// rows fill).
+// Which kernel, and its workspace, by the query rows per sequence and kv head in the mean: up to 8 take
+// paged_attn.cu's (three blocks per SM), up to 32 paged_rows.cu's (two with tiles of 16, one of 32), more
+// paged_wide.cu's (one).  No more blocks than there can be units of 128 tokens (a tile has at most the
+// table's, a sequence one tile more than its rows fill).
 struct AttnPlan {
-  int rows;  // of a tile: 8, 16 or 256
+  int rows;  // of a tile
   int blocks;
   size_t part_o, part_ml, open, bytes;
 };
 AttnPlan attn_plan(const csa2_paged_attn_args* a) {
   AttnPlan pl{};
-  const long long group = a->heads / a->kv_heads;
-  const bool wide = a->n_rows * group > 16LL * a->n_seq && a->n_seq <= 16384;
-  pl.rows = wide ? 256 : group <= 8 && a->n_rows <= a->n_seq ? 8 : 16;
-  const long long tiles = ((long long)a->n_rows * group + pl.rows - 1) / pl.rows + a->n_seq;
+  const long long group = a->heads / a->kv_heads, rows = a->n_rows * group;
+  pl.rows = rows <= 8LL * a->n_seq && a->n_rows <= a->n_seq ? 8 : rows <= 16LL * a->n_seq ? 16 : rows <= 32LL * a->n_seq ? 32 : 256;
+  if (pl.rows == 256 && a->n_seq > 16384) pl.rows = 32;
+  const long long tiles = (rows + pl.rows - 1) / pl.rows + a->n_seq;
   const long long units = ((long long)a->table_cols * a->page_size + 127) / 128 + 1;
-  const long long most = (wide ? 1 : 3) * device_sm_count();
+  const long long most = (pl.rows == 8 ? 3 : pl.rows == 16 ? 2 : 1) * device_sm_count();
   const double all = (double)tiles * a->kv_heads * units;
   pl.blocks = all < (double)most ? (int)all : (int)most;
   size_t at = 0;
@@ -71,7 +71,8 @@ csa2_status check_attn_sizes(const csa2_paged_attn_args* a) {
     return CSA2_EINVAL;
   if ((a->head_dim != 64 && a->head_dim != 128) || !page_shift(a->page_size)) return CSA2_EUNSUPPORTED;
   if ((long long)a->n_rows * (a->heads / a->kv_heads) > 0x7fffffffLL - 1024 ||
-      (long long)a->table_cols * a->page_size > 0x7fffffffLL - 1024)
+      (long long)a->table_cols * a->page_size > 0x7fffffffLL - 1024 ||
+      (long long)a->n_pages * a->kv_heads > 0x7fffffffLL)
     return CSA2_EUNSUPPORTED;
   return CSA2_OK;
 }
@@ -206,7 +207,8 @@ csa2_status csa2_paged_attn(const csa2_paged_attn_args* a, void* stream) {
   p.dev_status = a->dev_status;
   cudaStream_t on = static_cast<cudaStream_t>(stream);
   return cuda_status(pl.rows == 256 ? launch_paged_wide(p, a->q_dtype, a->head_dim, pl.blocks, on)
-                                    : launch_paged_attn(p, a->q_dtype, a->head_dim, pl.rows == 8, pl.blocks, on));
+                     : pl.rows > 8  ? launch_paged_rows(p, a->q_dtype, a->head_dim, pl.rows, pl.blocks, on)
+                                    : launch_paged_attn(p, a->q_dtype, a->head_dim, true, pl.blocks, on));
 }
 
 }  // extern "C"

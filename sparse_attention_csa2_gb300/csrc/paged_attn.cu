@@ -237,7 +237,7 @@ __global__ void __launch_bounds__(kWarps * 32, 3)
       if (tok < t_end) copy(&maps.v, ST + slot, tok, id0, id1);
     };
     auto arrived = [&](int which) {
-      if (!dead && !tc05::mbar_wait(&full[warp][which], (phases >> which) & 1)) dead = true;
+      if (!dead && !paged_wait(&full[warp][which], (phases >> which) & 1)) dead = true;
       phases ^= 1u << which;
       __syncwarp();
     };

@@ -15,6 +15,47 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
+// Bounded wait for an mbarrier's phase that lets the hardware suspend the warp for about a microsecond at a
+// time: the default suspension is a few tens of cycles, and the parts of these kernels that wait then take
+// issue slots from those that work.  Gives up after 2^22 tries (some 0.1 to 4 seconds).
+__device__ __forceinline__ bool paged_wait(uint64_t* bar, uint32_t parity) {
+  const uint32_t a = smem_u32(bar);
+#pragma unroll 1
+  for (uint32_t i = 0; i < (1u << 22); ++i) {
+    uint32_t done;
+    asm volatile(
+        "{\n .reg .pred P1;\n mbarrier.try_wait.parity.shared::cta.b64 P1, [%1], %2, %3;\n selp.b32 %0, 1, 0, P1;\n}\n"
+        : "=r"(done)
+        : "r"(a), "r"(parity), "r"(1000u)
+        : "memory");
+    if (done) return true;
+  }
+  return false;
+}
+
+// Two fp32 at once.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;\n"
+      : "=l"(reinterpret_cast<uint64_t&>(d))
+      : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)), "l"(reinterpret_cast<uint64_t&>(c)));
+  return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("add.rn.f32x2 %0, %1, %2;\n"
+      : "=l"(reinterpret_cast<uint64_t&>(d))
+      : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)));
+  return d;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 d;
+  asm("mul.rn.f32x2 %0, %1, %2;\n"
+      : "=l"(reinterpret_cast<uint64_t&>(d))
+      : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)));
+  return d;
+}
+
 // The four codes of a register (low byte first) as two pairs of f16.
 __device__ __forceinline__ void f16_pairs(uint32_t v, uint32_t& lo, uint32_t& hi) {
   asm("{\n .reg .b16 a, b;\n mov.b32 {a, b}, %2;\n cvt.rn.f16x2.e4m3x2 %0, a;\n cvt.rn.f16x2.e4m3x2 %1, b;\n}\n"
@@ -38,6 +79,18 @@ __device__ __forceinline__ void paged_store(const PagedAttnParams& p, int row, i
     const uint2 u = h ? make_uint2(pack_f16x2(o.x, o.y), pack_f16x2(o.z, o.w)) : make_uint2(pack_bf16x2(o.x, o.y), pack_bf16x2(o.z, o.w));
     *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + at) = u;
   }
+}
+
+// One value.
+template <int D>
+__device__ __forceinline__ void paged_store_one(const PagedAttnParams& p, int row, int head, int d, float o, float M, float L) {
+  float den = L;
+  if (p.sink != nullptr && M > -INFINITY) den += ex2(p.sink[head] * 1.4426950408889634f - M + kPagedLift);
+  o *= L == 0.f ? 0.f : __fdividef(1.f, den);
+  const long long at = ((long long)row * (p.kv_heads * p.group) + head) * D + d;
+  if (p.out_dtype == CSA2_T_F32) static_cast<float*>(p.out)[at] = o;
+  else if (p.out_dtype == CSA2_T_F16) static_cast<__half*>(p.out)[at] = __float2half_rn(o);
+  else static_cast<__nv_bfloat16*>(p.out)[at] = __float2bfloat16_rn(o);
 }
 
 // n / group of a row index.  (The inverse is too large by less than one 2^64th, n below 2^31: exact.)

@@ -89,8 +89,14 @@ cudaError_t join(const PagedAttnParams& p, int blocks, cudaStream_t stream) {
 
 cudaError_t launch_paged_join(const PagedAttnParams& p, int head_dim, int rows, int blocks, cudaStream_t stream) {
   if (head_dim == 128)
-    return rows == 8 ? join<128, 8>(p, blocks, stream) : rows == 16 ? join<128, 16>(p, blocks, stream) : join<128, 256>(p, blocks, stream);
-  return rows == 8 ? join<64, 8>(p, blocks, stream) : rows == 16 ? join<64, 16>(p, blocks, stream) : join<64, 256>(p, blocks, stream);
+    return rows == 8    ? join<128, 8>(p, blocks, stream)
+           : rows == 16 ? join<128, 16>(p, blocks, stream)
+           : rows == 32 ? join<128, 32>(p, blocks, stream)
+                        : join<128, 256>(p, blocks, stream);
+  return rows == 8    ? join<64, 8>(p, blocks, stream)
+         : rows == 16 ? join<64, 16>(p, blocks, stream)
+         : rows == 32 ? join<64, 32>(p, blocks, stream)
+                      : join<64, 256>(p, blocks, stream);
 }
 
 }  // namespace csa2

@@ -1,0 +1,716 @@
+// Attention over a paged cache of E4M3 codes, some query rows per key-value head (shared heads, drafted
+// tokens): tiles of 16 or 32 rows on the tensor cores' 5th generation form, tokens as its rows.
+//
+// The same sums as the split attention (paged_attn.cu), which serves up to 8 rows: beyond, its warps issue
+// too many instructions per cached byte (1,185 for 32 tokens of 16 rows, three times what the codes' way
+// from memory allows).  Here, per 128 tokens,
+//
+//   S^T [128 tokens x rows] = K Q^T      kind::f8f6f4, K's codes as they come from memory (no conversion),
+//                                        the query rows as E4M3 pieces added up in the accumulator
+//   P^T = fp16 weights, a token per thread
+//   O^T [dim x rows] += V^T P^T          kind::f16, V's codes converted to fp16 (exact)
+//
+// with accumulators in tensor memory, so that a thread holds one token's few scores and no outputs.  Bound by
+// the codes' way from memory: 2 * dim bytes per cached token and head.
+//
+//   4 warps  weights (a token per thread), and at a tile's end its output (a dim per thread)
+//   4 warps  V to fp16, and the next tile's query pieces
+//   1 warp   copies of whole pages into rings of K and of V (TMA), page ids and scales ahead of them
+//   1 thread products; the next scores are computed while the present weights are formed
+//
+// The parts run through the block's tiles without a common barrier, so that one tile's end overlaps the next
+// one's copies; work is split over the blocks as in the split attention.  Two blocks per SM with 16 rows.
+#include <cudaTypedefs.h>
+
+#include "common.cuh"
+#include "paged.h"
+#include "paged_dev.cuh"
+#include "tc05.cuh"
+
+namespace csa2 {
+namespace {
+
+constexpr int kTile = 128;              // tokens of a unit
+constexpr int kLead = 2;                // units that a tile's beginning and end take (see paged_attn.cu)
+constexpr int kThreads = 10 * 32;       // warps: weights 0 .. 3, conversion 4 .. 7, copies 8, products 9
+constexpr int kInfos = 8;
+
+struct CopyMaps {
+  CUtensorMap k, v;
+};
+
+// What the copies tell the weights about 128 tokens.
+struct TileInfo {
+  float k_scale[8];   // of each 16 tokens
+  float v_log[8];     // log2 of their V scale over the reference, at least -100
+  float v_back[8];    // 2^-v_log
+  float v_factor;     // what the outputs so far are to be multiplied by: the V reference grew
+  float v_ref;
+  uint32_t flags;     // bits 0-7: 16 tokens have a page; 8-15: their scales say NaN
+};
+
+// A tile, as its end needs it.
+struct TileEnd {
+  int first_row, row0, rows, head, blk;
+  long long end;  // behind its last unit
+};
+
+template <int R, int STAGES>
+struct Shared {
+  uint64_t k_full[STAGES], k_free[STAGES], v_full[STAGES], v_free[STAGES], s_full[2], s_free[2], info_full[kInfos];
+  uint64_t w_full, p_full, pv_done, q_full, q_free, o_full;
+  TileInfo info[kInfos];
+  float factor[2][R];  // of a query row: score in log2 units = factor * k_scale * sum of products
+  int pos[2][R];       // its position
+  float top[R];        // running maxima
+  float alpha[R];
+  float part[4][R];    // of the four warps
+  TileEnd tile;
+  uint32_t tmem;
+  int place_seq;
+  long long place_first;
+  long long scan[kThreads / 32];
+};
+
+// A tile's part in a block: tokens lo + 128 blk .. of n units, none behind hi.
+struct Segment {
+  PagedSeq s;
+  int head, row0, rows, blk, n, blocks, lo, hi, pos_first, pos_last;
+};
+template <int R>
+struct Walk {
+  const PagedAttnParams& p;
+  long long u, u_end, first;  // first: the sequence's first unit
+  int b;
+  __device__ __forceinline__ static int lo_of(const PagedAttnParams& p, const PagedSeq& s) {  // a page's first token
+    return p.window > 0 ? max(s.ctx - p.window + 1, 0) >> p.page_shift << p.page_shift : 0;
+  }
+  __device__ __forceinline__ static int blocks_of(const PagedAttnParams& p, const PagedSeq& s) {
+    return max((max(s.kv - lo_of(p, s), 0) + kTile - 1) / kTile, 1);
+  }
+  __device__ __forceinline__ static long long units_of(const PagedAttnParams& p, const PagedSeq& s) {
+    return (long long)s.tiles * p.kv_heads * (blocks_of(p, s) + kLead);
+  }
+  __device__ __forceinline__ bool next(Segment& x) {
+    while (u < u_end) {
+      x.s = paged_seq<R>(p, b);
+      const long long units = units_of(p, x.s);
+      if (u >= first + units) {
+        first += units;
+        ++b;
+        continue;
+      }
+      x.blocks = blocks_of(p, x.s);
+      const long long item = div_rarely_long(u - first, x.blocks + kLead);
+      const int from = (int)(u - first - item * (x.blocks + kLead)) - kLead;
+      const int run = (int)min((long long)(x.blocks - from), u_end - u);
+      u += run;
+      x.blk = max(from, 0), x.n = from + run - x.blk;
+      if (x.n <= 0) continue;
+      x.head = (int)div_rarely_long(item, x.s.tiles);
+      x.row0 = (int)(item - (long long)x.head * x.s.tiles) * R;
+      x.rows = min(R, x.s.rows - x.row0);
+      x.pos_first = x.s.ctx + by_group(p, x.row0);
+      x.pos_last = x.s.ctx + by_group(p, x.row0 + x.rows - 1);
+      x.lo = lo_of(p, x.s);
+      x.hi = min(x.s.kv, x.pos_last + 1);
+      // units behind the last token that a row sees add nothing; one stays, so that every piece has its sums
+      x.n = min(x.n, max((max(x.hi - x.lo, 0) + kTile - 1) / kTile - x.blk, 1));
+      return true;
+    }
+    return false;
+  }
+  // The place on the line of the segment that next() gave last: its tile's first unit.
+  __device__ __forceinline__ long long tile_first(const Segment& x) const {
+    const long long tile = (long long)x.head * x.s.tiles + x.row0 / R;
+    return first + tile * (x.blocks + kLead) + kLead;
+  }
+};
+
+// Shared-memory descriptors: rows of 128, 64 or 32 bytes in the swizzle of that width, groups of 8 rows one
+// after the other; lbo: distance of the next panel along the dense dimension.
+__device__ __forceinline__ uint64_t desc(uint32_t saddr, int row_bytes, uint32_t lbo) {
+  const uint64_t mode = row_bytes == 128 ? 2 : row_bytes == 64 ? 4 : 6;
+  return (uint64_t)((saddr & 0x3ffffu) >> 4) | (uint64_t)(lbo >> 4) << 16 | (uint64_t)(8 * row_bytes >> 4) << 32 | 1ull << 46 | mode << 61;
+}
+// Byte offset of a 16-byte chunk in such rows.
+template <int B>
+__device__ __forceinline__ int swizzled(int row, int chunk) {
+  return row * B + ((B == 128 ? chunk ^ (row & 7) : B == 64 ? chunk ^ (row >> 1 & 3) : chunk ^ (row >> 2 & 1)) << 4);
+}
+__device__ __forceinline__ void mma_f16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  tc05::mma_bf16(d, a, b, idesc, acc);  // kind::f16; the types are idesc's
+}
+__device__ __forceinline__ uint32_t e4m3_word(float a, float b, float c, float d) {
+  uint32_t r;
+  asm("{\n .reg .b16 x, y;\n cvt.rn.satfinite.e4m3x2.f32 x, %2, %1;\n cvt.rn.satfinite.e4m3x2.f32 y, %4, %3;\n"
+      " mov.b32 %0, {x, y};\n}\n"
+      : "=r"(r)
+      : "f"(a), "f"(b), "f"(c), "f"(d));
+  return r;
+}
+__device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* tm, int x, int y, int z, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];\n" ::"r"(
+          smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(tm)), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
+      : "memory");
+}
+// Barrier of the four weight warps.
+__device__ __forceinline__ void weights_sync() { asm volatile("bar.sync 1, 128;\n" ::: "memory"); }
+__device__ __forceinline__ bool weights_any(bool v) {
+  uint32_t r;
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n bar.red.or.pred q, 1, 128, p;\n selp.u32 %0, 1, 0, q;\n}\n"
+      : "=r"(r)
+      : "r"((uint32_t)v)
+      : "memory");
+  return r != 0;
+}
+
+template <int D, int R, int PIECES, bool F16, int STAGES>
+__global__ void __launch_bounds__(kThreads, R == 16 ? 2 : 1)
+    paged_rows_kernel(const PagedAttnParams p, const __grid_constant__ CopyMaps maps) {
+  constexpr int kCodes = kTile * D;            // bytes of a tile's codes
+  constexpr int kPanel = kTile * 128;          // 64 dims of V in fp16
+  constexpr int kW = D / 64 * kPanel;
+  constexpr int kQ = R * D;                    // bytes of a query piece
+  constexpr int kP = kTile * 2 * R;
+  constexpr int kCols = R == 16 ? 64 : 128;    // of tensor memory: S0, S1, O
+  using Sh = Shared<R, STAGES>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  uint8_t* k_ring = smem;
+  uint8_t* v_ring = k_ring + STAGES * kCodes;
+  uint8_t* w_tile = v_ring + STAGES * kCodes;
+  uint8_t* q_tile = w_tile + kW;
+  uint8_t* p_tile = q_tile + PIECES * kQ;
+  __shared__ Sh sh;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (warp == 9) tc05::tmem_alloc(&sh.tmem, kCols);
+  if (tid == 0) {
+    for (int i = 0; i < STAGES; ++i) {
+      tc05::mbar_init(&sh.k_full[i], 1), tc05::mbar_init(&sh.k_free[i], 1);
+      tc05::mbar_init(&sh.v_full[i], 1), tc05::mbar_init(&sh.v_free[i], 128);
+    }
+    for (int i = 0; i < 2; ++i) tc05::mbar_init(&sh.s_full[i], 1), tc05::mbar_init(&sh.s_free[i], 128);
+    for (int i = 0; i < kInfos; ++i) tc05::mbar_init(&sh.info_full[i], 1);
+    tc05::mbar_init(&sh.w_full, 128), tc05::mbar_init(&sh.p_full, 128), tc05::mbar_init(&sh.pv_done, 1);
+    tc05::mbar_init(&sh.q_full, 128), tc05::mbar_init(&sh.q_free, 1), tc05::mbar_init(&sh.o_full, 1);
+    tc05::fence_barrier_init();
+  }
+
+  // ---- this block's piece of the line of units
+  long long all, u, u_end;
+  int used;
+  {
+    const int run = (p.n_seq + kThreads - 1) / kThreads;
+    const int q0 = min(tid * run, p.n_seq), q1 = min(q0 + run, p.n_seq);
+    long long mine = 0;
+    for (int i = q0; i < q1; ++i) mine += Walk<R>::units_of(p, paged_seq<R>(p, i));
+    long long x = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    if (lane == 31) sh.scan[warp] = x;
+    __syncthreads();
+    long long before = 0;
+    all = 0;
+    for (int w = 0; w < kThreads / 32; ++w) {
+      if (w < warp) before += sh.scan[w];
+      all += sh.scan[w];
+    }
+    before += x - mine;
+    used = (int)min((long long)gridDim.x, all);
+    u = (int)blockIdx.x < used ? div_rarely_long(all * blockIdx.x, used) : 0;
+    u_end = (int)blockIdx.x < used ? div_rarely_long(all * (blockIdx.x + 1), used) : 0;
+    if (u < u_end && before <= u && u < before + mine) {
+      int i = q0;
+      for (;; ++i) {
+        const long long n = Walk<R>::units_of(p, paged_seq<R>(p, i));
+        if (u < before + n) break;
+        before += n;
+      }
+      sh.place_seq = i;
+      sh.place_first = before;
+    }
+    tc05::fence_before();
+    __syncthreads();
+    tc05::fence_after();
+  }
+  const uint32_t tmem = sh.tmem;
+  Walk<R> walk{p, u, u_end, sh.place_first, sh.place_seq};
+  Segment x;
+  bool dead = false, bad = false;
+  uint32_t count = 0, segs = 0;  // units, tiles of the block so far
+  auto wait = [&](uint64_t* bar, uint32_t parity) {
+    if (!dead && !paged_wait(bar, parity)) dead = true;
+    if (warp < 9) dead = __any_sync(0xffffffffu, dead);
+  };
+
+  if (warp < 4) {
+    // ------------------------------------------------------------------ weights: a token per thread
+    const uint32_t lanes = tmem + ((uint32_t)(32 * warp) << 16);
+    const uint32_t o_cols = lanes + 2 * R;
+    int pieces = 0;
+    while (walk.next(x) && !dead) {
+      const int par = segs & 1;
+      // what the units need of the tile, the rest waits in shared memory
+      const int units = x.n, hi = x.hi;
+      int tok0 = x.lo + x.blk * kTile;
+      // every row sees all 128 tokens of a unit that begins in [seen_lo, seen_hi]
+      const int seen_lo = p.window == 0 ? 0 : x.pos_last - p.window + 1, seen_hi = min(x.pos_first, x.hi - 1) - kTile + 1;
+      const int window = p.window == 0 ? 0x7fffffff : p.window;
+      const long long tile_first = walk.tile_first(x);
+      if (tid == 0) sh.tile = {x.s.first, x.row0, x.rows, x.head, x.blk, tile_first + x.blocks};
+      float2 l[R / 2], low[R / 2];  // sums and minus the maxima of the rows
+      float v_ref = 0.f;
+#pragma unroll
+      for (int r = 0; r < R / 2; ++r) l[r] = make_float2(0.f, 0.f), low[r] = make_float2(INFINITY, INFINITY);
+      for (int j = 0; j < units && !dead; ++j, ++count, tok0 += kTile) {
+        const int buf = count & 1;
+        wait(&sh.s_full[buf], count >> 1 & 1);
+        if (dead) break;
+        tc05::fence_after();
+        uint32_t s[R];
+        tc05::tmem_ld<R>(lanes + R * buf, s);
+        const TileInfo& info = sh.info[count % kInfos];
+        const int tok = tok0 + tid, g = tid >> 4;
+        const uint32_t flags = info.flags;
+        const float ks = flags >> (8 + g) & 1 ? __uint_as_float(0x7fc00000u) : info.k_scale[g];
+        const float lift = kPagedLift + info.v_log[g], v_back = info.v_back[g], v_factor = info.v_factor;
+        v_ref = info.v_ref;
+        const bool whole = flags == 0xffu && tok0 <= seen_hi && tok0 >= seen_lo;
+        uint32_t sees = 0xffffffffu;  // bit r: row r sees the token
+        if (!whole) {
+          sees = 0;
+          if (tok < hi && (flags >> g & 1)) {
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+              const int ps = sh.pos[par][r];
+              if (tok <= ps && ps - tok < window) sees |= 1u << r;
+            }
+          }
+        }
+        tc05::tmem_ld_wait();
+        tc05::fence_before();
+        tc05::mbar_arrive(&sh.s_free[buf]);
+        float2 t[R / 2];  // scores, then over the maxima
+        const float2 ks2 = make_float2(ks, ks);
+        float over = -INFINITY;
+#pragma unroll
+        for (int r = 0; r < R / 2; ++r)
+          t[r] = mul2(make_float2(__uint_as_float(s[2 * r]), __uint_as_float(s[2 * r + 1])),
+                      mul2(*reinterpret_cast<const float2*>(&sh.factor[par][2 * r]), ks2));
+        if (whole) {
+#pragma unroll
+          for (int r = 0; r < R / 2; ++r) {
+            const float2 y = add2(t[r], low[r]);
+            over = fmaxf(over, fmaxf(y.x, y.y));
+          }
+        } else {
+#pragma unroll
+          for (int r = 0; r < R / 2; ++r) {
+            const float2 y = add2(t[r], low[r]);
+            if (sees >> (2 * r) & 1) over = fmaxf(over, y.x);
+            if (sees >> (2 * r + 1) & 1) over = fmaxf(over, y.y);
+          }
+        }
+        // a first unit, a score 2^4 above its row's maximum, or a larger V reference: everything moves there
+        if (j == 0 || weights_any(over > kPagedSlack) || v_factor != 1.f) {
+#pragma unroll
+          for (int r = 0; r < R; ++r) {
+            const float2 tt = t[r / 2];
+            float top = sees >> r & 1 ? (r & 1 ? tt.y : tt.x) : -INFINITY;
+            top = warp_max(top);
+            if (lane == 0) sh.part[warp][r] = top;
+          }
+          weights_sync();
+          if (tid < R) {
+            const float old = j == 0 ? -INFINITY : sh.top[tid];
+            const float now = fmaxf(old, fmaxf(fmaxf(sh.part[0][tid], sh.part[1][tid]), fmaxf(sh.part[2][tid], sh.part[3][tid])));
+            sh.top[tid] = now;
+            sh.alpha[tid] = old == -INFINITY ? 0.f : ex2(old - now);
+          }
+          weights_sync();
+#pragma unroll
+          for (int r = 0; r < R / 2; ++r) {
+            const float2 m = *reinterpret_cast<const float2*>(&sh.top[2 * r]);
+            low[r] = make_float2(-m.x, -m.y);
+          }
+          if (j > 0) {
+            wait(&sh.pv_done, (count - 1) & 1);
+            if (dead) break;
+            tc05::fence_after();
+            uint32_t o[R];
+            tc05::tmem_ld<R>(o_cols, o);
+            tc05::tmem_ld_wait();
+#pragma unroll
+            for (int r = 0; r < R / 2; ++r) {
+              const float2 a = *reinterpret_cast<const float2*>(&sh.alpha[2 * r]);
+              l[r] = mul2(l[r], a);
+              o[2 * r] = __float_as_uint(__uint_as_float(o[2 * r]) * (a.x * v_factor));
+              o[2 * r + 1] = __float_as_uint(__uint_as_float(o[2 * r + 1]) * (a.y * v_factor));
+            }
+            if constexpr (R == 16) tc05::tmem_st16(o_cols, o);
+            else tc05::tmem_st32(o_cols, o);
+            tc05::tmem_st_wait();
+          }
+        }
+        // weights
+        uint32_t w[R / 2];
+        const float2 lift2 = make_float2(lift, lift), back2 = make_float2(v_back, v_back);
+        if (whole) {
+#pragma unroll
+          for (int r = 0; r < R / 2; ++r) {
+            const float2 z = add2(add2(t[r], low[r]), lift2);
+            const float2 e = make_float2(ex2(z.x), ex2(z.y));
+            l[r] = fma2(e, back2, l[r]);
+            w[r] = pack_f16x2(e.x, e.y);
+          }
+        } else {
+#pragma unroll
+          for (int r = 0; r < R / 2; ++r) {
+            const float2 z = add2(add2(t[r], low[r]), lift2);
+            const float2 e = make_float2(sees >> (2 * r) & 1 ? ex2(z.x) : 0.f, sees >> (2 * r + 1) & 1 ? ex2(z.y) : 0.f);
+            l[r] = fma2(e, back2, l[r]);
+            w[r] = pack_f16x2(e.x, e.y);
+          }
+        }
+        if (count > 0) wait(&sh.pv_done, (count - 1) & 1);  // the weights before have been read
+        if (dead) break;
+#pragma unroll
+        for (int k = 0; k < R / 8; ++k)
+          *reinterpret_cast<uint4*>(p_tile + swizzled<2 * R>(tid, k)) = make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
+        asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
+        tc05::fence_before();
+        tc05::mbar_arrive(&sh.p_full);
+      }
+      if (dead) break;
+      // ---- the tile's outputs, or its partial sums
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        const float t = warp_sum(r & 1 ? l[r / 2].y : l[r / 2].x);
+        if (lane == 0) sh.part[warp][r] = t;
+      }
+      weights_sync();
+      wait(&sh.o_full, segs & 1);
+      ++segs;
+      if (dead) break;
+      tc05::fence_after();
+      const auto tile = sh.tile;
+      const bool starts = tile.blk == 0, ends = tile.end <= u_end;
+      const long long slot = (2LL * blockIdx.x + (starts ? 1 : 0)) * R;
+      uint32_t o[R];
+      tc05::tmem_ld<R>(o_cols, o);
+      tc05::tmem_ld_wait();
+      tc05::fence_before();
+      // D = 64: 64 accumulator rows lie in 16 lanes of each warp
+      const int d = D == 128 ? tid : 16 * warp + lane;
+      if (D == 128 || lane < 16) {
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+          if (r >= tile.rows) break;
+          const float M = sh.top[r], L = sh.part[0][r] + sh.part[1][r] + sh.part[2][r] + sh.part[3][r];
+          const float val = __uint_as_float(o[r]) * v_ref;
+          if (starts && ends) {
+            const int rr = tile.row0 + r, i = by_group(p, rr);
+            paged_store_one<D>(p, tile.first_row + i, tile.head * p.group + rr - i * p.group, d, val, M, L);
+          } else {
+            p.part_o[(slot + r) * D + d] = val;
+            if (d == 0) *reinterpret_cast<float2*>(p.part_ml + (slot + r) * 2) = make_float2(M, L);
+          }
+        }
+      }
+      weights_sync();  // maxima and sums are read before the next tile's
+      if (starts && !ends) {
+        pieces = (int)((tile.end * used - 1) / all) - (int)blockIdx.x + 1;
+        if (tid == 0) {
+          PagedOpen& open = p.open[blockIdx.x];
+          open.row0 = tile.row0, open.n = tile.rows, open.first_row = tile.first_row, open.kv_head = tile.head;
+        }
+      } else {
+        pieces = 0;
+      }
+    }
+    if (tid == 0) p.open[blockIdx.x].pieces = dead ? 0 : pieces;
+  } else if (warp < 8) {
+    // ------------------------------------------------------------------ query pieces; V to fp16
+    const int gt = tid - 128;
+    constexpr int TR = 128 / R;                // threads of a query row
+    constexpr int QD = D / TR;                 // dims of a thread
+    const int qr = gt / TR, qc = gt % TR;
+    constexpr int PR = D / 16;                 // 16-byte pieces of a token's codes
+    constexpr int RPL = 128 / PR;              // tokens that the threads' pieces cover at once
+    const int row_in = gt / PR, c16 = gt % PR;
+    while (walk.next(x) && !dead) {
+      const int par = segs & 1;
+      // the tile's query rows: scaled by a power of two to a maximum in [224, 448), as E4M3 pieces
+      const int rr = x.row0 + min(qr, x.rows - 1), i = by_group(p, rr);
+      float y[QD];
+      float amax = 0.f;
+      bool odd = false;
+      {
+        const uint16_t* src = static_cast<const uint16_t*>(p.q) + (long long)(x.s.first + i) * p.q_row +
+                              (long long)(x.head * p.group + rr - i * p.group) * p.q_head + QD * qc;
+#pragma unroll
+        for (int k = 0; k < QD / 8; ++k) {
+          const uint4 v4 = qr < x.rows ? *reinterpret_cast<const uint4*>(src + 8 * k) : make_uint4(0, 0, 0, 0);
+          const uint32_t w[4] = {v4.x, v4.y, v4.z, v4.w};
+#pragma unroll
+          for (int n = 0; n < 4; ++n) {
+            const float2 v = F16 ? __half22float2(*reinterpret_cast<const __half2*>(&w[n])) : make_float2(bf16_lo(w[n]), bf16_hi(w[n]));
+            y[8 * k + 2 * n] = v.x, y[8 * k + 2 * n + 1] = v.y;
+            odd |= !(fabsf(v.x) < INFINITY) || !(fabsf(v.y) < INFINITY);
+            amax = fmaxf(amax, fmaxf(fabsf(v.x), fabsf(v.y)));
+          }
+        }
+      }
+#pragma unroll
+      for (int o = 1; o < TR; o <<= 1) {
+        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+        odd = __shfl_xor_sync(0xffffffffu, (int)odd, o) | odd;
+      }
+      const uint32_t ua = __float_as_uint(amax);
+      int e = (int)(ua >> 23) - 127 - 8 + ((ua & 0x7fffffu) >= 0x600000u ? 1 : 0);
+      e = min(max(e, -110), 119);
+      const float down = odd ? 0.f : __uint_as_float((uint32_t)(127 - e) << 23), up = __uint_as_float((uint32_t)(127 + e) << 23);
+#pragma unroll
+      for (int k = 0; k < QD; ++k) y[k] = odd ? 0.f : y[k] * down;
+      // the weights of the tile before the last have been formed: its factors may go
+      if (segs > 0) wait(&sh.q_free, (segs - 1) & 1);
+      if (dead) break;
+      if (qc == 0) {
+        sh.factor[par][qr] = odd ? __uint_as_float(0x7fc00000u) : p.scale_log2 * up;
+        sh.pos[par][qr] = x.s.ctx + i;
+      }
+#pragma unroll
+      for (int m = 0; m < PIECES; ++m)
+#pragma unroll
+        for (int k = 0; k < QD / 4; ++k) {
+          float* z = y + 4 * k;
+          const uint32_t w = e4m3_word(z[0], z[1], z[2], z[3]);
+          if (m + 1 < PIECES) {
+            uint32_t h0, h1;
+            f16_pairs(w, h0, h1);
+            const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&h0));
+            const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&h1));
+            z[0] -= a.x, z[1] -= a.y, z[2] -= b.x, z[3] -= b.y;  // exact
+          }
+          const int at = QD * qc + 4 * k;  // byte of the row
+          *reinterpret_cast<uint32_t*>(q_tile + m * kQ + swizzled<D>(qr, at >> 4) + (at & 15)) = w;
+        }
+      asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
+      tc05::mbar_arrive(&sh.q_full);
+      ++segs;
+      for (int j = 0; j < x.n && !dead; ++j, ++count) {
+        const int stage = count % STAGES;
+        wait(&sh.v_full[stage], count / STAGES & 1);
+        wait(&sh.info_full[count % kInfos], count / kInfos & 1);
+        if (count > 0) wait(&sh.pv_done, (count - 1) & 1);
+        if (dead) break;
+        const uint8_t* raw = v_ring + stage * kCodes + row_in * D + 16 * c16;
+        // fp16 pieces 2 c16 and 2 c16 + 1 of the row's panel; the second panel's lanes store them in the other
+        // order, so that a phase's eight lanes meet all banks.  (RPL is a multiple of 8: one swizzle for all.)
+        const int sw = c16 >> 2, a = 2 * (c16 & 3);
+        uint8_t* to = w_tile + sw * kPanel + row_in * 128;
+        uint8_t* to0 = to + (((a + sw) ^ (row_in & 7)) << 4);
+        uint8_t* to1 = to + (((a + 1 - sw) ^ (row_in & 7)) << 4);
+        auto piece = [&](int q, uint4 w) {
+          uint4 h0, h1;
+          f16_pairs(sw ? w.z : w.x, h0.x, h0.y);
+          f16_pairs(sw ? w.w : w.y, h0.z, h0.w);
+          f16_pairs(sw ? w.x : w.z, h1.x, h1.y);
+          f16_pairs(sw ? w.y : w.w, h1.z, h1.w);
+          *reinterpret_cast<uint4*>(to0 + q * RPL * 128) = h0;
+          *reinterpret_cast<uint4*>(to1 + q * RPL * 128) = h1;
+        };
+        const uint32_t flags = sh.info[count % kInfos].flags;
+        const int left = x.hi - x.lo - (x.blk + j) * kTile;  // tokens that are there: what lies behind may be anything
+        if (left >= kTile && (flags & 0xffu) == 0xffu) {
+#pragma unroll
+          for (int q = 0; q < kTile / RPL; ++q) piece(q, *reinterpret_cast<const uint4*>(raw + q * RPL * D));
+        } else {
+#pragma unroll 1
+          for (int q = 0; q < kTile / RPL; ++q) {
+            const int row = q * RPL + row_in;
+            piece(q, row < left && (flags >> (row >> 4) & 1) ? *reinterpret_cast<const uint4*>(raw + q * RPL * D) : make_uint4(0, 0, 0, 0));
+          }
+        }
+        asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
+        tc05::mbar_arrive(&sh.w_full);
+        tc05::mbar_arrive(&sh.v_free[stage]);
+      }
+    }
+  } else if (warp == 8) {
+    // ------------------------------------------------------------------ copies
+    const int page = 1 << p.page_shift, mask = page - 1;
+    while (walk.next(x) && !dead) {
+      const int32_t* trow = p.table + (long long)x.s.index * p.table_cols;
+      float v_ref = 0.f;
+      // lane l (as l & 7) knows the page of tokens 16 l .. of a unit
+      auto ids = [&](int j) {
+        const int tok = x.lo + (x.blk + j) * kTile + 16 * (lane & 7);
+        if (j >= x.n || tok >= x.hi) return -1;
+        const int id = __ldg(trow + (tok >> p.page_shift));
+        return (unsigned)id < (unsigned)p.n_pages ? id : -2;
+      };
+      int id = ids(0);
+      for (int j = 0; j < x.n && !dead; ++j, ++count) {
+        const int id_next = ids(j + 1);
+        const int stage = count % STAGES;
+        const uint32_t parity = (count / STAGES & 1) ^ 1;
+        const long long slab = id >= 0 ? (long long)id * p.kv_heads + x.head : 0;
+        const float sk = id >= 0 ? __ldg(p.k_scale + slab) : 0.f, sv = id >= 0 ? __ldg(p.v_scale + slab) : 0.f;
+        bad |= id == -2;
+        // a lane whose 16 tokens begin a page (or, in pages of 128, the unit) copies it
+        const bool copies = lane < 8 && id >= 0 && (16 * lane & mask & (kTile - 1)) == 0;
+        const int rows = min(page, kTile);
+        const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, copies)) * rows * D;
+        const int tok = x.lo + (x.blk + j) * kTile + 16 * lane;
+        wait(&sh.k_free[stage], parity);
+        if (dead) break;
+        if (lane == 0) tc05::mbar_expect_tx(&sh.k_full[stage], bytes);
+        __syncwarp();
+        if (copies) tma_load_3d(k_ring + stage * kCodes + 16 * lane * D, &maps.k, 0, tok & mask, (int)slab, &sh.k_full[stage]);
+        wait(&sh.v_free[stage], parity);
+        if (dead) break;
+        if (lane == 0) tc05::mbar_expect_tx(&sh.v_full[stage], bytes);
+        __syncwarp();
+        if (copies) tma_load_3d(v_ring + stage * kCodes + 16 * lane * D, &maps.v, 0, tok & mask, (int)slab, &sh.v_full[stage]);
+        // scales
+        const uint32_t pages = __ballot_sync(0xffffffffu, id != -2) & 0xffu;
+        const uint32_t nans = __ballot_sync(0xffffffffu, sk != sk || sv != sv) & 0xffu;
+        const float sv_here = sv > 0.f ? sv : 0.f;
+        float vm = sv_here;
+        vm = fmaxf(vm, __shfl_xor_sync(0xffffffffu, vm, 1));
+        vm = fmaxf(vm, __shfl_xor_sync(0xffffffffu, vm, 2));
+        vm = fmaxf(vm, __shfl_xor_sync(0xffffffffu, vm, 4));
+        const float v_new = fmaxf(v_ref, vm);
+        const float v_inv = v_new > 0.f ? __fdiv_rn(1.f, v_new) : 0.f;
+        TileInfo& info = sh.info[count % kInfos];
+        if (lane < 8) {
+          const float ratio = fmaxf(sv_here * v_inv, 7.888609e-31f);  // 2^-100
+          info.k_scale[lane] = sk == sk ? sk : 0.f;
+          info.v_log[lane] = log2f(ratio);
+          info.v_back[lane] = __fdiv_rn(1.f, ratio);
+          if (lane == 0) {
+            info.v_factor = v_new > v_ref ? v_ref * v_inv : 1.f;
+            info.v_ref = v_new;
+            info.flags = pages | nans << 8;
+          }
+        }
+        v_ref = v_new;
+        __syncwarp();
+        if (lane == 0) tc05::mbar_arrive(&sh.info_full[count % kInfos]);
+        id = id_next;
+      }
+    }
+  } else if (lane == 0) {
+    // ------------------------------------------------------------------ products
+    constexpr uint32_t id_s = tc05::idesc_e4m3(128, R);
+    // fp32 D, fp16 A and B, both with their other dimension dense
+    constexpr uint32_t id_o = (1u << 4) | (1u << 15) | (1u << 16) | ((uint32_t)(R >> 3) << 17) | ((uint32_t)(D >> 4) << 24);
+    const uint64_t k_d = desc(smem_u32(k_ring), D, 16), q_d = desc(smem_u32(q_tile), D, 16);
+    const uint64_t w_d = desc(smem_u32(w_tile), 128, kPanel), p_d = desc(smem_u32(p_tile), 2 * R, 16);
+    auto scores = [&](uint32_t n) {
+      const int stage = n % STAGES, buf = n & 1;
+      wait(&sh.k_full[stage], n / STAGES & 1);
+      wait(&sh.info_full[n % kInfos], n / kInfos & 1);  // for the weights, that wait for the scores alone
+      wait(&sh.s_free[buf], (n >> 1 & 1) ^ 1);
+      if (dead) return;
+      tc05::fence_after();
+      const uint64_t a = tc05::desc_adv(k_d, stage * kCodes);
+#pragma unroll
+      for (int m = 0; m < PIECES; ++m)
+#pragma unroll
+        for (int k = 0; k < D / 32; ++k)
+          tc05::mma_e4m3(tmem + R * buf, tc05::desc_adv(a, 32 * k), tc05::desc_adv(q_d, m * kQ + 32 * k), id_s, m + k > 0);
+      tc05::mma_commit(&sh.s_full[buf]);
+      tc05::mma_commit(&sh.k_free[stage]);
+    };
+    while (walk.next(x) && !dead) {
+      wait(&sh.q_full, segs & 1);
+      ++segs;
+      scores(count);
+      if (x.n == 1) tc05::mma_commit(&sh.q_free);
+      for (int j = 0; j < x.n && !dead; ++j, ++count) {
+        if (j + 1 < x.n) {
+          scores(count + 1);
+          if (j + 2 == x.n) tc05::mma_commit(&sh.q_free);
+        }
+        wait(&sh.w_full, count & 1);
+        wait(&sh.p_full, count & 1);
+        if (dead) break;
+        tc05::fence_after();
+#pragma unroll
+        for (int k = 0; k < kTile / 16; ++k)
+          mma_f16(tmem + 2 * R, tc05::desc_adv(w_d, 2048 * k), tc05::desc_adv(p_d, 16 * 2 * R * k), id_o, j > 0 || k > 0);
+        tc05::mma_commit(&sh.pv_done);
+        if (j + 1 == x.n) tc05::mma_commit(&sh.o_full);
+      }
+    }
+  }
+  if (dead && p.dev_status) atomicExch(p.dev_status, (int)CSA2_ETIMEOUT);
+  if (bad && p.dev_status) atomicExch(p.dev_status, (int)CSA2_EDEVICE_INDEX);
+  __syncwarp();
+  __syncthreads();
+  if (warp == 9) tc05::tmem_dealloc(tmem, kCols);
+}
+
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      f = nullptr;
+    return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
+  }();
+  return fn;
+}
+
+// Codes as [pages x heads, page, dim]; a copy takes a page (of pages of 128: 128 tokens).
+bool make_map(CUtensorMap* map, const uint8_t* codes, const PagedAttnParams& p, int dim, CUtensorMapSwizzle swizzle) {
+  if (p.n_pages == 0 || p.table_cols == 0) return true;  // no page is ever read
+  const PFN_cuTensorMapEncodeTiled_v12000 fn = encode_fn();
+  if (fn == nullptr) return false;
+  const cuuint64_t page = 1ull << p.page_shift;
+  const cuuint64_t dims[3] = {(cuuint64_t)dim, page, (cuuint64_t)p.n_pages * p.kv_heads};
+  const cuuint64_t strides[2] = {(cuuint64_t)dim, dim * page};
+  const cuuint32_t box[3] = {(cuuint32_t)dim, (cuuint32_t)(page < kTile ? page : kTile), 1}, one[3] = {1, 1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<uint8_t*>(codes), dims, strides, box, one,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D, int R, int PIECES, bool F16, int STAGES>
+cudaError_t launch(const PagedAttnParams& p, int blocks, cudaStream_t stream) {
+  constexpr int smem = 2 * STAGES * kTile * D + D / 64 * kTile * 128 + PIECES * R * D + kTile * 2 * R + 1024;
+  CopyMaps maps{};
+  if (!make_map(&maps.k, p.k, p, D, D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B) ||
+      !make_map(&maps.v, p.v, p, D, CU_TENSOR_MAP_SWIZZLE_NONE))
+    return cudaErrorNotSupported;
+  const cudaError_t e = allow_smem<paged_rows_kernel<D, R, PIECES, F16, STAGES>>(smem);
+  if (e != cudaSuccess) return e;
+  paged_rows_kernel<D, R, PIECES, F16, STAGES><<<blocks, kThreads, smem, stream>>>(p, maps);
+  return cudaGetLastError();
+}
+template <int D, int R>
+cudaError_t launch_of(const PagedAttnParams& p, bool f16, int blocks, cudaStream_t stream) {
+  constexpr int STAGES = D == 64 || R == 32 ? 4 : 2;
+  return f16 ? launch<D, R, 3, true, STAGES>(p, blocks, stream) : launch<D, R, 2, false, STAGES>(p, blocks, stream);
+}
+
+}  // namespace
+
+cudaError_t launch_paged_rows(const PagedAttnParams& p, int q_dtype, int head_dim, int rows, int blocks, cudaStream_t stream) {
+  const bool f16 = q_dtype == CSA2_T_F16;
+  const cudaError_t e = head_dim == 128 ? (rows == 16 ? launch_of<128, 16>(p, f16, blocks, stream) : launch_of<128, 32>(p, f16, blocks, stream))
+                                        : (rows == 16 ? launch_of<64, 16>(p, f16, blocks, stream) : launch_of<64, 32>(p, f16, blocks, stream));
+  return e != cudaSuccess ? e : launch_paged_join(p, head_dim, rows, blocks, stream);
+}
+
+}  // namespace csa2

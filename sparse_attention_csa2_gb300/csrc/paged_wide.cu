@@ -60,20 +60,6 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint3
       " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %3, p;\n}\n" ::"r"(d), "r"(a), "r"(b), "r"(idesc), "r"(acc), "r"(kDescHi)
       : "memory");
 }
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-  float2 d;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;\n"
-      : "=l"(reinterpret_cast<uint64_t&>(d))
-      : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)), "l"(reinterpret_cast<uint64_t&>(c)));
-  return d;
-}
-__device__ __forceinline__ float2 add2(float2 a, float2 b) {
-  float2 d;
-  asm("add.rn.f32x2 %0, %1, %2;\n"
-      : "=l"(reinterpret_cast<uint64_t&>(d))
-      : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)));
-  return d;
-}
 // What the conversion tells the softmax about 128 tokens.
 struct TileInfo {
   float k_scale[8];   // of each 16 tokens
@@ -240,7 +226,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_wide_kernel(const PagedAttn
   int pieces = 0;
   bool dead = false, bad = false;
   auto wait = [&](uint64_t* bar, uint32_t parity) {
-    if (!dead && !tc05::mbar_wait(bar, parity)) dead = true;
+    if (!dead && !paged_wait(bar, parity)) dead = true;
     if (warp < 12) dead = __any_sync(0xffffffffu, dead);
   };
 
