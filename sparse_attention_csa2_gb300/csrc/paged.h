@@ -106,12 +106,10 @@ struct PagedAttnParams {
   PagedOpen* open;                  // [blocks]
   int32_t* dev_status;
 };
-// Few query rows per (sequence, kv head): tiles of 8 or 16.
-cudaError_t launch_paged_attn(const PagedAttnParams& p, int q_dtype, int head_dim, bool rows8, int blocks,
-                              cudaStream_t stream);
-
-// Some: tiles of 16 or 32.
-cudaError_t launch_paged_rows(const PagedAttnParams& p, int q_dtype, int head_dim, int rows, int blocks, cudaStream_t stream);
+// Few query rows per (sequence, kv head): tiles of 8, or (dim 64) of 16.
+cudaError_t launch_paged_attn(const PagedAttnParams& p, int q_dtype, int head_dim, int rows, int blocks, cudaStream_t stream);
+// Some: tiles of 16 or 32, dim 128.
+cudaError_t launch_paged_rows(const PagedAttnParams& p, int q_dtype, int rows, int blocks, cudaStream_t stream);
 // Many: tiles of 256.
 cudaError_t launch_paged_wide(const PagedAttnParams& p, int q_dtype, int head_dim, int blocks, cudaStream_t stream);
 // The open tiles' pieces; both launch it.

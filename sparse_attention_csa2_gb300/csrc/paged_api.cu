@@ -37,10 +37,15 @@ const uint64_t* rope_turns(float theta, int rot_dim) {
   return turns;
 }
 
-// Which kernel, and its workspace, by the query rows per sequence and kv head in the mean: up to 8 take
-// paged_attn.cu's (three blocks per SM), up to 32 paged_rows.cu's (two with tiles of 16, one of 32), more
-// paged_wide.cu's (one).  No more blocks than there can be units of 128 tokens (a tile has at most the
-// table's, a sequence one tile more than its rows fill).
+// Which kernel, and its workspace, by the query rows per sequence and kv head in the mean.
+//   up to 8      paged_attn.cu's tiles of 8, three blocks per SM
+//   up to 32     at dim 64 its tiles of 16 (64 sequences x 4 heads x 1,000 tokens, 16 / 32 rows: 25 / 36 us against
+//                30 / 48 by paged_rows.cu's form; of 16,000 tokens, 32 sequences: 80 / 146 against 76 / 139);
+//                at dim 128 paged_rows.cu's tiles of 16 (two blocks per SM) or 32 (one): 33 / 52 us against 40 / 59
+//                by tiles of 16 of paged_attn.cu, 98 / 156 against 159 / 300
+//   more         paged_wide.cu's tiles of 256, one block per SM (64 rows in the last case: 248 us)
+// No more blocks than there can be units of 128 tokens (a tile has at most the table's, a sequence one tile
+// more than its rows fill).
 struct AttnPlan {
   int rows;  // of a tile
   int blocks;
@@ -49,11 +54,14 @@ struct AttnPlan {
 AttnPlan attn_plan(const csa2_paged_attn_args* a) {
   AttnPlan pl{};
   const long long group = a->heads / a->kv_heads, rows = a->n_rows * group;
-  pl.rows = rows <= 8LL * a->n_seq && a->n_rows <= a->n_seq ? 8 : rows <= 16LL * a->n_seq ? 16 : rows <= 32LL * a->n_seq ? 32 : 256;
-  if (pl.rows == 256 && a->n_seq > 16384) pl.rows = 32;
+  pl.rows = rows <= 8LL * a->n_seq && a->n_rows <= a->n_seq                ? 8
+            : rows <= (a->head_dim == 64 ? 32LL : 16LL) * a->n_seq         ? 16
+            : rows <= 32LL * a->n_seq                                      ? 32
+                                                                           : 256;
+  if (pl.rows == 256 && a->n_seq > 16384) pl.rows = a->head_dim == 64 ? 16 : 32;  // its sequences' tiles fit shared memory
   const long long tiles = (rows + pl.rows - 1) / pl.rows + a->n_seq;
   const long long units = ((long long)a->table_cols * a->page_size + 127) / 128 + 1;
-  const long long most = (pl.rows == 8 ? 3 : pl.rows == 16 ? 2 : 1) * device_sm_count();
+  const long long most = (pl.rows == 256 ? 1 : a->head_dim == 64 || pl.rows == 8 ? 3 : pl.rows == 16 ? 2 : 1) * device_sm_count();
   const double all = (double)tiles * a->kv_heads * units;
   pl.blocks = all < (double)most ? (int)all : (int)most;
   size_t at = 0;
@@ -206,9 +214,9 @@ csa2_status csa2_paged_attn(const csa2_paged_attn_args* a, void* stream) {
   p.open = reinterpret_cast<PagedOpen*>(ws + pl.open);
   p.dev_status = a->dev_status;
   cudaStream_t on = static_cast<cudaStream_t>(stream);
-  return cuda_status(pl.rows == 256 ? launch_paged_wide(p, a->q_dtype, a->head_dim, pl.blocks, on)
-                     : pl.rows > 8  ? launch_paged_rows(p, a->q_dtype, a->head_dim, pl.rows, pl.blocks, on)
-                                    : launch_paged_attn(p, a->q_dtype, a->head_dim, true, pl.blocks, on));
+  return cuda_status(pl.rows == 256                        ? launch_paged_wide(p, a->q_dtype, a->head_dim, pl.blocks, on)
+                     : a->head_dim == 128 && pl.rows > 8 ? launch_paged_rows(p, a->q_dtype, pl.rows, pl.blocks, on)
+                                                         : launch_paged_attn(p, a->q_dtype, a->head_dim, pl.rows, pl.blocks, on));
 }
 
 }  // extern "C"

@@ -551,7 +551,7 @@ __global__ void __launch_bounds__(kWarps * 32, 3)
       }
       if (starts && ends) {
         const int rr = row0 + r, tokn = by_group(p, rr), hq = head * p.group + rr - tokn * p.group;
-        paged_store<D>(p, s.first + tokn, hq, d, o, M, L);
+        paged_put<D>(p, s.first + tokn, hq, d, o, paged_factor(p, hq, M, L));
       } else {
         *reinterpret_cast<float4*>(p.part_o + ((long long)slot_of * NR + r) * D + d) = o;
         if (d == 0) *reinterpret_cast<float2*>(p.part_ml + ((long long)slot_of * NR + r) * 2) = make_float2(M, L);
@@ -616,15 +616,11 @@ cudaError_t launch(const PagedAttnParams& p, int blocks, cudaStream_t stream) {
 
 }  // namespace
 
-cudaError_t launch_paged_attn(const PagedAttnParams& p, int q_dtype, int head_dim, bool rows8, int blocks,
-                              cudaStream_t stream) {
+cudaError_t launch_paged_attn(const PagedAttnParams& p, int q_dtype, int head_dim, int rows, int blocks, cudaStream_t stream) {
   const bool f16 = q_dtype == CSA2_T_F16;
-  if (head_dim == 128) {
-    if (f16) return rows8 ? launch<128, 1, 3, true>(p, blocks, stream) : launch<128, 2, 3, true>(p, blocks, stream);
-    return rows8 ? launch<128, 1, 2, false>(p, blocks, stream) : launch<128, 2, 2, false>(p, blocks, stream);
-  }
-  if (f16) return rows8 ? launch<64, 1, 3, true>(p, blocks, stream) : launch<64, 2, 3, true>(p, blocks, stream);
-  return rows8 ? launch<64, 1, 2, false>(p, blocks, stream) : launch<64, 2, 2, false>(p, blocks, stream);
+  if (head_dim == 128) return f16 ? launch<128, 1, 3, true>(p, blocks, stream) : launch<128, 1, 2, false>(p, blocks, stream);
+  if (f16) return rows == 8 ? launch<64, 1, 3, true>(p, blocks, stream) : launch<64, 2, 3, true>(p, blocks, stream);
+  return rows == 8 ? launch<64, 1, 2, false>(p, blocks, stream) : launch<64, 2, 2, false>(p, blocks, stream);
 }
 
 }  // namespace csa2

@@ -63,15 +63,18 @@ __device__ __forceinline__ void f16_pairs(uint32_t v, uint32_t& lo, uint32_t& hi
       : "r"(v));
 }
 
-// Four values of an output row: sums o relative to maximum M (log2 units) over the row's denominator.
-// A row that saw no key is 0.
-template <int D>
-__device__ __forceinline__ void paged_store(const PagedAttnParams& p, int row, int head, int d, float4 o, float M, float L) {
+// What a row's sums of weighted values, relative to its maximum M (log2 units), are to be multiplied by: one over
+// its denominator.  A row that saw no key is 0.
+__device__ __forceinline__ float paged_factor(const PagedAttnParams& p, int head, float M, float L) {
   float den = L;
   if (p.sink != nullptr && M > -INFINITY) den += ex2(p.sink[head] * 1.4426950408889634f - M + kPagedLift);
-  const float inv = L == 0.f ? 0.f : __fdividef(1.f, den);
+  return L == 0.f ? 0.f : __fdividef(1.f, den);
+}
+// Four values of an output row.
+template <int D>
+__device__ __forceinline__ void paged_put(const PagedAttnParams& p, int row, int head, int d, float4 o, float factor) {
   const long long at = ((long long)row * (p.kv_heads * p.group) + head) * D + d;
-  o.x *= inv, o.y *= inv, o.z *= inv, o.w *= inv;
+  o.x *= factor, o.y *= factor, o.z *= factor, o.w *= factor;
   if (p.out_dtype == CSA2_T_F32) {
     *reinterpret_cast<float4*>(static_cast<float*>(p.out) + at) = o;
   } else {
@@ -79,18 +82,6 @@ __device__ __forceinline__ void paged_store(const PagedAttnParams& p, int row, i
     const uint2 u = h ? make_uint2(pack_f16x2(o.x, o.y), pack_f16x2(o.z, o.w)) : make_uint2(pack_bf16x2(o.x, o.y), pack_bf16x2(o.z, o.w));
     *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + at) = u;
   }
-}
-
-// One value.
-template <int D>
-__device__ __forceinline__ void paged_store_one(const PagedAttnParams& p, int row, int head, int d, float o, float M, float L) {
-  float den = L;
-  if (p.sink != nullptr && M > -INFINITY) den += ex2(p.sink[head] * 1.4426950408889634f - M + kPagedLift);
-  o *= L == 0.f ? 0.f : __fdividef(1.f, den);
-  const long long at = ((long long)row * (p.kv_heads * p.group) + head) * D + d;
-  if (p.out_dtype == CSA2_T_F32) static_cast<float*>(p.out)[at] = o;
-  else if (p.out_dtype == CSA2_T_F16) static_cast<__half*>(p.out)[at] = __float2half_rn(o);
-  else static_cast<__nv_bfloat16*>(p.out)[at] = __float2bfloat16_rn(o);
 }
 
 // n / group of a row index.  (The inverse is too large by less than one 2^64th, n below 2^31: exact.)

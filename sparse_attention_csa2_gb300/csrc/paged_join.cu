@@ -68,7 +68,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) paged_join_kernel(const Paged
     t.x += v.x * f, t.y += v.y * f, t.z += v.z * f, t.w += v.w * f;
   }
   const int rr = o.row0 + r, tokn = by_group(p, rr), hq = o.kv_head * p.group + rr - tokn * p.group;
-  paged_store<D>(p, o.first_row + tokn, hq, threadIdx.x * 4, t, T, N);
+  paged_put<D>(p, o.first_row + tokn, hq, threadIdx.x * 4, t, paged_factor(p, hq, T, N));
 }
 
 template <int D, int ROWS>
@@ -95,7 +95,6 @@ cudaError_t launch_paged_join(const PagedAttnParams& p, int head_dim, int rows, 
                         : join<128, 256>(p, blocks, stream);
   return rows == 8    ? join<64, 8>(p, blocks, stream)
          : rows == 16 ? join<64, 16>(p, blocks, stream)
-         : rows == 32 ? join<64, 32>(p, blocks, stream)
                       : join<64, 256>(p, blocks, stream);
 }
 

@@ -1,5 +1,5 @@
 // Attention over a paged cache of E4M3 codes, some query rows per key-value head (shared heads, drafted
-// tokens): tiles of 16 or 32 rows on the tensor cores' 5th generation form, tokens as its rows.
+// tokens), dim 128: tiles of 16 or 32 rows on the tensor cores' 5th generation form, tokens as its rows.
 //
 // The same sums as the split attention (paged_attn.cu), which serves up to 8 rows: beyond, its warps issue
 // too many instructions per cached byte (1,185 for 32 tokens of 16 rows, three times what the codes' way
@@ -8,10 +8,10 @@
 //   S^T [128 tokens x rows] = K Q^T      kind::f8f6f4, K's codes as they come from memory (no conversion),
 //                                        the query rows as E4M3 pieces added up in the accumulator
 //   P^T = fp16 weights, a token per thread
-//   O^T [dim x rows] += V^T P^T          kind::f16, V's codes converted to fp16 (exact)
+//   O^T [128 dims x rows] += V^T P^T     kind::f16, V's codes converted to fp16 (exact)
 //
 // with accumulators in tensor memory, so that a thread holds one token's few scores and no outputs.  Bound by
-// the codes' way from memory: 2 * dim bytes per cached token and head.
+// the codes' way from memory: 256 bytes per cached token and head.
 //
 //   4 warps  weights (a token per thread), and at a tile's end its output (a dim per thread)
 //   4 warps  V to fp16, and the next tile's query pieces
@@ -31,7 +31,7 @@ namespace csa2 {
 namespace {
 
 constexpr int kTile = 128;              // tokens of a unit
-constexpr int kLead = 2;                // units that a tile's beginning and end take (see paged_attn.cu)
+constexpr int kLead = 4;                // units that a tile's beginning and end take (see paged_attn.cu)
 constexpr int kThreads = 10 * 32;       // warps: weights 0 .. 3, conversion 4 .. 7, copies 8, products 9
 constexpr int kInfos = 8;
 
@@ -63,7 +63,7 @@ struct Shared {
   float factor[2][R];  // of a query row: score in log2 units = factor * k_scale * sum of products
   int pos[2][R];       // its position
   float top[R];        // running maxima
-  float alpha[R];
+  float alpha[R], sum[R];
   float part[4][R];    // of the four warps
   TileEnd tile;
   uint32_t tmem;
@@ -81,7 +81,7 @@ template <int R>
 struct Walk {
   const PagedAttnParams& p;
   long long u, u_end, first;  // first: the sequence's first unit
-  int b;
+  int b, known;               // known: the sequence that the segment holds
   __device__ __forceinline__ static int lo_of(const PagedAttnParams& p, const PagedSeq& s) {  // a page's first token
     return p.window > 0 ? max(s.ctx - p.window + 1, 0) >> p.page_shift << p.page_shift : 0;
   }
@@ -93,7 +93,8 @@ struct Walk {
   }
   __device__ __forceinline__ bool next(Segment& x) {
     while (u < u_end) {
-      x.s = paged_seq<R>(p, b);
+      if (known != b) x.s = paged_seq<R>(p, b);
+      known = b;
       const long long units = units_of(p, x.s);
       if (u >= first + units) {
         first += units;
@@ -156,6 +157,24 @@ __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* tm, in
       "l"(reinterpret_cast<uint64_t>(tm)), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
       : "memory");
 }
+// R values of each of the warp's lanes (v[r], 0 <= r < R; rows of a tile) to one value per row: halves are
+// exchanged and joined until a lane holds row_of_lane<R>'s, in R shuffles or so instead of 5 R.
+template <int R>
+__device__ __forceinline__ int row_of_lane(int lane) { return R == 32 ? lane : lane >> 1; }
+template <int R, typename Op>
+__device__ __forceinline__ float over_rows(float (&v)[R], int lane, Op op) {
+#pragma unroll
+  for (int n = R / 2, o = 16; n > 0; n /= 2, o /= 2) {
+    const bool up = lane & o;
+#pragma unroll
+    for (int k = 0; k < n; ++k) {
+      const float keep = up ? v[k + n] : v[k], give = up ? v[k] : v[k + n];
+      v[k] = op(keep, __shfl_xor_sync(0xffffffffu, give, o));
+    }
+  }
+  if (R == 16) v[0] = op(v[0], __shfl_xor_sync(0xffffffffu, v[0], 1));
+  return v[0];
+}
 // Barrier of the four weight warps.
 __device__ __forceinline__ void weights_sync() { asm volatile("bar.sync 1, 128;\n" ::: "memory"); }
 __device__ __forceinline__ bool weights_any(bool v) {
@@ -168,9 +187,10 @@ __device__ __forceinline__ bool weights_any(bool v) {
   return r != 0;
 }
 
-template <int D, int R, int PIECES, bool F16, int STAGES>
+template <int R, int PIECES, bool F16, int STAGES>
 __global__ void __launch_bounds__(kThreads, R == 16 ? 2 : 1)
     paged_rows_kernel(const PagedAttnParams p, const __grid_constant__ CopyMaps maps) {
+  constexpr int D = 128;
   constexpr int kCodes = kTile * D;            // bytes of a tile's codes
   constexpr int kPanel = kTile * 128;          // 64 dims of V in fp16
   constexpr int kW = D / 64 * kPanel;
@@ -241,7 +261,7 @@ __global__ void __launch_bounds__(kThreads, R == 16 ? 2 : 1)
     tc05::fence_after();
   }
   const uint32_t tmem = sh.tmem;
-  Walk<R> walk{p, u, u_end, sh.place_first, sh.place_seq};
+  Walk<R> walk{p, u, u_end, sh.place_first, sh.place_seq, -1};
   Segment x;
   bool dead = false, bad = false;
   uint32_t count = 0, segs = 0;  // units, tiles of the block so far
@@ -320,13 +340,10 @@ __global__ void __launch_bounds__(kThreads, R == 16 ? 2 : 1)
         }
         // a first unit, a score 2^4 above its row's maximum, or a larger V reference: everything moves there
         if (j == 0 || weights_any(over > kPagedSlack) || v_factor != 1.f) {
+          float top[R];
 #pragma unroll
-          for (int r = 0; r < R; ++r) {
-            const float2 tt = t[r / 2];
-            float top = sees >> r & 1 ? (r & 1 ? tt.y : tt.x) : -INFINITY;
-            top = warp_max(top);
-            if (lane == 0) sh.part[warp][r] = top;
-          }
+          for (int r = 0; r < R; ++r) top[r] = sees >> r & 1 ? (r & 1 ? t[r / 2].y : t[r / 2].x) : -INFINITY;
+          sh.part[warp][row_of_lane<R>(lane)] = over_rows<R>(top, lane, [](float a, float b) { return fmaxf(a, b); });
           weights_sync();
           if (tid < R) {
             const float old = j == 0 ? -INFINITY : sh.top[tid];
@@ -390,10 +407,22 @@ __global__ void __launch_bounds__(kThreads, R == 16 ? 2 : 1)
       }
       if (dead) break;
       // ---- the tile's outputs, or its partial sums
+      {
+        float sum[R];
 #pragma unroll
-      for (int r = 0; r < R; ++r) {
-        const float t = warp_sum(r & 1 ? l[r / 2].y : l[r / 2].x);
-        if (lane == 0) sh.part[warp][r] = t;
+        for (int r = 0; r < R; ++r) sum[r] = r & 1 ? l[r / 2].y : l[r / 2].x;
+        sh.part[warp][row_of_lane<R>(lane)] = over_rows<R>(sum, lane, [](float a, float b) { return a + b; });
+      }
+      weights_sync();
+      if (tid < R) {  // a row's sum, and what its outputs are to be multiplied by
+        const float L = sh.part[0][tid] + sh.part[1][tid] + sh.part[2][tid] + sh.part[3][tid], M = sh.top[tid];
+        float den = L;
+        if (p.sink != nullptr && M > -INFINITY && tid < sh.tile.rows) {
+          const int rr = sh.tile.row0 + tid;
+          den += ex2(p.sink[sh.tile.head * p.group + rr - by_group(p, rr) * p.group] * 1.4426950408889634f - M + kPagedLift);
+        }
+        sh.sum[tid] = L;
+        sh.alpha[tid] = L == 0.f ? 0.f : v_ref * __fdividef(1.f, den);
       }
       weights_sync();
       wait(&sh.o_full, segs & 1);
@@ -407,21 +436,20 @@ __global__ void __launch_bounds__(kThreads, R == 16 ? 2 : 1)
       tc05::tmem_ld<R>(o_cols, o);
       tc05::tmem_ld_wait();
       tc05::fence_before();
-      // D = 64: 64 accumulator rows lie in 16 lanes of each warp
-      const int d = D == 128 ? tid : 16 * warp + lane;
-      if (D == 128 || lane < 16) {
+      const int d = tid;
 #pragma unroll
-        for (int r = 0; r < R; ++r) {
-          if (r >= tile.rows) break;
-          const float M = sh.top[r], L = sh.part[0][r] + sh.part[1][r] + sh.part[2][r] + sh.part[3][r];
-          const float val = __uint_as_float(o[r]) * v_ref;
-          if (starts && ends) {
-            const int rr = tile.row0 + r, i = by_group(p, rr);
-            paged_store_one<D>(p, tile.first_row + i, tile.head * p.group + rr - i * p.group, d, val, M, L);
-          } else {
-            p.part_o[(slot + r) * D + d] = val;
-            if (d == 0) *reinterpret_cast<float2*>(p.part_ml + (slot + r) * 2) = make_float2(M, L);
-          }
+      for (int r = 0; r < R; ++r) {
+        if (r >= tile.rows) break;
+        if (starts && ends) {
+          const int rr = tile.row0 + r, i = by_group(p, rr);
+          const long long at = ((long long)(tile.first_row + i) * (p.kv_heads * p.group) + tile.head * p.group + rr - i * p.group) * D + d;
+          const float val = __uint_as_float(o[r]) * sh.alpha[r];
+          if (p.out_dtype == CSA2_T_F32) static_cast<float*>(p.out)[at] = val;
+          else if (p.out_dtype == CSA2_T_F16) static_cast<__half*>(p.out)[at] = __float2half_rn(val);
+          else static_cast<__nv_bfloat16*>(p.out)[at] = __float2bfloat16_rn(val);
+        } else {
+          p.part_o[(slot + r) * D + d] = __uint_as_float(o[r]) * v_ref;
+          if (d == 0) *reinterpret_cast<float2*>(p.part_ml + (slot + r) * 2) = make_float2(sh.top[r], sh.sum[r]);
         }
       }
       weights_sync();  // maxima and sums are read before the next tile's
@@ -686,31 +714,26 @@ bool make_map(CUtensorMap* map, const uint8_t* codes, const PagedAttnParams& p, 
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int D, int R, int PIECES, bool F16, int STAGES>
+template <int R, int PIECES, bool F16, int STAGES>
 cudaError_t launch(const PagedAttnParams& p, int blocks, cudaStream_t stream) {
-  constexpr int smem = 2 * STAGES * kTile * D + D / 64 * kTile * 128 + PIECES * R * D + kTile * 2 * R + 1024;
+  constexpr int D = 128;
+  constexpr int smem = 2 * STAGES * kTile * D + kTile * D * 2 + PIECES * R * D + kTile * 2 * R + 1024;
   CopyMaps maps{};
-  if (!make_map(&maps.k, p.k, p, D, D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B) ||
-      !make_map(&maps.v, p.v, p, D, CU_TENSOR_MAP_SWIZZLE_NONE))
+  if (!make_map(&maps.k, p.k, p, D, CU_TENSOR_MAP_SWIZZLE_128B) || !make_map(&maps.v, p.v, p, D, CU_TENSOR_MAP_SWIZZLE_NONE))
     return cudaErrorNotSupported;
-  const cudaError_t e = allow_smem<paged_rows_kernel<D, R, PIECES, F16, STAGES>>(smem);
+  const cudaError_t e = allow_smem<paged_rows_kernel<R, PIECES, F16, STAGES>>(smem);
   if (e != cudaSuccess) return e;
-  paged_rows_kernel<D, R, PIECES, F16, STAGES><<<blocks, kThreads, smem, stream>>>(p, maps);
+  paged_rows_kernel<R, PIECES, F16, STAGES><<<blocks, kThreads, smem, stream>>>(p, maps);
   return cudaGetLastError();
-}
-template <int D, int R>
-cudaError_t launch_of(const PagedAttnParams& p, bool f16, int blocks, cudaStream_t stream) {
-  constexpr int STAGES = D == 64 || R == 32 ? 4 : 2;
-  return f16 ? launch<D, R, 3, true, STAGES>(p, blocks, stream) : launch<D, R, 2, false, STAGES>(p, blocks, stream);
 }
 
 }  // namespace
 
-cudaError_t launch_paged_rows(const PagedAttnParams& p, int q_dtype, int head_dim, int rows, int blocks, cudaStream_t stream) {
+cudaError_t launch_paged_rows(const PagedAttnParams& p, int q_dtype, int rows, int blocks, cudaStream_t stream) {
   const bool f16 = q_dtype == CSA2_T_F16;
-  const cudaError_t e = head_dim == 128 ? (rows == 16 ? launch_of<128, 16>(p, f16, blocks, stream) : launch_of<128, 32>(p, f16, blocks, stream))
-                                        : (rows == 16 ? launch_of<64, 16>(p, f16, blocks, stream) : launch_of<64, 32>(p, f16, blocks, stream));
-  return e != cudaSuccess ? e : launch_paged_join(p, head_dim, rows, blocks, stream);
+  const cudaError_t e = rows == 16 ? (f16 ? launch<16, 3, true, 2>(p, blocks, stream) : launch<16, 2, false, 2>(p, blocks, stream))
+                                   : (f16 ? launch<32, 3, true, 4>(p, blocks, stream) : launch<32, 2, false, 4>(p, blocks, stream));
+  return e != cudaSuccess ? e : launch_paged_join(p, 128, rows, blocks, stream);
 }
 
 }  // namespace csa2

@@ -404,6 +404,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_wide_kernel(const PagedAttn
       const bool starts = x.blk == 0, ends = x.blk + x.n == x.g.blocks;
       const float L = l2.x + l2.y;
       const long long slot = (2LL * blockIdx.x + (starts ? 1 : 0)) * kRows + r;
+      const int head = x.h * p.group + rr - i * p.group;
+      const float factor = starts && ends ? v_ref * paged_factor(p, head, m, L) : v_ref;
 #pragma unroll 1
       for (int c = 0; c < D / 32; ++c) {
         uint32_t v[32];
@@ -412,10 +414,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_wide_kernel(const PagedAttn
 #pragma unroll
         for (int k = 0; k < 32; k += 4) {
           if (!has) break;
-          const float4 o = make_float4(__uint_as_float(v[k]) * v_ref, __uint_as_float(v[k + 1]) * v_ref,
-                                       __uint_as_float(v[k + 2]) * v_ref, __uint_as_float(v[k + 3]) * v_ref);
-          if (starts && ends) paged_store<D>(p, x.s.first + i, x.h * p.group + rr - i * p.group, 32 * c + k, o, m, L);
-          else *reinterpret_cast<float4*>(p.part_o + slot * D + 32 * c + k) = o;
+          const float4 o = make_float4(__uint_as_float(v[k]), __uint_as_float(v[k + 1]), __uint_as_float(v[k + 2]), __uint_as_float(v[k + 3]));
+          if (starts && ends) paged_put<D>(p, x.s.first + i, head, 32 * c + k, o, factor);
+          else *reinterpret_cast<float4*>(p.part_o + slot * D + 32 * c + k) = make_float4(o.x * factor, o.y * factor, o.z * factor, o.w * factor);
         }
       }
       if (has && !(starts && ends)) *reinterpret_cast<float2*>(p.part_ml + slot * 2) = make_float2(m, L);
