@@ -7,74 +7,85 @@ namespace csa2 {
 namespace {
 
 // Joins the pieces of the tile that block x of the attention left open: its own sums and those of the
-// blocks after it up to the tile's end.  A block takes a row: its warps take the pieces in turn (every
-// load independent of the others), then are summed in order.
+// blocks after it up to the tile's end.  WPR warps take a row: they take its pieces in turn (every load
+// independent of the others), then are summed in order.  Four warps where a tile has few rows and may have
+// a hundred pieces, one where it has 256 and the pieces are few.
 constexpr int kJoinWarps = 4;
-template <int D, int ROWS>
+template <int D, int ROWS, int WPR>
 __global__ void __launch_bounds__(kJoinWarps * 32) paged_join_kernel(const PagedAttnParams p) {
   __shared__ float weight[kJoinWarps][32];
   __shared__ float4 sum[kJoinWarps][D / 4];
   __shared__ float2 stat[kJoinWarps];
   asm volatile("griddepcontrol.wait;\n" ::: "memory");
   const PagedOpen o = p.open[blockIdx.x];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (o.pieces == 0) return;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, of_row = warp % WPR;
   constexpr int L4 = D / 4, SUB = 32 / L4;  // lanes of a piece, pieces of a warp's load
-  const int r = blockIdx.y;
-  if (o.pieces == 0 || r >= o.n) return;
-  const float* part = p.part_o + (2LL * blockIdx.x * ROWS + r) * D + lane % L4 * 4;  // a piece further: 2 * ROWS rows further
-  const float* part_ml = p.part_ml + (2LL * blockIdx.x * ROWS + r) * 2;
-  auto at = [](int i) { return i == 0 ? ROWS : 2 * ROWS * i; };  // row of piece i: the first block's second slot, then first slots
-  float M = -INFINITY, L = 0.f;
-  float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int i0 = 0; i0 < o.pieces; i0 += 32 * kJoinWarps) {  // a round: pieces i0 + warp, + 4, ..
-    const int mine = i0 + lane * kJoinWarps + warp;
-    const float2 ml = mine < o.pieces ? *reinterpret_cast<const float2*>(part_ml + 2 * at(mine)) : make_float2(-INFINITY, 0.f);
-    const float m = fmaxf(M, warp_max(ml.x));
-    const float old = M == -INFINITY ? 1.f : ex2(M - m);
-    const float w = ml.x == -INFINITY ? (ml.y == 0.f ? 0.f : 1.f) : ex2(ml.x - m);
-    weight[warp][lane] = w;
-    __syncwarp();
-    L = L * old + warp_sum(ml.y * w);
-    a.x *= old, a.y *= old, a.z *= old, a.w *= old;
-    M = m;
-    const int n = min(32, (o.pieces - i0 - warp + kJoinWarps - 1) / kJoinWarps);
+  constexpr int AT_ONCE = kJoinWarps / WPR;
+  for (int r0 = blockIdx.y * AT_ONCE; r0 < o.n; r0 += gridDim.y * AT_ONCE) {
+    const int r = min(r0 + warp / WPR, o.n - 1);
+    const float* part = p.part_o + (2LL * blockIdx.x * ROWS + r) * D + lane % L4 * 4;  // a piece further: 2 * ROWS rows further
+    const float* part_ml = p.part_ml + (2LL * blockIdx.x * ROWS + r) * 2;
+    auto at = [](int i) { return i == 0 ? ROWS : 2 * ROWS * i; };  // row of piece i: the first block's second slot, then first slots
+    float M = -INFINITY, L = 0.f;
+    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i0 = 0; i0 < o.pieces; i0 += 32 * WPR) {  // a round: pieces i0 + of_row, + WPR, ..
+      const int mine = i0 + lane * WPR + of_row;
+      const float2 ml = mine < o.pieces ? *reinterpret_cast<const float2*>(part_ml + 2LL * at(mine)) : make_float2(-INFINITY, 0.f);
+      const float m = fmaxf(M, warp_max(ml.x));
+      const float old = M == -INFINITY ? 1.f : ex2(M - m);
+      const float w = ml.x == -INFINITY ? (ml.y == 0.f ? 0.f : 1.f) : ex2(ml.x - m);
+      weight[warp][lane] = w;
+      __syncwarp();
+      L = L * old + warp_sum(ml.y * w);
+      a.x *= old, a.y *= old, a.z *= old, a.w *= old;
+      M = m;
+      const int n = min(32, (o.pieces - i0 - of_row + WPR - 1) / WPR);
 #pragma unroll 8
-    for (int i = lane / L4; i < n; i += SUB) {
-      const float f = weight[warp][i];
-      const float4 v = *reinterpret_cast<const float4*>(part + (long long)at(i0 + i * kJoinWarps + warp) * D);
-      a.x += v.x * f, a.y += v.y * f, a.z += v.z * f, a.w += v.w * f;
+      for (int i = lane / L4; i < n; i += SUB) {
+        const float f = weight[warp][i];
+        const float4 v = *reinterpret_cast<const float4*>(part + (long long)at(i0 + i * WPR + of_row) * D);
+        a.x += v.x * f, a.y += v.y * f, a.z += v.z * f, a.w += v.w * f;
+      }
+      __syncwarp();
     }
-    __syncwarp();
-  }
-  if (SUB == 2) {
-    a.x += __shfl_xor_sync(0xffffffffu, a.x, 16), a.y += __shfl_xor_sync(0xffffffffu, a.y, 16);
-    a.z += __shfl_xor_sync(0xffffffffu, a.z, 16), a.w += __shfl_xor_sync(0xffffffffu, a.w, 16);
-  }
-  if (lane < L4) sum[warp][lane] = a;
-  if (lane == 0) stat[warp] = make_float2(M, L);
-  __syncthreads();
-  if (threadIdx.x >= L4) return;
-  float T = -INFINITY, N = 0.f;
-  float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (SUB == 2) {
+      a.x += __shfl_xor_sync(0xffffffffu, a.x, 16), a.y += __shfl_xor_sync(0xffffffffu, a.y, 16);
+      a.z += __shfl_xor_sync(0xffffffffu, a.z, 16), a.w += __shfl_xor_sync(0xffffffffu, a.w, 16);
+    }
+    const int rr = o.row0 + r, tokn = by_group(p, rr), hq = o.kv_head * p.group + rr - tokn * p.group;
+    if (WPR == 1) {
+      if (lane < L4) paged_put<D>(p, o.first_row + tokn, hq, lane * 4, a, paged_factor(p, hq, M, L));
+      continue;
+    }
+    if (lane < L4) sum[warp][lane] = a;
+    if (lane == 0) stat[warp] = make_float2(M, L);
+    __syncthreads();
+    if (threadIdx.x < L4) {
+      float T = -INFINITY, N = 0.f;
+      float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-  for (int w = 0; w < kJoinWarps; ++w) T = fmaxf(T, stat[w].x);
+      for (int w = 0; w < kJoinWarps; ++w) T = fmaxf(T, stat[w].x);
 #pragma unroll
-  for (int w = 0; w < kJoinWarps; ++w) {
-    const float2 ml = stat[w];
-    if (ml.x == -INFINITY && ml.y == 0.f) continue;
-    const float f = ml.x == -INFINITY ? 1.f : ex2(ml.x - T);
-    const float4 v = sum[w][threadIdx.x];
-    N += ml.y * f;
-    t.x += v.x * f, t.y += v.y * f, t.z += v.z * f, t.w += v.w * f;
+      for (int w = 0; w < kJoinWarps; ++w) {
+        const float2 ml = stat[w];
+        if (ml.x == -INFINITY && ml.y == 0.f) continue;
+        const float f = ml.x == -INFINITY ? 1.f : ex2(ml.x - T);
+        const float4 v = sum[w][threadIdx.x];
+        N += ml.y * f;
+        t.x += v.x * f, t.y += v.y * f, t.z += v.z * f, t.w += v.w * f;
+      }
+      paged_put<D>(p, o.first_row + tokn, hq, threadIdx.x * 4, t, paged_factor(p, hq, T, N));
+    }
+    __syncthreads();
   }
-  const int rr = o.row0 + r, tokn = by_group(p, rr), hq = o.kv_head * p.group + rr - tokn * p.group;
-  paged_put<D>(p, o.first_row + tokn, hq, threadIdx.x * 4, t, paged_factor(p, hq, T, N));
 }
 
 template <int D, int ROWS>
 cudaError_t join(const PagedAttnParams& p, int blocks, cudaStream_t stream) {
+  constexpr int WPR = ROWS == 256 ? 1 : kJoinWarps;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(blocks, ROWS);
+  cfg.gridDim = dim3(blocks, ROWS == 256 ? 32 : ROWS);
   cfg.blockDim = dim3(kJoinWarps * 32);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
@@ -82,7 +93,7 @@ cudaError_t join(const PagedAttnParams& p, int blocks, cudaStream_t stream) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, paged_join_kernel<D, ROWS>, p);
+  return cudaLaunchKernelEx(&cfg, paged_join_kernel<D, ROWS, WPR>, p);
 }
 
 }  // namespace

@@ -123,6 +123,7 @@ struct Shared {
   uint64_t k_full[2], k_free[2], v_full[2], v_free[2], s_full[2], p_ready[2], o_full[2], q_full[2];
   uint64_t info_full[4];
   TileInfo info[4];
+  float factor[8][32];  // of the rows of the softmax warps: score in log2 units = factor * k_scale * product
   uint32_t tmem;
   Place place;
   long long scan[kThreads / 32];
@@ -236,7 +237,6 @@ __global__ void __launch_bounds__(kThreads, 1) paged_wide_kernel(const PagedAttn
     const int t = warp >> 2, row = (warp & 3) * 32 + lane;  // row of the tile of 128
     const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     const uint32_t s_cols = lanes + 128 * t, o_cols = lanes + 256 + D * t;
-    uint8_t* q_row = q_tiles + t * kTileBytes + row * 128;
     uint32_t turn = 0, done = 0;  // uses of s_full, of o_full
     uint32_t count = 0;           // units of the block
     while (walk.next(x) && !dead) {
@@ -248,46 +248,48 @@ __global__ void __launch_bounds__(kThreads, 1) paged_wide_kernel(const PagedAttn
       const bool has = r < x.g.n;
       const int rr = x.g.row0 + min(r, x.g.n - 1), i = by_group(p, rr);
       const int pos = x.s.ctx + i;
-      // the query row to fp16, scaled to a maximum in [2^13, 2^14); a negative softmax scale turns its sign
-      float f;
+      // the warp's query rows to fp16, scaled to a maximum in [2^13, 2^14): a row at a time by PL lanes, 16 bytes
+      // each.  A negative softmax scale turns the sign.
       {
-        const uint16_t* src = static_cast<const uint16_t*>(p.q) + (long long)(x.s.first + i) * p.q_row +
-                              (long long)(x.h * p.group + rr - i * p.group) * p.q_head;
-        float amax = 0.f;
-        bool odd = false;
+        constexpr int PL = D / 8, AT_ONCE = 32 / PL;
+        const int c = lane % PL;
 #pragma unroll 4
-        for (int c = 0; c < D / 8; ++c) {
-          const uint4 v4 = has ? *reinterpret_cast<const uint4*>(src + 8 * c) : make_uint4(0, 0, 0, 0);
+        for (int k = 0; k < PL; ++k) {
+          const int in_warp = k * AT_ONCE + lane / PL, in_tile = (warp & 3) * 32 + in_warp, q_r = 128 * t + in_tile;
+          const int q_rr = x.g.row0 + min(q_r, x.g.n - 1), q_i = by_group(p, q_rr);
+          const uint16_t* src = static_cast<const uint16_t*>(p.q) + (long long)(x.s.first + q_i) * p.q_row +
+                                (long long)(x.h * p.group + q_rr - q_i * p.group) * p.q_head + 8 * c;
+          const uint4 v4 = q_r < x.g.n ? *reinterpret_cast<const uint4*>(src) : make_uint4(0, 0, 0, 0);
           const uint32_t w[4] = {v4.x, v4.y, v4.z, v4.w};
+          float2 v[4];
+          float amax = 0.f;
+          bool odd = false;
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const float2 v = F16 ? __half22float2(*reinterpret_cast<const __half2*>(&w[k])) : make_float2(bf16_lo(w[k]), bf16_hi(w[k]));
-            odd |= !(fabsf(v.x) < INFINITY) || !(fabsf(v.y) < INFINITY);
-            amax = fmaxf(amax, fmaxf(fabsf(v.x), fabsf(v.y)));
+          for (int n = 0; n < 4; ++n) {
+            v[n] = F16 ? __half22float2(*reinterpret_cast<const __half2*>(&w[n])) : make_float2(bf16_lo(w[n]), bf16_hi(w[n]));
+            odd |= !(fabsf(v[n].x) < INFINITY) || !(fabsf(v[n].y) < INFINITY);
+            amax = fmaxf(amax, fmaxf(fabsf(v[n].x), fabsf(v[n].y)));
           }
-        }
-        int e = (int)(__float_as_uint(amax) >> 23) - 127 - 13;
-        e = min(max(e, -110), 119);
-        float down = __uint_as_float((uint32_t)(127 - e) << 23);
-        const float up = __uint_as_float((uint32_t)(127 + e) << 23);
-        f = odd ? __uint_as_float(0x7fc00000u) : fabsf(p.scale_log2) * up;
-        if (odd) down = 0.f;
-        if (p.scale_log2 < 0.f) down = -down;
-#pragma unroll 4
-        for (int c = 0; c < D / 8; ++c) {
-          const uint4 v4 = has ? *reinterpret_cast<const uint4*>(src + 8 * c) : make_uint4(0, 0, 0, 0);
-          const uint32_t w[4] = {v4.x, v4.y, v4.z, v4.w};
+#pragma unroll
+          for (int o = 1; o < PL; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+          odd = (__ballot_sync(0xffffffffu, odd) >> (lane / PL * PL) & (PL == 16 ? 0xffffu : 0xffu)) != 0;
+          int e = (int)(__float_as_uint(amax) >> 23) - 127 - 13;
+          e = min(max(e, -110), 119);
+          float down = odd ? 0.f : __uint_as_float((uint32_t)(127 - e) << 23);
+          const float up = __uint_as_float((uint32_t)(127 + e) << 23);
+          if (p.scale_log2 < 0.f) down = -down;
           uint32_t o[4];
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const float2 v = F16 ? __half22float2(*reinterpret_cast<const __half2*>(&w[k])) : make_float2(bf16_lo(w[k]), bf16_hi(w[k]));
-            o[k] = odd ? 0u : pack_f16x2(v.x * down, v.y * down);
-          }
-          *reinterpret_cast<uint4*>(q_row + (c >> 3) * kPanel + (((c & 7) ^ (row & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+          for (int n = 0; n < 4; ++n) o[n] = odd ? 0u : pack_f16x2(v[n].x * down, v[n].y * down);
+          *reinterpret_cast<uint4*>(q_tiles + t * kTileBytes + (c >> 3) * kPanel + in_tile * 128 + (((c & 7) ^ (in_tile & 7)) << 4)) =
+              make_uint4(o[0], o[1], o[2], o[3]);
+          if (c == 0) sh.factor[warp][in_warp] = odd ? __uint_as_float(0x7fc00000u) : fabsf(p.scale_log2) * up;
         }
         asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
         tc05::mbar_arrive(&sh.q_full[t]);
+        __syncwarp();
       }
+      const float f = sh.factor[warp][lane];
       float m = -INFINITY, v_ref = 0.f;
       float2 l2 = make_float2(0.f, 0.f);
       const int see_hi = min(pos + 1, x.g.hi), see_lo = p.window > 0 ? pos - p.window + 1 : 0;
@@ -305,9 +307,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_wide_kernel(const PagedAttn
         v_ref = info.v_ref;
         const float v_factor = info.v_factor;
         // the scores' maximum: of a tile that all rows of the warp see whole from registers, where the
-        // scores then stay; otherwise column by column in tensor memory
+        // scores then stay; otherwise 32 columns at a time from tensor memory, hidden ones left out
         float top = -INFINITY;
         uint32_t v[4][32];
+        const uint32_t from = (uint32_t)max(lo, 0), span = (uint32_t)max(min(hi, kTile) - max(lo, 0), 0);
         if (whole) {
 #pragma unroll
           for (int c = 0; c < 4; ++c) tc05::tmem_ld32(s_cols + 32 * c, v[c]);
@@ -321,14 +324,19 @@ __global__ void __launch_bounds__(kThreads, 1) paged_wide_kernel(const PagedAttn
           }
         } else {
 #pragma unroll 1
-          for (int c = 0; c < 8; ++c) {  // 16 columns, of one page
-            uint32_t y[16];
-            tc05::tmem_ld16(s_cols + 16 * c, y);
+          for (int c = 0; c < 4; ++c) {
+            uint32_t y[32];
+            tc05::tmem_ld32(s_cols + 32 * c, y);
             tc05::tmem_ld_wait();
-            float a = -INFINITY;
+            const uint32_t col = 32u * c - from;
+            float a = -INFINITY, b = -INFINITY;
 #pragma unroll
-            for (int k = 0; k < 16; ++k) a = 16 * c + k < hi && 16 * c + k >= lo ? fmaxf(a, __uint_as_float(y[k])) : a;
-            if ((flags >> c & 1) && a > -INFINITY) top = fmaxf(top, a * (f * info.k_scale[c]));
+            for (int k = 0; k < 16; ++k) {
+              if (col + k < span) a = fmaxf(a, __uint_as_float(y[k]));
+              if (col + 16 + k < span) b = fmaxf(b, __uint_as_float(y[16 + k]));
+            }
+            if ((flags >> (2 * c) & 1) && a > -INFINITY) top = fmaxf(top, a * (f * info.k_scale[2 * c]));
+            if ((flags >> (2 * c + 1) & 1) && b > -INFINITY) top = fmaxf(top, b * (f * info.k_scale[2 * c + 1]));
           }
         }
         const bool grows = top > m + kPagedSlack;
@@ -372,24 +380,28 @@ __global__ void __launch_bounds__(kThreads, 1) paged_wide_kernel(const PagedAttn
           }
         } else {
 #pragma unroll 1
-          for (int c = 0; c < 8; ++c) {
-            uint32_t y[16], w[8];
-            tc05::tmem_ld16(s_cols + 16 * c, y);
+          for (int c = 0; c < 4; ++c) {
+            uint32_t y[32], w[16];
+            tc05::tmem_ld32(s_cols + 32 * c, y);
             tc05::tmem_ld_wait();
-            const float ks = flags >> (8 + c) & 1 ? __uint_as_float(0x7fc00000u) : f * info.k_scale[c];
-            const bool page = flags >> c & 1;
-            const float o = off + info.v_log[c];
-            float sum = 0.f;
+            const uint32_t col = 32u * c - from;
 #pragma unroll
-            for (int k = 0; k < 16; ++k) {
-              const bool sees = page && 16 * c + k < hi && 16 * c + k >= lo;
-              y[k] = __float_as_uint(sees ? ex2(fmaf(__uint_as_float(y[k]), ks, o)) : 0.f);
-              sum += __uint_as_float(y[k]);
+            for (int h = 0; h < 2; ++h) {
+              const int g = 2 * c + h;
+              const float ks = flags >> (8 + g) & 1 ? __uint_as_float(0x7fc00000u) : f * info.k_scale[g];
+              const float o = off + info.v_log[g];
+              const uint32_t here = flags >> g & 1 ? span : 0;  // a page that is not there hides its columns
+              float sum = 0.f;
+#pragma unroll
+              for (int k = 16 * h; k < 16 * h + 16; ++k) {
+                y[k] = __float_as_uint(col + k < here ? ex2(fmaf(__uint_as_float(y[k]), ks, o)) : 0.f);
+                sum += __uint_as_float(y[k]);
+              }
+              l2.x = fmaf(sum, info.v_back[g], l2.x);
             }
-            l2.x = fmaf(sum, info.v_back[c], l2.x);
 #pragma unroll
-            for (int k = 0; k < 8; ++k) w[k] = pack_f16x2(__uint_as_float(y[2 * k]), __uint_as_float(y[2 * k + 1]));
-            tc05::tmem_st8(s_cols + 8 * c, w);
+            for (int k = 0; k < 16; ++k) w[k] = pack_f16x2(__uint_as_float(y[2 * k]), __uint_as_float(y[2 * k + 1]));
+            tc05::tmem_st16(s_cols + 16 * c, w);
           }
         }
         tc05::tmem_st_wait();
