@@ -26,12 +26,10 @@
 // exp2(z - max + 11), where the maximum follows a larger score only when that exceeds it by 2^4:
 // weights are at most 2^15, those down to 2^-21 of the largest keep 11 bits, and the output is rarely
 // rescaled.  A page's V scale enters the weight relative to the largest seen.  Maxima, sums and outputs are fp32.
-#include <cudaTypedefs.h>
-
 #include "common.cuh"
 #include "paged.h"
 #include "paged_dev.cuh"
-#include "tc05.cuh"
+#include "paged_tma.cuh"
 
 namespace csa2 {
 namespace {
@@ -69,19 +67,6 @@ __device__ __forceinline__ Seq seq_of(const PagedAttnParams& p, int b) {
   return s;
 }
 
-// Byte offset of a 16-byte chunk of a row in a stage as the copies lay it out (rows of D bytes,
-// TMA's 128-byte or 64-byte swizzle): the lanes of a phase then meet different banks.
-template <int D>
-__device__ __forceinline__ int phys(int row, int chunk) {
-  return row * D + ((D == 128 ? chunk ^ (row & 7) : chunk ^ ((row >> 1) & 3)) << 4);
-}
-__device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* tm, int x, int y, int z, uint64_t* bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];\n" ::"r"(
-          smem_u32(dst)),
-      "l"(reinterpret_cast<uint64_t>(tm)), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
-      : "memory");
-}
 // 8x8 matrix of 16-bit values over a warp, transposed.
 __device__ __forceinline__ uint32_t transpose8(uint32_t v) {
   uint32_t r;
@@ -91,10 +76,6 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t v) {
 // Stages of the ring: 64 KB a block.
 template <int D>
 constexpr int kStages = 256 / D;
-
-struct CopyMaps {
-  CUtensorMap k, v;
-};
 
 template <int D, int NB, int PIECES, bool F16>
 __global__ void __launch_bounds__(kWarps * 32, 3)
@@ -218,8 +199,8 @@ __global__ void __launch_bounds__(kWarps * 32, 3)
       }
       if (lane == 0) {
         tc05::mbar_expect_tx(bar, (id0 >= 0 ? kHalf : 0) + (id1 >= 0 ? kHalf : 0));
-        if (id0 >= 0) tma_load_3d(to, map, 0, tok & page_mask, id0 * p.kv_heads + head, bar);
-        if (id1 >= 0) tma_load_3d(to + kHalf, map, 0, (tok + 16) & page_mask, id1 * p.kv_heads + head, bar);
+        if (id0 >= 0) tma_load_codes(to, map, tok & page_mask, id0 * p.kv_heads + head, bar);
+        if (id1 >= 0) tma_load_codes(to + kHalf, map, (tok + 16) & page_mask, id1 * p.kv_heads + head, bar);
       }
     };
     auto copy_k = [&](int slot, int tok, int id0, int id1) {
@@ -361,8 +342,8 @@ __global__ void __launch_bounds__(kWarps * 32, 3)
         uint32_t wa[2 * KS], wb[2 * KS];
 #pragma unroll
         for (int k = 0; k < D / 64; ++k) {
-          const uint4 v = *reinterpret_cast<const uint4*>(kt + phys<D>(16 * h + g, D / 64 * c + k));
-          const uint4 x = *reinterpret_cast<const uint4*>(kt + phys<D>(16 * h + 8 + g, D / 64 * c + k));
+          const uint4 v = *reinterpret_cast<const uint4*>(kt + swizzled<D>(16 * h + g, D / 64 * c + k));
+          const uint4 x = *reinterpret_cast<const uint4*>(kt + swizzled<D>(16 * h + 8 + g, D / 64 * c + k));
           wa[4 * k] = v.x, wa[4 * k + 1] = v.y, wa[4 * k + 2] = v.z, wa[4 * k + 3] = v.w;
           wb[4 * k] = x.x, wb[4 * k + 1] = x.y, wb[4 * k + 2] = x.z, wb[4 * k + 3] = x.w;
         }
@@ -478,10 +459,10 @@ __global__ void __launch_bounds__(kWarps * 32, 3)
         for (int j = 0; j < 4; ++j) {
           const int row = 16 * h + 2 * c + (j & 1) + 8 * (j >> 1);
           if constexpr (D == 128) {
-            const uint4 v = *reinterpret_cast<const uint4*>(vt + phys<D>(row, g));
+            const uint4 v = *reinterpret_cast<const uint4*>(vt + swizzled<D>(row, g));
             w[j][0] = v.x, w[j][1] = v.y, w[j][2] = v.z, w[j][3] = v.w;
           } else {
-            const uint2 v = *reinterpret_cast<const uint2*>(vt + phys<D>(row, g >> 1) + 8 * (g & 1));
+            const uint2 v = *reinterpret_cast<const uint2*>(vt + swizzled<D>(row, g >> 1) + 8 * (g & 1));
             w[j][0] = v.x, w[j][1] = v.y;
           }
         }
@@ -575,38 +556,13 @@ __global__ void __launch_bounds__(kWarps * 32, 3)
   if (bad && p.dev_status && lane == 0) atomicExch(p.dev_status, (int)CSA2_EDEVICE_INDEX);
 }
 
-PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
-  static PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
-    void* f = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) != cudaSuccess ||
-        q != cudaDriverEntryPointSuccess)
-      f = nullptr;
-    return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
-  }();
-  return fn;
-}
-
-// Codes as [pages x heads, page, dim]; a copy takes 16 tokens of a page.
-bool make_map(CUtensorMap* map, const uint8_t* codes, const PagedAttnParams& p, int dim) {
-  if (p.n_pages == 0 || p.table_cols == 0) return true;  // no page is ever read
-  const PFN_cuTensorMapEncodeTiled_v12000 fn = encode_fn();
-  if (fn == nullptr) return false;
-  const cuuint64_t page = 1ull << p.page_shift;
-  const cuuint64_t dims[3] = {(cuuint64_t)dim, page, (cuuint64_t)p.n_pages * p.kv_heads};
-  const cuuint64_t strides[2] = {(cuuint64_t)dim, dim * page};
-  const cuuint32_t box[3] = {(cuuint32_t)dim, 16, 1}, one[3] = {1, 1, 1};
-  return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<uint8_t*>(codes), dims, strides, box, one,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, dim == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
-            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 template <int D, int NB, int PIECES, bool F16>
 cudaError_t launch(const PagedAttnParams& p, int blocks, cudaStream_t stream) {
   constexpr int smem = kWarps * 2 * kStages<D> * kTok * D + 1024;
   static_assert(smem - 1024 >= kWarps * 8 * NB * D * 4, "the joined sums fit the ring");
   CopyMaps maps{};
-  if (!make_map(&maps.k, p.k, p, D) || !make_map(&maps.v, p.v, p, D)) return cudaErrorNotSupported;
+  constexpr CUtensorMapSwizzle swizzle = D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B;
+  if (!make_codes_map(&maps.k, p.k, p, D, 16, swizzle) || !make_codes_map(&maps.v, p.v, p, D, 16, swizzle)) return cudaErrorNotSupported;
   cudaError_t e = allow_smem<paged_attn_kernel<D, NB, PIECES, F16>>(smem);
   if (e != cudaSuccess) return e;
   paged_attn_kernel<D, NB, PIECES, F16><<<blocks, kWarps * 32, smem, stream>>>(p, maps);

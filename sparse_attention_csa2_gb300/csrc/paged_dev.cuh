@@ -56,6 +56,16 @@ __device__ __forceinline__ float2 mul2(float2 a, float2 b) {
   return d;
 }
 
+// Four values as a register of codes.
+__device__ __forceinline__ uint32_t e4m3_word(float a, float b, float c, float d) {
+  uint32_t r;
+  asm("{\n .reg .b16 x, y;\n cvt.rn.satfinite.e4m3x2.f32 x, %2, %1;\n cvt.rn.satfinite.e4m3x2.f32 y, %4, %3;\n"
+      " mov.b32 %0, {x, y};\n}\n"
+      : "=r"(r)
+      : "f"(a), "f"(b), "f"(c), "f"(d));
+  return r;
+}
+
 // The four codes of a register (low byte first) as two pairs of f16.
 __device__ __forceinline__ void f16_pairs(uint32_t v, uint32_t& lo, uint32_t& hi) {
   asm("{\n .reg .b16 a, b;\n mov.b32 {a, b}, %2;\n cvt.rn.f16x2.e4m3x2 %0, a;\n cvt.rn.f16x2.e4m3x2 %1, b;\n}\n"
@@ -82,6 +92,40 @@ __device__ __forceinline__ void paged_put(const PagedAttnParams& p, int row, int
     const uint2 u = h ? make_uint2(pack_f16x2(o.x, o.y), pack_f16x2(o.z, o.w)) : make_uint2(pack_bf16x2(o.x, o.y), pack_bf16x2(o.z, o.w));
     *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + at) = u;
   }
+}
+
+// What the warp that finds the pages tells the others about 128 tokens (kernels with a running V reference).
+struct PagedInfo {
+  float k_scale[8];   // of each 16 tokens
+  float v_log[8];     // log2 of their V scale over the reference, at least -100
+  float v_back[8];    // 2^-v_log
+  float v_factor;     // what the outputs so far are to be multiplied by: the V reference grew
+  float v_ref;
+  uint32_t flags;     // bits 0-7: 16 tokens have a page; 8-15: their scales say NaN
+};
+// Filled in by a whole warp, lane l (as l & 7) with the page id (-1: no token, -2: a bad entry) and scales of
+// tokens 16 l ..; the reference before becomes the one behind.
+__device__ __forceinline__ void paged_tell(PagedInfo& info, int lane, int id, float sk, float sv, float& v_ref) {
+  const uint32_t pages = __ballot_sync(0xffffffffu, id != -2) & 0xffu;
+  const uint32_t nans = __ballot_sync(0xffffffffu, sk != sk || sv != sv) & 0xffu;
+  const float sv_here = sv > 0.f ? sv : 0.f;
+  float vm = sv_here;
+  vm = fmaxf(vm, __shfl_xor_sync(0xffffffffu, vm, 1));
+  vm = fmaxf(vm, __shfl_xor_sync(0xffffffffu, vm, 2));
+  vm = fmaxf(vm, __shfl_xor_sync(0xffffffffu, vm, 4));
+  const float v_new = fmaxf(v_ref, vm), v_inv = v_new > 0.f ? __fdiv_rn(1.f, v_new) : 0.f;
+  if (lane < 8) {
+    const float ratio = fmaxf(sv_here * v_inv, 7.888609e-31f);  // 2^-100
+    info.k_scale[lane] = sk == sk ? sk : 0.f;
+    info.v_log[lane] = log2f(ratio);
+    info.v_back[lane] = __fdiv_rn(1.f, ratio);
+    if (lane == 0) {
+      info.v_factor = v_new > v_ref ? v_ref * v_inv : 1.f;
+      info.v_ref = v_new;
+      info.flags = pages | nans << 8;
+    }
+  }
+  v_ref = v_new;
 }
 
 // n / group of a row index.  (The inverse is too large by less than one 2^64th, n below 2^31: exact.)

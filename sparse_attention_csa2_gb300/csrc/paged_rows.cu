@@ -20,12 +20,10 @@
 //
 // The parts run through the block's tiles without a common barrier, so that one tile's end overlaps the next
 // one's copies; work is split over the blocks as in the split attention.  Two blocks per SM with 16 rows.
-#include <cudaTypedefs.h>
-
 #include "common.cuh"
 #include "paged.h"
 #include "paged_dev.cuh"
-#include "tc05.cuh"
+#include "paged_tma.cuh"
 
 namespace csa2 {
 namespace {
@@ -34,20 +32,6 @@ constexpr int kTile = 128;              // tokens of a unit
 constexpr int kLead = 4;                // units that a tile's beginning and end take (see paged_attn.cu)
 constexpr int kThreads = 10 * 32;       // warps: weights 0 .. 3, conversion 4 .. 7, copies 8, products 9
 constexpr int kInfos = 8;
-
-struct CopyMaps {
-  CUtensorMap k, v;
-};
-
-// What the copies tell the weights about 128 tokens.
-struct TileInfo {
-  float k_scale[8];   // of each 16 tokens
-  float v_log[8];     // log2 of their V scale over the reference, at least -100
-  float v_back[8];    // 2^-v_log
-  float v_factor;     // what the outputs so far are to be multiplied by: the V reference grew
-  float v_ref;
-  uint32_t flags;     // bits 0-7: 16 tokens have a page; 8-15: their scales say NaN
-};
 
 // A tile, as its end needs it.
 struct TileEnd {
@@ -59,7 +43,7 @@ template <int R, int STAGES>
 struct Shared {
   uint64_t k_full[STAGES], k_free[STAGES], v_full[STAGES], v_free[STAGES], s_full[2], s_free[2], info_full[kInfos];
   uint64_t w_full, p_full, pv_done, q_full, q_free, o_full;
-  TileInfo info[kInfos];
+  PagedInfo info[kInfos];
   float factor[2][R];  // of a query row: score in log2 units = factor * k_scale * sum of products
   int pos[2][R];       // its position
   float top[R];        // running maxima
@@ -128,35 +112,6 @@ struct Walk {
   }
 };
 
-// Shared-memory descriptors: rows of 128, 64 or 32 bytes in the swizzle of that width, groups of 8 rows one
-// after the other; lbo: distance of the next panel along the dense dimension.
-__device__ __forceinline__ uint64_t desc(uint32_t saddr, int row_bytes, uint32_t lbo) {
-  const uint64_t mode = row_bytes == 128 ? 2 : row_bytes == 64 ? 4 : 6;
-  return (uint64_t)((saddr & 0x3ffffu) >> 4) | (uint64_t)(lbo >> 4) << 16 | (uint64_t)(8 * row_bytes >> 4) << 32 | 1ull << 46 | mode << 61;
-}
-// Byte offset of a 16-byte chunk in such rows.
-template <int B>
-__device__ __forceinline__ int swizzled(int row, int chunk) {
-  return row * B + ((B == 128 ? chunk ^ (row & 7) : B == 64 ? chunk ^ (row >> 1 & 3) : chunk ^ (row >> 2 & 1)) << 4);
-}
-__device__ __forceinline__ void mma_f16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
-  tc05::mma_bf16(d, a, b, idesc, acc);  // kind::f16; the types are idesc's
-}
-__device__ __forceinline__ uint32_t e4m3_word(float a, float b, float c, float d) {
-  uint32_t r;
-  asm("{\n .reg .b16 x, y;\n cvt.rn.satfinite.e4m3x2.f32 x, %2, %1;\n cvt.rn.satfinite.e4m3x2.f32 y, %4, %3;\n"
-      " mov.b32 %0, {x, y};\n}\n"
-      : "=r"(r)
-      : "f"(a), "f"(b), "f"(c), "f"(d));
-  return r;
-}
-__device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* tm, int x, int y, int z, uint64_t* bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];\n" ::"r"(
-          smem_u32(dst)),
-      "l"(reinterpret_cast<uint64_t>(tm)), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
-      : "memory");
-}
 // R values of each of the warp's lanes (v[r], 0 <= r < R; rows of a tile) to one value per row: halves are
 // exchanged and joined until a lane holds row_of_lane<R>'s, in R shuffles or so instead of 5 R.
 template <int R>
@@ -195,7 +150,6 @@ __global__ void __launch_bounds__(kThreads, R == 16 ? 2 : 1)
   constexpr int kPanel = kTile * 128;          // 64 dims of V in fp16
   constexpr int kW = D / 64 * kPanel;
   constexpr int kQ = R * D;                    // bytes of a query piece
-  constexpr int kP = kTile * 2 * R;
   constexpr int kCols = R == 16 ? 64 : 128;    // of tensor memory: S0, S1, O
   using Sh = Shared<R, STAGES>;
   extern __shared__ uint8_t smem_raw[];
@@ -266,8 +220,7 @@ __global__ void __launch_bounds__(kThreads, R == 16 ? 2 : 1)
   bool dead = false, bad = false;
   uint32_t count = 0, segs = 0;  // units, tiles of the block so far
   auto wait = [&](uint64_t* bar, uint32_t parity) {
-    if (!dead && !paged_wait(bar, parity)) dead = true;
-    if (warp < 9) dead = __any_sync(0xffffffffu, dead);
+    if (!dead && !paged_wait(bar, parity)) dead = true;  // a warp's lanes try together and see the same
   };
 
   if (warp < 4) {
@@ -296,7 +249,7 @@ __global__ void __launch_bounds__(kThreads, R == 16 ? 2 : 1)
         tc05::fence_after();
         uint32_t s[R];
         tc05::tmem_ld<R>(lanes + R * buf, s);
-        const TileInfo& info = sh.info[count % kInfos];
+        const PagedInfo& info = sh.info[count % kInfos];
         const int tok = tok0 + tid, g = tid >> 4;
         const uint32_t flags = info.flags;
         const float ks = flags >> (8 + g) & 1 ? __uint_as_float(0x7fc00000u) : info.k_scale[g];
@@ -602,35 +555,13 @@ __global__ void __launch_bounds__(kThreads, R == 16 ? 2 : 1)
         if (dead) break;
         if (lane == 0) tc05::mbar_expect_tx(&sh.k_full[stage], bytes);
         __syncwarp();
-        if (copies) tma_load_3d(k_ring + stage * kCodes + 16 * lane * D, &maps.k, 0, tok & mask, (int)slab, &sh.k_full[stage]);
+        if (copies) tma_load_codes(k_ring + stage * kCodes + 16 * lane * D, &maps.k, tok & mask, (int)slab, &sh.k_full[stage]);
         wait(&sh.v_free[stage], parity);
         if (dead) break;
         if (lane == 0) tc05::mbar_expect_tx(&sh.v_full[stage], bytes);
         __syncwarp();
-        if (copies) tma_load_3d(v_ring + stage * kCodes + 16 * lane * D, &maps.v, 0, tok & mask, (int)slab, &sh.v_full[stage]);
-        // scales
-        const uint32_t pages = __ballot_sync(0xffffffffu, id != -2) & 0xffu;
-        const uint32_t nans = __ballot_sync(0xffffffffu, sk != sk || sv != sv) & 0xffu;
-        const float sv_here = sv > 0.f ? sv : 0.f;
-        float vm = sv_here;
-        vm = fmaxf(vm, __shfl_xor_sync(0xffffffffu, vm, 1));
-        vm = fmaxf(vm, __shfl_xor_sync(0xffffffffu, vm, 2));
-        vm = fmaxf(vm, __shfl_xor_sync(0xffffffffu, vm, 4));
-        const float v_new = fmaxf(v_ref, vm);
-        const float v_inv = v_new > 0.f ? __fdiv_rn(1.f, v_new) : 0.f;
-        TileInfo& info = sh.info[count % kInfos];
-        if (lane < 8) {
-          const float ratio = fmaxf(sv_here * v_inv, 7.888609e-31f);  // 2^-100
-          info.k_scale[lane] = sk == sk ? sk : 0.f;
-          info.v_log[lane] = log2f(ratio);
-          info.v_back[lane] = __fdiv_rn(1.f, ratio);
-          if (lane == 0) {
-            info.v_factor = v_new > v_ref ? v_ref * v_inv : 1.f;
-            info.v_ref = v_new;
-            info.flags = pages | nans << 8;
-          }
-        }
-        v_ref = v_new;
+        if (copies) tma_load_codes(v_ring + stage * kCodes + 16 * lane * D, &maps.v, tok & mask, (int)slab, &sh.v_full[stage]);
+        paged_tell(sh.info[count % kInfos], lane, id, sk, sv, v_ref);
         __syncwarp();
         if (lane == 0) tc05::mbar_arrive(&sh.info_full[count % kInfos]);
         id = id_next;
@@ -641,8 +572,8 @@ __global__ void __launch_bounds__(kThreads, R == 16 ? 2 : 1)
     constexpr uint32_t id_s = tc05::idesc_e4m3(128, R);
     // fp32 D, fp16 A and B, both with their other dimension dense
     constexpr uint32_t id_o = (1u << 4) | (1u << 15) | (1u << 16) | ((uint32_t)(R >> 3) << 17) | ((uint32_t)(D >> 4) << 24);
-    const uint64_t k_d = desc(smem_u32(k_ring), D, 16), q_d = desc(smem_u32(q_tile), D, 16);
-    const uint64_t w_d = desc(smem_u32(w_tile), 128, kPanel), p_d = desc(smem_u32(p_tile), 2 * R, 16);
+    const uint32_t k_d = desc_lo(smem_u32(k_ring), 16), q_d = desc_lo(smem_u32(q_tile), 16);
+    const uint32_t w_d = desc_lo(smem_u32(w_tile), kPanel), p_d = desc_lo(smem_u32(p_tile), 16);
     auto scores = [&](uint32_t n) {
       const int stage = n % STAGES, buf = n & 1;
       wait(&sh.k_full[stage], n / STAGES & 1);
@@ -650,12 +581,12 @@ __global__ void __launch_bounds__(kThreads, R == 16 ? 2 : 1)
       wait(&sh.s_free[buf], (n >> 1 & 1) ^ 1);
       if (dead) return;
       tc05::fence_after();
-      const uint64_t a = tc05::desc_adv(k_d, stage * kCodes);
+      const uint32_t a = k_d + (stage * kCodes >> 4);
 #pragma unroll
       for (int m = 0; m < PIECES; ++m)
 #pragma unroll
         for (int k = 0; k < D / 32; ++k)
-          tc05::mma_e4m3(tmem + R * buf, tc05::desc_adv(a, 32 * k), tc05::desc_adv(q_d, m * kQ + 32 * k), id_s, m + k > 0);
+          mma_f8_ss(tmem + R * buf, a + (32 * k >> 4), q_d + (m * kQ + 32 * k >> 4), desc_hi(D), id_s, m + k > 0);
       tc05::mma_commit(&sh.s_full[buf]);
       tc05::mma_commit(&sh.k_free[stage]);
     };
@@ -675,7 +606,7 @@ __global__ void __launch_bounds__(kThreads, R == 16 ? 2 : 1)
         tc05::fence_after();
 #pragma unroll
         for (int k = 0; k < kTile / 16; ++k)
-          mma_f16(tmem + 2 * R, tc05::desc_adv(w_d, 2048 * k), tc05::desc_adv(p_d, 16 * 2 * R * k), id_o, j > 0 || k > 0);
+          mma_f16_ss(tmem + 2 * R, w_d + (2048 * k >> 4), desc_hi(128), p_d + (16 * 2 * R * k >> 4), desc_hi(2 * R), id_o, j > 0 || k > 0);
         tc05::mma_commit(&sh.pv_done);
         if (j + 1 == x.n) tc05::mma_commit(&sh.o_full);
       }
@@ -688,38 +619,13 @@ __global__ void __launch_bounds__(kThreads, R == 16 ? 2 : 1)
   if (warp == 9) tc05::tmem_dealloc(tmem, kCols);
 }
 
-PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
-  static PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
-    void* f = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) != cudaSuccess ||
-        q != cudaDriverEntryPointSuccess)
-      f = nullptr;
-    return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
-  }();
-  return fn;
-}
-
-// Codes as [pages x heads, page, dim]; a copy takes a page (of pages of 128: 128 tokens).
-bool make_map(CUtensorMap* map, const uint8_t* codes, const PagedAttnParams& p, int dim, CUtensorMapSwizzle swizzle) {
-  if (p.n_pages == 0 || p.table_cols == 0) return true;  // no page is ever read
-  const PFN_cuTensorMapEncodeTiled_v12000 fn = encode_fn();
-  if (fn == nullptr) return false;
-  const cuuint64_t page = 1ull << p.page_shift;
-  const cuuint64_t dims[3] = {(cuuint64_t)dim, page, (cuuint64_t)p.n_pages * p.kv_heads};
-  const cuuint64_t strides[2] = {(cuuint64_t)dim, dim * page};
-  const cuuint32_t box[3] = {(cuuint32_t)dim, (cuuint32_t)(page < kTile ? page : kTile), 1}, one[3] = {1, 1, 1};
-  return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<uint8_t*>(codes), dims, strides, box, one,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 template <int R, int PIECES, bool F16, int STAGES>
 cudaError_t launch(const PagedAttnParams& p, int blocks, cudaStream_t stream) {
   constexpr int D = 128;
   constexpr int smem = 2 * STAGES * kTile * D + kTile * D * 2 + PIECES * R * D + kTile * 2 * R + 1024;
   CopyMaps maps{};
-  if (!make_map(&maps.k, p.k, p, D, CU_TENSOR_MAP_SWIZZLE_128B) || !make_map(&maps.v, p.v, p, D, CU_TENSOR_MAP_SWIZZLE_NONE))
+  const int page = min(1 << p.page_shift, kTile);
+  if (!make_codes_map(&maps.k, p.k, p, D, page, CU_TENSOR_MAP_SWIZZLE_128B) || !make_codes_map(&maps.v, p.v, p, D, page, CU_TENSOR_MAP_SWIZZLE_NONE))
     return cudaErrorNotSupported;
   const cudaError_t e = allow_smem<paged_rows_kernel<R, PIECES, F16, STAGES>>(smem);
   if (e != cudaSuccess) return e;

@@ -6,16 +6,15 @@
 //
 // A block holds a tile of 256 rows (tokens x heads of a group) as two of 128 and walks its cached
 // tokens 128 at a time:
-//   4 warps   codes of K and V from the pages to fp16 tiles in shared memory (exact), two stages;
-//             both row tiles use what they convert, so that the conversion costs an eighth of the
-//             block's issue slots
-//   1 thread  tcgen05.mma: S_t = Q_t K^T into tensor memory, O_t += P_t V with P_t read from tensor
-//             memory, in an order that computes one row tile's products during the other's softmax
+//   1 warp    copies of whole pages into rings of K and of V (TMA), page ids and scales ahead of them
+//   4 warps   V's codes to fp16 (exact), once for both row tiles
+//   1 thread  tcgen05.mma: S_t = Q_t K^T into tensor memory (kind::f8f6f4: K's codes as they come, the query
+//             rows as E4M3 pieces added up in the accumulator), O_t += P_t V with P_t read from tensor
+//             memory (kind::f16), in an order that computes one row tile's products during the other's softmax
 //   2 x 4 warps  softmax, a row per thread: maximum, weights as fp16 over the scores' own columns,
 //             sum; the output is rescaled only where a score exceeds the running maximum by 2^4
 //
-// fp16 holds every E4M3 value; a bf16 query row is scaled by a power of two into fp16's range.  K's
-// page scale multiplies the fp32 scores, V's (relative to the largest seen) is an addition to the
+// K's page scale multiplies the fp32 scores, V's (relative to the largest seen) is an addition to the
 // weight's exponent, taken back from each 16 tokens' sum.  Weights as in the split attention: at most
 // 2^15, 11 bits down to 2^-21 of the largest.
 //
@@ -24,51 +23,21 @@
 #include "common.cuh"
 #include "paged.h"
 #include "paged_dev.cuh"
-#include "tc05.cuh"
+#include "paged_tma.cuh"
 
 namespace csa2 {
 namespace {
 
 constexpr int kRows = 256;
 constexpr int kTile = 128;              // tokens of a unit
-constexpr int kThreads = 16 * 32;       // warps: softmax 0 .. 7, conversion 8 .. 11, products 12 (13 .. 15 idle)
+constexpr int kThreads = 16 * 32;       // warps: softmax 0 .. 7, conversion 8 .. 11, products 12, copies 13 (14, 15 idle)
+constexpr int kInfos = 8;
 // Registers of a thread of each part, from 128 at launch: 2 * 192 + 72 + 56 = 4 * 128.
 constexpr int kSoftmaxRegs = 192, kConvertRegs = 72, kProductRegs = 56;
 template <int N>
 __device__ __forceinline__ void more_registers() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(N)); }
 template <int N>
 __device__ __forceinline__ void fewer_registers() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(N)); }
-
-__device__ __forceinline__ uint32_t idesc_f16(int m, int n, bool b_mn_major) {
-  return (1u << 4) | (b_mn_major ? 1u << 16 : 0u) | (uint32_t)(n >> 3) << 17 | (uint32_t)(m >> 4) << 24;
-}
-// Shared-memory descriptors in the 128-byte swizzle, groups of 8 rows 1,024 bytes apart, in two halves: the
-// lower holds address >> 4 and leading offset >> 4 << 16, the upper is the same for all.
-__device__ __forceinline__ uint32_t desc_lo(uint32_t saddr, uint32_t lbo) { return (saddr & 0x3ffffu) >> 4 | (lbo >> 4) << 16; }
-constexpr uint32_t kDescHi = (1024u >> 4) | 1u << 14 | 2u << 29;
-// D[tmem] (+)= A[smem] * B[smem], kind::f16; descriptors by their lower halves.
-__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t acc) {
-  asm volatile(
-      "{\n .reg .pred p;\n .reg .b64 da, db;\n mov.b64 da, {%1, %5};\n mov.b64 db, {%2, %5};\n setp.ne.b32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n}\n" ::"r"(d), "r"(a), "r"(b), "r"(idesc), "r"(acc), "r"(kDescHi)
-      : "memory");
-}
-// D[tmem] (+)= A[tmem] * B[smem], kind::f16.
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t acc) {
-  asm volatile(
-      "{\n .reg .pred p;\n .reg .b64 db;\n mov.b64 db, {%2, %5};\n setp.ne.b32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %3, p;\n}\n" ::"r"(d), "r"(a), "r"(b), "r"(idesc), "r"(acc), "r"(kDescHi)
-      : "memory");
-}
-// What the conversion tells the softmax about 128 tokens.
-struct TileInfo {
-  float k_scale[8];   // of each 16 tokens
-  float v_log[8];     // log2 of their V scale over the reference, at least -100
-  float v_back[8];    // 2^-v_log
-  float v_factor;     // what the outputs so far are to be multiplied by: the V reference grew
-  float v_ref;
-  uint32_t flags;     // bits 0-7: 16 tokens have a page; 8-15: their scales say NaN
-};
 
 struct Tile {
   int row0, n, pos_first, pos_last, lo, hi, blocks;
@@ -80,7 +49,7 @@ __device__ __forceinline__ Tile tile_of(const PagedAttnParams& p, const PagedSeq
   g.pos_first = s.ctx + by_group(p, g.row0);
   g.pos_last = s.ctx + by_group(p, g.row0 + g.n - 1);
   g.hi = min(s.kv, g.pos_last + 1);
-  g.lo = p.window > 0 ? max(g.pos_first - p.window + 1, 0) & ~15 : 0;
+  g.lo = p.window > 0 ? max(g.pos_first - p.window + 1, 0) >> p.page_shift << p.page_shift : 0;  // a page's first token
   g.blocks = max((max(g.hi - g.lo, 0) + kTile - 1) / kTile, 1);
   return g;
 }
@@ -119,10 +88,11 @@ struct Walk {
   }
 };
 
+template <int KS, int VS>
 struct Shared {
-  uint64_t k_full[2], k_free[2], v_full[2], v_free[2], s_full[2], p_ready[2], o_full[2], q_full[2];
-  uint64_t info_full[4];
-  TileInfo info[4];
+  uint64_t k_full[KS], k_free[KS], r_full[VS], r_free[VS], v_full[2], v_free[2], s_full[2], p_ready[2], o_full[2], q_full[2];
+  uint64_t info_full[kInfos];
+  PagedInfo info[kInfos];
   float factor[8][32];  // of the rows of the softmax warps: score in log2 units = factor * k_scale * product
   uint32_t tmem;
   Place place;
@@ -130,36 +100,40 @@ struct Shared {
 };
 
 template <int D, bool F16>
-__global__ void __launch_bounds__(kThreads, 1) paged_wide_kernel(const PagedAttnParams p) {
-  constexpr int kPanel = 128 * 128;            // 128 rows of 64 fp16
-  constexpr int kPanels = D / 64;
-  constexpr int kTileBytes = kPanels * kPanel; // a tile of Q, K or V
+__global__ void __launch_bounds__(kThreads, 1) paged_wide_kernel(const PagedAttnParams p, const __grid_constant__ CopyMaps maps) {
+  constexpr int PIECES = F16 ? 3 : 2;          // of a query row: they hold an fp16's 11 bits, a bf16's 8
+  constexpr int KS = F16 && D == 128 ? 2 : 3;  // stages of the rings
+  constexpr int VS = F16 && D == 128 ? 1 : 2;
+  constexpr int kCodes = kTile * D;            // bytes of 128 tokens' (or rows') codes
+  constexpr int kPanel = kTile * 128;          // 64 dims of V in fp16
+  constexpr int kV = D / 64 * kPanel;
   extern __shared__ uint8_t smem_raw[];
-  __shared__ Shared sh;
+  __shared__ Shared<KS, VS> sh;
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-  uint8_t* q_tiles = smem;
-  uint8_t* k_tiles = smem + 2 * kTileBytes;
-  uint8_t* v_tiles = smem + 4 * kTileBytes;
-  uint8_t* raw = smem + 6 * kTileBytes;        // 32 KB of codes on their way
+  uint8_t* q_tiles = smem;                     // [row tile][piece]
+  uint8_t* k_ring = q_tiles + 2 * PIECES * kCodes;
+  uint8_t* v_ring = k_ring + KS * kCodes;
+  uint8_t* v_tiles = v_ring + VS * kCodes;     // fp16, two
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (warp == 12) tc05::tmem_alloc(&sh.tmem, 512);
   if (tid == 0) {
+    for (int i = 0; i < KS; ++i) tc05::mbar_init(&sh.k_full[i], 1), tc05::mbar_init(&sh.k_free[i], 1);
+    for (int i = 0; i < VS; ++i) tc05::mbar_init(&sh.r_full[i], 1), tc05::mbar_init(&sh.r_free[i], 128);
     for (int i = 0; i < 2; ++i) {
-      tc05::mbar_init(&sh.k_full[i], 128), tc05::mbar_init(&sh.k_free[i], 1);
       tc05::mbar_init(&sh.v_full[i], 128), tc05::mbar_init(&sh.v_free[i], 1);
       tc05::mbar_init(&sh.s_full[i], 1), tc05::mbar_init(&sh.p_ready[i], 128);
       tc05::mbar_init(&sh.o_full[i], 1), tc05::mbar_init(&sh.q_full[i], 128);
     }
-    for (int i = 0; i < 4; ++i) tc05::mbar_init(&sh.info_full[i], 1);
+    for (int i = 0; i < kInfos; ++i) tc05::mbar_init(&sh.info_full[i], 1);
     tc05::fence_barrier_init();
   }
 
-  // ---- this block's piece of the line: tiles of the sequences before each (in the space of K's tiles),
+  // ---- this block's piece of the line: tiles of the sequences before each (in the space of the tiles),
   // then units of the tiles before each thread's run of tiles
   long long all, u, u_end;
   int used;
   {
-    int* tiles_before = reinterpret_cast<int*>(k_tiles);  // [n_seq + 1]
+    int* tiles_before = reinterpret_cast<int*>(smem);  // [n_seq + 1]
     auto scan = [&](long long v, long long& total) {       // exclusive sum over the block's threads
       long long x = v;
 #pragma unroll
@@ -227,8 +201,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_wide_kernel(const PagedAttn
   int pieces = 0;
   bool dead = false, bad = false;
   auto wait = [&](uint64_t* bar, uint32_t parity) {
-    if (!dead && !paged_wait(bar, parity)) dead = true;
-    if (warp < 12) dead = __any_sync(0xffffffffu, dead);
+    if (!dead && !paged_wait(bar, parity)) dead = true;  // a warp's lanes try together and see the same
   };
 
   if (warp < 8) {
@@ -248,8 +221,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_wide_kernel(const PagedAttn
       const bool has = r < x.g.n;
       const int rr = x.g.row0 + min(r, x.g.n - 1), i = by_group(p, rr);
       const int pos = x.s.ctx + i;
-      // the warp's query rows to fp16, scaled to a maximum in [2^13, 2^14): a row at a time by PL lanes, 16 bytes
-      // each.  A negative softmax scale turns the sign.
+      // the warp's query rows, scaled to a maximum in [224, 448), as E4M3 pieces: a row at a time by PL lanes, 8
+      // values each.  A negative softmax scale turns the sign.
       {
         constexpr int PL = D / 8, AT_ONCE = 32 / PL;
         const int c = lane % PL;
@@ -273,16 +246,31 @@ __global__ void __launch_bounds__(kThreads, 1) paged_wide_kernel(const PagedAttn
 #pragma unroll
           for (int o = 1; o < PL; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
           odd = (__ballot_sync(0xffffffffu, odd) >> (lane / PL * PL) & (PL == 16 ? 0xffffu : 0xffu)) != 0;
-          int e = (int)(__float_as_uint(amax) >> 23) - 127 - 13;
+          const uint32_t ua = __float_as_uint(amax);
+          int e = (int)(ua >> 23) - 127 - 8 + ((ua & 0x7fffffu) >= 0x600000u ? 1 : 0);
           e = min(max(e, -110), 119);
           float down = odd ? 0.f : __uint_as_float((uint32_t)(127 - e) << 23);
           const float up = __uint_as_float((uint32_t)(127 + e) << 23);
           if (p.scale_log2 < 0.f) down = -down;
-          uint32_t o[4];
 #pragma unroll
-          for (int n = 0; n < 4; ++n) o[n] = odd ? 0u : pack_f16x2(v[n].x * down, v[n].y * down);
-          *reinterpret_cast<uint4*>(q_tiles + t * kTileBytes + (c >> 3) * kPanel + in_tile * 128 + (((c & 7) ^ (in_tile & 7)) << 4)) =
-              make_uint4(o[0], o[1], o[2], o[3]);
+          for (int n = 0; n < 4; ++n) v[n] = odd ? make_float2(0.f, 0.f) : make_float2(v[n].x * down, v[n].y * down);
+          uint8_t* to = q_tiles + t * PIECES * kCodes + swizzled<D>(in_tile, c >> 1) + 8 * (c & 1);
+#pragma unroll
+          for (int m = 0; m < PIECES; ++m) {
+            uint32_t o[2];
+#pragma unroll
+            for (int n = 0; n < 2; ++n) {
+              o[n] = e4m3_word(v[2 * n].x, v[2 * n].y, v[2 * n + 1].x, v[2 * n + 1].y);
+              if (m + 1 < PIECES) {
+                uint32_t h0, h1;
+                f16_pairs(o[n], h0, h1);
+                const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&h0));
+                const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&h1));
+                v[2 * n].x -= a.x, v[2 * n].y -= a.y, v[2 * n + 1].x -= b.x, v[2 * n + 1].y -= b.y;  // exact
+              }
+            }
+            *reinterpret_cast<uint2*>(to + m * kCodes) = make_uint2(o[0], o[1]);
+          }
           if (c == 0) sh.factor[warp][in_warp] = odd ? __uint_as_float(0x7fc00000u) : fabsf(p.scale_log2) * up;
         }
         asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
@@ -296,10 +284,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_wide_kernel(const PagedAttn
       for (int j = 0; j < x.n && !dead; ++j, ++count, ++turn) {
         wait(&sh.s_full[t], turn & 1);
         if (dead) break;
-        wait(&sh.info_full[count & 3], count >> 2 & 1);
-        if (dead) break;
         tc05::fence_after();
-        const TileInfo& info = sh.info[count & 3];
+        const PagedInfo& info = sh.info[count % kInfos];
         const int tok = x.g.lo + (x.blk + j) * kTile;
         const int hi = see_hi - tok, lo = see_lo - tok;  // the row sees columns lo .. hi - 1
         const uint32_t flags = info.flags;
@@ -436,190 +422,155 @@ __global__ void __launch_bounds__(kThreads, 1) paged_wide_kernel(const PagedAttn
     }
   } else if (warp < 12) {
     fewer_registers<kConvertRegs>();
-    // ------------------------------------------------------------------ codes to fp16 tiles
-    const int gt = tid - 256;                    // thread of the group
-    constexpr int PR = D / 16;                   // 16-byte pieces of a row's codes
-    constexpr int LD = 4;                        // pieces of a thread in a group: 64 rows, or 128 at dim 64
-    constexpr int RPL = 128 / PR;                // rows that the threads' pieces cover at once
-    constexpr int GR = LD * RPL;                 // rows of a group
-    constexpr int GROUPS = kTile / GR;           // groups of a tile
+    // ------------------------------------------------------------------ V's codes to fp16
+    const int gt = tid - 256;                  // thread of the group
+    constexpr int PR = D / 16;                 // 16-byte pieces of a token's codes
+    constexpr int RPL = 128 / PR;              // tokens that the threads' pieces cover at once
     const int row_in = gt / PR, c16 = gt % PR;
+    // fp16 pieces 2 c16 and 2 c16 + 1 of the row's panel; the second panel's lanes store them in the other
+    // order, so that a phase's eight lanes meet all banks.  (RPL is a multiple of 8: one swizzle for all.)
+    const int sw = c16 >> 2, at0 = 2 * (c16 & 3);
+    const int to = sw * kPanel + row_in * 128;
+    const int to0 = to + (((at0 + sw) ^ (row_in & 7)) << 4), to1 = to + (((at0 + 1 - sw) ^ (row_in & 7)) << 4);
     uint32_t count = 0;
     while (walk.next(x) && !dead) {
-      const int32_t* trow = p.table + (long long)x.s.index * p.table_cols;
-      const int mask = (1 << p.page_shift) - 1;
-      float v_ref = 0.f;
-      // lane l < 8 knows the page of tokens 16 l .. of a tile and its scales
-      auto ids = [&](int j) {
-        const int tok = x.g.lo + (x.blk + j) * kTile + 16 * (lane & 7);
-        if (j >= x.n || tok >= x.g.hi) return -1;
-        const int id = __ldg(trow + (tok >> p.page_shift));
-        return (unsigned)id < (unsigned)p.n_pages ? id : -2;
-      };
-      // and the place of their codes
-      auto place = [&](int j, int id) {
-        const int tok = x.g.lo + (x.blk + j) * kTile + 16 * (lane & 7);
-        return id < 0 ? -1LL : ((((long long)id * p.kv_heads + x.h) << p.page_shift) + (tok & mask)) * D;
-      };
-      // a group of K's or V's codes into this thread's own slots of the ring; two (four at dim 64) to a tile
-      auto load = [&](int slot, const uint8_t* codes, int group, int j, long long at) {
-        if (j < x.n) {
-          const int left = x.g.hi - x.g.lo - (x.blk + j) * kTile;  // tokens of the tile that are there
-#pragma unroll
-          for (int i = 0; i < LD; ++i) {
-            const int row = group * GR + i * RPL + row_in;
-            const long long from = __shfl_sync(0xffffffffu, at, row >> 4);
-            const bool ok = from >= 0 && row < left;
-            cp_async16(raw + (slot * LD + i) * 2048 + gt * 16, codes + (ok ? from + (row & 15) * D + 16 * c16 : 0), ok);
-          }
-        }
-        cp_async_commit();
-      };
-      auto store = [&](int slot, uint8_t* tile, int group) {
-        cp_async_wait<3>();
-#pragma unroll
-        for (int i = 0; i < LD; ++i) {
-          const int row = group * GR + i * RPL + row_in;
-          const uint4 w = *reinterpret_cast<const uint4*>(raw + (slot * LD + i) * 2048 + gt * 16);
-          // fp16 pieces 2 c16 and 2 c16 + 1 of the row's panel; the second panel's lanes store them in the
-          // other order, so that a phase's eight lanes meet all banks
-          const int a = 2 * (c16 & 3), sw = c16 >> 2;
+      for (int j = 0; j < x.n && !dead; ++j, ++count) {
+        const int stage = count % VS;
+        wait(&sh.r_full[stage], count / VS & 1);
+        wait(&sh.info_full[count % kInfos], count / kInfos & 1);
+        wait(&sh.v_free[count & 1], (count >> 1 & 1) ^ 1);
+        if (dead) break;
+        const uint8_t* raw = v_ring + stage * kCodes + row_in * D + 16 * c16;
+        uint8_t* tile = v_tiles + (count & 1) * kV;
+        auto piece = [&](int q, uint4 w) {
           uint4 h0, h1;
           f16_pairs(sw ? w.z : w.x, h0.x, h0.y);
           f16_pairs(sw ? w.w : w.y, h0.z, h0.w);
           f16_pairs(sw ? w.x : w.z, h1.x, h1.y);
           f16_pairs(sw ? w.y : w.w, h1.z, h1.w);
-          uint8_t* to = tile + (c16 >> 2) * kPanel + row * 128;
-          *reinterpret_cast<uint4*>(to + (((a + sw) ^ (row & 7)) << 4)) = h0;
-          *reinterpret_cast<uint4*>(to + (((a + 1 - sw) ^ (row & 7)) << 4)) = h1;
+          *reinterpret_cast<uint4*>(tile + to0 + q * RPL * 128) = h0;
+          *reinterpret_cast<uint4*>(tile + to1 + q * RPL * 128) = h1;
+        };
+        const uint32_t flags = sh.info[count % kInfos].flags;
+        const int left = x.g.hi - x.g.lo - (x.blk + j) * kTile;  // tokens that are there: what lies behind may be anything
+        if (left >= kTile && (flags & 0xffu) == 0xffu) {
+#pragma unroll
+          for (int q = 0; q < kTile / RPL; ++q) piece(q, *reinterpret_cast<const uint4*>(raw + q * RPL * D));
+        } else {
+#pragma unroll 1
+          for (int q = 0; q < kTile / RPL; ++q) {
+            const int row = q * RPL + row_in;
+            piece(q, row < left && (flags >> (row >> 4) & 1) ? *reinterpret_cast<const uint4*>(raw + q * RPL * D) : make_uint4(0, 0, 0, 0));
+          }
         }
-      };
-      auto done = [&](uint64_t* bar) {
         asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
-        tc05::mbar_arrive(bar);
-      };
-      auto scale = [&](const float* s, int pg) { return pg >= 0 ? __ldg(s + (long long)pg * p.kv_heads + x.h) : 0.f; };
-      constexpr int AHEAD = 2 / GROUPS;  // tiles that a load is ahead of its use
-      int id[AHEAD + 2];                 // page ids of tiles j .. j + AHEAD + 1
-#pragma unroll
-      for (int i = 0; i < AHEAD + 2; ++i) id[i] = ids(i);
-#pragma unroll
-      for (int i = 0; i < AHEAD; ++i) {
-        const long long at = place(i, id[i]);
-#pragma unroll
-        for (int q = 0; q < 2 * GROUPS; ++q) load(i * 2 * GROUPS + q, q < GROUPS ? p.k : p.v, q % GROUPS, i, at);
+        tc05::mbar_arrive(&sh.v_full[count & 1]);
+        tc05::mbar_arrive(&sh.r_free[stage]);
       }
-      float sk = scale(p.k_scale, id[0]), sv = scale(p.v_scale, id[0]);
-      int slot = 0;
-      for (int j = 0; j < x.n && !dead; ++j, ++count) {
-        const int stage = count & 1;
-        const uint32_t parity = (count >> 1 & 1) ^ 1;
-        bad |= id[0] == -2;
-        const uint32_t pages = __ballot_sync(0xffffffffu, id[0] != -2) & 0xffu;
-        const uint32_t nans = __ballot_sync(0xffffffffu, sk != sk || sv != sv) & 0xffu;
-        const float sv_here = sv > 0.f ? sv : 0.f;
-        float vm = sv_here;
-        vm = fmaxf(vm, __shfl_xor_sync(0xffffffffu, vm, 1));
-        vm = fmaxf(vm, __shfl_xor_sync(0xffffffffu, vm, 2));
-        vm = fmaxf(vm, __shfl_xor_sync(0xffffffffu, vm, 4));
-        const float v_new = fmaxf(v_ref, vm);
-        const float v_inv = v_new > 0.f ? __fdiv_rn(1.f, v_new) : 0.f;
-        wait(&sh.k_free[stage], parity);
-        if (gt < 8) {
-          TileInfo& info = sh.info[count & 3];
-          const float ratio = fmaxf(sv_here * v_inv, 7.888609e-31f);  // 2^-100
-          info.k_scale[gt] = sk == sk ? sk : 0.f;
-          info.v_log[gt] = log2f(ratio);
-          info.v_back[gt] = __fdiv_rn(1.f, ratio);
-          if (gt == 0) {
-            info.v_factor = v_new > v_ref ? v_ref * v_inv : 1.f;
-            info.v_ref = v_new;
-            info.flags = pages | nans << 8;
-          }
-        }
-        __syncwarp();
-        if (gt == 0) tc05::mbar_arrive(&sh.info_full[count & 3]);
-        v_ref = v_new;
-        const long long at = place(j + AHEAD, id[AHEAD]);
-        const int id_far = ids(j + AHEAD + 2);
-        sk = scale(p.k_scale, id[1]), sv = scale(p.v_scale, id[1]);
-        uint8_t* tiles[2] = {k_tiles + stage * kTileBytes, v_tiles + stage * kTileBytes};
-#pragma unroll
-        for (int kv = 0; kv < 2; ++kv) {
-          if (kv == 1) wait(&sh.v_free[stage], parity);
-#pragma unroll
-          for (int q = 0; q < GROUPS; ++q) {
-            store(slot, tiles[kv], q);
-            load(slot, kv ? p.v : p.k, q, j + AHEAD, at);
-            slot = (slot + 1) & 3;
-          }
-          done(kv ? &sh.v_full[stage] : &sh.k_full[stage]);
-        }
-#pragma unroll
-        for (int i = 0; i < AHEAD + 1; ++i) id[i] = id[i + 1];
-        id[AHEAD + 1] = id_far;
-      }
-      cp_async_wait<0>();
     }
   } else {
     fewer_registers<kProductRegs>();
-    if (warp == 12 && lane == 0) {
-    // ------------------------------------------------------------------ products
-    const uint32_t q_u = smem_u32(q_tiles), k_u = smem_u32(k_tiles), v_u = smem_u32(v_tiles);
-    const uint32_t id_s = idesc_f16(128, 128, false), id_o = idesc_f16(128, D, true);
-    uint32_t count = 0, segs = 0, turns = 0;  // bits 0, 1: parity of the halves' next use
-    const uint32_t q_d = desc_lo(q_u, 16), k_d = desc_lo(k_u, 16), v_d = desc_lo(v_u, kPanel);
-    auto scores = [&](int t, int stage) {
-      const uint32_t a = q_d + t * (kTileBytes >> 4), b = k_d + stage * (kTileBytes >> 4);
-#pragma unroll
-      for (int k = 0; k < D / 16; ++k) {
-        const uint32_t at = ((k >> 2) * kPanel + (k & 3) * 32) >> 4;
-        mma_ss(tmem + 128 * t, a + at, b + at, id_s, k > 0);
-      }
-    };
-    auto outputs = [&](int t, int stage, bool acc) {
-      const uint32_t b = v_d + stage * (kTileBytes >> 4);
-#pragma unroll
-      for (int k = 0; k < kTile / 16; ++k)
-        mma_ts(tmem + 256 + D * t, tmem + 128 * t + 8 * k, b + (2048 * k >> 4), id_o, acc || k > 0);
-    };
-    while (walk.next(x) && !dead) {
-      const int halves = x.g.n > 128 ? 2 : 1;
-      for (int t = 0; t < halves; ++t) {
-        wait(&sh.q_full[t], segs >> t & 1);
-        segs ^= 1u << t;
-      }
-      wait(&sh.k_full[count & 1], count >> 1 & 1);
-      tc05::fence_after();
-      for (int t = 0; t < halves && !dead; ++t) {
-        scores(t, count & 1);
-        tc05::mma_commit(&sh.s_full[t]);
-      }
-      tc05::mma_commit(&sh.k_free[count & 1]);
-      for (int j = 0; j < x.n && !dead; ++j, ++count) {
-        const int stage = count & 1, next = stage ^ 1;
-        const bool more = j + 1 < x.n;
-        wait(&sh.v_full[stage], count >> 1 & 1);
-        for (int t = 0; t < halves && !dead; ++t) {
-          wait(&sh.p_ready[t], turns >> t & 1);
-          turns ^= 1u << t;
+    if (warp == 13) {
+      // ---------------------------------------------------------------- copies
+      const int mask = (1 << p.page_shift) - 1, rows = min(1 << p.page_shift, kTile);
+      uint32_t count = 0;
+      while (walk.next(x) && !dead) {
+        const int32_t* trow = p.table + (long long)x.s.index * p.table_cols;
+        float v_ref = 0.f;
+        // lane l (as l & 7) knows the page of tokens 16 l .. of a unit
+        auto ids = [&](int j) {
+          const int tok = x.g.lo + (x.blk + j) * kTile + 16 * (lane & 7);
+          if (j >= x.n || tok >= x.g.hi) return -1;
+          const int id = __ldg(trow + (tok >> p.page_shift));
+          return (unsigned)id < (unsigned)p.n_pages ? id : -2;
+        };
+        int id = ids(0);
+        for (int j = 0; j < x.n && !dead; ++j, ++count) {
+          const int id_next = ids(j + 1);
+          const long long slab = id >= 0 ? (long long)id * p.kv_heads + x.h : 0;
+          const float sk = id >= 0 ? __ldg(p.k_scale + slab) : 0.f, sv = id >= 0 ? __ldg(p.v_scale + slab) : 0.f;
+          bad |= id == -2;
+          // a lane whose 16 tokens begin a page (or, in pages of 128, the unit) copies it
+          const bool copies = lane < 8 && id >= 0 && (16 * lane & mask & (kTile - 1)) == 0;
+          const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, copies)) * rows * D;
+          const int tok = x.g.lo + (x.blk + j) * kTile + 16 * lane;
+          const int ks = count % KS, vs = count % VS;
+          wait(&sh.k_free[ks], (count / KS & 1) ^ 1);
           if (dead) break;
-          tc05::fence_after();
-          outputs(t, stage, j > 0);
-          if (t == halves - 1) tc05::mma_commit(&sh.v_free[stage]);
-          if (more) {
-            if (t == 0) wait(&sh.k_full[next], (count + 1) >> 1 & 1);
+          if (lane == 0) tc05::mbar_expect_tx(&sh.k_full[ks], bytes);
+          __syncwarp();
+          if (copies) tma_load_codes(k_ring + ks * kCodes + 16 * lane * D, &maps.k, tok & mask, (int)slab, &sh.k_full[ks]);
+          paged_tell(sh.info[count % kInfos], lane, id, sk, sv, v_ref);
+          __syncwarp();
+          if (lane == 0) tc05::mbar_arrive(&sh.info_full[count % kInfos]);
+          wait(&sh.r_free[vs], (count / VS & 1) ^ 1);
+          if (dead) break;
+          if (lane == 0) tc05::mbar_expect_tx(&sh.r_full[vs], bytes);
+          __syncwarp();
+          if (copies) tma_load_codes(v_ring + vs * kCodes + 16 * lane * D, &maps.v, tok & mask, (int)slab, &sh.r_full[vs]);
+          id = id_next;
+        }
+      }
+    } else if (warp == 12 && lane == 0) {
+      // ---------------------------------------------------------------- products
+      constexpr uint32_t id_s = tc05::idesc_e4m3(128, 128);
+      constexpr uint32_t id_o = (1u << 4) | 1u << 16 | (uint32_t)(D >> 3) << 17 | (uint32_t)(128 >> 4) << 24;  // fp16, B's dims dense
+      const uint32_t q_d = desc_lo(smem_u32(q_tiles), 16), k_d = desc_lo(smem_u32(k_ring), 16), v_d = desc_lo(smem_u32(v_tiles), kPanel);
+      uint32_t count = 0, segs = 0, turns = 0;  // bits 0, 1: parity of the halves' next use
+      auto scores = [&](int t, int stage) {
+        const uint32_t a = q_d + t * (PIECES * kCodes >> 4), b = k_d + stage * (kCodes >> 4);
+#pragma unroll
+        for (int m = 0; m < PIECES; ++m)
+#pragma unroll
+          for (int k = 0; k < D / 32; ++k)
+            mma_f8_ss(tmem + 128 * t, a + (m * kCodes + 32 * k >> 4), b + (32 * k >> 4), desc_hi(D), id_s, m + k > 0);
+      };
+      auto outputs = [&](int t, int stage, bool acc) {
+        const uint32_t b = v_d + stage * (kV >> 4);
+#pragma unroll
+        for (int k = 0; k < kTile / 16; ++k)
+          mma_f16_ts(tmem + 256 + D * t, tmem + 128 * t + 8 * k, b + (2048 * k >> 4), desc_hi(128), id_o, acc || k > 0);
+      };
+      auto keys = [&](uint32_t n) {  // unit n's codes, and what the softmax, that waits for the scores alone, needs of it
+        wait(&sh.info_full[n % kInfos], n / kInfos & 1);
+        wait(&sh.k_full[n % KS], n / KS & 1);
+      };
+      while (walk.next(x) && !dead) {
+        const int halves = x.g.n > 128 ? 2 : 1;
+        for (int t = 0; t < halves; ++t) {
+          wait(&sh.q_full[t], segs >> t & 1);
+          segs ^= 1u << t;
+        }
+        keys(count);
+        tc05::fence_after();
+        for (int t = 0; t < halves && !dead; ++t) {
+          scores(t, count % KS);
+          tc05::mma_commit(&sh.s_full[t]);
+        }
+        tc05::mma_commit(&sh.k_free[count % KS]);
+        for (int j = 0; j < x.n && !dead; ++j, ++count) {
+          const bool more = j + 1 < x.n;
+          wait(&sh.v_full[count & 1], count >> 1 & 1);
+          for (int t = 0; t < halves && !dead; ++t) {
+            wait(&sh.p_ready[t], turns >> t & 1);
+            turns ^= 1u << t;
             if (dead) break;
             tc05::fence_after();
-            scores(t, next);
-            tc05::mma_commit(&sh.s_full[t]);
-            if (t == halves - 1) tc05::mma_commit(&sh.k_free[next]);
-          } else {
-            tc05::mma_commit(&sh.o_full[t]);
+            outputs(t, count & 1, j > 0);
+            if (t == halves - 1) tc05::mma_commit(&sh.v_free[count & 1]);
+            if (more) {
+              if (t == 0) keys(count + 1);
+              if (dead) break;
+              tc05::fence_after();
+              scores(t, (count + 1) % KS);
+              tc05::mma_commit(&sh.s_full[t]);
+              if (t == halves - 1) tc05::mma_commit(&sh.k_free[(count + 1) % KS]);
+            } else {
+              tc05::mma_commit(&sh.o_full[t]);
+            }
           }
         }
       }
-    }
     }
   }
   if (dead && p.dev_status) atomicExch(p.dev_status, (int)CSA2_ETIMEOUT);
@@ -643,10 +594,16 @@ __global__ void __launch_bounds__(kThreads, 1) paged_wide_kernel(const PagedAttn
 
 template <int D, bool F16>
 cudaError_t launch(const PagedAttnParams& p, int blocks, cudaStream_t stream) {
-  constexpr int smem = 6 * 128 * D * 2 + 32768 + 1024;
+  constexpr bool LARGE = F16 && D == 128;
+  constexpr int smem = (2 * (F16 ? 3 : 2) + (LARGE ? 3 : 5)) * kTile * D + 2 * kTile * D * 2 + 1024;
+  CopyMaps maps{};
+  const int page = min(1 << p.page_shift, kTile);
+  if (!make_codes_map(&maps.k, p.k, p, D, page, D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B) ||
+      !make_codes_map(&maps.v, p.v, p, D, page, CU_TENSOR_MAP_SWIZZLE_NONE))
+    return cudaErrorNotSupported;
   const cudaError_t e = allow_smem<paged_wide_kernel<D, F16>>(smem);
   if (e != cudaSuccess) return e;
-  paged_wide_kernel<D, F16><<<blocks, kThreads, smem, stream>>>(p);
+  paged_wide_kernel<D, F16><<<blocks, kThreads, smem, stream>>>(p, maps);
   return cudaGetLastError();
 }
 
