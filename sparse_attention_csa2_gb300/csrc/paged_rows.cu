@@ -567,14 +567,15 @@ __global__ void __launch_bounds__(kThreads, R == 16 ? 2 : 1)
         id = id_next;
       }
     }
-  } else if (lane == 0) {
+  } else {
     // ------------------------------------------------------------------ products
+    const uint32_t base = uniform(tmem);
     constexpr uint32_t id_s = tc05::idesc_e4m3(128, R);
     // fp32 D, fp16 A and B, both with their other dimension dense
     constexpr uint32_t id_o = (1u << 4) | (1u << 15) | (1u << 16) | ((uint32_t)(R >> 3) << 17) | ((uint32_t)(D >> 4) << 24);
     const uint32_t k_d = desc_lo(smem_u32(k_ring), 16), q_d = desc_lo(smem_u32(q_tile), 16);
     const uint32_t w_d = desc_lo(smem_u32(w_tile), kPanel), p_d = desc_lo(smem_u32(p_tile), 16);
-    auto scores = [&](uint32_t n) {
+    auto scores = [&](uint32_t n, bool last) {
       const int stage = n % STAGES, buf = n & 1;
       wait(&sh.k_full[stage], n / STAGES & 1);
       wait(&sh.info_full[n % kInfos], n / kInfos & 1);  // for the weights, that wait for the scores alone
@@ -582,33 +583,37 @@ __global__ void __launch_bounds__(kThreads, R == 16 ? 2 : 1)
       if (dead) return;
       tc05::fence_after();
       const uint32_t a = k_d + (stage * kCodes >> 4);
+      if (elected()) {
 #pragma unroll
       for (int m = 0; m < PIECES; ++m)
 #pragma unroll
         for (int k = 0; k < D / 32; ++k)
-          mma_f8_ss(tmem + R * buf, a + (32 * k >> 4), q_d + (m * kQ + 32 * k >> 4), desc_hi(D), id_s, m + k > 0);
-      tc05::mma_commit(&sh.s_full[buf]);
-      tc05::mma_commit(&sh.k_free[stage]);
+          mma_f8_ss(base + R * buf, a + (32 * k >> 4), q_d + (m * kQ + 32 * k >> 4), desc_hi(D), id_s, m + k > 0);
+        tc05::mma_commit(&sh.s_full[buf]);
+        tc05::mma_commit(&sh.k_free[stage]);
+        if (last) tc05::mma_commit(&sh.q_free);
+      }
+      __syncwarp();
     };
     while (walk.next(x) && !dead) {
+      const int n = uniform(x.n);
       wait(&sh.q_full, segs & 1);
       ++segs;
-      scores(count);
-      if (x.n == 1) tc05::mma_commit(&sh.q_free);
-      for (int j = 0; j < x.n && !dead; ++j, ++count) {
-        if (j + 1 < x.n) {
-          scores(count + 1);
-          if (j + 2 == x.n) tc05::mma_commit(&sh.q_free);
-        }
+      scores(count, n == 1);
+      for (int j = 0; j < n && !dead; ++j, ++count) {
+        if (j + 1 < n) scores(count + 1, j + 2 == n);
         wait(&sh.w_full, count & 1);
         wait(&sh.p_full, count & 1);
         if (dead) break;
         tc05::fence_after();
+        if (elected()) {
 #pragma unroll
-        for (int k = 0; k < kTile / 16; ++k)
-          mma_f16_ss(tmem + 2 * R, w_d + (2048 * k >> 4), desc_hi(128), p_d + (16 * 2 * R * k >> 4), desc_hi(2 * R), id_o, j > 0 || k > 0);
-        tc05::mma_commit(&sh.pv_done);
-        if (j + 1 == x.n) tc05::mma_commit(&sh.o_full);
+          for (int k = 0; k < kTile / 16; ++k)
+            mma_f16_ss(base + 2 * R, w_d + (2048 * k >> 4), desc_hi(128), p_d + (16 * 2 * R * k >> 4), desc_hi(2 * R), id_o, j > 0 || k > 0);
+          tc05::mma_commit(&sh.pv_done);
+          if (j + 1 == n) tc05::mma_commit(&sh.o_full);
+        }
+        __syncwarp();
       }
     }
   }

@@ -33,6 +33,17 @@ __device__ __forceinline__ uint32_t desc_lo(uint32_t saddr, uint32_t lbo) { retu
 __host__ __device__ constexpr uint32_t desc_hi(int row_bytes) {
   return (uint32_t)(8 * row_bytes >> 4) | 1u << 14 | (row_bytes == 128 ? 2u : row_bytes == 64 ? 4u : 6u) << 29;
 }
+// One lane of a converged warp.  The warp that issues products runs their loops as a whole, on values that are
+// the same in all lanes, and only the instructions themselves in one: the descriptors then stay in uniform
+// registers.  (One lane running the loops by itself issued a product every 70 to 85 cycles, slower than the
+// tensor cores take them.)
+__device__ __forceinline__ bool elected() {
+  uint32_t r;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(r));
+  return r != 0;
+}
+__device__ __forceinline__ int uniform(int v) { return __shfl_sync(0xffffffffu, v, 0); }
+
 // D[tmem] (+)= A[smem] * B[smem], kind::f16 and kind::f8f6f4, and D (+)= A[tmem] * B[smem], kind::f16.
 __device__ __forceinline__ void mma_f16_ss(uint32_t d, uint32_t a, uint32_t a_hi, uint32_t b, uint32_t b_hi, uint32_t idesc, uint32_t acc) {
   asm volatile(

@@ -10,7 +10,8 @@
 //   4 warps   V's codes to fp16 (exact), once for both row tiles
 //   1 thread  tcgen05.mma: S_t = Q_t K^T into tensor memory (kind::f8f6f4: K's codes as they come, the query
 //             rows as E4M3 pieces added up in the accumulator), O_t += P_t V with P_t read from tensor
-//             memory (kind::f16), in an order that computes one row tile's products during the other's softmax
+//             memory (kind::f16).  Scores come in halves of 64 tokens, so that the next half's are there when
+//             the softmax of one is done
 //   2 x 4 warps  softmax, a row per thread: maximum, weights as fp16 over the scores' own columns,
 //             sum; the output is rescaled only where a score exceeds the running maximum by 2^4
 //
@@ -32,8 +33,8 @@ constexpr int kRows = 256;
 constexpr int kTile = 128;              // tokens of a unit
 constexpr int kThreads = 16 * 32;       // warps: softmax 0 .. 7, conversion 8 .. 11, products 12, copies 13 (14, 15 idle)
 constexpr int kInfos = 8;
-// Registers of a thread of each part, from 128 at launch: 2 * 192 + 72 + 56 = 4 * 128.
-constexpr int kSoftmaxRegs = 192, kConvertRegs = 72, kProductRegs = 56;
+// Registers of a thread of each part, from 128 at launch: 2 * 152 + 104 + 104 = 4 * 128.
+constexpr int kSoftmaxRegs = 152, kConvertRegs = 104, kProductRegs = 104;
 template <int N>
 __device__ __forceinline__ void more_registers() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(N)); }
 template <int N>
@@ -90,7 +91,8 @@ struct Walk {
 
 template <int KS, int VS>
 struct Shared {
-  uint64_t k_full[KS], k_free[KS], r_full[VS], r_free[VS], v_full[2], v_free[2], s_full[2], p_ready[2], o_full[2], q_full[2];
+  uint64_t k_full[KS], k_free[KS], r_full[VS], r_free[VS], v_full[2], v_free[2], q_full[2];
+  uint64_t s_full[2][2], p_ready[2][2], o_done[2][2];  // [row tile][half]
   uint64_t info_full[kInfos];
   PagedInfo info[kInfos];
   float factor[8][32];  // of the rows of the softmax warps: score in log2 units = factor * k_scale * product
@@ -121,8 +123,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_wide_kernel(const PagedAttn
     for (int i = 0; i < VS; ++i) tc05::mbar_init(&sh.r_full[i], 1), tc05::mbar_init(&sh.r_free[i], 128);
     for (int i = 0; i < 2; ++i) {
       tc05::mbar_init(&sh.v_full[i], 128), tc05::mbar_init(&sh.v_free[i], 1);
-      tc05::mbar_init(&sh.s_full[i], 1), tc05::mbar_init(&sh.p_ready[i], 128);
-      tc05::mbar_init(&sh.o_full[i], 1), tc05::mbar_init(&sh.q_full[i], 128);
+      tc05::mbar_init(&sh.q_full[i], 128);
+      for (int h = 0; h < 2; ++h)
+        tc05::mbar_init(&sh.s_full[i][h], 1), tc05::mbar_init(&sh.p_ready[i][h], 128), tc05::mbar_init(&sh.o_done[i][h], 1);
     }
     for (int i = 0; i < kInfos; ++i) tc05::mbar_init(&sh.info_full[i], 1);
     tc05::fence_barrier_init();
@@ -195,7 +198,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_wide_kernel(const PagedAttn
     __syncthreads();
     tc05::fence_after();
   }
-  const uint32_t tmem = sh.tmem;
+  const uint32_t tmem = sh.tmem;  // all 512 columns: they begin at 0, as the products below know
   Walk walk{p, sh.place, u, u_end};
   Segment x;
   int pieces = 0;
@@ -209,8 +212,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_wide_kernel(const PagedAttn
     // ------------------------------------------------------------------ softmax: a row per thread
     const int t = warp >> 2, row = (warp & 3) * 32 + lane;  // row of the tile of 128
     const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-    const uint32_t s_cols = lanes + 128 * t, o_cols = lanes + 256 + D * t;
-    uint32_t turn = 0, done = 0;  // uses of s_full, of o_full
+    const uint32_t o_cols = lanes + 256 + D * t;
+    uint32_t turn = 0;            // units of this row tile
     uint32_t count = 0;           // units of the block
     while (walk.next(x) && !dead) {
       const int r = 128 * t + row;
@@ -282,121 +285,131 @@ __global__ void __launch_bounds__(kThreads, 1) paged_wide_kernel(const PagedAttn
       float2 l2 = make_float2(0.f, 0.f);
       const int see_hi = min(pos + 1, x.g.hi), see_lo = p.window > 0 ? pos - p.window + 1 : 0;
       for (int j = 0; j < x.n && !dead; ++j, ++count, ++turn) {
-        wait(&sh.s_full[t], turn & 1);
-        if (dead) break;
-        tc05::fence_after();
-        const PagedInfo& info = sh.info[count % kInfos];
         const int tok = x.g.lo + (x.blk + j) * kTile;
-        const int hi = see_hi - tok, lo = see_lo - tok;  // the row sees columns lo .. hi - 1
-        const uint32_t flags = info.flags;
-        const bool whole = __all_sync(0xffffffffu, hi >= kTile && lo <= 0) && flags == 0xffu;
-        v_ref = info.v_ref;
-        const float v_factor = info.v_factor;
-        // the scores' maximum: of a tile that all rows of the warp see whole from registers, where the
-        // scores then stay; otherwise 32 columns at a time from tensor memory, hidden ones left out
-        float top = -INFINITY;
-        uint32_t v[4][32];
-        const uint32_t from = (uint32_t)max(lo, 0), span = (uint32_t)max(min(hi, kTile) - max(lo, 0), 0);
-        if (whole) {
-#pragma unroll
-          for (int c = 0; c < 4; ++c) tc05::tmem_ld32(s_cols + 32 * c, v[c]);
-          tc05::tmem_ld_wait();
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            float a = __uint_as_float(v[c][0]), b = __uint_as_float(v[c][16]);
-#pragma unroll
-            for (int k = 1; k < 16; ++k) a = fmaxf(a, __uint_as_float(v[c][k])), b = fmaxf(b, __uint_as_float(v[c][16 + k]));
-            top = fmaxf(top, fmaxf(a * (f * info.k_scale[2 * c]), b * (f * info.k_scale[2 * c + 1])));
-          }
-        } else {
+        const PagedInfo& info = sh.info[count % kInfos];
 #pragma unroll 1
-          for (int c = 0; c < 4; ++c) {
-            uint32_t y[32];
-            tc05::tmem_ld32(s_cols + 32 * c, y);
+        for (int half = 0; half < 2; ++half) {  // 64 tokens
+          wait(&sh.s_full[t][half], turn & 1);
+          if (dead) break;
+          tc05::fence_after();
+          const uint32_t s_cols = lanes + 128 * t + 64 * half;
+          const float* k_scale = info.k_scale + 4 * half;
+          const float* v_log = info.v_log + 4 * half;
+          const float* v_back = info.v_back + 4 * half;
+          const int hi = see_hi - tok - 64 * half, lo = see_lo - tok - 64 * half;  // the row sees columns lo .. hi - 1
+          const uint32_t flags = info.flags >> 4 * half & 0xf0fu;                   // bits 0-3 and 8-11
+          const bool whole = __all_sync(0xffffffffu, hi >= 64 && lo <= 0) && flags == 0xfu;
+          // the scores' maximum: of columns that all rows of the warp see from registers, where the scores then
+          // stay; otherwise 32 at a time from tensor memory, hidden ones left out
+          float top = -INFINITY;
+          uint32_t v[2][32];
+          const uint32_t from = (uint32_t)max(lo, 0), span = (uint32_t)max(min(hi, 64) - max(lo, 0), 0);
+          if (whole) {
+#pragma unroll
+            for (int c = 0; c < 2; ++c) tc05::tmem_ld32(s_cols + 32 * c, v[c]);
             tc05::tmem_ld_wait();
-            const uint32_t col = 32u * c - from;
-            float a = -INFINITY, b = -INFINITY;
 #pragma unroll
-            for (int k = 0; k < 16; ++k) {
-              if (col + k < span) a = fmaxf(a, __uint_as_float(y[k]));
-              if (col + 16 + k < span) b = fmaxf(b, __uint_as_float(y[16 + k]));
+            for (int c = 0; c < 2; ++c) {
+              float a = __uint_as_float(v[c][0]), b = __uint_as_float(v[c][16]);
+#pragma unroll
+              for (int k = 1; k < 16; ++k) a = fmaxf(a, __uint_as_float(v[c][k])), b = fmaxf(b, __uint_as_float(v[c][16 + k]));
+              top = fmaxf(top, fmaxf(a * (f * k_scale[2 * c]), b * (f * k_scale[2 * c + 1])));
             }
-            if ((flags >> (2 * c) & 1) && a > -INFINITY) top = fmaxf(top, a * (f * info.k_scale[2 * c]));
-            if ((flags >> (2 * c + 1) & 1) && b > -INFINITY) top = fmaxf(top, b * (f * info.k_scale[2 * c + 1]));
-          }
-        }
-        const bool grows = top > m + kPagedSlack;
-        if (__any_sync(0xffffffffu, grows) || v_factor != 1.f) {
-          const float to = grows ? top : m;
-          const float e = m == -INFINITY ? 0.f : to == m ? 1.f : ex2(m - to);
-          l2.x *= e, l2.y *= e;
-          m = to;
-          if (j > 0) {
-            const float o = e * v_factor;
+          } else {
 #pragma unroll 1
-            for (int c = 0; c < D / 16; ++c) {
-              uint32_t y[16];
-              tc05::tmem_ld16(o_cols + 16 * c, y);
+            for (int c = 0; c < 2; ++c) {
+              uint32_t y[32];
+              tc05::tmem_ld32(s_cols + 32 * c, y);
               tc05::tmem_ld_wait();
+              const uint32_t col = 32u * c - from;
+              float a = -INFINITY, b = -INFINITY;
 #pragma unroll
-              for (int k = 0; k < 16; ++k) y[k] = __float_as_uint(__uint_as_float(y[k]) * o);
-              tc05::tmem_st16(o_cols + 16 * c, y);
-            }
-          }
-        }
-        const float off = m == -INFINITY ? 0.f : kPagedLift - m;
-        if (whole) {
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            uint32_t w[16];
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const float ks = f * info.k_scale[2 * c + h], o = off + info.v_log[2 * c + h], back = info.v_back[2 * c + h];
-              float2 sum = make_float2(0.f, 0.f);
-#pragma unroll
-              for (int k = 8 * h; k < 8 * h + 8; ++k) {
-                const float2 z = fma2(make_float2(__uint_as_float(v[c][2 * k]), __uint_as_float(v[c][2 * k + 1])), make_float2(ks, ks), make_float2(o, o));
-                const float2 e = make_float2(ex2(z.x), ex2(z.y));
-                sum = add2(sum, e);
-                w[k] = pack_f16x2(e.x, e.y);
+              for (int k = 0; k < 16; ++k) {
+                if (col + k < span) a = fmaxf(a, __uint_as_float(y[k]));
+                if (col + 16 + k < span) b = fmaxf(b, __uint_as_float(y[16 + k]));
               }
-              l2 = fma2(sum, make_float2(back, back), l2);
+              if ((flags >> (2 * c) & 1) && a > -INFINITY) top = fmaxf(top, a * (f * k_scale[2 * c]));
+              if ((flags >> (2 * c + 1) & 1) && b > -INFINITY) top = fmaxf(top, b * (f * k_scale[2 * c + 1]));
             }
-            tc05::tmem_st16(s_cols + 16 * c, w);
           }
-        } else {
+          v_ref = info.v_ref;
+          const float v_factor = half == 0 ? info.v_factor : 1.f;
+          const bool grows = top > m + kPagedSlack;
+          if (__any_sync(0xffffffffu, grows) || v_factor != 1.f) {
+            const float to = grows ? top : m;
+            const float e = m == -INFINITY ? 0.f : to == m ? 1.f : ex2(m - to);
+            l2.x *= e, l2.y *= e;
+            m = to;
+            if (j + half > 0) {
+              wait(&sh.o_done[t][half ^ 1], (turn - (half ^ 1)) & 1);  // the products before: this unit's, or the last one's
+              if (dead) break;
+              tc05::fence_after();
+              const float o = e * v_factor;
 #pragma unroll 1
-          for (int c = 0; c < 4; ++c) {
-            uint32_t y[32], w[16];
-            tc05::tmem_ld32(s_cols + 32 * c, y);
-            tc05::tmem_ld_wait();
-            const uint32_t col = 32u * c - from;
+              for (int c = 0; c < D / 16; ++c) {
+                uint32_t y[16];
+                tc05::tmem_ld16(o_cols + 16 * c, y);
+                tc05::tmem_ld_wait();
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const int g = 2 * c + h;
-              const float ks = flags >> (8 + g) & 1 ? __uint_as_float(0x7fc00000u) : f * info.k_scale[g];
-              const float o = off + info.v_log[g];
-              const uint32_t here = flags >> g & 1 ? span : 0;  // a page that is not there hides its columns
-              float sum = 0.f;
-#pragma unroll
-              for (int k = 16 * h; k < 16 * h + 16; ++k) {
-                y[k] = __float_as_uint(col + k < here ? ex2(fmaf(__uint_as_float(y[k]), ks, o)) : 0.f);
-                sum += __uint_as_float(y[k]);
+                for (int k = 0; k < 16; ++k) y[k] = __float_as_uint(__uint_as_float(y[k]) * o);
+                tc05::tmem_st16(o_cols + 16 * c, y);
               }
-              l2.x = fmaf(sum, info.v_back[g], l2.x);
             }
-#pragma unroll
-            for (int k = 0; k < 16; ++k) w[k] = pack_f16x2(__uint_as_float(y[2 * k]), __uint_as_float(y[2 * k + 1]));
-            tc05::tmem_st16(s_cols + 16 * c, w);
           }
+          // weights, over the score columns that have been read
+          const float off = m == -INFINITY ? 0.f : kPagedLift - m;
+          if (whole) {
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              uint32_t w[16];
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                const float ks = f * k_scale[2 * c + h], o = off + v_log[2 * c + h], back = v_back[2 * c + h];
+                float2 sum = make_float2(0.f, 0.f);
+#pragma unroll
+                for (int k = 8 * h; k < 8 * h + 8; ++k) {
+                  const float2 z = fma2(make_float2(__uint_as_float(v[c][2 * k]), __uint_as_float(v[c][2 * k + 1])), make_float2(ks, ks), make_float2(o, o));
+                  const float2 e = make_float2(ex2(z.x), ex2(z.y));
+                  sum = add2(sum, e);
+                  w[k] = pack_f16x2(e.x, e.y);
+                }
+                l2 = fma2(sum, make_float2(back, back), l2);
+              }
+              tc05::tmem_st16(s_cols + 16 * c, w);
+            }
+          } else {
+#pragma unroll 1
+            for (int c = 0; c < 2; ++c) {
+              uint32_t y[32], w[16];
+              tc05::tmem_ld32(s_cols + 32 * c, y);
+              tc05::tmem_ld_wait();
+              const uint32_t col = 32u * c - from;
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                const int g = 2 * c + h;
+                const float ks = flags >> (8 + g) & 1 ? __uint_as_float(0x7fc00000u) : f * k_scale[g];
+                const float o = off + v_log[g];
+                const uint32_t here = flags >> g & 1 ? span : 0;  // a page that is not there hides its columns
+                float sum = 0.f;
+#pragma unroll
+                for (int k = 16 * h; k < 16 * h + 16; ++k) {
+                  y[k] = __float_as_uint(col + k < here ? ex2(fmaf(__uint_as_float(y[k]), ks, o)) : 0.f);
+                  sum += __uint_as_float(y[k]);
+                }
+                l2.x = fmaf(sum, v_back[g], l2.x);
+              }
+#pragma unroll
+              for (int k = 0; k < 16; ++k) w[k] = pack_f16x2(__uint_as_float(y[2 * k]), __uint_as_float(y[2 * k + 1]));
+              tc05::tmem_st16(s_cols + 16 * c, w);
+            }
+          }
+          tc05::tmem_st_wait();
+          tc05::fence_before();
+          tc05::mbar_arrive(&sh.p_ready[t][half]);
         }
-        tc05::tmem_st_wait();
-        tc05::fence_before();
-        tc05::mbar_arrive(&sh.p_ready[t]);
       }
       // ---- the row's output, or its partial sums
-      wait(&sh.o_full[t], done & 1);
-      ++done;
+      wait(&sh.o_done[t][1], (turn - 1) & 1);
       if (dead) break;
       tc05::fence_after();
       const bool starts = x.blk == 0, ends = x.blk + x.n == x.g.blocks;
@@ -511,64 +524,70 @@ __global__ void __launch_bounds__(kThreads, 1) paged_wide_kernel(const PagedAttn
           id = id_next;
         }
       }
-    } else if (warp == 12 && lane == 0) {
+    } else if (warp == 12) {
       // ---------------------------------------------------------------- products
-      constexpr uint32_t id_s = tc05::idesc_e4m3(128, 128);
+      constexpr uint32_t id_s = tc05::idesc_e4m3(128, 64);
       constexpr uint32_t id_o = (1u << 4) | 1u << 16 | (uint32_t)(D >> 3) << 17 | (uint32_t)(128 >> 4) << 24;  // fp16, B's dims dense
       const uint32_t q_d = desc_lo(smem_u32(q_tiles), 16), k_d = desc_lo(smem_u32(k_ring), 16), v_d = desc_lo(smem_u32(v_tiles), kPanel);
-      uint32_t count = 0, segs = 0, turns = 0;  // bits 0, 1: parity of the halves' next use
-      auto scores = [&](int t, int stage) {
-        const uint32_t a = q_d + t * (PIECES * kCodes >> 4), b = k_d + stage * (kCodes >> 4);
+      uint32_t count = 0, segs = 0, turns = 0;  // bits 0, 1: parity of the row tiles' next use
+      // unit n's scores of one half (64 tokens) into the columns that its weights will take
+      auto scores = [&](int t, int half, uint32_t n) {
+        const uint32_t a = q_d + t * (PIECES * kCodes >> 4), b = k_d + (n % KS) * (kCodes >> 4) + half * (64 * D >> 4);
 #pragma unroll
         for (int m = 0; m < PIECES; ++m)
 #pragma unroll
           for (int k = 0; k < D / 32; ++k)
-            mma_f8_ss(tmem + 128 * t, a + (m * kCodes + 32 * k >> 4), b + (32 * k >> 4), desc_hi(D), id_s, m + k > 0);
+            mma_f8_ss(128 * t + 64 * half, a + (m * kCodes + 32 * k >> 4), b + (32 * k >> 4), desc_hi(D), id_s, m + k > 0);
+        tc05::mma_commit(&sh.s_full[t][half]);
       };
-      auto outputs = [&](int t, int stage, bool acc) {
-        const uint32_t b = v_d + stage * (kV >> 4);
+      auto outputs = [&](int t, int half, uint32_t n, bool acc) {
+        const uint32_t b = v_d + (n & 1) * (kV >> 4) + half * (64 * 128 >> 4);
 #pragma unroll
-        for (int k = 0; k < kTile / 16; ++k)
-          mma_f16_ts(tmem + 256 + D * t, tmem + 128 * t + 8 * k, b + (2048 * k >> 4), desc_hi(128), id_o, acc || k > 0);
+        for (int k = 0; k < 4; ++k)
+          mma_f16_ts(256 + D * t, 128 * t + 64 * half + 8 * k, b + (2048 * k >> 4), desc_hi(128), id_o, acc || k > 0);
+        tc05::mma_commit(&sh.o_done[t][half]);
       };
       auto keys = [&](uint32_t n) {  // unit n's codes, and what the softmax, that waits for the scores alone, needs of it
         wait(&sh.info_full[n % kInfos], n / kInfos & 1);
         wait(&sh.k_full[n % KS], n / KS & 1);
       };
       while (walk.next(x) && !dead) {
-        const int halves = x.g.n > 128 ? 2 : 1;
-        for (int t = 0; t < halves; ++t) {
-          wait(&sh.q_full[t], segs >> t & 1);
-          segs ^= 1u << t;
-        }
+        const int tiles = uniform(x.g.n) > 128 ? 2 : 1, n = uniform(x.n);
+        for (int t = 0; t < tiles; ++t) wait(&sh.q_full[t], segs >> t & 1);
+        segs ^= tiles == 2 ? 3u : 1u;
         keys(count);
+        if (dead) break;
         tc05::fence_after();
-        for (int t = 0; t < halves && !dead; ++t) {
-          scores(t, count % KS);
-          tc05::mma_commit(&sh.s_full[t]);
+        if (elected()) {
+          for (int half = 0; half < 2; ++half)
+            for (int t = 0; t < tiles; ++t) scores(t, half, count);
+          tc05::mma_commit(&sh.k_free[count % KS]);
         }
-        tc05::mma_commit(&sh.k_free[count % KS]);
-        for (int j = 0; j < x.n && !dead; ++j, ++count) {
-          const bool more = j + 1 < x.n;
+        __syncwarp();
+        for (int j = 0; j < n && !dead; ++j, ++count) {
+          const bool more = j + 1 < n;
           wait(&sh.v_full[count & 1], count >> 1 & 1);
-          for (int t = 0; t < halves && !dead; ++t) {
-            wait(&sh.p_ready[t], turns >> t & 1);
-            turns ^= 1u << t;
-            if (dead) break;
-            tc05::fence_after();
-            outputs(t, count & 1, j > 0);
-            if (t == halves - 1) tc05::mma_commit(&sh.v_free[count & 1]);
-            if (more) {
-              if (t == 0) keys(count + 1);
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+              if (t == tiles || dead) break;
+              wait(&sh.p_ready[t][half], turns >> t & 1);
+              if (half + t == 0 && more) keys(count + 1);
               if (dead) break;
               tc05::fence_after();
-              scores(t, (count + 1) % KS);
-              tc05::mma_commit(&sh.s_full[t]);
-              if (t == halves - 1) tc05::mma_commit(&sh.k_free[(count + 1) % KS]);
-            } else {
-              tc05::mma_commit(&sh.o_full[t]);
+              if (elected()) {
+                outputs(t, half, count, j + half > 0);
+                if (more) scores(t, half, count + 1);
+                if (half == 1 && t == tiles - 1) {
+                  tc05::mma_commit(&sh.v_free[count & 1]);
+                  if (more) tc05::mma_commit(&sh.k_free[(count + 1) % KS]);
+                }
+              }
+              __syncwarp();
             }
           }
+          turns ^= tiles == 2 ? 3u : 1u;
         }
       }
     }
