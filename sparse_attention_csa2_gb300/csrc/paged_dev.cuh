@@ -95,7 +95,7 @@ __device__ __forceinline__ void paged_put(const PagedAttnParams& p, int row, int
 }
 
 // What the warp that finds the pages tells the others about 128 tokens (kernels with a running V reference).
-struct PagedInfo {
+struct __align__(16) PagedInfo {
   float k_scale[8];   // of each 16 tokens
   float v_log[8];     // log2 of their V scale over the reference, at least -100
   float v_back[8];    // 2^-v_log

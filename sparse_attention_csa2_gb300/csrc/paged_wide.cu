@@ -293,9 +293,13 @@ __global__ void __launch_bounds__(kThreads, 1) paged_wide_kernel(const PagedAttn
           if (dead) break;
           tc05::fence_after();
           const uint32_t s_cols = lanes + 128 * t + 64 * half;
-          const float* k_scale = info.k_scale + 4 * half;
-          const float* v_log = info.v_log + 4 * half;
-          const float* v_back = info.v_back + 4 * half;
+          const float4 k4 = *reinterpret_cast<const float4*>(info.k_scale + 4 * half);
+          const float4 l4 = *reinterpret_cast<const float4*>(info.v_log + 4 * half);
+          const float4 b4 = *reinterpret_cast<const float4*>(info.v_back + 4 * half);
+          const float v_factor = half == 0 ? info.v_factor : 1.f;
+          v_ref = info.v_ref;
+          const float k_scale[4] = {f * k4.x, f * k4.y, f * k4.z, f * k4.w};  // of 16 tokens each
+          const float v_log[4] = {l4.x, l4.y, l4.z, l4.w}, v_back[4] = {b4.x, b4.y, b4.z, b4.w};
           const int hi = see_hi - tok - 64 * half, lo = see_lo - tok - 64 * half;  // the row sees columns lo .. hi - 1
           const uint32_t flags = info.flags >> 4 * half & 0xf0fu;                   // bits 0-3 and 8-11
           const bool whole = __all_sync(0xffffffffu, hi >= 64 && lo <= 0) && flags == 0xfu;
@@ -313,7 +317,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_wide_kernel(const PagedAttn
               float a = __uint_as_float(v[c][0]), b = __uint_as_float(v[c][16]);
 #pragma unroll
               for (int k = 1; k < 16; ++k) a = fmaxf(a, __uint_as_float(v[c][k])), b = fmaxf(b, __uint_as_float(v[c][16 + k]));
-              top = fmaxf(top, fmaxf(a * (f * k_scale[2 * c]), b * (f * k_scale[2 * c + 1])));
+              top = fmaxf(top, fmaxf(a * k_scale[2 * c], b * k_scale[2 * c + 1]));
             }
           } else {
 #pragma unroll 1
@@ -328,12 +332,11 @@ __global__ void __launch_bounds__(kThreads, 1) paged_wide_kernel(const PagedAttn
                 if (col + k < span) a = fmaxf(a, __uint_as_float(y[k]));
                 if (col + 16 + k < span) b = fmaxf(b, __uint_as_float(y[16 + k]));
               }
-              if ((flags >> (2 * c) & 1) && a > -INFINITY) top = fmaxf(top, a * (f * k_scale[2 * c]));
-              if ((flags >> (2 * c + 1) & 1) && b > -INFINITY) top = fmaxf(top, b * (f * k_scale[2 * c + 1]));
+              const float* ks = info.k_scale + 4 * half + 2 * c;
+              if ((flags >> (2 * c) & 1) && a > -INFINITY) top = fmaxf(top, a * (f * ks[0]));
+              if ((flags >> (2 * c + 1) & 1) && b > -INFINITY) top = fmaxf(top, b * (f * ks[1]));
             }
           }
-          v_ref = info.v_ref;
-          const float v_factor = half == 0 ? info.v_factor : 1.f;
           const bool grows = top > m + kPagedSlack;
           if (__any_sync(0xffffffffu, grows) || v_factor != 1.f) {
             const float to = grows ? top : m;
@@ -364,7 +367,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_wide_kernel(const PagedAttn
               uint32_t w[16];
 #pragma unroll
               for (int h = 0; h < 2; ++h) {
-                const float ks = f * k_scale[2 * c + h], o = off + v_log[2 * c + h], back = v_back[2 * c + h];
+                const float ks = k_scale[2 * c + h], o = off + v_log[2 * c + h], back = v_back[2 * c + h];
                 float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
                 for (int k = 8 * h; k < 8 * h + 8; ++k) {
@@ -387,8 +390,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_wide_kernel(const PagedAttn
 #pragma unroll
               for (int h = 0; h < 2; ++h) {
                 const int g = 2 * c + h;
-                const float ks = flags >> (8 + g) & 1 ? __uint_as_float(0x7fc00000u) : f * k_scale[g];
-                const float o = off + v_log[g];
+                const float ks = flags >> (8 + g) & 1 ? __uint_as_float(0x7fc00000u) : f * info.k_scale[4 * half + g];
+                const float o = off + info.v_log[4 * half + g];
                 const uint32_t here = flags >> g & 1 ? span : 0;  // a page that is not there hides its columns
                 float sum = 0.f;
 #pragma unroll
@@ -396,7 +399,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_wide_kernel(const PagedAttn
                   y[k] = __float_as_uint(col + k < here ? ex2(fmaf(__uint_as_float(y[k]), ks, o)) : 0.f);
                   sum += __uint_as_float(y[k]);
                 }
-                l2.x = fmaf(sum, v_back[g], l2.x);
+                l2.x = fmaf(sum, info.v_back[4 * half + g], l2.x);
               }
 #pragma unroll
               for (int k = 0; k < 16; ++k) w[k] = pack_f16x2(__uint_as_float(y[2 * k]), __uint_as_float(y[2 * k + 1]));
