@@ -24,6 +24,27 @@ cudaError_t allow_smem(int bytes) {
   return e;
 }
 
+// Launches a kernel behind the stream's work that may start before that is done: it calls prior_done() before
+// it reads or writes memory.  Decode steps are made of kernels of a few microseconds, of which a launch takes
+// two.  These kernels give no early leave themselves: what follows them may read what they write.
+template <typename... P, typename... A>
+cudaError_t launch_behind(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t stream, A&&... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, P(args)...);
+}
+#ifdef __CUDACC__
+__device__ __forceinline__ void prior_done() { asm volatile("griddepcontrol.wait;\n" ::: "memory"); }
+#endif
+
 struct PagePlanParams {
   const int32_t* ctx_len;
   const int32_t* new_len;

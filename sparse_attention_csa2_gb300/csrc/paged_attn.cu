@@ -25,7 +25,10 @@
 // its depth, and no conversion is needed.  V is converted to fp16 (exact), weights are fp16 of
 // exp2(z - max + 11), where the maximum follows a larger score only when that exceeds it by 2^4:
 // weights are at most 2^15, those down to 2^-21 of the largest keep 11 bits, and the output is rarely
-// rescaled.  A page's V scale enters the weight relative to the largest seen.  Maxima, sums and outputs are fp32.
+// rescaled.  A page's V scale enters the weight relative to the largest seen.  Maxima,
+// sums and outputs are fp32.  For fp16 rows, whose outputs round as finely as the weights (2^-11), what the
+// weights' rounding leaves is multiplied too: the error against 64 bits falls from 2.7e-4 to the output's own
+// 2.1e-4, at 5% of the time.
 #include "common.cuh"
 #include "paged.h"
 #include "paged_dev.cuh"
@@ -101,6 +104,8 @@ __global__ void __launch_bounds__(kWarps * 32, 3)
     for (int i = 0; i < kWarps * 2 * ST; ++i) tc05::mbar_init(&full[0][0] + i, 1);
     tc05::fence_barrier_init();
   }
+
+  prior_done();
 
   // ---- this block's piece of the line of units
   long long u, u_end, all;
@@ -425,7 +430,7 @@ __global__ void __launch_bounds__(kWarps * 32, 3)
             acc[i][nb][0] *= o[0], acc[i][nb][1] *= o[1], acc[i][nb][2] *= o[0], acc[i][nb][3] *= o[1];
         }
       }
-      uint32_t pw[2][NB][2];
+      uint32_t pw[2][NB][2], pr[2][NB][F16 ? 2 : 1];  // weights, and (fp16) what their rounding left
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb) {
         const float s0 = m[nb][0] == -INFINITY ? 0.f : kPagedLift - m[nb][0], s1 = m[nb][1] == -INFINITY ? 0.f : kPagedLift - m[nb][1];
@@ -436,7 +441,12 @@ __global__ void __launch_bounds__(kWarps * 32, 3)
           for (int j = 0; j < 2; ++j) {
             const float p0 = ex2(S[h][nb][2 * j] + s0), p1 = ex2(S[h][nb][2 * j + 1] + s1);
             l[nb][0] += p0, l[nb][1] += p1;
-            pw[h][nb][j] = transpose8(pack_f16x2(p0 * cv, p1 * cv));
+            const uint32_t w = pack_f16x2(p0 * cv, p1 * cv);
+            pw[h][nb][j] = transpose8(w);
+            if constexpr (F16) {
+              const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&w));
+              pr[h][nb][j] = transpose8(pack_f16x2(fmaf(p0, cv, -v.x), fmaf(p1, cv, -v.y)));
+            }
           }
         }
       }
@@ -473,7 +483,10 @@ __global__ void __launch_bounds__(kWarps * 32, 3)
           f16_pairs(__byte_perm(w[0][k], w[1][k], sel), a0, a1);
           f16_pairs(__byte_perm(w[2][k], w[3][k], sel), a2, a3);
 #pragma unroll
-          for (int nb = 0; nb < NB; ++nb) mma_f16(acc[i][nb], a0, a1, a2, a3, pw[h][nb][0], pw[h][nb][1]);
+          for (int nb = 0; nb < NB; ++nb) {
+            mma_f16(acc[i][nb], a0, a1, a2, a3, pw[h][nb][0], pw[h][nb][1]);
+            if constexpr (F16) mma_f16(acc[i][nb], a0, a1, a2, a3, pr[h][nb][0], pr[h][nb][1]);
+          }
         }
       }
       __syncwarp();
@@ -565,8 +578,7 @@ cudaError_t launch(const PagedAttnParams& p, int blocks, cudaStream_t stream) {
   if (!make_codes_map(&maps.k, p.k, p, D, 16, swizzle) || !make_codes_map(&maps.v, p.v, p, D, 16, swizzle)) return cudaErrorNotSupported;
   cudaError_t e = allow_smem<paged_attn_kernel<D, NB, PIECES, F16>>(smem);
   if (e != cudaSuccess) return e;
-  paged_attn_kernel<D, NB, PIECES, F16><<<blocks, kWarps * 32, smem, stream>>>(p, maps);
-  e = cudaGetLastError();
+  e = launch_behind(paged_attn_kernel<D, NB, PIECES, F16>, dim3(blocks), kWarps * 32, smem, stream, p, maps);
   return e != cudaSuccess ? e : launch_paged_join(p, D, 8 * NB, blocks, stream);
 }
 

@@ -16,7 +16,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) paged_join_kernel(const Paged
   __shared__ float weight[kJoinWarps][32];
   __shared__ float4 sum[kJoinWarps][D / 4];
   __shared__ float2 stat[kJoinWarps];
-  asm volatile("griddepcontrol.wait;\n" ::: "memory");
+  prior_done();
   const PagedOpen o = p.open[blockIdx.x];
   if (o.pieces == 0) return;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, of_row = warp % WPR;
@@ -84,16 +84,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) paged_join_kernel(const Paged
 template <int D, int ROWS>
 cudaError_t join(const PagedAttnParams& p, int blocks, cudaStream_t stream) {
   constexpr int WPR = ROWS == 256 ? 1 : kJoinWarps;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(blocks, ROWS == 256 ? 32 : ROWS);
-  cfg.blockDim = dim3(kJoinWarps * 32);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, paged_join_kernel<D, ROWS, WPR>, p);
+  return launch_behind(paged_join_kernel<D, ROWS, WPR>, dim3(blocks, ROWS == 256 ? 32 : ROWS), kJoinWarps * 32, 0, stream, p);
 }
 
 }  // namespace

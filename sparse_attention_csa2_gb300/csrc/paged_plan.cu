@@ -25,6 +25,7 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const PagePlanP
   int* page0 = sums + p.n_seq + 1;
   __shared__ unsigned long long warp_sum_s[kPlanThreads / 32];
   const int tid = threadIdx.x;
+  prior_done();
   // a thread sums a run of sequences, the block scans the threads' sums
   const int run = (p.n_seq + kPlanThreads - 1) / kPlanThreads;
   const int b0 = min(tid * run, p.n_seq), b1 = min(b0 + run, p.n_seq);
@@ -201,6 +202,7 @@ __global__ void __launch_bounds__(256) rope_axes_kernel(const __grid_constant__ 
   const long long u = (long long)blockIdx.x * blockDim.x + threadIdx.x;
   const int token = (int)(u / pieces), piece = (int)(u - (long long)token * pieces);
   if (token >= p.n_tokens) return;
+  prior_done();
   const int h0 = blockIdx.y * heads_per, h1 = min(h0 + heads_per, p.n_heads);
   const T* src = static_cast<const T*>(p.x) + token * p.x_row + h0 * p.x_head;
   T* dst = static_cast<T*>(p.out) + token * p.out_row + h0 * p.out_head;
@@ -258,14 +260,9 @@ cudaError_t rope_launch(const RopeAxesParams& p, bool half, bool inv, cudaStream
   while (per > 4 && (long long)blocks * ((p.n_heads + per - 1) / per) < 2432) per = (per + 1) / 2;
   while (per > 1 && (long long)blocks * ((p.n_heads + per - 1) / per) < 608) per = (per + 1) / 2;
   const dim3 grid(blocks, (p.n_heads + per - 1) / per);
-  if (half) {
-    if (inv) rope_axes_kernel<T, true, true><<<grid, 256, 0, stream>>>(p, pieces, turned, per);
-    else rope_axes_kernel<T, true, false><<<grid, 256, 0, stream>>>(p, pieces, turned, per);
-  } else {
-    if (inv) rope_axes_kernel<T, false, true><<<grid, 256, 0, stream>>>(p, pieces, turned, per);
-    else rope_axes_kernel<T, false, false><<<grid, 256, 0, stream>>>(p, pieces, turned, per);
-  }
-  return cudaGetLastError();
+  auto go = [&](auto kernel) { return launch_behind(kernel, grid, 256, 0, stream, p, pieces, turned, per); };
+  if (half) return inv ? go(rope_axes_kernel<T, true, true>) : go(rope_axes_kernel<T, true, false>);
+  return inv ? go(rope_axes_kernel<T, false, true>) : go(rope_axes_kernel<T, false, false>);
 }
 
 }  // namespace
@@ -280,8 +277,7 @@ cudaError_t launch_page_plan(const PagePlanParams& p, cudaStream_t stream) {
   long long blocks = (p.max_rows + per - 1) / per;
   if (blocks > 152) blocks = 152;
   if (blocks < 1) blocks = 1;
-  page_plan_kernel<<<(int)blocks, kPlanThreads, smem, stream>>>(p);
-  return cudaGetLastError();
+  return launch_behind(page_plan_kernel, dim3((unsigned)blocks), kPlanThreads, smem, stream, p);
 }
 
 cudaError_t launch_rope_axes(const RopeAxesParams& p, int dtype, bool half_pairs, bool inverse, cudaStream_t stream) {

@@ -174,6 +174,8 @@ __global__ void __launch_bounds__(kThreads, R == 16 ? 2 : 1)
     tc05::fence_barrier_init();
   }
 
+  prior_done();
+
   // ---- this block's piece of the line of units
   long long all, u, u_end;
   int used;
@@ -634,8 +636,7 @@ cudaError_t launch(const PagedAttnParams& p, int blocks, cudaStream_t stream) {
     return cudaErrorNotSupported;
   const cudaError_t e = allow_smem<paged_rows_kernel<R, PIECES, F16, STAGES>>(smem);
   if (e != cudaSuccess) return e;
-  paged_rows_kernel<R, PIECES, F16, STAGES><<<blocks, kThreads, smem, stream>>>(p, maps);
-  return cudaGetLastError();
+  return launch_behind(paged_rows_kernel<R, PIECES, F16, STAGES>, dim3(blocks), kThreads, smem, stream, p, maps);
 }
 
 }  // namespace

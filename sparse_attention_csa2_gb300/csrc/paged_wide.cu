@@ -131,6 +131,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_wide_kernel(const PagedAttn
     tc05::fence_barrier_init();
   }
 
+  prior_done();
+
   // ---- this block's piece of the line: tiles of the sequences before each (in the space of the tiles),
   // then units of the tiles before each thread's run of tiles
   long long all, u, u_end;
@@ -625,8 +627,7 @@ cudaError_t launch(const PagedAttnParams& p, int blocks, cudaStream_t stream) {
     return cudaErrorNotSupported;
   const cudaError_t e = allow_smem<paged_wide_kernel<D, F16>>(smem);
   if (e != cudaSuccess) return e;
-  paged_wide_kernel<D, F16><<<blocks, kThreads, smem, stream>>>(p, maps);
-  return cudaGetLastError();
+  return launch_behind(paged_wide_kernel<D, F16>, dim3(blocks), kThreads, smem, stream, p, maps);
 }
 
 }  // namespace

@@ -122,6 +122,7 @@ __global__ void __launch_bounds__(kThreads, HELD == 1 ? 6 : 4) page_write_kernel
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int page = 1 << p.page_shift;
   if (tid == 0) count = 0;
+  prior_done();
   __syncthreads();
   const int r0 = blockIdx.x * p.chunk;
   if (HELD == 1) {  // the rows' way from memory overlaps the lookups that say where they go
@@ -278,14 +279,9 @@ cudaError_t write_launch(const PageWriteParams& p, int head_dim, cudaStream_t st
   int y = 1;
   while (y < p.kv_heads && (long long)chunks * y < kBlocksWanted) y = y * 2 < p.kv_heads ? y * 2 : p.kv_heads;
   const dim3 grid(chunks, y);
-  if (p.chunk > 4) {
-    if (head_dim == 128) page_write_kernel<T, 128, 8><<<grid, kThreads, 0, stream>>>(p);
-    else page_write_kernel<T, 64, 8><<<grid, kThreads, 0, stream>>>(p);
-  } else {  // a row or two to a task
-    if (head_dim == 128) page_write_kernel<T, 128, 1><<<grid, kThreads, 0, stream>>>(p);
-    else page_write_kernel<T, 64, 1><<<grid, kThreads, 0, stream>>>(p);
-  }
-  return cudaGetLastError();
+  auto go = [&](auto kernel) { return launch_behind(kernel, grid, kThreads, 0, stream, p); };
+  if (p.chunk > 4) return head_dim == 128 ? go(page_write_kernel<T, 128, 8>) : go(page_write_kernel<T, 64, 8>);
+  return head_dim == 128 ? go(page_write_kernel<T, 128, 1>) : go(page_write_kernel<T, 64, 1>);  // a row or two to a task
 }
 
 }  // namespace
