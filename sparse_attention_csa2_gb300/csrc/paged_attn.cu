@@ -100,10 +100,11 @@ __global__ void __launch_bounds__(kWarps * 32, 3)
   __shared__ long long scan_warp[kWarps];
   __shared__ long long place[2];        // sequence, its first unit
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, c = lane & 3;
-  if (tid == 0) {
-    for (int i = 0; i < kWarps * 2 * ST; ++i) tc05::mbar_init(&full[0][0] + i, 1);
+  if (lane == 0) {  // a warp's barriers are its own
+    for (int i = 0; i < 2 * ST; ++i) tc05::mbar_init(&full[warp][i], 1);
     tc05::fence_barrier_init();
   }
+  __syncwarp();
 
   prior_done();
 
@@ -111,17 +112,32 @@ __global__ void __launch_bounds__(kWarps * 32, 3)
   long long u, u_end, all;
   int b, used;
   long long b_first;
-  {
-    const int run = (p.n_seq + kWarps * 32 - 1) / (kWarps * 32);
-    const int q0 = min(tid * run, p.n_seq), q1 = min(q0 + run, p.n_seq);
-    long long mine = 0;
-    for (int i = q0; i < q1; ++i) mine += seq_of<NR>(p, i).units;
-    long long x = mine;
+  auto share = [&](long long total) {
+    all = total;
+    used = (int)min((long long)gridDim.x, total);  // blocks with work: every one of them has some
+    u = (int)blockIdx.x < used ? div_rarely_long(total * blockIdx.x, used) : 0;
+    u_end = (int)blockIdx.x < used ? div_rarely_long(total * (blockIdx.x + 1), used) : 0;
+  };
+  auto warp_scan = [&](long long x) {  // inclusive sum over the lanes
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const long long y = __shfl_up_sync(0xffffffffu, x, o);
       if (lane >= o) x += y;
     }
+    return x;
+  };
+  if (p.n_seq <= 32) {  // every warp for itself: a sequence a lane
+    const long long mine = lane < p.n_seq ? seq_of<NR>(p, lane).units : 0, x = warp_scan(mine);
+    share(__shfl_sync(0xffffffffu, x, 31));
+    const uint32_t here = __ballot_sync(0xffffffffu, x - mine <= u && u < x);
+    b = here ? __ffs(here) - 1 : 0;
+    b_first = __shfl_sync(0xffffffffu, x - mine, b);
+  } else {
+    const int run = (p.n_seq + kWarps * 32 - 1) / (kWarps * 32);
+    const int q0 = min(tid * run, p.n_seq), q1 = min(q0 + run, p.n_seq);
+    long long mine = 0;
+    for (int i = q0; i < q1; ++i) mine += seq_of<NR>(p, i).units;
+    const long long x = warp_scan(mine);
     if (lane == 31) scan_warp[warp] = x;
     __syncthreads();
     long long before = 0, total = 0;
@@ -131,10 +147,7 @@ __global__ void __launch_bounds__(kWarps * 32, 3)
       total += scan_warp[w];
     }
     before += x - mine;
-    used = (int)min((long long)gridDim.x, total);  // blocks with work: every one of them has some
-    u = (int)blockIdx.x < used ? div_rarely_long(total * blockIdx.x, used) : 0;
-    u_end = (int)blockIdx.x < used ? div_rarely_long(total * (blockIdx.x + 1), used) : 0;
-    all = total;
+    share(total);
     if (u < u_end && before <= u && u < before + mine) {
       long long at = before;
       int i = q0;
@@ -147,12 +160,12 @@ __global__ void __launch_bounds__(kWarps * 32, 3)
       place[1] = at;
     }
     __syncthreads();
-    if (u >= u_end) {
-      if (tid == 0) p.open[blockIdx.x].pieces = 0;
-      return;
-    }
     b = (int)place[0];
     b_first = place[1];
+  }
+  if (u >= u_end) {
+    if (tid == 0) p.open[blockIdx.x].pieces = 0;
+    return;
   }
   uint8_t* ring = smem + warp * 2 * ST * kStage;  // K stages, V stages
   uint32_t phases = 0;                       // bit of each barrier of `full`: parity of its next completion
@@ -174,7 +187,7 @@ __global__ void __launch_bounds__(kWarps * 32, 3)
       u += run;
       continue;
     }
-    const int head = (int)div_rarely_long(item, s.tiles), tile = (int)(item - (long long)head * s.tiles);
+    const int head = s.tiles == 1 ? (int)item : (int)div_rarely_long(item, s.tiles), tile = (int)(item - (long long)head * s.tiles);
     const int row0 = tile * NR, n = min(NR, s.rows - row0);
     const int pos_first = s.ctx + by_group(p, row0), pos_last = s.ctx + by_group(p, row0 + n - 1);
     const int t_begin = s.lo + blk0 * kUnit;
