@@ -206,21 +206,25 @@ __global__ void __launch_bounds__(256) rope_axes_kernel(const __grid_constant__ 
   const int h0 = blockIdx.y * heads_per, h1 = min(h0 + heads_per, p.n_heads);
   const T* src = static_cast<const T*>(p.x) + token * p.x_row + h0 * p.x_head;
   T* dst = static_cast<T*>(p.out) + token * p.out_row + h0 * p.out_head;
-  if (piece >= turned) {  // dims outside the rotary range
-    int d = (piece - turned) * N;
-    if (d >= p.rot_first) d += p.rot_dim;
+  const bool turns = piece < turned;
+  int d0 = p.rot_first + piece * N;
+  if (!turns) {  // dims outside the rotary range
+    d0 = (piece - turned) * N;
+    if (d0 >= p.rot_first) d0 += p.rot_dim;
+  }
+  if (HALF && !turns) {
 #pragma unroll 4
     for (int h = h0; h < h1; ++h, src += p.x_head, dst += p.out_head)
-      __stcs(reinterpret_cast<uint4*>(dst + d), __ldcs(reinterpret_cast<const uint4*>(src + d)));
+      __stcs(reinterpret_cast<uint4*>(dst + d0), __ldcs(reinterpret_cast<const uint4*>(src + d0)));
     return;
   }
-  float c[NP], s[NP];
+  float c[NP] = {}, s[NP] = {};
 #pragma unroll
   for (int k = 0; k < NP; ++k) {
-    turn(p, piece * NP + k, token, c[k], s[k]);
+    if (turns) turn(p, piece * NP + k, token, c[k], s[k]);
     if (INV) s[k] = -s[k];
   }
-  const int d0 = p.rot_first + piece * N, d1 = d0 + p.rot_dim / 2;
+  const int d1 = d0 + p.rot_dim / 2;
 #pragma unroll 4
   for (int h = h0; h < h1; ++h, src += p.x_head, dst += p.out_head) {
     float a[N];
@@ -242,7 +246,7 @@ __global__ void __launch_bounds__(256) rope_axes_kernel(const __grid_constant__ 
         x[2 * k] = a[2 * k] * c[k] - a[2 * k + 1] * s[k];
         x[2 * k + 1] = a[2 * k] * s[k] + a[2 * k + 1] * c[k];
       }
-      __stcs(reinterpret_cast<uint4*>(dst + d0), Vec<T>::put(x));
+      __stcs(reinterpret_cast<uint4*>(dst + d0), turns ? Vec<T>::put(x) : ua);  // one way for both: a warp has both
     }
   }
 }
