@@ -636,7 +636,7 @@ typedef struct {
   int32_t dtype;              /* csa2_type of x and out */
   const void* x;              /* element (t, h, d) at t * x_row + h * x_head + d */
   int64_t x_row, x_head;      /* strides in elements, multiples of 16 bytes */
-  void* out;                  /* likewise; may be x itself with the same strides */
+  void* out;                  /* likewise; x itself with the same strides, or memory apart from x */
   int64_t out_row, out_head;
   const int64_t* pos;         /* [n_axes, n_tokens] */
   int32_t n_axes;             /* 1 .. 16 */

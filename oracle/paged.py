@@ -133,5 +133,5 @@ def paged_attn(q, k_codes, v_codes, k_scale, v_scale, row_start, kv_len, table, 
                 w = e / den[:, None]
                 out[r, h * G:(h + 1) * G] = w @ vv
                 spread[r, h * G:(h + 1) * G] = w @ np.abs(vv)
-                reach[r, h * G:(h + 1) * G] = scale * np.abs(kk).sum(-1).max()
+                reach[r, h * G:(h + 1) * G] = abs(scale) * np.abs(kk).sum(-1).max()
     return out, spread, reach

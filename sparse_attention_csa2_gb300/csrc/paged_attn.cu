@@ -64,7 +64,7 @@ template <int NR>
 __device__ __forceinline__ Seq seq_of(const PagedAttnParams& p, int b) {
   Seq s;
   static_cast<PagedSeq&>(s) = paged_seq<NR>(p, b);
-  s.lo = p.window > 0 ? max(s.ctx - p.window + 1, 0) & (p.page_shift == 4 ? ~15 : ~31) : 0;
+  s.lo = first_seen(p, s.ctx) & (p.page_shift == 4 ? ~15 : ~31);
   s.blocks = max((max(s.kv - s.lo, 0) + kUnit - 1) / kUnit, 1);
   s.units = (long long)s.tiles * p.kv_heads * (s.blocks + kLead);
   return s;
@@ -192,7 +192,7 @@ __global__ void __launch_bounds__(kWarps * 32, 3)
     const int pos_first = s.ctx + by_group(p, row0), pos_last = s.ctx + by_group(p, row0 + n - 1);
     const int t_begin = s.lo + blk0 * kUnit;
     const int t_end = min(min(t_begin + seg * kUnit, s.kv), pos_last + 1);
-    const int lo_last = p.window > 0 ? pos_last - p.window + 1 : 0;
+    const int lo_last = first_seen(p, pos_last);
 
     // ---- loads: page ids one step ahead of the copies, copies up to two steps ahead of their use
     const int32_t* trow = p.table + (long long)b * p.table_cols;

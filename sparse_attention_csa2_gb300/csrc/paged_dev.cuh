@@ -132,6 +132,10 @@ __device__ __forceinline__ void paged_tell(PagedInfo& info, int lane, int id, fl
 __device__ __forceinline__ int by_group(const PagedAttnParams& p, int n) {
   return p.group == 1 ? n : (int)__umul64hi((uint64_t)n, p.group_inv);
 }
+// The first token that a row at a position sees.
+__device__ __forceinline__ int first_seen(const PagedAttnParams& p, int pos) {
+  return p.window > 0 && pos >= p.window ? pos - p.window + 1 : 0;
+}
 // Division of numbers that rarely need 64 bits.
 __device__ __forceinline__ long long div_rarely_long(long long a, int b) {
   return (unsigned long long)a >> 32 ? a / b : (long long)((unsigned)a / (unsigned)b);

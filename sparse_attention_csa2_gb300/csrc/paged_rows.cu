@@ -67,7 +67,7 @@ struct Walk {
   long long u, u_end, first;  // first: the sequence's first unit
   int b, known;               // known: the sequence that the segment holds
   __device__ __forceinline__ static int lo_of(const PagedAttnParams& p, const PagedSeq& s) {  // a page's first token
-    return p.window > 0 ? max(s.ctx - p.window + 1, 0) >> p.page_shift << p.page_shift : 0;
+    return first_seen(p, s.ctx) >> p.page_shift << p.page_shift;
   }
   __device__ __forceinline__ static int blocks_of(const PagedAttnParams& p, const PagedSeq& s) {
     return max((max(s.kv - lo_of(p, s), 0) + kTile - 1) / kTile, 1);
@@ -161,7 +161,6 @@ __global__ void __launch_bounds__(kThreads, R == 16 ? 2 : 1)
   uint8_t* p_tile = q_tile + PIECES * kQ;
   __shared__ Sh sh;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  if (warp == 9) tc05::tmem_alloc(&sh.tmem, kCols);
   if (tid == 0) {
     for (int i = 0; i < STAGES; ++i) {
       tc05::mbar_init(&sh.k_full[i], 1), tc05::mbar_init(&sh.k_free[i], 1);
@@ -175,6 +174,7 @@ __global__ void __launch_bounds__(kThreads, R == 16 ? 2 : 1)
   }
 
   prior_done();
+  if (warp == 9) tc05::tmem_alloc(&sh.tmem, kCols);  // not before: the work before may still want tensor memory
 
   // ---- this block's piece of the line of units
   long long all, u, u_end;
@@ -236,7 +236,7 @@ __global__ void __launch_bounds__(kThreads, R == 16 ? 2 : 1)
       const int units = x.n, hi = x.hi;
       int tok0 = x.lo + x.blk * kTile;
       // every row sees all 128 tokens of a unit that begins in [seen_lo, seen_hi]
-      const int seen_lo = p.window == 0 ? 0 : x.pos_last - p.window + 1, seen_hi = min(x.pos_first, x.hi - 1) - kTile + 1;
+      const int seen_lo = first_seen(p, x.pos_last), seen_hi = min(x.pos_first, x.hi - 1) - kTile + 1;
       const int window = p.window == 0 ? 0x7fffffff : p.window;
       const long long tile_first = walk.tile_first(x);
       if (tid == 0) sh.tile = {x.s.first, x.row0, x.rows, x.head, x.blk, tile_first + x.blocks};

@@ -50,7 +50,7 @@ __device__ __forceinline__ Tile tile_of(const PagedAttnParams& p, const PagedSeq
   g.pos_first = s.ctx + by_group(p, g.row0);
   g.pos_last = s.ctx + by_group(p, g.row0 + g.n - 1);
   g.hi = min(s.kv, g.pos_last + 1);
-  g.lo = p.window > 0 ? max(g.pos_first - p.window + 1, 0) >> p.page_shift << p.page_shift : 0;  // a page's first token
+  g.lo = first_seen(p, g.pos_first) >> p.page_shift << p.page_shift;  // a page's first token
   g.blocks = max((max(g.hi - g.lo, 0) + kTile - 1) / kTile, 1);
   return g;
 }
@@ -117,7 +117,6 @@ __global__ void __launch_bounds__(kThreads, 1) paged_wide_kernel(const PagedAttn
   uint8_t* v_ring = k_ring + KS * kCodes;
   uint8_t* v_tiles = v_ring + VS * kCodes;     // fp16, two
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  if (warp == 12) tc05::tmem_alloc(&sh.tmem, 512);
   if (tid == 0) {
     for (int i = 0; i < KS; ++i) tc05::mbar_init(&sh.k_full[i], 1), tc05::mbar_init(&sh.k_free[i], 1);
     for (int i = 0; i < VS; ++i) tc05::mbar_init(&sh.r_full[i], 1), tc05::mbar_init(&sh.r_free[i], 128);
@@ -132,6 +131,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_wide_kernel(const PagedAttn
   }
 
   prior_done();
+  if (warp == 12) tc05::tmem_alloc(&sh.tmem, 512);  // not before: the work before may still want tensor memory
 
   // ---- this block's piece of the line: tiles of the sequences before each (in the space of the tiles),
   // then units of the tiles before each thread's run of tiles
@@ -285,7 +285,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_wide_kernel(const PagedAttn
       const float f = sh.factor[warp][lane];
       float m = -INFINITY, v_ref = 0.f;
       float2 l2 = make_float2(0.f, 0.f);
-      const int see_hi = min(pos + 1, x.g.hi), see_lo = p.window > 0 ? pos - p.window + 1 : 0;
+      const int see_hi = min(pos + 1, x.g.hi), see_lo = first_seen(p, pos);
       for (int j = 0; j < x.n && !dead; ++j, ++count, ++turn) {
         const int tok = x.g.lo + (x.blk + j) * kTile;
         const PagedInfo& info = sh.info[count % kInfos];

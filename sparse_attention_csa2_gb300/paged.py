@@ -209,6 +209,8 @@ class RopeAxes(_Prepared):
             out = torch.empty((T, H, D), dtype=x.dtype, device=dev)
         if out.shape != x.shape or out.dtype != x.dtype:
             raise ValueError("out must have x's shape and type")
+        if any(n > 1 and t == 0 for n, t in zip(out.shape, out.stride())):
+            raise ValueError("out must not be a broadcast tensor")
         self.out = out
         a.out, a.out_row, a.out_head = _heads(out, "out", dev)
         a.n_tokens, a.n_heads, a.head_dim, a.dtype, a.n_axes = T, H, D, _TYPES[x.dtype], pos.shape[0]

@@ -345,6 +345,67 @@ def test_paged_attn_leaves_rows_behind_the_last_and_takes_strided_queries():
         assert torch.equal(S.paged_attn(dev[:, 2:10], *args)[: c["rows"]], dense)
 
 
+@pytest.mark.parametrize("batch", ["decode", "drafts", "prompts", "shorter"])
+@pytest.mark.parametrize("G", [2, 12])
+def test_paged_attn_scales_and_windows_at_their_ends(batch, G):
+    """A softmax scale of 0 weighs all visible keys alike, a negative one turns the order; the largest window
+    is none, also for sequences with fewer tokens than queries."""
+    c = make(*BATCHES[batch], 16, 2, 128, seed=21)
+    for scale in (0.0, -0.1):
+        got, ref, tol = _attend(c, 2 * G, "bf16", scale=scale)
+        assert np.all(np.abs(got - ref[0]) <= tol)
+    plain, _, _ = _attend(c, 2 * G, "bf16")
+    wide, _, _ = _attend(c, 2 * G, "bf16", window=2 ** 31 - 1)
+    assert np.array_equal(plain, wide)
+
+
+@pytest.mark.parametrize("batch", ["decode", "drafts", "prompts"])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+def test_paged_attn_query_that_is_not_finite_spoils_its_own_row(batch, D, bad):
+    c = make(*BATCHES[batch], 32, 2, D, seed=22)
+    T = c["rows"]
+    q, _ = values((T, 8, D), np.random.default_rng(3), "bf16")
+    cache = S.PageCache(cuda(c["k"]), cuda(c["v"]), cuda(c["ks"]), cuda(c["vs"]))
+    args = (cache, cuda(c["row_start"]), cuda(c["kv"]), cuda(c["table"]), D ** -0.5)
+    clean = S.paged_attn(q.cuda(), *args)
+    r, h = T // 2, 5
+    q[r, h, 7] = bad
+    got = S.paged_attn(q.cuda(), *args)
+    assert bool(torch.isnan(got[r, h]).all())
+    got[r, h] = clean[r, h]
+    assert torch.equal(got, clean)
+
+
+def test_paged_attn_between_other_kernels_of_the_framework():
+    """Behind and before projections, whose kernels hold tensor memory and let the next kernel start early:
+    every form of the attention in turn, on two streams at once."""
+    cases = [make(*BATCHES[b], 64, 2, 128, seed=23) for b in ("decode", "drafts", "prompts")]
+    rng = np.random.default_rng(4)
+    x, _ = values((32, 512), rng, "bf16")
+    w, _ = values((1024, 512), rng, "bf16")
+    x, w = x.cuda(), w.cuda()
+    calls = []
+    for c in cases:
+        q, _ = values((c["rows"], 8, 128), rng, "bf16")
+        cache = S.PageCache(cuda(c["k"]), cuda(c["v"]), cuda(c["ks"]), cuda(c["vs"]))
+        calls.append((q.cuda(), cache, cuda(c["row_start"]), cuda(c["kv"]), cuda(c["table"]), 128 ** -0.5))
+    want_y = S.linear(x, w)
+    want = [S.paged_attn(*a) for a in calls]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = []
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(s):
+            for _ in range(20):
+                for a in calls:
+                    got.append((S.linear(x, w), S.paged_attn(*a)))
+    torch.cuda.synchronize()
+    for i, (y, o) in enumerate(got):
+        assert torch.equal(y, want_y) and torch.equal(o, want[i % 3])
+
+
 # ------------------------------------------------------------------ together
 @pytest.mark.parametrize("D,G", [(128, 4), (64, 9)])
 def test_serving_steps(D, G):
