@@ -25,7 +25,7 @@ cudaError_t allow_smem(int bytes) {
 }
 
 // Launches a kernel behind the stream's work that may start before that is done: it calls prior_done() before
-// it reads or writes memory.  Decode steps are made of kernels of a few microseconds, of which a launch takes
+// it reads or writes memory, and reads nothing by the non-coherent path, whose loads may move ahead of it.  Decode steps are made of kernels of a few microseconds, of which a launch takes
 // two.  These kernels give no early leave themselves: what follows them may read what they write.
 template <typename... P, typename... A>
 cudaError_t launch_behind(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t stream, A&&... args) {
@@ -44,6 +44,10 @@ cudaError_t launch_behind(void (*kernel)(P...), dim3 grid, int threads, size_t s
 #ifdef __CUDACC__
 __device__ __forceinline__ void prior_done() { asm volatile("griddepcontrol.wait;\n" ::: "memory"); }
 #endif
+
+// Places of a sequence's tokens that the attention computes with stay below the largest int: a table has no more
+// columns, and what a length says beyond is cut.
+constexpr int kPagedMostTokens = 0x7fffffff - 8192;
 
 struct PagePlanParams {
   const int32_t* ctx_len;

@@ -79,7 +79,7 @@ csa2_status check_attn_sizes(const csa2_paged_attn_args* a) {
     return CSA2_EINVAL;
   if ((a->head_dim != 64 && a->head_dim != 128) || !page_shift(a->page_size)) return CSA2_EUNSUPPORTED;
   if ((long long)a->n_rows * (a->heads / a->kv_heads) > 0x7fffffffLL - 1024 ||
-      (long long)a->table_cols * a->page_size > 0x7fffffffLL - 1024 ||
+      (long long)a->table_cols * a->page_size > kPagedMostTokens ||
       (long long)a->n_pages * a->kv_heads > 0x7fffffffLL)
     return CSA2_EUNSUPPORTED;
   return CSA2_OK;

@@ -199,7 +199,7 @@ __global__ void __launch_bounds__(kWarps * 32, 3)
     const int page_mask = (1 << p.page_shift) - 1;
     auto page_id = [&](int tok) -> int {  // -1: no such token, -2: a bad entry
       if (tok >= t_end) return -1;
-      const int id = __ldg(trow + (tok >> p.page_shift));
+      const int id = trow[tok >> p.page_shift];
       return (unsigned)id < (unsigned)p.n_pages ? id : -2;
     };
     auto second_id = [&](int tok, int id0) -> int {  // pages of 32 tokens and more hold a whole step

@@ -155,10 +155,9 @@ __device__ __forceinline__ PagedSeq paged_seq(const PagedAttnParams& p, int b) {
   s.index = b;
   s.first = min(max(r0, 0), p.n_rows);
   const int n = max(min(r1, p.n_rows) - s.first, 0);
-  const long long cap = (long long)p.table_cols << p.page_shift;
-  const int kv = max(p.kv_len[b], 0);
-  s.ctx = kv - (r1 - r0);
-  s.kv = (int)min((long long)kv, cap);
+  const int kv = min(max(p.kv_len[b], 0), kPagedMostTokens);
+  s.ctx = n > 0 ? kv - (r1 - s.first) : 0;
+  s.kv = min(kv, p.table_cols << p.page_shift);
   s.rows = n * p.group;
   s.tiles = (s.rows + NR - 1) / NR;
   return s;

@@ -17,59 +17,66 @@ namespace {
 constexpr int kPlanThreads = 512;
 constexpr int kPlanRows = 4;  // consecutive rows of a thread: one search, 16-byte stores
 
+constexpr int kMostTokens = 1 << 30;  // of a sequence, cached and new: their sum and a row's position fit an int
+constexpr unsigned kMostSum = 0x7fffffffu;
+
+// A sum that stays at the largest int: lengths that have it are reported, and the table and rows below stay in
+// their bounds.
+__device__ __forceinline__ unsigned sum_of(unsigned a, unsigned b) { return min(a + b, kMostSum); }
+__device__ __forceinline__ int cached(const PagePlanParams& p, int b) { return min(max(p.ctx_len[b], 0), kMostTokens); }
 __device__ __forceinline__ int pages_of(int tokens, int page) { return (int)(((unsigned)tokens + page - 1) / (unsigned)page); }
 
 __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const PagePlanParams p) {
   extern __shared__ int sums[];  // [n_seq + 1] first rows, [n_seq + 1] first new pages
   int* row0 = sums;
   int* page0 = sums + p.n_seq + 1;
-  __shared__ unsigned long long warp_sum_s[kPlanThreads / 32];
+  __shared__ uint2 warp_sum_s[kPlanThreads / 32];
   const int tid = threadIdx.x;
   prior_done();
   // a thread sums a run of sequences, the block scans the threads' sums
   const int run = (p.n_seq + kPlanThreads - 1) / kPlanThreads;
   const int b0 = min(tid * run, p.n_seq), b1 = min(b0 + run, p.n_seq);
-  int rows = 0, need = 0;
+  bool bad = false;
+  unsigned rows = 0, need = 0;
   for (int b = b0; b < b1; ++b) {
-    const int c = max(p.ctx_len[b], 0), n = max(p.new_len[b], 0);
-    row0[b] = rows;
-    page0[b] = need;
-    rows += n;
-    need += pages_of(c + n, p.page_size) - pages_of(c, p.page_size);
+    const int c = cached(p, b), n = min(max(p.new_len[b], 0), kMostTokens - 1);
+    bad |= p.ctx_len[b] > kMostTokens || p.new_len[b] >= kMostTokens;
+    row0[b] = (int)rows;
+    page0[b] = (int)need;
+    rows = sum_of(rows, n);
+    need = sum_of(need, pages_of(c + n, p.page_size) - pages_of(c, p.page_size));
   }
-  // both sums in one scan, a half of 64 bits each (both below 2^31: no carry between them)
-  unsigned long long x = (unsigned long long)(unsigned)rows << 32 | (unsigned)need;
-  const unsigned long long own = x;
   const int lane = tid & 31, warp = tid >> 5;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const unsigned long long y = __shfl_up_sync(0xffffffffu, x, o);
-    if (lane >= o) x += y;
+    const unsigned y = __shfl_up_sync(0xffffffffu, rows, o), z = __shfl_up_sync(0xffffffffu, need, o);
+    if (lane >= o) rows = sum_of(rows, y), need = sum_of(need, z);
   }
-  if (lane == 31) warp_sum_s[warp] = x;
+  if (lane == 31) warp_sum_s[warp] = make_uint2(rows, need);
+  rows = __shfl_up_sync(0xffffffffu, rows, 1), need = __shfl_up_sync(0xffffffffu, need, 1);
+  if (lane == 0) rows = need = 0;
   __syncthreads();
-  unsigned long long before = 0, total = 0;
+  uint2 before = make_uint2(0, 0), total = make_uint2(0, 0);
 #pragma unroll
   for (int w = 0; w < kPlanThreads / 32; ++w) {
-    if (w < warp) before += warp_sum_s[w];
-    total += warp_sum_s[w];
+    const uint2 of = warp_sum_s[w];
+    if (w < warp) before = make_uint2(sum_of(before.x, of.x), sum_of(before.y, of.y));
+    total = make_uint2(sum_of(total.x, of.x), sum_of(total.y, of.y));
   }
-  before += x - own;
-  const int total_rows = (int)(total >> 32), total_need = (int)(unsigned)total;
-  const int first_row = (int)(before >> 32), first_need = (int)(unsigned)before;
+  const int total_rows = (int)total.x, total_need = (int)total.y;
+  const unsigned first_row = sum_of(before.x, rows), first_need = sum_of(before.y, need);
   for (int b = b0; b < b1; ++b) {
-    row0[b] += first_row;
-    page0[b] += first_need;
+    row0[b] = (int)sum_of(row0[b], first_row);
+    page0[b] = (int)sum_of(page0[b], first_need);
   }
   if (tid == 0) row0[p.n_seq] = total_rows, page0[p.n_seq] = total_need;
   __syncthreads();
 
-  bool bad = false;
   const int at = blockIdx.x * kPlanThreads + tid, all = gridDim.x * kPlanThreads;
   for (int b = at; b <= p.n_seq; b += all) {
     p.row_start[b] = row0[b];
     if (b < p.n_seq) {
-      const int c = max(p.ctx_len[b], 0), kv = c + row0[b + 1] - row0[b];
+      const int c = cached(p, b), kv = c + row0[b + 1] - row0[b];
       p.kv_len[b] = kv;
       bad |= pages_of(kv, p.page_size) > p.table_cols;
     }
@@ -79,13 +86,14 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const PagePlanP
     bad |= total_need > p.n_free || total_rows > p.max_rows;
   }
   // the new pages' table entries
-  for (int f = at; f < total_need; f += all) {
+  for (unsigned u = at; u < (unsigned)total_need; u += all) {
+    const int f = (int)u;
     int lo = 0, hi = p.n_seq;  // page0[lo] <= f < page0[hi]
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
       if (page0[mid] <= f) lo = mid; else hi = mid;
     }
-    const int col = pages_of(max(p.ctx_len[lo], 0), p.page_size) + f - page0[lo];
+    const int col = pages_of(cached(p, lo), p.page_size) + f - page0[lo];
     if (col < p.table_cols) p.table[(long long)lo * p.table_cols + col] = f < p.n_free ? p.free_pages[f] : -1;
   }
   // rows
@@ -105,7 +113,7 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const PagePlanP
       if (r + k >= total_rows) continue;
       while (row0[b + 1] <= r + k) ++b;  // empty sequences too
       if (b != known) {
-        c = max(p.ctx_len[b], 0);
+        c = cached(p, b);
         held = pages_of(c, p.page_size);
         known = b;
       }
@@ -189,7 +197,7 @@ struct Vec<float> {
 
 // Sine and cosine of pair i's angle at a position.
 __device__ __forceinline__ void turn(const RopeAxesParams& p, int i, int token, float& c, float& s) {
-  const int64_t at = __ldg(p.pos + (long long)p.axis[i] * p.n_tokens + token);
+  const int64_t at = p.pos[(long long)p.axis[i] * p.n_tokens + token];
   const int32_t frac = (int32_t)(((uint64_t)at * p.turns[i] + 0x80000000ull) >> 32);  // of a turn, nearest 2^-32
   sincospif((float)frac * 4.656612873077393e-10f, &s, &c);                            // 2^-31: half turns
 }

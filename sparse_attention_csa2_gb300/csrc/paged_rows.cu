@@ -537,7 +537,7 @@ __global__ void __launch_bounds__(kThreads, R == 16 ? 2 : 1)
       auto ids = [&](int j) {
         const int tok = x.lo + (x.blk + j) * kTile + 16 * (lane & 7);
         if (j >= x.n || tok >= x.hi) return -1;
-        const int id = __ldg(trow + (tok >> p.page_shift));
+        const int id = trow[tok >> p.page_shift];
         return (unsigned)id < (unsigned)p.n_pages ? id : -2;
       };
       int id = ids(0);
@@ -546,7 +546,7 @@ __global__ void __launch_bounds__(kThreads, R == 16 ? 2 : 1)
         const int stage = count % STAGES;
         const uint32_t parity = (count / STAGES & 1) ^ 1;
         const long long slab = id >= 0 ? (long long)id * p.kv_heads + x.head : 0;
-        const float sk = id >= 0 ? __ldg(p.k_scale + slab) : 0.f, sv = id >= 0 ? __ldg(p.v_scale + slab) : 0.f;
+        const float sk = id >= 0 ? p.k_scale[slab] : 0.f, sv = id >= 0 ? p.v_scale[slab] : 0.f;
         bad |= id == -2;
         // a lane whose 16 tokens begin a page (or, in pages of 128, the unit) copies it
         const bool copies = lane < 8 && id >= 0 && (16 * lane & mask & (kTile - 1)) == 0;

@@ -499,14 +499,14 @@ __global__ void __launch_bounds__(kThreads, 1) paged_wide_kernel(const PagedAttn
         auto ids = [&](int j) {
           const int tok = x.g.lo + (x.blk + j) * kTile + 16 * (lane & 7);
           if (j >= x.n || tok >= x.g.hi) return -1;
-          const int id = __ldg(trow + (tok >> p.page_shift));
+          const int id = trow[tok >> p.page_shift];
           return (unsigned)id < (unsigned)p.n_pages ? id : -2;
         };
         int id = ids(0);
         for (int j = 0; j < x.n && !dead; ++j, ++count) {
           const int id_next = ids(j + 1);
           const long long slab = id >= 0 ? (long long)id * p.kv_heads + x.h : 0;
-          const float sk = id >= 0 ? __ldg(p.k_scale + slab) : 0.f, sv = id >= 0 ? __ldg(p.v_scale + slab) : 0.f;
+          const float sk = id >= 0 ? p.k_scale[slab] : 0.f, sv = id >= 0 ? p.v_scale[slab] : 0.f;
           bad |= id == -2;
           // a lane whose 16 tokens begin a page (or, in pages of 128, the unit) copies it
           const bool copies = lane < 8 && id >= 0 && (16 * lane & mask & (kTile - 1)) == 0;

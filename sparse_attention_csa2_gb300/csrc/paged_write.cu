@@ -174,7 +174,7 @@ __global__ void __launch_bounds__(kThreads, HELD == 1 ? 6 : 4) page_write_kernel
     const int row0 = gt / PR, rows_at_once = gn / PR;
     const T* from = src + row0 * p.x_row[kv] + gt % PR * N;
     const long long step = rows_at_once * p.x_row[kv];
-    auto piece = [&](const T* at) { return __ldg(reinterpret_cast<const uint4*>(at)); };
+    auto piece = [&](const T* at) { return *reinterpret_cast<const uint4*>(at); };
     auto group_sync = [&]() {
       if (wpt > 1) asm volatile("bar.sync %0, %1;\n" ::"r"(1 + group), "r"(gn) : "memory");
       else __syncwarp();

@@ -77,6 +77,25 @@ def test_page_plan_without_sequences_and_with_negative_lengths():
     assert p.kv_len.tolist() == [2, 4] and p.seq_of_row.tolist() == [0, 0, -1]
 
 
+def test_page_plan_lengths_beyond_an_int_stay_in_bounds_and_are_reported():
+    """2^30 cached and as many new tokens are the most of a sequence; sums stay at the largest int."""
+    top = 2 ** 31 - 1
+    ctx, new = np.array([top, 7, 5, 3], np.int32), np.array([9, top, top, 1], np.int32)
+    whole, st = np.arange(-100, 116, dtype=np.int32).reshape(54, 4), _status()
+    t = cuda(whole)
+    p = S.page_plan(cuda(ctx), cuda(new), t[25:29], cuda(np.array([500, 501, 502], np.int32)), 16, 60, dev_status=st)
+    assert S.read_device_status(st) == S.EDEVICE_INDEX
+    want = whole.copy()
+    want[26, 1:], want[27, 1:], want[28, 1:] = [501, 502, -1], -1, whole[28, 1:]
+    assert _same(t, want)
+    assert p.row_start.tolist() == [0, 9, 9 + 2 ** 30 - 1, top, top]
+    assert p.kv_len.tolist() == [2 ** 30 + 9, 2 ** 30 + 6, 2 ** 30 - 4, 3]
+    assert p.seq_of_row.tolist() == [0] * 9 + [1] * 51
+    assert p.pos.tolist() == list(range(2 ** 30, 2 ** 30 + 9)) + list(range(7, 58))
+    pages = [whole[26, 0], 501, 502, -1]
+    assert p.slot.tolist() == [-1] * 9 + [pages[i // 16] * 16 + i % 16 if pages[i // 16] >= 0 else -1 for i in range(7, 58)]
+
+
 # ------------------------------------------------------------------ rotary axes
 @pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
 @pytest.mark.parametrize("half", [True, False])
@@ -328,6 +347,25 @@ def test_paged_attn_bad_pages_and_lengths_are_hidden_and_reported():
     kv[0] = c["table"].shape[1] * 16 + 50
     S.paged_attn(q.cuda(), cache, cuda(c["row_start"]), cuda(kv), cuda(c["table"]), 0.125, dev_status=st)
     torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("batch", ["decode", "drafts", "prompts"])
+@pytest.mark.parametrize("D", [64, 128])
+def test_paged_attn_lengths_beyond_every_table(batch, D):
+    """A length at the largest int: the rows' places lie behind the table's tokens, all of which they see without a
+    window, none with one."""
+    c = make(*BATCHES[batch], 16, 2, D, seed=24)
+    q, _ = values((c["rows"], 8, D), np.random.default_rng(5), "bf16")
+    cache = S.PageCache(cuda(c["k"]), cuda(c["v"]), cuda(c["ks"]), cuda(c["vs"]))
+    long = torch.full((len(c["kv"]),), 2 ** 31 - 1, dtype=torch.int32, device="cuda")
+    out = torch.zeros(q.shape, dtype=torch.float32, device="cuda")
+    got = S.paged_attn(q.cuda(), cache, cuda(c["row_start"]), long, cuda(c["table"]), D ** -0.5, window=4000, out=out)
+    assert not bool(got.any())
+    table = cuda(np.zeros_like(c["table"]))  # page 0 all along
+    full = torch.full_like(long, 16 * table.shape[1] + 10 ** 6)
+    a = S.paged_attn(q.cuda(), cache, cuda(c["row_start"]), long, table, D ** -0.5)
+    b = S.paged_attn(q.cuda(), cache, cuda(c["row_start"]), full, table, D ** -0.5)
+    assert torch.equal(a, b) and bool(torch.isfinite(a.float()).all())
 
 
 def test_paged_attn_leaves_rows_behind_the_last_and_takes_strided_queries():
