@@ -598,11 +598,12 @@ typedef enum csa2_type { CSA2_T_BF16 = 0, CSA2_T_F16 = 1, CSA2_T_F32 = 2 } csa2_
  *   slot[r]       = table[b, pos / page] * page + pos % page       (csa2_write_records' dst_row)
  * Rows behind the last sequence get -1 in all three.  Where free_pages or table_cols do not
  * suffice, the missing entries and slots are -1; where rows exceed max_rows, the rest are left
- * out; both, and a negative entry among a sequence's cached pages, are reported as
- * CSA2_EDEVICE_INDEX through dev_status.  Running a plan again on its own table repeats it. */
+ * out; both, a negative entry among a sequence's cached pages, and lengths above 2^30 (a
+ * sequence's most, cached and new) or whose sums reach 2^31 are reported as CSA2_EDEVICE_INDEX
+ * through dev_status.  Running a plan again on its own table repeats it. */
 typedef struct {
   const int32_t* ctx_len;     /* [n_seq] */
-  const int32_t* new_len;     /* [n_seq] (sums below 2^31) */
+  const int32_t* new_len;     /* [n_seq] */
   int32_t n_seq;              /* 0 .. 8192 */
   int32_t page_size;          /* 1 .. 65536 */
   int32_t* table;             /* in / out [n_seq, table_cols] */

@@ -84,6 +84,14 @@ def _on(t, name, device=None):
     return t.data_ptr()
 
 
+def _int(v, name):
+    """A number that the C struct holds whole."""
+    v = int(v)
+    if not 0 <= v < 2 ** 31:
+        raise ValueError(f"{name} must be at least 0 and below 2^31, got {v}")
+    return v
+
+
 def _heads(t, name, device=None):
     """Address and strides of a [rows, heads, dim] tensor whose last dimension is dense."""
     if t.dim() != 3:
@@ -147,10 +155,8 @@ class PagePlan(_Prepared):
             raise ValueError("table must be [sequences, columns]")
         a.table = _dense(table, "table", torch.int32, (n, table.shape[1]), dev)
         a.free_pages = _dense(free_pages, "free_pages", torch.int32, (free_pages.numel(),), dev)
-        a.n_seq, a.page_size, a.table_cols = n, int(page_size), table.shape[1]
-        a.n_free, a.max_rows = free_pages.numel(), int(max_rows)
-        if max_rows < 0:
-            raise ValueError("max_rows must not be negative")
+        a.n_seq, a.page_size, a.table_cols = n, _int(page_size, "page_size"), table.shape[1]
+        a.n_free, a.max_rows = free_pages.numel(), _int(max_rows, "max_rows")
         self.table = table
         self.row_start = torch.empty(n + 1, dtype=torch.int32, device=dev)
         self.kv_len = torch.empty(n, dtype=torch.int32, device=dev)
@@ -214,7 +220,7 @@ class RopeAxes(_Prepared):
         self.out = out
         a.out, a.out_row, a.out_head = _heads(out, "out", dev)
         a.n_tokens, a.n_heads, a.head_dim, a.dtype, a.n_axes = T, H, D, _TYPES[x.dtype], pos.shape[0]
-        a.rot_first, a.rot_dim, a.half_pairs, a.inverse = int(rot_first), R, pairing == "half", bool(inverse)
+        a.rot_first, a.rot_dim, a.half_pairs, a.inverse = _int(rot_first, "rot_first"), R, pairing == "half", bool(inverse)
         a.theta = float(theta)
         a.axis_of_pair[:R // 2] = list(axis_of_pair)
         self._bind(_rope_axes, a, dev, (out,), (x, pos))
@@ -318,7 +324,7 @@ class PagedAttn(_Prepared):
         a.out = _dense(out, "out", out.dtype, q.shape, dev)
         a.sink = None if sink is None else _dense(sink, "sink", torch.float32, (q.shape[1],), dev)
         a.n_rows, a.heads, a.q_dtype, a.out_dtype = q.shape[0], q.shape[1], _TYPES[q.dtype], _TYPES[out.dtype]
-        a.softmax_scale, a.window = float(softmax_scale), int(window)
+        a.softmax_scale, a.window = float(softmax_scale), _int(window, "window")
         a.dev_status = None if dev_status is None else _dense(dev_status, "dev_status", torch.int32, (1,), dev)
         self._wsp, a.workspace_bytes = _ws(int(_paged_attn_ws(C.byref(a))), dev)
         a.workspace = None if self._wsp is None else self._wsp.data_ptr()

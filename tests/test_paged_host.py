@@ -92,6 +92,13 @@ def test_python_calls_refuse_cpu_tensors_and_wrong_shapes():
 
 
 # ------------------------------------------------------------------ the oracle's pins
+@pytest.mark.parametrize("v", [-1, 2 ** 31, 2 ** 32, 2 ** 32 + 16])
+def test_python_calls_refuse_numbers_that_the_struct_would_cut(v):
+    with pytest.raises(ValueError):
+        P._int(v, "window")
+    assert P._int(2 ** 31 - 1, "window") == 2 ** 31 - 1
+
+
 def test_oracle_e4m3_rounding_matches_torch():
     rng = np.random.default_rng(0)
     x = np.concatenate([rng.standard_normal(4000) * np.exp2(rng.integers(-12, 9, 4000)), OP.e4m3_values()[:127],
