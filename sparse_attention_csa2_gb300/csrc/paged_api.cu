@@ -38,7 +38,7 @@ const uint64_t* rope_turns(float theta, int rot_dim) {
 }
 
 // Which kernel, and its workspace, by the query rows per sequence and kv head in the mean.
-//   up to 8      paged_attn.cu's tiles of 8, three blocks per SM
+//   up to 8      paged_attn.cu's tiles of 8, three blocks per SM (four at dim 64)
 //   up to 32     at dim 64 its tiles of 16 (64 sequences x 4 heads x 1,000 tokens, 16 / 32 rows: 25 / 36 us against
 //                30 / 48 by paged_rows.cu's form; of 16,000 tokens, 32 sequences: 80 / 146 against 76 / 139);
 //                at dim 128 paged_rows.cu's tiles of 16 (two blocks per SM) or 32 (one): 33 / 52 us against 40 / 59
@@ -61,7 +61,7 @@ AttnPlan attn_plan(const csa2_paged_attn_args* a) {
   if (pl.rows == 256 && a->n_seq > 16384) pl.rows = a->head_dim == 64 ? 16 : 32;  // its sequences' tiles fit shared memory
   const long long tiles = (rows + pl.rows - 1) / pl.rows + a->n_seq;
   const long long units = ((long long)a->table_cols * a->page_size + 127) / 128 + 1;
-  const long long most = (pl.rows == 256 ? 1 : a->head_dim == 64 || pl.rows == 8 ? 3 : pl.rows == 16 ? 2 : 1) * device_sm_count();
+  const long long most = (pl.rows == 256 ? 1 : pl.rows == 8 ? (a->head_dim == 64 ? 4 : 3) : a->head_dim == 64 ? 3 : pl.rows == 16 ? 2 : 1) * device_sm_count();
   const double all = (double)tiles * a->kv_heads * units;
   pl.blocks = all < (double)most ? (int)all : (int)most;
   size_t at = 0;

@@ -18,11 +18,12 @@
 // until the tile's end) and keeps its own running maximum, sum and output.
 //
 // Arithmetic.  Tokens are the MMAs' rows and query rows their columns, eight to a column block, so that
-// the few query rows of a decode step fill the tensor cores' shape.  K stays in its 8 bits: a query
-// row, scaled by a power of two to a maximum in [224, 448), is split into E4M3 pieces (two hold a
-// bf16's 8 bits, three an fp16's 11, to 2^-10 absolute), and the scores are the sum of the pieces'
-// E4M3 products in fp32: mma.m16n8k32 runs at twice the fp16 form's rate per instruction with twice
-// its depth, and no conversion is needed.  V is converted to fp16 (exact), weights are fp16 of
+// the few query rows of a decode step fill the tensor cores' shape.  Codes are converted to fp16 (exact).
+// A query row is scaled by a power of two to a maximum in [2^14, 2^15): as fp16 its values keep all their
+// bits down to 2^-29 of that, and products are summed in fp32.  (K left in its 8 bits against rows as two or
+// three E4M3 pieces took more instructions, not fewer: an E4M3 mma.sync counts as two fp16 ones with the
+// conversions of both operands and four additions.  Per 32 tokens of 16 rows at dim 64, fp16: 808 against 614;
+// 96 sequences of 5 drafted tokens each, window 1,024: 74 against 60 us.)  Weights are fp16 of
 // exp2(z - max + 11), where the maximum follows a larger score only when that exceeds it by 2^4:
 // weights are at most 2^15, those down to 2^-21 of the largest keep 11 bits, and the output is rarely
 // rescaled.  A page's V scale enters the weight relative to the largest seen.  Maxima,
@@ -42,19 +43,6 @@ constexpr int kTok = 32;                // tokens of a warp's step
 constexpr int kUnit = kWarps * kTok;    // tokens of a unit
 constexpr int kLead = 4;                // units that a tile's beginning and end take: each tile lies on the line
                                         // behind so many empty ones
-__device__ __forceinline__ void mma_e4m3(float* c, const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
-      "{%0,%1,%2,%3};\n"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-__device__ __forceinline__ uint32_t e4m3_pair(float lo, float hi) {
-  uint16_t r;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;\n" : "=h"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-
 // A sequence with its units.
 struct Seq : PagedSeq {
   int lo, blocks;      // first token any row sees, down to a step within its page; units of a tile
@@ -76,26 +64,24 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t v) {
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;\n" : "=r"(r) : "r"(v));
   return r;
 }
-// Stages of the ring: 64 KB a block.
-template <int D>
-constexpr int kStages = 256 / D;
+// Stages of the ring: 64 KB a block, 48 KB where four blocks share an SM (dim 64 and 8 rows: 32 sequences of
+// 16,384 tokens in the mean with 8 heads 414 -> 380 us by the fourth block; with 16 rows its registers spill).
+template <int D, int NB>
+constexpr int kStages = D == 128 ? 2 : NB == 1 ? 3 : 4;
 
-template <int D, int NB, int PIECES, bool F16>
-__global__ void __launch_bounds__(kWarps * 32, 3)
+template <int D, int NB, bool F16>
+__global__ void __launch_bounds__(kWarps * 32, D == 64 && NB == 1 ? 4 : 3)
     paged_attn_kernel(const PagedAttnParams p, const __grid_constant__ CopyMaps maps) {
   constexpr int NR = 8 * NB;            // query rows of a tile
-  constexpr int KS = D / 32;            // MMA steps of a score
+  constexpr int KS = D / 16;            // MMA steps of a score
   constexpr int MT = D / 16;            // MMA rows of an output, in sixteens
   constexpr int kStage = kTok * D;      // bytes of K (or V) of a step
   constexpr int kHalf = kStage / 2;     // of 16 tokens: a copy
-  constexpr int ST = kStages<D>;
-  constexpr bool QS = NB > 1;           // the query pieces lie in shared memory: two column blocks of them
-                                        // and of outputs do not fit the registers of three blocks per SM
+  constexpr int ST = kStages<D, NB>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   __shared__ __align__(16) float scales[kWarps][ST][4];
   __shared__ __align__(8) uint64_t full[kWarps][2 * ST];  // K stages, V stages
-  __shared__ __align__(16) uint2 qs[QS ? NB * PIECES * KS * 32 : 1];
   __shared__ float ml[kWarps][NR][3];
   __shared__ long long scan_warp[kWarps];
   __shared__ long long place[2];        // sequence, its first unit
@@ -274,68 +260,43 @@ __global__ void __launch_bounds__(kWarps * 32, 3)
       }
     }
 
-    // ---- the query rows as E4M3 pieces: this thread's dims are D/4 * c .. of rows 8 nb + g
-    uint32_t qb[QS ? 1 : NB][PIECES][KS][2];
+    // ---- the query rows as fp16: this thread's dims are D/4 * c .. of rows 8 nb + g
+    uint32_t qb[NB][KS][2];
     float f[NB][2];   // rows 8 nb + 2c, + 1: score in log2 units = f * sum of products * k_scale
     int pos[NB][2];   // their positions
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) {
-      float x[D / 4];
+      auto pair = [&](int i) -> float2 {  // dims 2i, 2i + 1 of this thread's
+        const uint4 u = raw[nb][i >> 2];
+        const uint32_t w = (i & 3) == 0 ? u.x : (i & 3) == 1 ? u.y : (i & 3) == 2 ? u.z : u.w;
+        return F16 ? __half22float2(*reinterpret_cast<const __half2*>(&w)) : make_float2(bf16_lo(w), bf16_hi(w));
+      };
       float amax = 0.f;
       bool odd = false;
 #pragma unroll
-      for (int k = 0; k < D / 32; ++k) {
-        const uint32_t w[4] = {raw[nb][k].x, raw[nb][k].y, raw[nb][k].z, raw[nb][k].w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          float2 v;
-          if (F16) v = __half22float2(*reinterpret_cast<const __half2*>(&w[j]));
-          else v = make_float2(bf16_lo(w[j]), bf16_hi(w[j]));
-          x[8 * k + 2 * j] = v.x, x[8 * k + 2 * j + 1] = v.y;
-          odd |= !(fabsf(v.x) < INFINITY) || !(fabsf(v.y) < INFINITY);
-          amax = fmaxf(amax, fmaxf(fabsf(v.x), fabsf(v.y)));
-        }
+      for (int i = 0; i < D / 8; ++i) {
+        const float2 v = pair(i);
+        odd |= !(fabsf(v.x) < INFINITY) || !(fabsf(v.y) < INFINITY);
+        amax = fmaxf(amax, fmaxf(fabsf(v.x), fabsf(v.y)));
       }
       amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
       amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
       odd = (__ballot_sync(0xffffffffu, odd) >> (4 * g) & 15u) != 0;
-      // 2^e with amax / 2^e in [224, 448): e = exponent of amax - 8 (1.75 * 2^8 = 448), or one more
-      const uint32_t ua = __float_as_uint(amax);
-      int e = (int)(ua >> 23) - 127 - 8 + ((ua & 0x7fffffu) >= 0x600000u ? 1 : 0);
-      e = min(max(e, -110), 119);
+      // 2^e with amax / 2^e in [2^14, 2^15)
+      const int e = min(max((int)(__float_as_uint(amax) >> 23) - 127 - 14, -110), 119);
       const float down = __uint_as_float((uint32_t)(127 - e) << 23), up = __uint_as_float((uint32_t)(127 + e) << 23);
       const float factor = odd ? __uint_as_float(0x7fc00000u) : p.scale_log2 * up;  // a NaN or infinity: the row is NaN
 #pragma unroll
-      for (int k = 0; k < D / 4; ++k) x[k] = odd ? 0.f : x[k] * down;
-#pragma unroll
-      for (int m = 0; m < PIECES; ++m)
-#pragma unroll
-        for (int ks = 0; ks < KS; ++ks)
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {  // words of 4 dims: j = 0 the MMA's k 4c .. , j = 1 its k 16 + 4c ..
-            float* y = x + 8 * ks + 4 * j;
-            const uint32_t w = e4m3_pair(y[0], y[1]) | e4m3_pair(y[2], y[3]) << 16;
-            if (QS) {
-              if (warp == nb % kWarps) reinterpret_cast<uint32_t*>(qs + ((nb * PIECES + m) * KS + ks) * 32 + lane)[j] = w;
-            } else {
-              qb[nb][m][ks][j] = w;
-            }
-            if (m + 1 < PIECES) {
-              uint32_t h0, h1;
-              f16_pairs(w, h0, h1);
-              const float2 v0 = __half22float2(*reinterpret_cast<const __half2*>(&h0));
-              const float2 v1 = __half22float2(*reinterpret_cast<const __half2*>(&h1));
-              y[0] -= v0.x, y[1] -= v0.y, y[2] -= v1.x, y[3] -= v1.y;  // exact
-            }
-          }
+      for (int i = 0; i < D / 8; ++i) {
+        const float2 v = pair(i);
+        qb[nb][i >> 1][i & 1] = odd ? 0u : pack_f16x2(v.x * down, v.y * down);
+      }
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         f[nb][j] = __shfl_sync(0xffffffffu, factor, 4 * (2 * c + j));
         pos[nb][j] = s.ctx + by_group(p, row0 + min(8 * nb + 2 * c + j, n - 1));
       }
     }
-
-    if (QS) __syncthreads();
 
     float acc[MT][NB][4];
 #pragma unroll
@@ -357,7 +318,7 @@ __global__ void __launch_bounds__(kWarps * 32, 3)
       const uint8_t* kt = ring + slot * kStage;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        uint32_t wa[2 * KS], wb[2 * KS];
+        uint32_t wa[KS], wb[KS];
 #pragma unroll
         for (int k = 0; k < D / 64; ++k) {
           const uint4 v = *reinterpret_cast<const uint4*>(kt + swizzled<D>(16 * h + g, D / 64 * c + k));
@@ -366,18 +327,14 @@ __global__ void __launch_bounds__(kWarps * 32, 3)
           wb[4 * k] = x.x, wb[4 * k + 1] = x.y, wb[4 * k + 2] = x.z, wb[4 * k + 3] = x.w;
         }
 #pragma unroll
-        for (int nb = 0; nb < NB; ++nb) {
-          S[h][nb][0] = S[h][nb][1] = S[h][nb][2] = S[h][nb][3] = 0.f;
+        for (int nb = 0; nb < NB; ++nb) S[h][nb][0] = S[h][nb][1] = S[h][nb][2] = S[h][nb][3] = 0.f;
 #pragma unroll
-          for (int q = 0; q < PIECES; ++q)
+        for (int ks = 0; ks < KS; ++ks) {
+          uint32_t a0, a1, a2, a3;
+          f16_pairs(wa[ks], a0, a2);
+          f16_pairs(wb[ks], a1, a3);
 #pragma unroll
-            for (int ks = 0; ks < KS; ++ks) {
-              const uint32_t a[4] = {wa[2 * ks], wb[2 * ks], wa[2 * ks + 1], wb[2 * ks + 1]};
-              uint2 b2;
-              if (QS) b2 = qs[((nb * PIECES + q) * KS + ks) * 32 + lane];
-              else b2 = make_uint2(qb[nb][q][ks][0], qb[nb][q][ks][1]);
-              mma_e4m3(S[h][nb], a, b2.x, b2.y);
-            }
+          for (int nb = 0; nb < NB; ++nb) mma_f16(S[h][nb], a0, a1, a2, a3, qb[nb][ks][0], qb[nb][ks][1]);
         }
       }
       const float4 sc = *reinterpret_cast<const float4*>(scales[warp][slot]);  // k scales, v scales
@@ -582,16 +539,16 @@ __global__ void __launch_bounds__(kWarps * 32, 3)
   if (bad && p.dev_status && lane == 0) atomicExch(p.dev_status, (int)CSA2_EDEVICE_INDEX);
 }
 
-template <int D, int NB, int PIECES, bool F16>
+template <int D, int NB, bool F16>
 cudaError_t launch(const PagedAttnParams& p, int blocks, cudaStream_t stream) {
-  constexpr int smem = kWarps * 2 * kStages<D> * kTok * D + 1024;
+  constexpr int smem = kWarps * 2 * kStages<D, NB> * kTok * D + 1024;
   static_assert(smem - 1024 >= kWarps * 8 * NB * D * 4, "the joined sums fit the ring");
   CopyMaps maps{};
   constexpr CUtensorMapSwizzle swizzle = D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B;
   if (!make_codes_map(&maps.k, p.k, p, D, 16, swizzle) || !make_codes_map(&maps.v, p.v, p, D, 16, swizzle)) return cudaErrorNotSupported;
-  cudaError_t e = allow_smem<paged_attn_kernel<D, NB, PIECES, F16>>(smem);
+  cudaError_t e = allow_smem<paged_attn_kernel<D, NB, F16>>(smem);
   if (e != cudaSuccess) return e;
-  e = launch_behind(paged_attn_kernel<D, NB, PIECES, F16>, dim3(blocks), kWarps * 32, smem, stream, p, maps);
+  e = launch_behind(paged_attn_kernel<D, NB, F16>, dim3(blocks), kWarps * 32, smem, stream, p, maps);
   return e != cudaSuccess ? e : launch_paged_join(p, D, 8 * NB, blocks, stream);
 }
 
@@ -599,9 +556,9 @@ cudaError_t launch(const PagedAttnParams& p, int blocks, cudaStream_t stream) {
 
 cudaError_t launch_paged_attn(const PagedAttnParams& p, int q_dtype, int head_dim, int rows, int blocks, cudaStream_t stream) {
   const bool f16 = q_dtype == CSA2_T_F16;
-  if (head_dim == 128) return f16 ? launch<128, 1, 3, true>(p, blocks, stream) : launch<128, 1, 2, false>(p, blocks, stream);
-  if (f16) return rows == 8 ? launch<64, 1, 3, true>(p, blocks, stream) : launch<64, 2, 3, true>(p, blocks, stream);
-  return rows == 8 ? launch<64, 1, 2, false>(p, blocks, stream) : launch<64, 2, 2, false>(p, blocks, stream);
+  if (head_dim == 128) return f16 ? launch<128, 1, true>(p, blocks, stream) : launch<128, 1, false>(p, blocks, stream);
+  if (f16) return rows == 8 ? launch<64, 1, true>(p, blocks, stream) : launch<64, 2, true>(p, blocks, stream);
+  return rows == 8 ? launch<64, 1, false>(p, blocks, stream) : launch<64, 2, false>(p, blocks, stream);
 }
 
 }  // namespace csa2
