@@ -26,7 +26,8 @@ cudaError_t allow_smem(int bytes) {
 
 // Launches a kernel behind the stream's work that may start before that is done: it calls prior_done() before
 // it reads or writes memory, and reads nothing by the non-coherent path, whose loads may move ahead of it.  Decode steps are made of kernels of a few microseconds, of which a launch takes
-// two.  These kernels give no early leave themselves: what follows them may read what they write.
+// two.  These kernels give no early leave themselves: what follows them may read what they write.  (Leave from the
+// attention to its join, at its start or at a tile's end, measured no gain.)
 template <typename... P, typename... A>
 cudaError_t launch_behind(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t stream, A&&... args) {
   cudaLaunchConfig_t cfg{};
@@ -129,6 +130,7 @@ struct PagedAttnParams {
   float* part_o;                    // [2 * blocks, rows of a tile, dim]: a block's first tile where it began before
   float* part_ml;                   // [.., 2] the block, its last where it goes on behind it
   PagedOpen* open;                  // [blocks]
+  int few_pieces;                   // a tile lies in a few blocks in the mean, not in many
   int32_t* dev_status;
 };
 // Few query rows per (sequence, kv head): tiles of 8, or (dim 64) of 16.

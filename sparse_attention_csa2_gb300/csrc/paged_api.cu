@@ -49,6 +49,7 @@ const uint64_t* rope_turns(float theta, int rot_dim) {
 struct AttnPlan {
   int rows;  // of a tile
   int blocks;
+  bool few_pieces;
   size_t part_o, part_ml, open, bytes;
 };
 AttnPlan attn_plan(const csa2_paged_attn_args* a) {
@@ -64,6 +65,7 @@ AttnPlan attn_plan(const csa2_paged_attn_args* a) {
   const long long most = (pl.rows == 256 ? 1 : pl.rows == 8 ? (a->head_dim == 64 ? 4 : 3) : a->head_dim == 64 ? 3 : pl.rows == 16 ? 2 : 1) * device_sm_count();
   const double all = (double)tiles * a->kv_heads * units;
   pl.blocks = all < (double)most ? (int)all : (int)most;
+  pl.few_pieces = tiles * a->kv_heads * 4 >= pl.blocks;
   size_t at = 0;
   const size_t slots = 2 * (size_t)pl.blocks * pl.rows;
   pl.part_o = at, at += align_up(slots * a->head_dim * 4);
@@ -212,6 +214,7 @@ csa2_status csa2_paged_attn(const csa2_paged_attn_args* a, void* stream) {
   p.part_o = reinterpret_cast<float*>(ws + pl.part_o);
   p.part_ml = reinterpret_cast<float*>(ws + pl.part_ml);
   p.open = reinterpret_cast<PagedOpen*>(ws + pl.open);
+  p.few_pieces = pl.few_pieces;
   p.dev_status = a->dev_status;
   cudaStream_t on = static_cast<cudaStream_t>(stream);
   return cuda_status(pl.rows == 256                        ? launch_paged_wide(p, a->q_dtype, a->head_dim, pl.blocks, on)

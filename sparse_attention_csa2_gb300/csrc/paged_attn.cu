@@ -65,7 +65,7 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t v) {
   return r;
 }
 // Stages of the ring: 64 KB a block, 48 KB where four blocks share an SM (dim 64 and 8 rows: 32 sequences of
-// 16,384 tokens in the mean with 8 heads 414 -> 380 us by the fourth block; with 16 rows its registers spill).
+// 65,536 tokens with 8 heads 414 -> 380 us by the fourth block; with 16 rows its registers spill).
 template <int D, int NB>
 constexpr int kStages = D == 128 ? 2 : NB == 1 ? 3 : 4;
 

@@ -8,8 +8,9 @@ namespace {
 
 // Joins the pieces of the tile that block x of the attention left open: its own sums and those of the
 // blocks after it up to the tile's end.  WPR warps take a row: they take its pieces in turn (every load
-// independent of the others), then are summed in order.  Four warps where a tile has few rows and may have
-// a hundred pieces, one where it has 256 and the pieces are few.
+// independent of the others), then are summed in order.  Four warps where there are few tiles, each in many
+// blocks, one where the tiles are many or of 256 rows and their pieces few (96 sequences x 8 heads of 15 rows,
+// 456 blocks: 3 us less than with four).
 constexpr int kJoinWarps = 4;
 template <int D, int ROWS, int WPR>
 __global__ void __launch_bounds__(kJoinWarps * 32) paged_join_kernel(const PagedAttnParams p) {
@@ -83,8 +84,9 @@ __global__ void __launch_bounds__(kJoinWarps * 32) paged_join_kernel(const Paged
 
 template <int D, int ROWS>
 cudaError_t join(const PagedAttnParams& p, int blocks, cudaStream_t stream) {
-  constexpr int WPR = ROWS == 256 ? 1 : kJoinWarps;
-  return launch_behind(paged_join_kernel<D, ROWS, WPR>, dim3(blocks, ROWS == 256 ? 32 : ROWS), kJoinWarps * 32, 0, stream, p);
+  if (ROWS == 256) return launch_behind(paged_join_kernel<D, ROWS, 1>, dim3(blocks, 32), kJoinWarps * 32, 0, stream, p);
+  if (p.few_pieces) return launch_behind(paged_join_kernel<D, ROWS, 1>, dim3(blocks, ROWS / kJoinWarps), kJoinWarps * 32, 0, stream, p);
+  return launch_behind(paged_join_kernel<D, ROWS, kJoinWarps>, dim3(blocks, ROWS), kJoinWarps * 32, 0, stream, p);
 }
 
 }  // namespace
