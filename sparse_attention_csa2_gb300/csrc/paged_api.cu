@@ -39,11 +39,12 @@ const uint64_t* rope_turns(float theta, int rot_dim) {
 
 // Which kernel, and its workspace, by the query rows per sequence and kv head in the mean.
 //   up to 8      paged_attn.cu's tiles of 8, three blocks per SM (four at dim 64)
-//   up to 32     at dim 64 its tiles of 16 (64 sequences x 4 heads x 1,000 tokens, 16 / 32 rows: 25 / 36 us against
-//                30 / 48 by paged_rows.cu's form; of 16,000 tokens, 32 sequences: 80 / 146 against 76 / 139);
-//                at dim 128 paged_rows.cu's tiles of 16 (two blocks per SM) or 32 (one): 33 / 52 us against 40 / 59
-//                by tiles of 16 of paged_attn.cu, 98 / 156 against 159 / 300
-//   more         paged_wide.cu's tiles of 256, one block per SM (64 rows in the last case: 248 us)
+//   up to 32     at dim 64 its tiles of 16 (64 sequences x 4 heads x 1,000 tokens, 16 / 32 rows: 19 / 28 us against
+//                30 / 48 by paged_rows.cu's form; 32 sequences x 16,000 tokens and 32 rows 117 against 139);
+//                at dim 128 paged_rows.cu's tiles of 16 (two blocks per SM) or 32 (one): 8 heads of 16 rows x 16
+//                sequences x 65,535 tokens 325 us against 354 by tiles of 16 of paged_attn.cu (two blocks per SM
+//                there), one head x 4 sequences x 1M tokens in fp16 183 against 232; at 1,000 tokens 47 against 43
+//   more         paged_wide.cu's tiles of 256, one block per SM (dim 64, 64 rows, the second case: 153 us)
 // No more blocks than there can be units of 128 tokens (a tile has at most the table's, a sequence one tile
 // more than its rows fill).
 struct AttnPlan {

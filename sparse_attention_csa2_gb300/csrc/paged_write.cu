@@ -11,10 +11,12 @@
 //
 // A task is one page and head of K or of V.  A block looks at `chunk` rows for those that open a page
 // or a sequence, and spreads these tasks over its eight warps: eight tasks of a warp in a decode step
-// (a row each), two of four warps for a whole page.  The rows are read once into registers (up to 8
+// (a row each), two of four warps for a page of 64.  The rows are read once into registers (up to 8
 // pieces a thread; what a long page has beyond is read again from L2), reduced to the largest
-// magnitude, and written as codes; four blocks per SM keep the loads of some in flight while others
-// reduce and write.  Bound by memory: 2 (or 4) bytes read and one written per value.
+// magnitude, and written as codes; four blocks per SM (six where a thread holds one piece) keep the
+// loads of some in flight while others reduce and write.  Bound by memory: 2 (or 4) bytes read and one
+// written per value.  32,768 rows of 8 heads of 128, bf16 (202 MB): 34.6 us, 5.8 TB/s (86% of a copy's
+// rate); 512 rows that append to their pages: 8.3 us, the chain of lookups, rows, scale and older codes.
 #include "common.cuh"
 #include "paged.h"
 
