@@ -85,13 +85,13 @@ __global__ void __launch_bounds__(kWarps * 32, D == 64 && NB == 1 ? 4 : 3)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   __shared__ __align__(16) float scales[kWarps][ST][4];
-  __shared__ __align__(8) uint64_t full[kWarps][2 * ST];  // K stages, V stages
+  __shared__ __align__(8) uint64_t full[kWarps][ST];
   __shared__ float ml[kWarps][NR][3];
   __shared__ long long scan_warp[kWarps];
   __shared__ long long place[2];        // sequence, its first unit
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, c = lane & 3;
   if (lane == 0) {  // a warp's barriers are its own
-    for (int i = 0; i < 2 * ST; ++i) tc05::mbar_init(&full[warp][i], 1);
+    for (int i = 0; i < ST; ++i) tc05::mbar_init(&full[warp][i], 1);
     tc05::fence_barrier_init();
   }
   __syncwarp();
@@ -157,7 +157,7 @@ __global__ void __launch_bounds__(kWarps * 32, D == 64 && NB == 1 ? 4 : 3)
     if (tid == 0) p.open[blockIdx.x].pieces = 0;
     return;
   }
-  uint8_t* ring = smem + warp * 2 * ST * kStage;  // K stages, V stages
+  uint8_t* ring = smem + warp * 2 * ST * kStage;  // stages of K and V
   uint32_t phases = 0;                       // bit of each barrier of `full`: parity of its next completion
   int pieces = 0;                            // of the tile that this block leaves open
   bool bad = false, dead = false;
@@ -195,25 +195,29 @@ __global__ void __launch_bounds__(kWarps * 32, D == 64 && NB == 1 ? 4 : 3)
     auto second_id = [&](int tok, int id0) -> int {  // pages of 32 tokens and more hold a whole step
       return p.page_shift == 4 ? page_id(tok + 16) : id0;
     };
-    auto copy = [&](const CUtensorMap* map, int which, int tok, int id0, int id1) {
-      uint8_t* to = ring + which * kStage;
-      uint64_t* bar = &full[warp][which];
-      if (id0 < 0 || id1 < 0) {  // a half without a page reads as zeros
-#pragma unroll
-        for (int i = 0; i < kStage / 512; ++i)
-          if ((i < kHalf / 512 ? id0 : id1) < 0) reinterpret_cast<uint4*>(to + 512 * i)[lane] = make_uint4(0, 0, 0, 0);
-        asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
-        __syncwarp();
-      }
-      if (lane == 0) {
-        tc05::mbar_expect_tx(bar, (id0 >= 0 ? kHalf : 0) + (id1 >= 0 ? kHalf : 0));
-        if (id0 >= 0) tma_load_codes(to, map, tok & page_mask, id0 * p.kv_heads + head, bar);
-        if (id1 >= 0) tma_load_codes(to + kHalf, map, (tok + 16) & page_mask, id1 * p.kv_heads + head, bar);
-      }
-    };
-    auto copy_k = [&](int slot, int tok, int id0, int id1) {
+    auto copy = [&](int slot, int tok, int id0, int id1) {
       if (tok < t_end) {
-        copy(&maps.k, slot, tok, id0, id1);
+        uint8_t* to = ring + 2 * slot * kStage;
+        if (id0 < 0 || id1 < 0) {  // a half without a page reads as zeros
+#pragma unroll
+          for (int i = 0; i < 2 * kStage / 512; ++i)
+            if ((i % (kStage / 512) < kHalf / 512 ? id0 : id1) < 0) reinterpret_cast<uint4*>(to + 512 * i)[lane] = make_uint4(0, 0, 0, 0);
+          asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
+          __syncwarp();
+        }
+        if (lane == 0) {
+          uint64_t* bar = &full[warp][slot];
+          const int at0 = tok & page_mask, at1 = (tok + 16) & page_mask;
+          tc05::mbar_expect_tx(bar, (id0 >= 0 ? kStage : 0) + (id1 >= 0 ? kStage : 0));
+          if (id0 >= 0) {
+            tma_load_codes(to, &maps.k, at0, id0 * p.kv_heads + head, bar);
+            tma_load_codes(to + kStage, &maps.v, at0, id0 * p.kv_heads + head, bar);
+          }
+          if (id1 >= 0) {
+            tma_load_codes(to + kHalf, &maps.k, at1, id1 * p.kv_heads + head, bar);
+            tma_load_codes(to + kStage + kHalf, &maps.v, at1, id1 * p.kv_heads + head, bar);
+          }
+        }
         if (lane < 4) {
           const int id = lane & 1 ? id1 : id0;
           const float* sc = lane < 2 ? p.k_scale : p.v_scale;
@@ -222,12 +226,9 @@ __global__ void __launch_bounds__(kWarps * 32, D == 64 && NB == 1 ? 4 : 3)
       }
       cp_async_commit();
     };
-    auto copy_v = [&](int slot, int tok, int id0, int id1) {
-      if (tok < t_end) copy(&maps.v, ST + slot, tok, id0, id1);
-    };
-    auto arrived = [&](int which) {
-      if (!dead && !paged_wait(&full[warp][which], (phases >> which) & 1)) dead = true;
-      phases ^= 1u << which;
+    auto arrived = [&](int slot) {
+      if (!dead && !paged_wait(&full[warp][slot], (phases >> slot) & 1)) dead = true;
+      phases ^= 1u << slot;
       __syncwarp();
     };
     int tok = t_begin + warp * kTok;
@@ -259,8 +260,7 @@ __global__ void __launch_bounds__(kWarps * 32, D == 64 && NB == 1 ? 4 : 3)
 #pragma unroll
       for (int i = 0; i < ST; ++i) {
         note(i, id0[i], id1[i]);
-        copy_k(i, tok + i * kUnit, id0[i], id1[i]);
-        copy_v(i, tok + i * kUnit, id0[i], id1[i]);
+        copy(i, tok + i * kUnit, id0[i], id1[i]);
       }
     }
 
@@ -319,7 +319,7 @@ __global__ void __launch_bounds__(kWarps * 32, D == 64 && NB == 1 ? 4 : 3)
       arrived(slot);
       // ---- scores of 32 tokens: S[half][rows of 8][..], tokens 16 half + g (0, 1) and + 8 (2, 3), rows 2c, 2c + 1
       float S[2][NB][4];
-      const uint8_t* kt = ring + slot * kStage;
+      const uint8_t* kt = ring + 2 * slot * kStage;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         uint32_t wa[KS], wb[KS];
@@ -342,9 +342,6 @@ __global__ void __launch_bounds__(kWarps * 32, D == 64 && NB == 1 ? 4 : 3)
         }
       }
       const float4 sc = *reinterpret_cast<const float4*>(scales[warp][slot]);  // k scales, v scales
-      __syncwarp();
-      note(slot, idc0, idc1);
-      copy_k(slot, next, idc0, idc1);
 
       // a NaN in either scale marks the page: its visible tokens give NaN
       const float k0 = sc.x + 0.f * sc.z, k1 = sc.y + 0.f * sc.w;
@@ -425,8 +422,7 @@ __global__ void __launch_bounds__(kWarps * 32, D == 64 && NB == 1 ? 4 : 3)
         }
       }
       // ---- outputs: this thread's tokens 2c, 2c + 1, 2c + 8, 2c + 9 of each half, dims D/8 * g ..
-      arrived(ST + slot);
-      uint8_t* vt = ring + (ST + slot) * kStage;
+      uint8_t* vt = ring + (2 * slot + 1) * kStage;
       if (tok + kTok > t_end) {  // slots behind the last token may hold anything: 0 * NaN is not 0
         if (tok + lane >= t_end) {
 #pragma unroll
@@ -464,7 +460,8 @@ __global__ void __launch_bounds__(kWarps * 32, D == 64 && NB == 1 ? 4 : 3)
         }
       }
       __syncwarp();
-      copy_v(slot, next, idc0, idc1);
+      note(slot, idc0, idc1);
+      copy(slot, next, idc0, idc1);
     }
     cp_async_wait<0>();
 
