@@ -18,7 +18,7 @@
 // sums, and a second kernel joins the pieces in order.
 //
 // Within a block each of the four warps streams its own 32 tokens of a unit through a ring in shared
-// memory (TMA copies of 16 tokens of a page, two stages of K and of V, four at dim 64; no block barrier
+// memory (TMA copies of 32 tokens of a page, or of two pages of 16, two stages of K and of V, four at dim 64; no block barrier
 // until the tile's end) and keeps its own running maximum, sum and output.
 //
 // Arithmetic.  Tokens are the MMAs' rows and query rows their columns, eight to a column block, so that
@@ -207,15 +207,22 @@ __global__ void __launch_bounds__(kWarps * 32, D == 64 && NB == 1 ? 4 : 3)
         }
         if (lane == 0) {
           uint64_t* bar = &full[warp][slot];
-          const int at0 = tok & page_mask, at1 = (tok + 16) & page_mask;
-          tc05::mbar_expect_tx(bar, (id0 >= 0 ? kStage : 0) + (id1 >= 0 ? kStage : 0));
-          if (id0 >= 0) {
-            tma_load_codes(to, &maps.k, at0, id0 * p.kv_heads + head, bar);
-            tma_load_codes(to + kStage, &maps.v, at0, id0 * p.kv_heads + head, bar);
-          }
-          if (id1 >= 0) {
-            tma_load_codes(to + kHalf, &maps.k, at1, id1 * p.kv_heads + head, bar);
-            tma_load_codes(to + kStage + kHalf, &maps.v, at1, id1 * p.kv_heads + head, bar);
+          if (p.page_shift > 4) {  // the maps' boxes are whole steps
+            tc05::mbar_expect_tx(bar, id0 >= 0 ? 2 * kStage : 0);
+            if (id0 >= 0) {
+              tma_load_codes(to, &maps.k, tok & page_mask, id0 * p.kv_heads + head, bar);
+              tma_load_codes(to + kStage, &maps.v, tok & page_mask, id0 * p.kv_heads + head, bar);
+            }
+          } else {
+            tc05::mbar_expect_tx(bar, (id0 >= 0 ? kStage : 0) + (id1 >= 0 ? kStage : 0));
+            if (id0 >= 0) {
+              tma_load_codes(to, &maps.k, 0, id0 * p.kv_heads + head, bar);
+              tma_load_codes(to + kStage, &maps.v, 0, id0 * p.kv_heads + head, bar);
+            }
+            if (id1 >= 0) {
+              tma_load_codes(to + kHalf, &maps.k, 0, id1 * p.kv_heads + head, bar);
+              tma_load_codes(to + kStage + kHalf, &maps.v, 0, id1 * p.kv_heads + head, bar);
+            }
           }
         }
         if (lane < 4) {
@@ -546,7 +553,8 @@ cudaError_t launch(const PagedAttnParams& p, int blocks, cudaStream_t stream) {
   static_assert(smem - 1024 >= kWarps * 8 * NB * D * 4, "the joined sums fit the ring");
   CopyMaps maps{};
   constexpr CUtensorMapSwizzle swizzle = D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B;
-  if (!make_codes_map(&maps.k, p.k, p, D, 16, swizzle) || !make_codes_map(&maps.v, p.v, p, D, 16, swizzle)) return cudaErrorNotSupported;
+  const int box = p.page_shift == 4 ? 16 : kTok;
+  if (!make_codes_map(&maps.k, p.k, p, D, box, swizzle) || !make_codes_map(&maps.v, p.v, p, D, box, swizzle)) return cudaErrorNotSupported;
   cudaError_t e = allow_smem<paged_attn_kernel<D, NB, F16>>(smem);
   if (e != cudaSuccess) return e;
   e = launch_behind(paged_attn_kernel<D, NB, F16>, dim3(blocks), kWarps * 32, smem, stream, p, maps);
