@@ -356,9 +356,15 @@ __global__ void __launch_bounds__(kWarps * 32, D == 64 && NB == 1 ? 4 : 3)
       bool grows = false;
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb) {
-        const float fa0 = f[nb][0] * k0, fb0 = f[nb][1] * k0, fa1 = f[nb][0] * k1, fb1 = f[nb][1] * k1;
-        S[0][nb][0] *= fa0, S[0][nb][1] *= fb0, S[0][nb][2] *= fa0, S[0][nb][3] *= fb0;
-        S[1][nb][0] *= fa1, S[1][nb][1] *= fb1, S[1][nb][2] *= fa1, S[1][nb][3] *= fb1;
+        const float2 f2 = make_float2(f[nb][0], f[nb][1]);
+        const float2 by[2] = {mul2(f2, make_float2(k0, k0)), mul2(f2, make_float2(k1, k1))};
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int j = 0; j < 4; j += 2) {
+            const float2 z = mul2(make_float2(S[h][nb][j], S[h][nb][j + 1]), by[h]);
+            S[h][nb][j] = z.x, S[h][nb][j + 1] = z.y;
+          }
       }
       if (!whole) {
 #pragma unroll
@@ -411,22 +417,25 @@ __global__ void __launch_bounds__(kWarps * 32, D == 64 && NB == 1 ? 4 : 3)
       uint32_t pw[2][NB][2], pr[2][NB][F16 ? 2 : 1];  // weights, and (fp16) what their rounding left
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb) {
-        const float s0 = m[nb][0] == -INFINITY ? 0.f : kPagedLift - m[nb][0], s1 = m[nb][1] == -INFINITY ? 0.f : kPagedLift - m[nb][1];
+        const float2 over = make_float2(m[nb][0] == -INFINITY ? 0.f : kPagedLift - m[nb][0], m[nb][1] == -INFINITY ? 0.f : kPagedLift - m[nb][1]);
+        float2 sum = make_float2(l[nb][0], l[nb][1]);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           const float cv = (h ? v1 : v0) * vinv;
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
-            const float p0 = ex2(S[h][nb][2 * j] + s0), p1 = ex2(S[h][nb][2 * j + 1] + s1);
-            l[nb][0] += p0, l[nb][1] += p1;
-            const uint32_t w = pack_f16x2(p0 * cv, p1 * cv);
+            const float2 z = add2(make_float2(S[h][nb][2 * j], S[h][nb][2 * j + 1]), over);
+            const float2 e = make_float2(ex2(z.x), ex2(z.y)), ev = mul2(e, make_float2(cv, cv));
+            sum = add2(sum, e);
+            const uint32_t w = pack_f16x2(ev.x, ev.y);
             pw[h][nb][j] = transpose8(w);
             if constexpr (F16) {
-              const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&w));
-              pr[h][nb][j] = transpose8(pack_f16x2(fmaf(p0, cv, -v.x), fmaf(p1, cv, -v.y)));
+              const float2 r = fma2(__half22float2(*reinterpret_cast<const __half2*>(&w)), make_float2(-1.f, -1.f), ev);
+              pr[h][nb][j] = transpose8(pack_f16x2(r.x, r.y));
             }
           }
         }
+        l[nb][0] = sum.x, l[nb][1] = sum.y;
       }
       // ---- outputs: this thread's tokens 2c, 2c + 1, 2c + 8, 2c + 9 of each half, dims D/8 * g ..
       uint8_t* vt = ring + (2 * slot + 1) * kStage;
