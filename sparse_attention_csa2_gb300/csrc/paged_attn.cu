@@ -5,10 +5,11 @@
 //   o_i  = sum_j exp(z_ij) v_j / (sum_j exp(z_ij) + exp(sink))
 //
 // Bound by the codes' way from memory: 2 * dim bytes per cached token and head, each read once.  32 sequences of
-// 65,536 tokens, 8 heads of 8 rows (4.3 GB at dim 128): 660 us, 6.5 TB/s, 96% of a copy's rate; at dim 64 348 us,
-// 91%.  Many short tiles are bound by instructions instead (per 32 tokens at dim 64 a warp issues 459 for 8 rows,
-// 542 for 16) and by their beginnings and ends: 96 sequences of 5 tokens, 8 heads, window 1,024 (101 MB) 55 us, of
-// which 28 are steps; one sequence of 2,048 tokens 9.3 us, the chain of two launches, lengths, pages, codes.
+// 65,536 tokens, 8 heads of 8 rows (4.3 GB at dim 128): 652 us, 6.6 TB/s, 97% of a copy's rate; at dim 64 352 us,
+// 90%.  Many short tiles are bound by instructions instead (per 32 tokens at dim 64 a warp issues 352 for 8 rows,
+// 417 for 16) and by their beginnings and ends: 96 sequences of 5 tokens, 8 heads, window 1,024 (101 MB) 51 us, of
+// which 23 are steps; one sequence of 2,048 tokens 8.9 us, the chain of two launches, lengths, pages, codes.
+// (Sending a tile's first copies out before the one before is joined gained nothing: the SM's other blocks work then.)
 //
 // Split.  A tile is up to 8 or 16 query rows (tokens x heads of the group) of one sequence and kv head;
 // its unit of work is 128 cached tokens.  The units of all tiles of the call form one line, of which
@@ -18,16 +19,17 @@
 // sums, and a second kernel joins the pieces in order.
 //
 // Within a block each of the four warps streams its own 32 tokens of a unit through a ring in shared
-// memory (TMA copies of 32 tokens of a page, or of two pages of 16, two stages of K and of V, four at dim 64; no block barrier
-// until the tile's end) and keeps its own running maximum, sum and output.
+// memory (TMA copies of 32 tokens of a page, or of two pages of 16; two stages, at dim 64 three or four; a step's keys
+// and values arrive on one barrier, which 96 sequences of 5 tokens take 52.0 us with and 55.4 without; no block
+// barrier until the tile's end) and keeps its own running maximum, sum and output.
 //
 // Arithmetic.  Tokens are the MMAs' rows and query rows their columns, eight to a column block, so that
 // the few query rows of a decode step fill the tensor cores' shape.  Codes are converted to fp16 (exact).
 // A query row is scaled by a power of two to a maximum in [2^14, 2^15): as fp16 its values keep all their
 // bits down to 2^-29 of that, and products are summed in fp32.  (K left in its 8 bits against rows as two or
 // three E4M3 pieces took more instructions, not fewer: an E4M3 mma.sync counts as two fp16 ones with the
-// conversions of both operands and four additions.  Per 32 tokens of 16 rows at dim 64, fp16: 808 against 614;
-// 96 sequences of 5 drafted tokens each, window 1,024: 74 against 60 us.)  Weights are fp16 of
+// conversions of both operands and four additions.  Per 32 tokens of 16 rows at dim 64, fp16: 808 against 614
+// at that time; 96 sequences of 5 drafted tokens each, window 1,024: 74 against 60 us.)  Weights are fp16 of
 // exp2(z - max + 11), where the maximum follows a larger score only when that exceeds it by 2^4:
 // weights are at most 2^15, those down to 2^-21 of the largest keep 11 bits, and the output is rarely
 // rescaled.  A page's V scale enters the weight relative to the largest seen.  Maxima,
@@ -69,7 +71,7 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t v) {
   return r;
 }
 // Stages of the ring: 64 KB a block, 48 KB where four blocks share an SM (dim 64 and 8 rows: 32 sequences of
-// 65,536 tokens with 8 heads 414 -> 380 us by the fourth block; with 16 rows its registers spill).
+// 65,536 tokens with 8 heads 380 us with the fourth block, 414 without; with 16 rows its registers spill).
 template <int D, int NB>
 constexpr int kStages = D == 128 ? 2 : NB == 1 ? 3 : 4;
 

@@ -48,8 +48,9 @@ def cuda(x):
 
 def bound(q, case, oracle, out_eps):
     """How far each output may be off.  Per weight: its rounding to fp16 (2^-11) and 2^-15 for exp2, the
-    running sums and their joining; per score 2^-16 of max|q| * reach: the query's pieces hold it to
-    2^-17.8 of its row's maximum, its at most 16 fp32 additions and three products to 2^-19.  A score's
+    running sums and their joining; per score 2^-16 of max|q| * reach: the query's E4M3 pieces hold it to
+    2^-17.8 of its row's maximum (as fp16, with few rows, to 2^-25), its at most 16 fp32 additions and three
+    products to 2^-19.  A score's
     error moves a weight and the denominator, twice its size in all.  Weights below fp16's normal range
     are 2^-36 of the largest off at most.  Then the output's own rounding."""
     out, spread, reach = oracle
