@@ -696,7 +696,8 @@ csa2_status csa2_write_pages(const csa2_write_pages_args* a, void* stream);
  * A row without such a token is 0.  Rows outside [0, row_start[n_seq]) of q and out are left.
  * A table entry outside [0, n_pages) hides its tokens and is reported; kv_len beyond the table
  * counts as its end.  Codes 0x7f and 0xff (E4M3's NaN, which csa2_write_pages does not write)
- * must not occur among a sequence's tokens; scales are >= 0 or NaN. */
+ * must not occur among a sequence's tokens; scales are >= 0 or NaN, and code * scale of V is at
+ * most 2^80 (sums of 2^15 times a value per token are held in fp32). */
 typedef struct {
   int32_t n_rows;             /* rows of q and out (>= 0) */
   int32_t n_seq;

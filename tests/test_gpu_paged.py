@@ -444,6 +444,57 @@ def test_paged_attn_between_other_kernels_of_the_framework():
         assert torch.equal(y, want_y) and torch.equal(o, want[i % 3])
 
 
+@pytest.mark.parametrize("D,batch", [(64, "decode"), (128, "decode"), (128, "drafts"), (64, "prompts"), (128, "prompts")])
+def test_pages_beyond_32_bit_offsets(D, batch):
+    """The same tokens in the last pages of caches of more than 2^32 bytes and of their own pages only: codes, scales
+    and outputs are equal bit for bit."""
+    new, kv = BATCHES[batch]
+    new = np.minimum(new, kv)
+    c = make(new, kv, 64, 8, D, seed=25)
+    n = len(c["k"])
+    far = 2 ** 32 // (8 * 64 * D) + 7
+    rng = np.random.default_rng(6)
+    T = c["rows"]
+    q, k, v = (values((T, h, D), rng, "bf16")[0].cuda() for h in (16, 8, 8))
+    seq = cuda(np.repeat(np.arange(len(new)), new).astype(np.int32))
+    row_start, kv_len = cuda(c["row_start"]), cuda(c["kv"])
+    near, wide = S.PageCache(*(cuda(c[t]) for t in ("k", "v", "ks", "vs"))), S.PageCache.empty(far + n, 8, 64, D)
+    outs = []
+    for cache, shift in ((near, 0), (wide, far)):
+        for t, key in zip(cache, ("k", "v", "ks", "vs")):
+            t[shift:] = cuda(c[key])
+        table = cuda(np.where(c["table"] < 0, -1, c["table"] + shift).astype(np.int32))
+        S.write_pages(cache, k, v, row_start, kv_len, seq, table)
+        outs.append(S.paged_attn(q, cache, row_start, kv_len, table, D ** -0.5))
+    assert torch.equal(*outs) and bool(torch.isfinite(outs[0].float()).all())
+    for x, y in zip(near, wide):
+        assert torch.equal(x.view(torch.uint8), y[far:].contiguous().view(torch.uint8))
+
+
+def test_rope_axes_beyond_32_bit_offsets():
+    T, H, D = 70000, 256, 128  # 2.3e9 elements
+    x = torch.empty((T, H, D), dtype=torch.bfloat16, device="cuda")
+    x[-40:] = torch.randn((40, H, D), device="cuda").bfloat16()
+    pos = torch.arange(T, device="cuda")
+    want = S.rope_axes(x[-40:].contiguous(), pos[-40:].contiguous())
+    S.rope_axes(x, pos, out=x)
+    assert torch.equal(x[-40:], want)
+
+
+def test_paged_attn_of_a_cache_without_pages():
+    z = torch.zeros(3, dtype=torch.int32, device="cuda")
+    rows = torch.tensor([0, 1, 2, 3], dtype=torch.int32, device="cuda")
+    q = torch.randn((3, 4, 64), device="cuda").bfloat16()
+    empty = S.PageCache.empty(0, 2, 16, 64)
+    out = S.paged_attn(q, empty, rows, z, torch.zeros((3, 0), dtype=torch.int32, device="cuda"), 0.125)
+    assert not bool(out.any())
+    one = S.PageCache.empty(1, 2, 16, 64)
+    for t in one:
+        t.view(torch.uint8).fill_(0x7F)
+    out = S.paged_attn(q, one, rows, z, torch.zeros((3, 2), dtype=torch.int32, device="cuda"), 0.125)
+    assert not bool(out.any())
+
+
 # ------------------------------------------------------------------ together
 @pytest.mark.parametrize("D,G", [(128, 4), (64, 9)])
 def test_serving_steps(D, G):
