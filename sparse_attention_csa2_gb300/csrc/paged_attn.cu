@@ -8,7 +8,7 @@
 // 65,536 tokens, 8 heads of 8 rows (4.3 GB at dim 128): 652 us, 6.6 TB/s, 97% of a copy's rate; at dim 64 352 us,
 // 90%.  Many short tiles are bound by instructions instead (per 32 tokens at dim 64 a warp issues 352 for 8 rows,
 // 417 for 16) and by their beginnings and ends: 96 sequences of 5 tokens, 8 heads, window 1,024 (101 MB) 51 us, of
-// which 23 are steps; one sequence of 2,048 tokens 8.9 us, the chain of two launches, lengths, pages, codes.
+// which 23 are steps; one sequence of 2,048 tokens 8.5 us, the chain of two launches, lengths, pages, codes.
 // (Sending a tile's first copies out before the one before is joined gained nothing: the SM's other blocks work then.)
 //
 // Split.  A tile is up to 8 or 16 query rows (tokens x heads of the group) of one sequence and kv head;
