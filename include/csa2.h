@@ -767,6 +767,10 @@ csa2_status csa2_set_tuning(int32_t knob, int32_t value);
  * the device int32 *dev_status, as the kernels do, and the block returns normally.  Returns
  * CSA2_EINVAL for a NULL dev_status or tries out of range, CSA2_ECUDA for a failed launch. */
 csa2_status csa2_selftest_wait_timeout(int32_t* dev_status, int32_t tries, void* stream);
+/* The same for the waits of csa2_paged_attn: the call with at most `tries` (0 .. 2^20) tries in each
+ * wait, so that some or all give up while their copies are under way.  Where one does, dev_status
+ * (required) reads CSA2_ETIMEOUT and `out` holds anything; the kernels end as usual otherwise. */
+csa2_status csa2_selftest_paged_waits(const csa2_paged_attn_args* a, int32_t tries, void* stream);
 
 #ifdef __cplusplus
 }

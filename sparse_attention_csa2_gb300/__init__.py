@@ -626,4 +626,4 @@ def expand_mxfp4(codes, exps):
 
 # ------------------------------------------------------------------ paged 8-bit cache
 from .paged import (PageCache, PagedAttn, PagePlan, PageWriter, RopeAxes, page_plan, paged_attn, rope_axes,  # noqa: E402
-                    write_pages)
+                    selftest_paged_waits, write_pages)

@@ -109,6 +109,8 @@ struct PagedOpen {
   int kv_head;
 };
 
+constexpr uint32_t kPagedTries = 1u << 22;  // of a wait: each may suspend for about a microsecond, some 0.1 to 4 seconds
+
 struct PagedAttnParams {
   const void* q;
   long long q_row, q_head;          // strides in elements
@@ -131,6 +133,7 @@ struct PagedAttnParams {
   float* part_ml;                   // [.., 2] the block, its last where it goes on behind it
   PagedOpen* open;                  // [blocks]
   int few_pieces;                   // a tile lies in a few blocks in the mean, not in many
+  uint32_t wait_tries;              // of a wait for a barrier (kPagedTries, or fewer in a self-test)
   int32_t* dev_status;
 };
 // Few query rows per (sequence, kv head): tiles of 8, or (dim 64) of 16.

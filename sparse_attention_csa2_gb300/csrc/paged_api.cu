@@ -186,7 +186,7 @@ size_t csa2_paged_attn_workspace_size(const csa2_paged_attn_args* a) {
   return attn_plan(a).bytes;
 }
 
-csa2_status csa2_paged_attn(const csa2_paged_attn_args* a, void* stream) {
+static csa2_status paged_attn(const csa2_paged_attn_args* a, uint32_t wait_tries, void* stream) {
   const csa2_status st = check_attn_sizes(a);
   if (st != CSA2_OK) return st;
   if (!type_ok(a->q_dtype) || a->q_dtype == CSA2_T_F32 || !type_ok(a->out_dtype) || a->window < 0 ||
@@ -216,11 +216,19 @@ csa2_status csa2_paged_attn(const csa2_paged_attn_args* a, void* stream) {
   p.part_ml = reinterpret_cast<float*>(ws + pl.part_ml);
   p.open = reinterpret_cast<PagedOpen*>(ws + pl.open);
   p.few_pieces = pl.few_pieces;
+  p.wait_tries = wait_tries;
   p.dev_status = a->dev_status;
   cudaStream_t on = static_cast<cudaStream_t>(stream);
   return cuda_status(pl.rows == 256                        ? launch_paged_wide(p, a->q_dtype, a->head_dim, pl.blocks, on)
                      : a->head_dim == 128 && pl.rows > 8 ? launch_paged_rows(p, a->q_dtype, pl.rows, pl.blocks, on)
                                                          : launch_paged_attn(p, a->q_dtype, a->head_dim, pl.rows, pl.blocks, on));
+}
+
+csa2_status csa2_paged_attn(const csa2_paged_attn_args* a, void* stream) { return paged_attn(a, kPagedTries, stream); }
+
+csa2_status csa2_selftest_paged_waits(const csa2_paged_attn_args* a, int32_t tries, void* stream) {
+  if (!a || !a->dev_status || tries < 0 || tries > (1 << 20)) return CSA2_EINVAL;
+  return paged_attn(a, (uint32_t)tries, stream);
 }
 
 }  // extern "C"

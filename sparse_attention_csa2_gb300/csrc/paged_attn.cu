@@ -238,9 +238,9 @@ __global__ void __launch_bounds__(kWarps * 32, D == 64 && NB == 1 ? 4 : 3)
       cp_async_commit();
     };
     auto arrived = [&](int slot) {
-      if (!dead && !paged_wait(&full[warp][slot], (phases >> slot) & 1)) dead = true;
+      if (!paged_wait(&full[warp][slot], phases >> slot & 1, p.wait_tries)) return false;
       phases ^= 1u << slot;
-      __syncwarp();
+      return true;
     };
     int tok = t_begin + warp * kTok;
     // the query rows set out first: they and the page ids come together
@@ -322,12 +322,14 @@ __global__ void __launch_bounds__(kWarps * 32, D == 64 && NB == 1 ? 4 : 3)
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) m[nb][0] = m[nb][1] = -INFINITY, l[nb][0] = l[nb][1] = 0.f;
 
-    for (int slot = 0; tok < t_end && !dead; tok += kUnit, slot = slot + 1 == ST ? 0 : slot + 1) {
+    int slot = 0;
+    for (; tok < t_end; tok += kUnit, slot = slot + 1 == ST ? 0 : slot + 1) {
       const int next = tok + ST * kUnit;
       const int idc0 = page_id(next), idc1 = second_id(next, idc0);
       const bool ok0 = okay >> 2 * slot & 1, ok1 = okay >> 2 * slot & 2;
       cp_async_wait<ST - 1>();
-      arrived(slot);
+      dead = !arrived(slot);
+      if (dead) break;
       // ---- scores of 32 tokens: S[half][rows of 8][..], tokens 16 half + g (0, 1) and + 8 (2, 3), rows 2c, 2c + 1
       float S[2][NB][4];
       const uint8_t* kt = ring + 2 * slot * kStage;
@@ -484,6 +486,11 @@ __global__ void __launch_bounds__(kWarps * 32, D == 64 && NB == 1 ? 4 : 3)
       copy(slot, next, idc0, idc1);
     }
     cp_async_wait<0>();
+    if (dead)  // the copies of this step and of those behind it are still under way
+      for (int k = 0; k < ST && tok + k * kUnit < t_end; ++k) {
+        const int i = (slot + k) % ST;
+        paged_wait(&full[warp][i], phases >> i & 1, kPagedTries);
+      }
 
     // ---- the four warps' sums joined
 #pragma unroll
@@ -494,7 +501,7 @@ __global__ void __launch_bounds__(kWarps * 32, D == 64 && NB == 1 ? 4 : 3)
         l[nb][j] += __shfl_xor_sync(0xffffffffu, l[nb][j], 8);
         l[nb][j] += __shfl_xor_sync(0xffffffffu, l[nb][j], 16);
       }
-    if (__syncthreads_or(dead)) {  // a copy never came: nothing of this block's is in flight any more that will
+    if (__syncthreads_or(dead)) {  // a copy never came
       if (tid == 0) {
         if (p.dev_status) atomicExch(p.dev_status, (int)CSA2_ETIMEOUT);
         p.open[blockIdx.x].pieces = 0;

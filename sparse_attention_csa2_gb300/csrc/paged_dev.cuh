@@ -15,22 +15,28 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
-// Bounded wait for an mbarrier's phase that lets the hardware suspend the warp for about a microsecond at a
-// time: the default suspension is a few tens of cycles, and the parts of these kernels that wait then take
-// issue slots from those that work.  Gives up after 2^22 tries (some 0.1 to 4 seconds).
-__device__ __forceinline__ bool paged_wait(uint64_t* bar, uint32_t parity) {
+// Bounded wait of a whole warp for an mbarrier's phase that lets the hardware suspend it for about a microsecond
+// at a time: the default suspension is a few tens of cycles, and the parts of these kernels that wait then take
+// issue slots from those that work.  Gives up after so many tries; its lanes agree on the answer.
+__device__ __forceinline__ bool paged_wait(uint64_t* bar, uint32_t parity, uint32_t tries) {
   const uint32_t a = smem_u32(bar);
 #pragma unroll 1
-  for (uint32_t i = 0; i < (1u << 22); ++i) {
+  for (uint32_t i = 0; i < tries; ++i) {
     uint32_t done;
     asm volatile(
         "{\n .reg .pred P1;\n mbarrier.try_wait.parity.shared::cta.b64 P1, [%1], %2, %3;\n selp.b32 %0, 1, 0, P1;\n}\n"
         : "=r"(done)
         : "r"(a), "r"(parity), "r"(1000u)
         : "memory");
-    if (done) return true;
+    if (__all_sync(0xffffffffu, done)) return true;
   }
   return false;
+}
+// A block whose waits ran out leaves nothing in flight: the copies' warp waits for the last of the `sent` copies
+// (the n-th on barrier n % STAGES, one phase each) before the block ends.
+template <int STAGES>
+__device__ __forceinline__ void paged_drain(uint64_t (&full)[STAGES], uint32_t sent) {
+  for (uint32_t i = sent > STAGES ? sent - STAGES : 0; i < sent; ++i) paged_wait(&full[i % STAGES], i / STAGES & 1, kPagedTries);
 }
 
 // Two fp32 at once.

@@ -43,7 +43,7 @@ struct TileEnd {
 template <int R, int STAGES>
 struct Shared {
   uint64_t k_full[STAGES], k_free[STAGES], v_full[STAGES], v_free[STAGES], s_full[2], s_free[2], info_full[kInfos];
-  uint64_t w_full, p_full, pv_done, q_full, q_free, o_full;
+  uint64_t w_full, p_full, pv_done, q_full, q_free, o_full, drained;
   PagedInfo info[kInfos];
   float factor[2][R];  // of a query row: score in log2 units = factor * k_scale * sum of products
   int pos[2][R];       // its position
@@ -171,6 +171,7 @@ __global__ void __launch_bounds__(kThreads, R == 16 ? 2 : 1)
     for (int i = 0; i < kInfos; ++i) tc05::mbar_init(&sh.info_full[i], 1);
     tc05::mbar_init(&sh.w_full, 128), tc05::mbar_init(&sh.p_full, 128), tc05::mbar_init(&sh.pv_done, 1);
     tc05::mbar_init(&sh.q_full, 128), tc05::mbar_init(&sh.q_free, 1), tc05::mbar_init(&sh.o_full, 1);
+    tc05::mbar_init(&sh.drained, 1);
     tc05::fence_barrier_init();
   }
 
@@ -222,8 +223,9 @@ __global__ void __launch_bounds__(kThreads, R == 16 ? 2 : 1)
   Segment x;
   bool dead = false, bad = false;
   uint32_t count = 0, segs = 0;  // units, tiles of the block so far
+  uint32_t k_sent = 0;           // K's copies (V's: count)
   auto wait = [&](uint64_t* bar, uint32_t parity) {
-    if (!dead && !paged_wait(bar, parity)) dead = true;  // a warp's lanes try together and see the same
+    if (!dead && !paged_wait(bar, parity, p.wait_tries)) dead = true;
   };
 
   if (warp < 4) {
@@ -559,6 +561,7 @@ __global__ void __launch_bounds__(kThreads, R == 16 ? 2 : 1)
         if (lane == 0) tc05::mbar_expect_tx(&sh.k_full[stage], bytes);
         __syncwarp();
         if (copies) tma_load_codes(k_ring + stage * kCodes + 16 * lane * D, &maps.k, tok & mask, (int)slab, &sh.k_full[stage]);
+        k_sent = count + 1;
         wait(&sh.v_free[stage], parity);
         if (dead) break;
         if (lane == 0) tc05::mbar_expect_tx(&sh.v_full[stage], bytes);
@@ -623,7 +626,17 @@ __global__ void __launch_bounds__(kThreads, R == 16 ? 2 : 1)
   if (dead && p.dev_status) atomicExch(p.dev_status, (int)CSA2_ETIMEOUT);
   if (bad && p.dev_status) atomicExch(p.dev_status, (int)CSA2_EDEVICE_INDEX);
   __syncwarp();
-  __syncthreads();
+  if (__syncthreads_or(dead)) {  // copies and products that are under way come to their end before the block does
+    if (warp == 8) {
+      paged_drain(sh.k_full, k_sent);
+      paged_drain(sh.v_full, count);
+    } else if (warp == 9) {
+      if (elected()) tc05::mma_commit(&sh.drained);
+      __syncwarp();
+      paged_wait(&sh.drained, 0, kPagedTries);
+    }
+    __syncthreads();
+  }
   if (warp == 9) tc05::tmem_dealloc(tmem, kCols);
 }
 

@@ -97,7 +97,7 @@ template <int KS, int VS>
 struct Shared {
   uint64_t k_full[KS], k_free[KS], r_full[VS], r_free[VS], v_full[2], v_free[2], q_full[2];
   uint64_t s_full[2][2], p_ready[2][2], o_done[2][2];  // [row tile][half]
-  uint64_t info_full[kInfos];
+  uint64_t info_full[kInfos], drained;
   PagedInfo info[kInfos];
   float factor[8][32];  // of the rows of the softmax warps: score in log2 units = factor * k_scale * product
   uint32_t tmem;
@@ -131,6 +131,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_wide_kernel(const PagedAttn
         tc05::mbar_init(&sh.s_full[i][h], 1), tc05::mbar_init(&sh.p_ready[i][h], 128), tc05::mbar_init(&sh.o_done[i][h], 1);
     }
     for (int i = 0; i < kInfos; ++i) tc05::mbar_init(&sh.info_full[i], 1);
+    tc05::mbar_init(&sh.drained, 1);
     tc05::fence_barrier_init();
   }
 
@@ -209,8 +210,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_wide_kernel(const PagedAttn
   Segment x;
   int pieces = 0;
   bool dead = false, bad = false;
+  uint32_t k_sent = 0, v_sent = 0;  // copies
   auto wait = [&](uint64_t* bar, uint32_t parity) {
-    if (!dead && !paged_wait(bar, parity)) dead = true;  // a warp's lanes try together and see the same
+    if (!dead && !paged_wait(bar, parity, p.wait_tries)) dead = true;
   };
 
   if (warp < 8) {
@@ -522,6 +524,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_wide_kernel(const PagedAttn
           if (lane == 0) tc05::mbar_expect_tx(&sh.k_full[ks], bytes);
           __syncwarp();
           if (copies) tma_load_codes(k_ring + ks * kCodes + 16 * lane * D, &maps.k, tok & mask, (int)slab, &sh.k_full[ks]);
+          k_sent = count + 1;
           paged_tell(sh.info[count % kInfos], lane, id, sk, sv, v_ref);
           __syncwarp();
           if (lane == 0) tc05::mbar_arrive(&sh.info_full[count % kInfos]);
@@ -530,6 +533,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_wide_kernel(const PagedAttn
           if (lane == 0) tc05::mbar_expect_tx(&sh.r_full[vs], bytes);
           __syncwarp();
           if (copies) tma_load_codes(v_ring + vs * kCodes + 16 * lane * D, &maps.v, tok & mask, (int)slab, &sh.r_full[vs]);
+          v_sent = count + 1;
           id = id_next;
         }
       }
@@ -617,6 +621,17 @@ __global__ void __launch_bounds__(kThreads, 1) paged_wide_kernel(const PagedAttn
   __syncwarp();
   const int any_dead = __syncthreads_or(dead);
   if (tid == 0) p.open[blockIdx.x].pieces = any_dead ? 0 : pieces;
+  if (any_dead) {  // copies and products that are under way come to their end before the block does
+    if (warp == 13) {
+      paged_drain(sh.k_full, k_sent);
+      paged_drain(sh.r_full, v_sent);
+    } else if (warp == 12) {
+      if (elected()) tc05::mma_commit(&sh.drained);
+      __syncwarp();
+      paged_wait(&sh.drained, 0, kPagedTries);
+    }
+    __syncthreads();
+  }
   if (warp == 12) tc05::tmem_dealloc(tmem, 512);
 }
 

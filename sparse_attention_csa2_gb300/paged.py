@@ -63,6 +63,7 @@ _rope_axes = _sig("csa2_rope_axes", [C.POINTER(RopeAxesArgs), _vp], C.c_int)
 _write_pages = _sig("csa2_write_pages", [C.POINTER(WritePagesArgs), _vp], C.c_int)
 _paged_attn_ws = _sig("csa2_paged_attn_workspace_size", [C.POINTER(PagedAttnArgs)], _sz)
 _paged_attn = _sig("csa2_paged_attn", [C.POINTER(PagedAttnArgs), _vp], C.c_int)
+_paged_waits = _sig("csa2_selftest_paged_waits", [C.POINTER(PagedAttnArgs), _i32, _vp], C.c_int)
 
 
 _raw_stream = torch._C._cuda_getCurrentRawStream  # a device's current stream as a number
@@ -340,3 +341,10 @@ def paged_attn(q, cache: PageCache, row_start, kv_len, table, softmax_scale: flo
                out_dtype=None, dev_status=None):
     """Attention of the new tokens' queries over a paged 8-bit cache (see PagedAttn)."""
     return PagedAttn(q, cache, row_start, kv_len, table, softmax_scale, window, sink, out, out_dtype, dev_status)()
+
+
+def selftest_paged_waits(call: PagedAttn, tries: int) -> None:
+    """Runs a prepared call (with a dev_status) whose waits give up after `tries` tries
+    (csa2_selftest_paged_waits): its status then reads ETIMEOUT and its output holds anything."""
+    with torch.cuda.device(call._device):
+        _check(_paged_waits(call._ref, int(tries), _raw_stream(call._index)), "csa2_selftest_paged_waits")
