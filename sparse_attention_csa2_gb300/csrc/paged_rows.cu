@@ -222,6 +222,7 @@ __global__ void __launch_bounds__(kThreads, R == 16 ? 2 : 1)
   Walk<R> walk{p, u, u_end, sh.place_first, sh.place_seq, -1};
   Segment x;
   bool dead = false, bad = false;
+  int pieces = 0;                // of the tile that this block leaves open
   uint32_t count = 0, segs = 0;  // units, tiles of the block so far
   uint32_t k_sent = 0;           // K's copies (V's: count)
   auto wait = [&](uint64_t* bar, uint32_t parity) {
@@ -230,10 +231,11 @@ __global__ void __launch_bounds__(kThreads, R == 16 ? 2 : 1)
 
   if (warp < 4) {
     // ------------------------------------------------------------------ weights: a token per thread
+    // These warps meet at barriers of their own.  One whose wait ran out while another's was just in time must not
+    // leave it there: it goes on through all units and barriers, without waiting, to the block's end.
     const uint32_t lanes = tmem + ((uint32_t)(32 * warp) << 16);
     const uint32_t o_cols = lanes + 2 * R;
-    int pieces = 0;
-    while (walk.next(x) && !dead) {
+    while (walk.next(x)) {
       const int par = segs & 1;
       // what the units need of the tile, the rest waits in shared memory
       const int units = x.n, hi = x.hi;
@@ -247,10 +249,9 @@ __global__ void __launch_bounds__(kThreads, R == 16 ? 2 : 1)
       float v_ref = 0.f;
 #pragma unroll
       for (int r = 0; r < R / 2; ++r) l[r] = make_float2(0.f, 0.f), low[r] = make_float2(INFINITY, INFINITY);
-      for (int j = 0; j < units && !dead; ++j, ++count, tok0 += kTile) {
+      for (int j = 0; j < units; ++j, ++count, tok0 += kTile) {
         const int buf = count & 1;
         wait(&sh.s_full[buf], count >> 1 & 1);
-        if (dead) break;
         tc05::fence_after();
         uint32_t s[R];
         tc05::tmem_ld<R>(lanes + R * buf, s);
@@ -297,7 +298,7 @@ __global__ void __launch_bounds__(kThreads, R == 16 ? 2 : 1)
           }
         }
         // a first unit, a score 2^4 above its row's maximum, or a larger V reference: everything moves there
-        if (j == 0 || weights_any(over > kPagedSlack) || v_factor != 1.f) {
+        if (j == 0 || weights_any(over > kPagedSlack || v_factor != 1.f)) {
           float top[R];
 #pragma unroll
           for (int r = 0; r < R; ++r) top[r] = sees >> r & 1 ? (r & 1 ? t[r / 2].y : t[r / 2].x) : -INFINITY;
@@ -317,7 +318,6 @@ __global__ void __launch_bounds__(kThreads, R == 16 ? 2 : 1)
           }
           if (j > 0) {
             wait(&sh.pv_done, (count - 1) & 1);
-            if (dead) break;
             tc05::fence_after();
             uint32_t o[R];
             tc05::tmem_ld<R>(o_cols, o);
@@ -355,7 +355,6 @@ __global__ void __launch_bounds__(kThreads, R == 16 ? 2 : 1)
           }
         }
         if (count > 0) wait(&sh.pv_done, (count - 1) & 1);  // the weights before have been read
-        if (dead) break;
 #pragma unroll
         for (int k = 0; k < R / 8; ++k)
           *reinterpret_cast<uint4*>(p_tile + swizzled<2 * R>(tid, k)) = make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
@@ -363,7 +362,6 @@ __global__ void __launch_bounds__(kThreads, R == 16 ? 2 : 1)
         tc05::fence_before();
         tc05::mbar_arrive(&sh.p_full);
       }
-      if (dead) break;
       // ---- the tile's outputs, or its partial sums
       {
         float sum[R];
@@ -385,7 +383,6 @@ __global__ void __launch_bounds__(kThreads, R == 16 ? 2 : 1)
       weights_sync();
       wait(&sh.o_full, segs & 1);
       ++segs;
-      if (dead) break;
       tc05::fence_after();
       const auto tile = sh.tile;
       const bool starts = tile.blk == 0, ends = tile.end <= u_end;
@@ -397,7 +394,7 @@ __global__ void __launch_bounds__(kThreads, R == 16 ? 2 : 1)
       const int d = tid;
 #pragma unroll
       for (int r = 0; r < R; ++r) {
-        if (r >= tile.rows) break;
+        if (r >= tile.rows || dead) break;
         if (starts && ends) {
           const int rr = tile.row0 + r, i = by_group(p, rr);
           const long long at = ((long long)(tile.first_row + i) * (p.kv_heads * p.group) + tile.head * p.group + rr - i * p.group) * D + d;
@@ -421,7 +418,6 @@ __global__ void __launch_bounds__(kThreads, R == 16 ? 2 : 1)
         pieces = 0;
       }
     }
-    if (tid == 0) p.open[blockIdx.x].pieces = dead ? 0 : pieces;
   } else if (warp < 8) {
     // ------------------------------------------------------------------ query pieces; V to fp16
     const int gt = tid - 128;
@@ -626,7 +622,9 @@ __global__ void __launch_bounds__(kThreads, R == 16 ? 2 : 1)
   if (dead && p.dev_status) atomicExch(p.dev_status, (int)CSA2_ETIMEOUT);
   if (bad && p.dev_status) atomicExch(p.dev_status, (int)CSA2_EDEVICE_INDEX);
   __syncwarp();
-  if (__syncthreads_or(dead)) {  // copies and products that are under way come to their end before the block does
+  const int any_dead = __syncthreads_or(dead);
+  if (tid == 0) p.open[blockIdx.x].pieces = any_dead ? 0 : pieces;
+  if (any_dead) {  // copies and products that are under way come to their end before the block does
     if (warp == 8) {
       paged_drain(sh.k_full, k_sent);
       paged_drain(sh.v_full, count);

@@ -14,6 +14,8 @@ FORMS = {  # (new tokens, dim, heads of a group)
     "tiles of 8, dim 64": (1, 64, 8),
     "tiles of 8, dim 128": (1, 128, 8),
     "tiles of 16, dim 64": (1, 64, 16),
+    "tiles of 16, dim 128": (1, 128, 16),
+    "tiles of 32, dim 128": (1, 128, 32),
     "tiles of 256, dim 64": (40, 64, 4),
     "tiles of 256, dim 128": (40, 128, 4),
 }
