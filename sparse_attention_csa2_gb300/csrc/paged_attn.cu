@@ -30,10 +30,9 @@
 // three E4M3 pieces took more instructions, not fewer: an E4M3 mma.sync counts as two fp16 ones with the
 // conversions of both operands and four additions.  Per 32 tokens of 16 rows at dim 64, fp16: 808 against 614
 // at that time; 96 sequences of 5 drafted tokens each, window 1,024: 74 against 60 us.)  Weights are fp16 of
-// exp2(z - max + 11), where the maximum follows a larger score only when that exceeds it by 2^4:
-// weights are at most 2^15, those down to 2^-21 of the largest keep 11 bits, and the output is rarely
-// rescaled.  A page's V scale enters the weight relative to the largest seen.  Maxima,
-// sums and outputs are fp32.  For fp16 rows, whose outputs round as finely as the weights (2^-11), what the
+// exp2(u - max + 11), u = z + log2(the page's V scale), where the row's maximum of u follows a larger one only when
+// that exceeds it by 2^4: weights are at most 2^15, those down to 2^-25 of the largest keep 11 bits, and the output is
+// rarely rescaled (paged_dev.cuh).  Maxima, sums and outputs are fp32.  For fp16 rows, whose outputs round as finely as the weights (2^-11), what the
 // weights' rounding leaves is multiplied too: the error against 64 bits falls from 2.7e-4 to the output's own
 // 2.1e-4, at 5% of the time.
 #include "common.cuh"
@@ -90,7 +89,7 @@ __global__ void __launch_bounds__(kWarps * 32, D == 64 && NB == 1 ? 4 : 3)
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   __shared__ __align__(16) float scales[kWarps][ST][4];
   __shared__ __align__(8) uint64_t full[kWarps][ST];
-  __shared__ float ml[kWarps][NR][3];
+  __shared__ float ml[kWarps][NR][2];
   __shared__ long long scan_warp[kWarps];
   __shared__ long long place[2];        // sequence, its first unit
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, c = lane & 3;
@@ -318,7 +317,7 @@ __global__ void __launch_bounds__(kWarps * 32, D == 64 && NB == 1 ? 4 : 3)
     for (int i = 0; i < MT; ++i)
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb) acc[i][nb][0] = acc[i][nb][1] = acc[i][nb][2] = acc[i][nb][3] = 0.f;
-    float m[NB][2], l[NB][2], vref = 0.f, vinv = 0.f;
+    float m[NB][2], l[NB][2];
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) m[nb][0] = m[nb][1] = -INFINITY, l[nb][0] = l[nb][1] = 0.f;
 
@@ -358,6 +357,7 @@ __global__ void __launch_bounds__(kWarps * 32, D == 64 && NB == 1 ? 4 : 3)
 
       // a NaN in either scale marks the page: its visible tokens give NaN
       const float k0 = sc.x + 0.f * sc.z, k1 = sc.y + 0.f * sc.w;
+      const float v_log[2] = {paged_v_log(sc.z), paged_v_log(sc.w)};
       const bool whole = tok + kTok - 1 <= min(pos_first, t_end - 1) && tok >= lo_last && ok0 && ok1;
       bool grows = false;
 #pragma unroll
@@ -368,7 +368,7 @@ __global__ void __launch_bounds__(kWarps * 32, D == 64 && NB == 1 ? 4 : 3)
         for (int h = 0; h < 2; ++h)
 #pragma unroll
           for (int j = 0; j < 4; j += 2) {
-            const float2 z = mul2(make_float2(S[h][nb][j], S[h][nb][j + 1]), by[h]);
+            const float2 z = fma2(make_float2(S[h][nb][j], S[h][nb][j + 1]), by[h], make_float2(v_log[h], v_log[h]));
             S[h][nb][j] = z.x, S[h][nb][j + 1] = z.y;
           }
       }
@@ -394,13 +394,7 @@ __global__ void __launch_bounds__(kWarps * 32, D == 64 && NB == 1 ? 4 : 3)
           top[nb][j] = fmaxf(fmaxf(S[0][nb][j], S[0][nb][2 + j]), fmaxf(S[1][nb][j], S[1][nb][2 + j]));
           grows |= top[nb][j] > m[nb][j] + kPagedSlack;
         }
-      const float v0 = sc.z > 0.f ? sc.z : 0.f, v1 = sc.w > 0.f ? sc.w : 0.f;
-      grows |= fmaxf(v0, v1) > vref;
-      if (__any_sync(0xffffffffu, grows)) {  // a new maximum, of a row or of the V scales: what is there moves to it
-        const float vnew = fmaxf(vref, fmaxf(v0, v1));
-        if (vnew > vref) vinv = __fdiv_rn(1.f, vnew);
-        const float vf = vref * vinv;
-        vref = vnew;
+      if (__any_sync(0xffffffffu, grows)) {  // a new maximum: what is there moves to it
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) {
           float o[2];
@@ -412,7 +406,7 @@ __global__ void __launch_bounds__(kWarps * 32, D == 64 && NB == 1 ? 4 : 3)
             x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
             const float e = m[nb][j] == -INFINITY ? 0.f : ex2(m[nb][j] - x);
             l[nb][j] *= e;
-            o[j] = e * vf;
+            o[j] = e;
             m[nb][j] = x;
           }
 #pragma unroll
@@ -427,16 +421,16 @@ __global__ void __launch_bounds__(kWarps * 32, D == 64 && NB == 1 ? 4 : 3)
         float2 sum = make_float2(l[nb][0], l[nb][1]);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const float cv = (h ? v1 : v0) * vinv;
+          const float back = paged_v_back(v_log[h]);
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
             const float2 z = add2(make_float2(S[h][nb][2 * j], S[h][nb][2 * j + 1]), over);
-            const float2 e = make_float2(ex2(z.x), ex2(z.y)), ev = mul2(e, make_float2(cv, cv));
-            sum = add2(sum, e);
-            const uint32_t w = pack_f16x2(ev.x, ev.y);
+            const float2 e = make_float2(ex2(z.x), ex2(z.y));
+            sum = fma2(e, make_float2(back, back), sum);
+            const uint32_t w = pack_f16x2(e.x, e.y);
             pw[h][nb][j] = transpose8(w);
             if constexpr (F16) {
-              const float2 r = fma2(__half22float2(*reinterpret_cast<const __half2*>(&w)), make_float2(-1.f, -1.f), ev);
+              const float2 r = fma2(__half22float2(*reinterpret_cast<const __half2*>(&w)), make_float2(-1.f, -1.f), e);
               pr[h][nb][j] = transpose8(pack_f16x2(r.x, r.y));
             }
           }
@@ -519,7 +513,7 @@ __global__ void __launch_bounds__(kWarps * 32, D == 64 && NB == 1 ? 4 : 3)
           *reinterpret_cast<float4*>(to + 2 * i) = make_float4(acc[i][nb][j], acc[i][nb][2 + j], acc[i + 1][nb][j], acc[i + 1][nb][2 + j]);
         if (g == 0) {
           float* to_ml = ml[warp][8 * nb + 2 * c + j];
-          to_ml[0] = m[nb][j], to_ml[1] = l[nb][j], to_ml[2] = vref;
+          to_ml[0] = m[nb][j], to_ml[1] = l[nb][j];
         }
       }
     }
@@ -536,10 +530,10 @@ __global__ void __launch_bounds__(kWarps * 32, D == 64 && NB == 1 ? 4 : 3)
       for (int w = 0; w < kWarps; ++w) {
         const float mw = ml[w][r][0];
         if (mw == -INFINITY && ml[w][r][1] == 0.f) continue;  // a warp that saw nothing (not one whose sum is NaN)
-        const float e = mw == -INFINITY ? 1.f : ex2(mw - M), fw = e * ml[w][r][2];
+        const float e = mw == -INFINITY ? 1.f : ex2(mw - M);
         const float4 a = *reinterpret_cast<const float4*>(part + (w * NR + r) * D + d);
         L += ml[w][r][1] * e;
-        o.x += a.x * fw, o.y += a.y * fw, o.z += a.z * fw, o.w += a.w * fw;
+        o.x += a.x * e, o.y += a.y * e, o.z += a.z * e, o.w += a.w * e;
       }
       if (starts && ends) {
         const int rr = row0 + r, tokn = by_group(p, rr), hq = head * p.group + rr - tokn * p.group;

@@ -6,14 +6,31 @@
 
 namespace csa2 {
 
-constexpr float kPagedLift = 11.f;   // weights are held times 2^11,
-constexpr float kPagedSlack = 4.f;   // relative to a maximum that may be 2^4 too small
+// A row's weight of a token, as it multiplies the token's codes of V, is the softmax's times the V scale of the
+// token's page.  All forms hold it as 2^(u - M + 11) in fp16, u = z + log2(v scale) with the score z in log2 units
+// and M the running maximum of u over the tokens that the row has seen, which may be 2^4 too small: it stays 11 bits
+// down to 2^-25 of the row's largest, whatever the scales of pages that the row does not see or gives no weight.  The
+// softmax's sum takes each weight's fp32 value over its V scale, times 2^-20, which keeps the sum within
+// fp32 for V scales from 2^-100 (what lies below counts as that) to 2^100.
+constexpr float kPagedLift = 11.f;
+constexpr float kPagedSlack = 4.f;
+constexpr float kPagedBias = 20.f;
 
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
   return y;
 }
+
+// log2 of a page's V scale.  The exponent is taken out: near 1 the approximation's error is absolute, 2^-22.
+__device__ __forceinline__ float paged_v_log(float scale) {
+  const uint32_t u = __float_as_uint(fmaxf(scale, 7.888609e-31f));  // 2^-100; a NaN counts as that
+  float m;
+  asm("lg2.approx.ftz.f32 %0, %1;\n" : "=f"(m) : "f"(__uint_as_float((u & 0x7fffffu) | 0x3f800000u)));
+  return (float)((int)(u >> 23) - 127) + m;
+}
+// What a weight is multiplied by in the softmax's sum.
+__device__ __forceinline__ float paged_v_back(float v_log) { return ex2(-v_log - kPagedBias); }
 
 // Bounded wait of a whole warp for an mbarrier's phase that lets the hardware suspend it for about a microsecond
 // at a time: the default suspension is a few tens of cycles, and the parts of these kernels that wait then take
@@ -79,12 +96,12 @@ __device__ __forceinline__ void f16_pairs(uint32_t v, uint32_t& lo, uint32_t& hi
       : "r"(v));
 }
 
-// What a row's sums of weighted values, relative to its maximum M (log2 units), are to be multiplied by: one over
+// What a row's sums of weighted codes, relative to its maximum M (log2 units), are to be multiplied by: one over
 // its denominator.  A row that saw no key is 0.
 __device__ __forceinline__ float paged_factor(const PagedAttnParams& p, int head, float M, float L) {
   float den = L;
-  if (p.sink != nullptr && M > -INFINITY) den += ex2(p.sink[head] * 1.4426950408889634f - M + kPagedLift);
-  return L == 0.f ? 0.f : __fdividef(1.f, den);
+  if (p.sink != nullptr && M > -INFINITY) den += ex2(p.sink[head] * 1.4426950408889634f - M + (kPagedLift - kPagedBias));
+  return L == 0.f ? 0.f : __fdividef(9.5367432e-7f, den);  // 2^-kPagedBias
 }
 // Four values of an output row.
 template <int D>
@@ -100,38 +117,25 @@ __device__ __forceinline__ void paged_put(const PagedAttnParams& p, int row, int
   }
 }
 
-// What the warp that finds the pages tells the others about 128 tokens (kernels with a running V reference).
+// What the warp that finds the pages tells the others about 128 tokens.
 struct __align__(16) PagedInfo {
   float k_scale[8];   // of each 16 tokens
-  float v_log[8];     // log2 of their V scale over the reference, at least -100
-  float v_back[8];    // 2^-v_log
-  float v_factor;     // what the outputs so far are to be multiplied by: the V reference grew
-  float v_ref;
+  float v_log[8];     // paged_v_log of their V scale
+  float v_back[8];    // paged_v_back of that
   uint32_t flags;     // bits 0-7: 16 tokens have a page; 8-15: their scales say NaN
 };
 // Filled in by a whole warp, lane l (as l & 7) with the page id (-1: no token, -2: a bad entry) and scales of
-// tokens 16 l ..; the reference before becomes the one behind.
-__device__ __forceinline__ void paged_tell(PagedInfo& info, int lane, int id, float sk, float sv, float& v_ref) {
+// tokens 16 l ...
+__device__ __forceinline__ void paged_tell(PagedInfo& info, int lane, int id, float sk, float sv) {
   const uint32_t pages = __ballot_sync(0xffffffffu, id != -2) & 0xffu;
   const uint32_t nans = __ballot_sync(0xffffffffu, sk != sk || sv != sv) & 0xffu;
-  const float sv_here = sv > 0.f ? sv : 0.f;
-  float vm = sv_here;
-  vm = fmaxf(vm, __shfl_xor_sync(0xffffffffu, vm, 1));
-  vm = fmaxf(vm, __shfl_xor_sync(0xffffffffu, vm, 2));
-  vm = fmaxf(vm, __shfl_xor_sync(0xffffffffu, vm, 4));
-  const float v_new = fmaxf(v_ref, vm), v_inv = v_new > 0.f ? __fdiv_rn(1.f, v_new) : 0.f;
   if (lane < 8) {
-    const float ratio = fmaxf(sv_here * v_inv, 7.888609e-31f);  // 2^-100
+    const float v_log = paged_v_log(sv);
     info.k_scale[lane] = sk == sk ? sk : 0.f;
-    info.v_log[lane] = log2f(ratio);
-    info.v_back[lane] = __fdiv_rn(1.f, ratio);
-    if (lane == 0) {
-      info.v_factor = v_new > v_ref ? v_ref * v_inv : 1.f;
-      info.v_ref = v_new;
-      info.flags = pages | nans << 8;
-    }
+    info.v_log[lane] = v_log;
+    info.v_back[lane] = paged_v_back(v_log);
+    if (lane == 0) info.flags = pages | nans << 8;
   }
-  v_ref = v_new;
 }
 
 // n / group of a row index.  (The inverse is too large by less than one 2^64th, n below 2^31: exact.)

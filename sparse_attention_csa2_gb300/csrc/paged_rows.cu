@@ -246,7 +246,6 @@ __global__ void __launch_bounds__(kThreads, R == 16 ? 2 : 1)
       const long long tile_first = walk.tile_first(x);
       if (tid == 0) sh.tile = {x.s.first, x.row0, x.rows, x.head, x.blk, tile_first + x.blocks};
       float2 l[R / 2], low[R / 2];  // sums and minus the maxima of the rows
-      float v_ref = 0.f;
 #pragma unroll
       for (int r = 0; r < R / 2; ++r) l[r] = make_float2(0.f, 0.f), low[r] = make_float2(INFINITY, INFINITY);
       for (int j = 0; j < units; ++j, ++count, tok0 += kTile) {
@@ -259,8 +258,7 @@ __global__ void __launch_bounds__(kThreads, R == 16 ? 2 : 1)
         const int tok = tok0 + tid, g = tid >> 4;
         const uint32_t flags = info.flags;
         const float ks = flags >> (8 + g) & 1 ? __uint_as_float(0x7fc00000u) : info.k_scale[g];
-        const float lift = kPagedLift + info.v_log[g], v_back = info.v_back[g], v_factor = info.v_factor;
-        v_ref = info.v_ref;
+        const float v_log = info.v_log[g], v_back = info.v_back[g], lift = kPagedLift + v_log;
         const bool whole = flags == 0xffu && tok0 <= seen_hi && tok0 >= seen_lo;
         uint32_t sees = 0xffffffffu;  // bit r: row r sees the token
         if (!whole) {
@@ -276,7 +274,7 @@ __global__ void __launch_bounds__(kThreads, R == 16 ? 2 : 1)
         tc05::tmem_ld_wait();
         tc05::fence_before();
         tc05::mbar_arrive(&sh.s_free[buf]);
-        float2 t[R / 2];  // scores, then over the maxima
+        float2 t[R / 2];  // scores
         const float2 ks2 = make_float2(ks, ks);
         float over = -INFINITY;
 #pragma unroll
@@ -297,11 +295,11 @@ __global__ void __launch_bounds__(kThreads, R == 16 ? 2 : 1)
             if (sees >> (2 * r + 1) & 1) over = fmaxf(over, y.y);
           }
         }
-        // a first unit, a score 2^4 above its row's maximum, or a larger V reference: everything moves there
-        if (j == 0 || weights_any(over > kPagedSlack || v_factor != 1.f)) {
+        // a first unit, or a weight 2^4 above its row's maximum: everything moves there
+        if (j == 0 || weights_any(over + v_log > kPagedSlack)) {
           float top[R];
 #pragma unroll
-          for (int r = 0; r < R; ++r) top[r] = sees >> r & 1 ? (r & 1 ? t[r / 2].y : t[r / 2].x) : -INFINITY;
+          for (int r = 0; r < R; ++r) top[r] = sees >> r & 1 ? (r & 1 ? t[r / 2].y : t[r / 2].x) + v_log : -INFINITY;
           sh.part[warp][row_of_lane<R>(lane)] = over_rows<R>(top, lane, [](float a, float b) { return fmaxf(a, b); });
           weights_sync();
           if (tid < R) {
@@ -326,8 +324,8 @@ __global__ void __launch_bounds__(kThreads, R == 16 ? 2 : 1)
             for (int r = 0; r < R / 2; ++r) {
               const float2 a = *reinterpret_cast<const float2*>(&sh.alpha[2 * r]);
               l[r] = mul2(l[r], a);
-              o[2 * r] = __float_as_uint(__uint_as_float(o[2 * r]) * (a.x * v_factor));
-              o[2 * r + 1] = __float_as_uint(__uint_as_float(o[2 * r + 1]) * (a.y * v_factor));
+              o[2 * r] = __float_as_uint(__uint_as_float(o[2 * r]) * a.x);
+              o[2 * r + 1] = __float_as_uint(__uint_as_float(o[2 * r + 1]) * a.y);
             }
             if constexpr (R == 16) tc05::tmem_st16(o_cols, o);
             else tc05::tmem_st32(o_cols, o);
@@ -375,10 +373,10 @@ __global__ void __launch_bounds__(kThreads, R == 16 ? 2 : 1)
         float den = L;
         if (p.sink != nullptr && M > -INFINITY && tid < sh.tile.rows) {
           const int rr = sh.tile.row0 + tid;
-          den += ex2(p.sink[sh.tile.head * p.group + rr - by_group(p, rr) * p.group] * 1.4426950408889634f - M + kPagedLift);
+          den += ex2(p.sink[sh.tile.head * p.group + rr - by_group(p, rr) * p.group] * 1.4426950408889634f - M + (kPagedLift - kPagedBias));
         }
         sh.sum[tid] = L;
-        sh.alpha[tid] = L == 0.f ? 0.f : v_ref * __fdividef(1.f, den);
+        sh.alpha[tid] = L == 0.f ? 0.f : __fdividef(9.5367432e-7f, den);
       }
       weights_sync();
       wait(&sh.o_full, segs & 1);
@@ -403,7 +401,7 @@ __global__ void __launch_bounds__(kThreads, R == 16 ? 2 : 1)
           else if (p.out_dtype == CSA2_T_F16) static_cast<__half*>(p.out)[at] = __float2half_rn(val);
           else static_cast<__nv_bfloat16*>(p.out)[at] = __float2bfloat16_rn(val);
         } else {
-          p.part_o[(slot + r) * D + d] = __uint_as_float(o[r]) * v_ref;
+          p.part_o[(slot + r) * D + d] = __uint_as_float(o[r]);
           if (d == 0) *reinterpret_cast<float2*>(p.part_ml + (slot + r) * 2) = make_float2(sh.top[r], sh.sum[r]);
         }
       }
@@ -531,7 +529,6 @@ __global__ void __launch_bounds__(kThreads, R == 16 ? 2 : 1)
     const int page = 1 << p.page_shift, mask = page - 1;
     while (walk.next(x) && !dead) {
       const int32_t* trow = p.table + (long long)x.s.index * p.table_cols;
-      float v_ref = 0.f;
       // lane l (as l & 7) knows the page of tokens 16 l .. of a unit
       auto ids = [&](int j) {
         const int tok = x.lo + (x.blk + j) * kTile + 16 * (lane & 7);
@@ -563,7 +560,7 @@ __global__ void __launch_bounds__(kThreads, R == 16 ? 2 : 1)
         if (lane == 0) tc05::mbar_expect_tx(&sh.v_full[stage], bytes);
         __syncwarp();
         if (copies) tma_load_codes(v_ring + stage * kCodes + 16 * lane * D, &maps.v, tok & mask, (int)slab, &sh.v_full[stage]);
-        paged_tell(sh.info[count % kInfos], lane, id, sk, sv, v_ref);
+        paged_tell(sh.info[count % kInfos], lane, id, sk, sv);
         __syncwarp();
         if (lane == 0) tc05::mbar_arrive(&sh.info_full[count % kInfos]);
         id = id_next;

@@ -19,9 +19,8 @@
 //   2 x 4 warps  softmax, a row per thread: maximum, weights as fp16 over the scores' own columns,
 //             sum; the output is rescaled only where a score exceeds the running maximum by 2^4
 //
-// K's page scale multiplies the fp32 scores, V's (relative to the largest seen) is an addition to the
-// weight's exponent, taken back from each 16 tokens' sum.  Weights as in the split attention: at most
-// 2^15, 11 bits down to 2^-21 of the largest.
+// K's page scale multiplies the fp32 scores, V's is an addition to the weight's exponent, taken back from each 16
+// tokens' sum.  Weights as in the split attention: at most 2^15, 11 bits down to 2^-25 of the largest.
 //
 // Work is split as there: the units (128 tokens of a tile) of the call form one line, of which each
 // block (one per SM) takes an equal piece; open tiles leave partial sums that a second kernel joins.
@@ -289,7 +288,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_wide_kernel(const PagedAttn
         __syncwarp();
       }
       const float f = sh.factor[warp][lane];
-      float m = -INFINITY, v_ref = 0.f;
+      float m = -INFINITY;
       float2 l2 = make_float2(0.f, 0.f);
       const int see_hi = min(pos + 1, x.g.hi), see_lo = first_seen(p, pos);
       for (int j = 0; j < x.n && !dead; ++j, ++count, ++turn) {
@@ -304,14 +303,12 @@ __global__ void __launch_bounds__(kThreads, 1) paged_wide_kernel(const PagedAttn
           const float4 k4 = *reinterpret_cast<const float4*>(info.k_scale + 4 * half);
           const float4 l4 = *reinterpret_cast<const float4*>(info.v_log + 4 * half);
           const float4 b4 = *reinterpret_cast<const float4*>(info.v_back + 4 * half);
-          const float v_factor = half == 0 ? info.v_factor : 1.f;
-          v_ref = info.v_ref;
           const float k_scale[4] = {f * k4.x, f * k4.y, f * k4.z, f * k4.w};  // of 16 tokens each
           const float v_log[4] = {l4.x, l4.y, l4.z, l4.w}, v_back[4] = {b4.x, b4.y, b4.z, b4.w};
           const int hi = see_hi - tok - 64 * half, lo = see_lo - tok - 64 * half;  // the row sees columns lo .. hi - 1
           const uint32_t flags = info.flags >> 4 * half & 0xf0fu;                   // bits 0-3 and 8-11
           const bool whole = __all_sync(0xffffffffu, hi >= 64 && lo <= 0) && flags == 0xfu;
-          // the scores' maximum: of columns that all rows of the warp see from registers, where the scores then
+          // the weights' maximum: of columns that all rows of the warp see from registers, where the scores then
           // stay; otherwise 32 at a time from tensor memory, hidden ones left out
           float top = -INFINITY;
           uint32_t v[2][32];
@@ -325,7 +322,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_wide_kernel(const PagedAttn
               float a = __uint_as_float(v[c][0]), b = __uint_as_float(v[c][16]);
 #pragma unroll
               for (int k = 1; k < 16; ++k) a = fmaxf(a, __uint_as_float(v[c][k])), b = fmaxf(b, __uint_as_float(v[c][16 + k]));
-              top = fmaxf(top, fmaxf(a * k_scale[2 * c], b * k_scale[2 * c + 1]));
+              top = fmaxf(top, fmaxf(fmaf(a, k_scale[2 * c], v_log[2 * c]), fmaf(b, k_scale[2 * c + 1], v_log[2 * c + 1])));
             }
           } else {
 #pragma unroll 1
@@ -340,13 +337,13 @@ __global__ void __launch_bounds__(kThreads, 1) paged_wide_kernel(const PagedAttn
                 if (col + k < span) a = fmaxf(a, __uint_as_float(y[k]));
                 if (col + 16 + k < span) b = fmaxf(b, __uint_as_float(y[16 + k]));
               }
-              const float* ks = info.k_scale + 4 * half + 2 * c;
-              if ((flags >> (2 * c) & 1) && a > -INFINITY) top = fmaxf(top, a * (f * ks[0]));
-              if ((flags >> (2 * c + 1) & 1) && b > -INFINITY) top = fmaxf(top, b * (f * ks[1]));
+              const float *ks = info.k_scale + 4 * half + 2 * c, *vl = info.v_log + 4 * half + 2 * c;
+              if ((flags >> (2 * c) & 1) && a > -INFINITY) top = fmaxf(top, fmaf(a, f * ks[0], vl[0]));
+              if ((flags >> (2 * c + 1) & 1) && b > -INFINITY) top = fmaxf(top, fmaf(b, f * ks[1], vl[1]));
             }
           }
           const bool grows = top > m + kPagedSlack;
-          if (__any_sync(0xffffffffu, grows) || v_factor != 1.f) {
+          if (__any_sync(0xffffffffu, grows)) {
             const float to = grows ? top : m;
             const float e = m == -INFINITY ? 0.f : to == m ? 1.f : ex2(m - to);
             l2.x *= e, l2.y *= e;
@@ -355,14 +352,13 @@ __global__ void __launch_bounds__(kThreads, 1) paged_wide_kernel(const PagedAttn
               wait(&sh.o_done[t][half ^ 1], (turn - (half ^ 1)) & 1);  // the products before: this unit's, or the last one's
               if (dead) break;
               tc05::fence_after();
-              const float o = e * v_factor;
 #pragma unroll 1
               for (int c = 0; c < D / 16; ++c) {
                 uint32_t y[16];
                 tc05::tmem_ld16(o_cols + 16 * c, y);
                 tc05::tmem_ld_wait();
 #pragma unroll
-                for (int k = 0; k < 16; ++k) y[k] = __float_as_uint(__uint_as_float(y[k]) * o);
+                for (int k = 0; k < 16; ++k) y[k] = __float_as_uint(__uint_as_float(y[k]) * e);
                 tc05::tmem_st16(o_cols + 16 * c, y);
               }
             }
@@ -427,7 +423,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_wide_kernel(const PagedAttn
       const float L = l2.x + l2.y;
       const long long slot = (2LL * blockIdx.x + (starts ? 1 : 0)) * kRows + r;
       const int head = x.h * p.group + rr - i * p.group;
-      const float factor = starts && ends ? v_ref * paged_factor(p, head, m, L) : v_ref;
+      const float factor = starts && ends ? paged_factor(p, head, m, L) : 1.f;
 #pragma unroll 1
       for (int c = 0; c < D / 32; ++c) {
         uint32_t v[32];
@@ -438,7 +434,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_wide_kernel(const PagedAttn
           if (!has) break;
           const float4 o = make_float4(__uint_as_float(v[k]), __uint_as_float(v[k + 1]), __uint_as_float(v[k + 2]), __uint_as_float(v[k + 3]));
           if (starts && ends) paged_put<D>(p, x.s.first + i, head, 32 * c + k, o, factor);
-          else *reinterpret_cast<float4*>(p.part_o + slot * D + 32 * c + k) = make_float4(o.x * factor, o.y * factor, o.z * factor, o.w * factor);
+          else *reinterpret_cast<float4*>(p.part_o + slot * D + 32 * c + k) = o;
         }
       }
       if (has && !(starts && ends)) *reinterpret_cast<float2*>(p.part_ml + slot * 2) = make_float2(m, L);
@@ -500,7 +496,6 @@ __global__ void __launch_bounds__(kThreads, 1) paged_wide_kernel(const PagedAttn
       uint32_t count = 0;
       while (walk.next(x) && !dead) {
         const int32_t* trow = p.table + (long long)x.s.index * p.table_cols;
-        float v_ref = 0.f;
         // lane l (as l & 7) knows the page of tokens 16 l .. of a unit
         auto ids = [&](int j) {
           const int tok = x.g.lo + (x.blk + j) * kTile + 16 * (lane & 7);
@@ -525,7 +520,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_wide_kernel(const PagedAttn
           __syncwarp();
           if (copies) tma_load_codes(k_ring + ks * kCodes + 16 * lane * D, &maps.k, tok & mask, (int)slab, &sh.k_full[ks]);
           k_sent = count + 1;
-          paged_tell(sh.info[count % kInfos], lane, id, sk, sv, v_ref);
+          paged_tell(sh.info[count % kInfos], lane, id, sk, sv);
           __syncwarp();
           if (lane == 0) tc05::mbar_arrive(&sh.info_full[count % kInfos]);
           wait(&sh.r_free[vs], (count / VS & 1) ^ 1);
