@@ -200,6 +200,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_wide_kernel(const PagedAttn
         first += n;
       });
     }
+    // with many sequences the list of tiles reaches into the ring that copies fill next
+    asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
     tc05::fence_before();
     __syncthreads();
     tc05::fence_after();

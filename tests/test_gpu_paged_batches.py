@@ -1,0 +1,58 @@
+"""Paged attention over many sequences: every form's way to find its place on the line of work, with
+several sequences per thread and where the choice of form changes."""
+import numpy as np
+import pytest
+import torch
+
+from paged_bounds import attend
+from paged_testlib import cuda, make, values
+
+pytestmark = pytest.mark.gpu
+
+S = pytest.importorskip("sparse_attention_csa2_gb300")
+
+
+@pytest.fixture(autouse=True)
+def _cuda():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+
+
+def _run(c, G, dtype="bf16", window=0, seed=0):
+    D, rng = c["D"], np.random.default_rng(seed)
+    q, qd = values((c["rows"], c["H"] * G, D), rng, dtype)
+    cache = S.PageCache(*(cuda(c[k]) for k in ("k", "v", "ks", "vs")))
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    got = S.paged_attn(q.cuda(), cache, cuda(c["row_start"]), cuda(c["kv"]), cuda(c["table"]), D ** -0.5, window=window,
+                       out_dtype=torch.float32, dev_status=status).double().cpu().numpy()
+    ref, tol = attend(qd, c, D ** -0.5, window, None, 2.0 ** -22)
+    assert S.read_device_status(status) == S.OK
+    assert np.all(np.abs(got - ref) <= tol)
+
+
+@pytest.mark.parametrize("n", [31, 32, 33, 128, 129, 400, 1100])
+@pytest.mark.parametrize("D,G", [(64, 2), (128, 2), (64, 16), (128, 16), (128, 32)])
+def test_a_decode_step_of_many_sequences(n, D, G):
+    rng = np.random.default_rng(n)
+    kv = rng.integers(0, 150, n)  # some rows see no token at all
+    kv[rng.integers(n)] = 900
+    _run(make([1] * n, kv, 16, 1, D, seed=n), G)
+
+
+@pytest.mark.parametrize("n", [33, 321, 513, 1100])
+@pytest.mark.parametrize("D,G,most", [(64, 4, 4), (128, 4, 4), (128, 4, 8), (64, 4, 30), (128, 4, 30)])
+def test_drafts_and_prompts_of_many_sequences(n, D, G, most):
+    """Ragged, every fourth without a row."""
+    rng = np.random.default_rng(n + most)
+    new = rng.integers(most // 2 + 1, most * 3 // 2 + 2, n)
+    new[rng.random(n) < 0.25] = 0
+    _run(make(new, new + rng.integers(0, 60, n), 16, 1, D, seed=n), G, window=0 if n % 2 else 40)
+
+
+@pytest.mark.parametrize("D,dtype", [(64, "bf16"), (64, "f16"), (128, "bf16")])
+@pytest.mark.parametrize("n", [9000, 16384, 16385])
+def test_prompts_of_thousands_of_sequences(n, D, dtype):
+    """Tiles of 256 up to 16,384 sequences, small tiles beyond."""
+    rng = np.random.default_rng(n)
+    new = rng.integers(2, 4, n)
+    _run(make(new, new + rng.integers(0, 20, n), 16, 1, D, seed=n), 16, dtype)
