@@ -628,7 +628,8 @@ csa2_status csa2_page_plan(const csa2_page_plan_args* a, void* stream);
  *   (u, v) -> (u cos - v sin, u sin + v cos),
  * pairs (2i, 2i+1) or, with half_pairs, (i, i + rot_dim/2), counted from dim rot_first.  `inverse`
  * turns back, which is also the gradient with respect to x.  The other dims are copied.  Angles
- * are formed modulo a turn in 64-bit fixed point (any position), the rotation in fp32. */
+ * are formed modulo a turn in 64-bit fixed point, |pos| * 2^-64 turns off at most (below fp32's own
+ * rounding up to positions of 2^38; theta >= 1), the rotation in fp32. */
 #define CSA2_ROPE_AXES_MAX_PAIRS 128
 typedef struct {
   int32_t n_tokens;           /* >= 0 */

@@ -20,21 +20,30 @@ int type_size(int32_t t) { return t == CSA2_T_F32 ? 4 : 2; }
 bool stride_ok(int64_t row, int64_t head, int32_t t) { return row % (16 / type_size(t)) == 0 && head % (16 / type_size(t)) == 0; }
 int page_shift(int32_t page) { return page == 16 ? 4 : page == 32 ? 5 : page == 64 ? 6 : page == 128 ? 7 : 0; }
 
-// Turns per position of each pair, times 2^64, whole turns left out: theta^(-2i/R) / (2 pi).  A model calls with
-// one theta and R, so the thread's last table is kept (64 powers take longer than a launch).
+// Turns per position of each pair, times 2^64, whole turns left out: theta^(-2i/R) / (2 pi).  A double's 53 bits
+// would be off by 2^-56 of a turn per position; long double (113 bits on Arm, 64 on x86) keeps 2^-64, as powers of one
+// root, whose errors of i roundings the powers' decay outruns.  A model calls with one theta and R, or some by turns,
+// so the thread's last tables are kept (a table takes longer than a launch).
 const uint64_t* rope_turns(float theta, int rot_dim) {
-  thread_local float last_theta = 0.f;
-  thread_local int last_dim = 0;
-  thread_local uint64_t turns[CSA2_ROPE_AXES_MAX_PAIRS];
-  if (theta != last_theta || rot_dim != last_dim) {
-    for (int i = 0; i < rot_dim / 2; ++i) {
-      double t = std::pow((double)theta, -2.0 * i / (double)rot_dim) / 6.283185307179586476925286766559;
-      t -= std::floor(t);
-      turns[i] = (uint64_t)std::ldexp(t, 64);
-    }
-    last_theta = theta, last_dim = rot_dim;
+  struct Table {
+    float theta;
+    int rot_dim;
+    uint64_t turns[CSA2_ROPE_AXES_MAX_PAIRS];
+  };
+  thread_local Table kept[4] = {};
+  thread_local int next = 0;
+  for (const Table& k : kept)
+    if (k.theta == theta && k.rot_dim == rot_dim) return k.turns;
+  Table& k = kept[next];
+  next = (next + 1) % 4;
+  const long double root = std::pow((long double)theta, -2.0L / rot_dim);
+  long double t = 1.0L / 6.283185307179586476925286766559005768L;
+  for (int i = 0; i < rot_dim / 2; ++i, t *= root) {
+    const long double units = std::rint(std::ldexp(t - std::floor(t), 64));
+    k.turns[i] = units < 18446744073709551616.0L ? (uint64_t)units : 0;
   }
-  return turns;
+  k.theta = theta, k.rot_dim = rot_dim;
+  return k.turns;
 }
 
 // Which kernel, and its workspace, by the query rows per sequence and kv head in the mean.

@@ -150,8 +150,9 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const PagePlanP
 // inverse turns by -angle, which is also the gradient: R is orthogonal.
 //
 // The angle is formed in turns as a 64-bit fixed-point product, position times frequency modulo one
-// turn: exact but for the frequency's own rounding to 2^-64 (53 bits of it significant), so that
-// positions of any size keep their full accuracy with one integer multiplication and no reduction.
+// turn: exact but for the frequency's own rounding to 2^-64, so that one integer multiplication
+// without a reduction keeps fp32's accuracy up to positions of some 2^38 (beyond, off by a 2^-64th of
+// the position in turns).
 //
 // A thread owns one 16-byte piece of a token's head (for half-split pairs: the two pieces of
 // partners) and walks the heads with it, so that its angles' sines are formed once and stay in
