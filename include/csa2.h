@@ -598,9 +598,9 @@ typedef enum csa2_type { CSA2_T_BF16 = 0, CSA2_T_F16 = 1, CSA2_T_F32 = 2 } csa2_
  *   slot[r]       = table[b, pos / page] * page + pos % page       (csa2_write_records' dst_row)
  * Rows behind the last sequence get -1 in all three.  Where free_pages or table_cols do not
  * suffice, the missing entries and slots are -1; where rows exceed max_rows, the rest are left
- * out; both, a negative entry among a sequence's cached pages, and lengths above 2^30 (a
- * sequence's most, cached and new) or whose sums reach 2^31 are reported as CSA2_EDEVICE_INDEX
- * through dev_status.  Running a plan again on its own table repeats it. */
+ * out; both, a negative entry for the partly filled page that a sequence's new rows join, and
+ * lengths above 2^30 (a sequence's most, cached and new) or whose sums reach 2^31 are reported as
+ * CSA2_EDEVICE_INDEX through dev_status.  Entries of pages that get no new row are not read.  Running a plan again on its own table repeats it. */
 typedef struct {
   const int32_t* ctx_len;     /* [n_seq] */
   const int32_t* new_len;     /* [n_seq] */

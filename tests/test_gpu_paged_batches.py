@@ -56,3 +56,17 @@ def test_prompts_of_thousands_of_sequences(n, D, dtype):
     rng = np.random.default_rng(n)
     new = rng.integers(2, 4, n)
     _run(make(new, new + rng.integers(0, 20, n), 16, 1, D, seed=n), 16, dtype)
+
+
+def test_the_plan_reads_only_the_page_that_new_rows_join():
+    """A negative entry there is reported, and its rows have no slot; entries of full pages are not read."""
+    for at, ctx, bad in ((1, 20, True), (0, 20, False), (1, 32, False)):
+        table = np.array([[4, 5, -1, -1]], np.int32)
+        table[0, at] = -7
+        t, status = cuda(table), torch.zeros(1, dtype=torch.int32, device="cuda")
+        p = S.page_plan(cuda(np.array([ctx], np.int32)), cuda(np.array([14], np.int32)), t, cuda(np.array([8, 9], np.int32)), 16, 14,
+                        dev_status=status)
+        assert (S.read_device_status(status) == S.EDEVICE_INDEX) == bad
+        join = 32 - ctx
+        assert p.slot.tolist() == [-1 if bad else 5 * 16 + (ctx + i) % 16 for i in range(join)] + [8 * 16 + i for i in range(14 - join)]
+        assert t.tolist() == [[*table[0, :2].tolist(), 8, -1]]
