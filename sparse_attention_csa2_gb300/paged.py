@@ -187,11 +187,15 @@ class RopeAxes(_Prepared):
     strided) turned by pos [axes, T] int64 ([T] for one axis).  `sections` gives each axis its number
     of consecutive pairs, `axis_of_pair` any other assignment; without either, one axis.  `pairing`:
     "half" pairs dim i with i + rot_dim / 2, "adjacent" 2i with 2i + 1.  `inverse` turns back, which is
-    the gradient.  `out` may be x itself."""
+    the gradient.  `out` may be x itself.  A prepared call builds no autograd graph: an x whose gradient
+    torch would track is refused (rope_axes without `out` takes it)."""
     _name = "csa2_rope_axes"
 
     def __init__(self, x, pos, sections=None, axis_of_pair=None, theta: float = 10000.0, rot_dim=None,
                  rot_first: int = 0, pairing: str = "half", inverse: bool = False, out=None):
+        if x.requires_grad and torch.is_grad_enabled():
+            raise ValueError("x requires a gradient, which a prepared call or one with `out` does not record: call rope_axes "
+                             "without `out`, or under torch.no_grad()")
         dev = x.device
         a = RopeAxesArgs()
         a.x, a.x_row, a.x_head = _heads(x, "x")
@@ -231,9 +235,29 @@ class RopeAxes(_Prepared):
         return self.out
 
 
+class _Turn(torch.autograd.Function):
+    """rope_axes where x's gradient is tracked: the gradient is turned back."""
+
+    @staticmethod
+    def forward(ctx, x, pos, how, inverse):
+        ctx.save_for_backward(pos)
+        ctx.how, ctx.inverse = how, inverse
+        return RopeAxes(x, pos, *how, inverse)()
+
+    @staticmethod
+    def backward(ctx, grad):
+        grad = grad.contiguous()  # a sum's gradient is a broadcast tensor
+        if grad.data_ptr() % 16:
+            grad = grad.clone()
+        return rope_axes(grad, ctx.saved_tensors[0], *ctx.how, not ctx.inverse), None, None, None
+
+
 def rope_axes(x, pos, sections=None, axis_of_pair=None, theta: float = 10000.0, rot_dim=None, rot_first: int = 0,
               pairing: str = "half", inverse: bool = False, out=None):
-    """x with its rotary dims turned by positions of several axes (see RopeAxes)."""
+    """x with its rotary dims turned by positions of several axes (see RopeAxes).  Differentiable in x
+    unless `out` is given."""
+    if out is None and x.requires_grad and torch.is_grad_enabled():
+        return _Turn.apply(x, pos, (sections, axis_of_pair, theta, rot_dim, rot_first, pairing), bool(inverse))
     return RopeAxes(x, pos, sections, axis_of_pair, theta, rot_dim, rot_first, pairing, inverse, out)()
 
 
