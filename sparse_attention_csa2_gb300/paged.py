@@ -78,6 +78,8 @@ def _dense(t, name, dtype, shape, device=None):
 
 
 def _on(t, name, device=None):
+    if any(n >= 2 ** 31 for n in t.shape):  # the C struct would cut it
+        raise ValueError(f"{name} must be below 2^31 in every dimension, got {tuple(t.shape)}")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
     if device is not None and t.device != device:
