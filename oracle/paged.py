@@ -90,9 +90,9 @@ def write_pages(codes, scale, x, row_start, kv_len, table):
                 while e < 119 and 448.0 * 2.0 ** e < peak:
                     e += 1
                 need = 2.0 ** e
-                if o and scale[g, h] > need:
-                    need = scale[g, h]
                 nan = bool(np.isnan(part).any()) or bool(o and np.isnan(scale[g, h]))
+                if o and not nan and scale[g, h] > need:
+                    need = scale[g, h]
                 if o and not nan and scale[g, h] < need:
                     codes[g, h, :o] = e4m3_codes(val[codes[g, h, :o]] * (scale[g, h] / need))
                 codes[g, h, o:o + n] = e4m3_codes(part / need)

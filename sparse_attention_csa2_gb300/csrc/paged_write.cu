@@ -222,7 +222,7 @@ __global__ void __launch_bounds__(kThreads, HELD == 1 ? 6 : 4) page_write_kernel
     }
     float s = amax > 0.f ? scale_for(amax) : __uint_as_float((uint32_t)(kExpMin + 127) << 23);
     nan |= old != old;
-    if (off && old > s) s = old;
+    if (off && !nan && old > s) s = old;  // codes of a page that says NaN go by its new rows alone: the same again
     if (off && !nan && old < s) {  // older tokens move to the larger scale
       const float f = __fdiv_rn(old, s);
       for (int i = gt; i < off * (D / 8); i += gn) {

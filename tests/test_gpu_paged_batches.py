@@ -4,6 +4,7 @@ import numpy as np
 import pytest
 import torch
 
+import oracle.paged as OP
 from paged_bounds import attend
 from paged_testlib import cuda, make, values
 
@@ -70,3 +71,25 @@ def test_the_plan_reads_only_the_page_that_new_rows_join():
         join = 32 - ctx
         assert p.slot.tolist() == [-1 if bad else 5 * 16 + (ctx + i) % 16 for i in range(join)] + [8 * 16 + i for i in range(14 - join)]
         assert t.tolist() == [[*table[0, :2].tolist(), 8, -1]]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+def test_writing_again_repeats_pages_with_a_nan(dtype):
+    """A NaN among the rows that join a page of larger, smaller or NaN scale: the second call leaves what the first wrote."""
+    c = make([3, 3, 3, 20], [40, 41, 42, 50], 16, 2, 64, seed=3)
+    k, kd = values((c["rows"], 2, 64), np.random.default_rng(4), dtype)
+    k[[1, 4, 7, 9], :, 5] = float("nan")
+    kd = k.double().numpy()
+    for b, s in enumerate((2.0 ** 8, 2.0 ** -20, np.nan, 2.0 ** 8)):
+        for j in range((c["kv"][b] - c["new"][b]) // 16, -(-c["kv"][b] // 16)):
+            c["ks"][c["table"][b, j]] = s
+    c["vs"] = c["ks"].copy()
+    cache = S.PageCache(*(cuda(c[x]) for x in ("k", "v", "ks", "vs")))
+    seq = cuda(np.repeat(np.arange(4), c["new"]).astype(np.int32))
+    args = (cache, k.cuda(), k.cuda(), cuda(c["row_start"]), cuda(c["kv"]), seq, cuda(c["table"]))
+    S.write_pages(*args)
+    once = [t.clone() for t in cache]
+    rc, rs = OP.write_pages(c["k"], c["ks"], kd, c["row_start"], c["kv"], c["table"])
+    assert np.array_equal(cache.k.cpu().numpy(), rc) and np.array_equal(cache.k_scale.cpu().numpy().astype(np.float64), rs, equal_nan=True)
+    S.write_pages(*args)
+    assert all(torch.equal(a.view(torch.uint8), b.view(torch.uint8)) for a, b in zip(once, cache))
