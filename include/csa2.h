@@ -679,8 +679,8 @@ typedef struct {
   const int32_t* row_start;   /* [n_seq + 1] */
   const int32_t* kv_len;      /* [n_seq] tokens with the new ones */
   const int32_t* seq_of_row;  /* [n_rows] */
-  const int32_t* table;       /* [n_seq, table_cols] */
-  uint8_t* k_codes;           /* [n_pages, kv_heads, page_size, head_dim] */
+  const int32_t* table;       /* [n_seq, table_cols]; may be NULL with no columns */
+  uint8_t* k_codes;           /* [n_pages, kv_heads, page_size, head_dim]; these four may be NULL with no pages */
   uint8_t* v_codes;
   float* k_scale;             /* [n_pages, kv_heads] */
   float* v_scale;
@@ -717,8 +717,8 @@ typedef struct {
   int64_t q_row, q_head;      /* strides in elements, multiples of 16 bytes */
   const int32_t* row_start;   /* [n_seq + 1] ascending */
   const int32_t* kv_len;      /* [n_seq] */
-  const int32_t* table;       /* [n_seq, table_cols] */
-  const uint8_t* k_codes;
+  const int32_t* table;       /* [n_seq, table_cols]; may be NULL with no columns */
+  const uint8_t* k_codes;     /* these four may be NULL with no pages */
   const uint8_t* v_codes;
   const float* k_scale;
   const float* v_scale;

@@ -167,8 +167,8 @@ csa2_status csa2_write_pages(const csa2_write_pages_args* a, void* stream) {
   if ((a->head_dim != 64 && a->head_dim != 128) || !page_shift(a->page_size) || a->kv_heads > 65535)
     return CSA2_EUNSUPPORTED;
   if (a->n_rows == 0 || a->n_seq == 0) return CSA2_OK;
-  if (!a->k || !a->v || !a->row_start || !a->kv_len || !a->seq_of_row || !a->table || !a->k_codes || !a->v_codes ||
-      !a->k_scale || !a->v_scale)
+  if (!a->k || !a->v || !a->row_start || !a->kv_len || !a->seq_of_row || (a->table_cols > 0 && !a->table) ||
+      (a->n_pages > 0 && (!a->k_codes || !a->v_codes || !a->k_scale || !a->v_scale)))
     return CSA2_EINVAL;
   if (!aligned(a->k, 16) || !aligned(a->v, 16) || !aligned(a->k_codes, 16) || !aligned(a->v_codes, 16) ||
       !stride_ok(a->k_row, a->k_head, a->dtype) || !stride_ok(a->v_row, a->v_head, a->dtype))
@@ -202,8 +202,8 @@ static csa2_status paged_attn(const csa2_paged_attn_args* a, uint32_t wait_tries
       !std::isfinite(a->softmax_scale))
     return CSA2_EINVAL;
   if (a->n_rows == 0 || a->n_seq == 0) return CSA2_OK;
-  if (!a->q || !a->out || !a->row_start || !a->kv_len ||
-      ((a->table_cols > 0) && (!a->table || !a->k_codes || !a->v_codes || !a->k_scale || !a->v_scale)))
+  if (!a->q || !a->out || !a->row_start || !a->kv_len || (a->table_cols > 0 && !a->table) ||
+      (a->table_cols > 0 && a->n_pages > 0 && (!a->k_codes || !a->v_codes || !a->k_scale || !a->v_scale)))
     return CSA2_EINVAL;
   if (!aligned(a->q, 16) || !aligned(a->out, 16) || !aligned(a->k_codes, 16) || !aligned(a->v_codes, 16) ||
       !stride_ok(a->q_row, a->q_head, a->q_dtype))
@@ -218,6 +218,7 @@ static csa2_status paged_attn(const csa2_paged_attn_args* a, uint32_t wait_tries
   p.row_start = a->row_start, p.kv_len = a->kv_len, p.table = a->table;
   p.table_cols = a->table_cols, p.n_pages = a->n_pages, p.page_shift = page_shift(a->page_size);
   p.k = a->k_codes, p.v = a->v_codes, p.k_scale = a->k_scale, p.v_scale = a->v_scale;
+  if (!p.k_scale || !p.v_scale) p.k_scale = p.v_scale = reinterpret_cast<const float*>(ws);  // no pages: copies of no bytes name an address
   p.scale_log2 = a->softmax_scale * 1.4426950408889634f;
   p.window = a->window, p.sink = a->sink;
   p.out = a->out, p.out_dtype = a->out_dtype;

@@ -93,3 +93,23 @@ def test_writing_again_repeats_pages_with_a_nan(dtype):
     assert np.array_equal(cache.k.cpu().numpy(), rc) and np.array_equal(cache.k_scale.cpu().numpy().astype(np.float64), rs, equal_nan=True)
     S.write_pages(*args)
     assert all(torch.equal(a.view(torch.uint8), b.view(torch.uint8)) for a, b in zip(once, cache))
+
+
+@pytest.mark.parametrize("D,G,new", [(64, 2, 1), (64, 16, 1), (128, 2, 1), (128, 16, 1), (128, 32, 1), (64, 2, 40), (128, 2, 40)])
+def test_a_cache_without_pages_under_a_table_with_columns(D, G, new):
+    """Tokens there are none of: rows of 0, nothing to report.  Tokens whose pages are not there: hidden and reported."""
+    T = 3 * new
+    i32 = lambda *v: torch.tensor(v, dtype=torch.int32, device="cuda")  # noqa: E731
+    cache, status = S.PageCache.empty(0, 2, 16, D), i32(0)
+    table = torch.full((3, 4), -1, dtype=torch.int32, device="cuda")
+    rows = i32(0, new, 2 * new, 3 * new)
+    q = torch.randn((T, 2 * G, D), device="cuda").bfloat16()
+    for kv, said in ((0, S.OK), (50, S.EDEVICE_INDEX)):
+        out = torch.full(q.shape, 7.0, dtype=torch.bfloat16, device="cuda")
+        S.paged_attn(q, cache, rows, i32(kv, kv, kv), table, 0.1, out=out, dev_status=status)
+        assert S.read_device_status(status) == said and not bool(out.any())
+    for t in (table, table[:, :0].contiguous()):
+        status.zero_()
+        seq = torch.arange(3, dtype=torch.int32, device="cuda").repeat_interleave(new)
+        S.write_pages(cache, q[:, :2], q[:, :2], rows, i32(new, new, new), seq, t, dev_status=status)
+        assert S.read_device_status(status) == S.EDEVICE_INDEX
