@@ -695,13 +695,14 @@ csa2_status csa2_write_pages(const csa2_write_pages_args* a, void* stream);
  *   z_j = softmax_scale * q . k_j  for tokens j <= p, and j > p - window where window > 0
  *   out = sum_j exp(z_j) v_j / (sum_j exp(z_j) + exp(sink[h]))
  * A row without such a token is 0.  Rows outside [0, row_start[n_seq]) of q and out are left.
- * A table entry outside [0, n_pages) hides its tokens and is reported; kv_len beyond the table
- * counts as its end.  Codes 0x7f and 0xff (E4M3's NaN, which csa2_write_pages does not write)
- * must not occur among a sequence's tokens; scales are >= 0 or NaN, and code * scale of V is at
- * most 2^80.  A V scale below 2^-100 counts as 2^-100.  A row is computed relative to the largest
- * weight * v_scale among its own tokens, in fp32 and (weights) fp16: pages that it does not see
- * or gives no weight may have any scale; among those with weight, tokens 2^110 below the largest
- * by their V scale may be missing from the row's softmax sum. */
+ * A table entry outside [0, n_pages) hides its tokens and is reported; of a kv_len beyond the
+ * table only the table's tokens are there (the rows' positions stay the length's).  Codes 0x7f and
+ * 0xff (E4M3's NaN, which csa2_write_pages does not write) must not occur among a sequence's
+ * tokens; scales are >= 0 or NaN, and code * scale of V is at most 2^80.  A V scale below 2^-100
+ * counts as 2^-100.  A row is computed relative to the largest weight * v_scale among its own
+ * tokens, in fp32 and (weights) fp16: pages that it does not see or gives no weight may have any
+ * scale; among those with weight, tokens 2^110 below the largest by their V scale may be missing
+ * from the row's softmax sum. */
 typedef struct {
   int32_t n_rows;             /* rows of q and out (>= 0) */
   int32_t n_seq;

@@ -113,3 +113,29 @@ def test_a_cache_without_pages_under_a_table_with_columns(D, G, new):
         seq = torch.arange(3, dtype=torch.int32, device="cuda").repeat_interleave(new)
         S.write_pages(cache, q[:, :2], q[:, :2], rows, i32(new, new, new), seq, t, dev_status=status)
         assert S.read_device_status(status) == S.EDEVICE_INDEX
+
+
+@pytest.mark.parametrize("D,G,new", [(64, 2, 1), (64, 8, 2), (128, 2, 1), (128, 8, 2), (128, 8, 4), (64, 2, 40), (128, 2, 40)])
+def test_lengths_beyond_the_table(D, G, new):
+    """Tokens beyond the table are not there; the rows' positions stay those of the length, so that each row sees all of
+    the table, and under a window what of it is left."""
+    c = make([new, new, new], [64, 64, 64], 16, 2, D, seed=7)
+    c["table"] = np.ascontiguousarray(c["table"][:, :4])  # four pages each, all held
+    rng = np.random.default_rng(8)
+    q, qd = values((3 * new, 2 * G, D), rng, "bf16")
+    cache = S.PageCache(*(cuda(c[x]) for x in ("k", "v", "ks", "vs")))
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    over = np.array([0, 13, 1 << 20])
+    for window in (0, 50):
+        got = S.paged_attn(q.cuda(), cache, cuda(c["row_start"]), cuda((64 + over).astype(np.int32)), cuda(c["table"]), D ** -0.5,
+                           window=window, out_dtype=torch.float32, dev_status=status).double().cpu().numpy()
+        assert S.read_device_status(status) == S.OK
+        for r in range(3 * new):
+            p = 64 + over[r // new] - new + r % new  # its position
+            seen, first = min(64, p + 1), max(0, p - window + 1) if window else 0
+            if first >= seen:
+                assert not got[r].any()
+                continue
+            one = dict(c, kv=np.array([seen], np.int32), row_start=np.array([0, 1], np.int32), table=c["table"][r // new][None])
+            ref, tol = attend(qd[r:r + 1], one, D ** -0.5, seen - first, None, 2.0 ** -22)
+            assert np.all(np.abs(got[r] - ref[0]) <= tol[0])
