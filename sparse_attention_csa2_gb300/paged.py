@@ -259,6 +259,7 @@ def rope_axes(x, pos, sections=None, axis_of_pair=None, theta: float = 10000.0, 
     """x with its rotary dims turned by positions of several axes (see RopeAxes).  Differentiable in x
     unless `out` is given."""
     if out is None and x.requires_grad and torch.is_grad_enabled():
+        sections, axis_of_pair = (None if v is None else tuple(v) for v in (sections, axis_of_pair))  # for both passes
         return _Turn.apply(x, pos, (sections, axis_of_pair, theta, rot_dim, rot_first, pairing), bool(inverse))
     return RopeAxes(x, pos, sections, axis_of_pair, theta, rot_dim, rot_first, pairing, inverse, out)()
 

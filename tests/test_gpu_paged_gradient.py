@@ -70,7 +70,7 @@ def test_gradient_against_differences_and_of_second_order():
 def test_gradients_of_broadcast_and_misaligned_tensors():
     x, _, _, _, pos, _ = _case("f32", 2)
     x = x[:, :3].contiguous().requires_grad_(True)
-    S.rope_axes(x, pos, sections=(16, 16)).sum().backward()
+    S.rope_axes(x, pos, sections=iter((16, 16))).sum().backward()
     want = S.rope_axes(torch.ones(x.shape, device="cuda"), pos, sections=(16, 16), inverse=True)
     assert torch.equal(x.grad, want)
     flat = torch.ones(x.numel() + 1, device="cuda")[1:].view(x.shape)  # 4 bytes behind an aligned address
