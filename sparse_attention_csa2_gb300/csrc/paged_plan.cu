@@ -4,6 +4,9 @@
 #include "paged.h"
 
 namespace csa2 {
+
+int device_sm_count();
+
 namespace {
 
 // ----------------------------------------------------------------------------- page plan
@@ -273,8 +276,9 @@ cudaError_t rope_launch(const RopeAxesParams& p, bool half, bool inv, cudaStream
   // heads split over blocks until some sixteen blocks per SM are there, so that their ends even out; below
   // four heads a thread only for the sake of four blocks per SM, since each forms its sines anew
   int per = p.n_heads;
-  while (per > 4 && (long long)blocks * ((p.n_heads + per - 1) / per) < 2432) per = (per + 1) / 2;
-  while (per > 1 && (long long)blocks * ((p.n_heads + per - 1) / per) < 608) per = (per + 1) / 2;
+  const int sms = device_sm_count();
+  while (per > 4 && (long long)blocks * ((p.n_heads + per - 1) / per) < 16LL * sms) per = (per + 1) / 2;
+  while (per > 1 && (long long)blocks * ((p.n_heads + per - 1) / per) < 4LL * sms) per = (per + 1) / 2;
   const dim3 grid(blocks, (p.n_heads + per - 1) / per);
   auto go = [&](auto kernel) { return launch_behind(kernel, grid, 256, 0, stream, p, pieces, turned, per); };
   if (half) return inv ? go(rope_axes_kernel<T, true, true>) : go(rope_axes_kernel<T, true, false>);
@@ -291,7 +295,7 @@ cudaError_t launch_page_plan(const PagePlanParams& p, cudaStream_t stream) {
   }
   const long long per = (long long)kPlanThreads * kPlanRows;
   long long blocks = (p.max_rows + per - 1) / per;
-  if (blocks > 152) blocks = 152;
+  if (blocks > device_sm_count()) blocks = device_sm_count();
   if (blocks < 1) blocks = 1;
   return launch_behind(page_plan_kernel, dim3((unsigned)blocks), kPlanThreads, smem, stream, p);
 }
