@@ -46,14 +46,22 @@ const uint64_t* rope_turns(float theta, int rot_dim) {
   return k.turns;
 }
 
-// Which kernel, and its workspace, by the query rows per sequence and kv head in the mean.
-//   up to 8      paged_attn.cu's tiles of 8, three blocks per SM (four at dim 64)
-//   up to 32     at dim 64 its tiles of 16 (64 sequences x 4 heads x 1,000 tokens, 16 / 32 rows: 19 / 28 us against
-//                30 / 48 by paged_rows.cu's form; 32 sequences x 16,000 tokens and 32 rows 117 against 139);
+// Which kernel, and its workspace, by the query rows per sequence and kv head in the mean (the host knows no more).
+//   up to 8      of single tokens (no more rows than sequences): paged_attn.cu's tiles of 8, three blocks per SM
+//                (four at dim 64).  Drafts, which may be ragged, take the tiles below from 2 tokens on: 64 sequences
+//                of 4,096 tokens, 8 heads of groups of 4, dim 128 / 64: 2 tokens each 97 / 60 us against 91 / 53
+//                by tiles of 8, but 3 and 1 by turns 98 / 61 against 130 / 69, 4 and 0 59 / 37 against 64 / 50
+//   up to 32     at dim 64 its tiles of 16 (64 sequences x 4 heads x 1,000 tokens, 16 / 32 rows: 18 / 26 us against
+//                30 / 48 by paged_rows.cu's form; 32 sequences x 16,000 tokens and 32 rows 102 against 139);
 //                at dim 128 paged_rows.cu's tiles of 16 (two blocks per SM) or 32 (one): 8 heads of 16 rows x 16
-//                sequences x 65,535 tokens 325 us against 354 by tiles of 16 of paged_attn.cu (two blocks per SM
-//                there), one head x 4 sequences x 1M tokens in fp16 183 against 232; at 1,000 tokens 47 against 43
-//   more         paged_wide.cu's tiles of 256, one block per SM (dim 64, 64 rows, the second case: 153 us)
+//                sequences x 65,535 tokens 326 us against 354 by tiles of 16 of paged_attn.cu (two blocks per SM
+//                there), one head x 4 sequences x 1M tokens in fp16 180 against 232; short contexts lose by it
+//                (64 sequences of 1,000 tokens 47 against 43) and stay here, as one form less.  (The other sides
+//                are from when both were there.)
+//   more         paged_wide.cu's tiles of 256, one block per SM (dim 64, 64 rows, the second case: 154 us)
+// A batch that mixes a prompt chunk with decodes takes one form for all, which the mean makes wrong for some: 255
+// sequences of 4,096 tokens and a chunk of 512 behind 32,768, 8 heads of groups of 8, dim 128: 2,100 us together,
+// 330 and 497 in two calls.  Sequences without rows lower the mean too (the chunk with 200 of them: 1,650 us).
 // No more blocks than there can be units of 128 tokens (a tile has at most the table's, a sequence one tile
 // more than its rows fill).
 struct AttnPlan {
@@ -218,7 +226,8 @@ static csa2_status paged_attn(const csa2_paged_attn_args* a, uint32_t wait_tries
   p.row_start = a->row_start, p.kv_len = a->kv_len, p.table = a->table;
   p.table_cols = a->table_cols, p.n_pages = a->n_pages, p.page_shift = page_shift(a->page_size);
   p.k = a->k_codes, p.v = a->v_codes, p.k_scale = a->k_scale, p.v_scale = a->v_scale;
-  if (!p.k_scale || !p.v_scale) p.k_scale = p.v_scale = reinterpret_cast<const float*>(ws);  // no pages: copies of no bytes name an address
+  // without pages, copies of no bytes still name an address
+  if (!p.k_scale || !p.v_scale) p.k_scale = p.v_scale = reinterpret_cast<const float*>(ws);
   p.scale_log2 = a->softmax_scale * 1.4426950408889634f;
   p.window = a->window, p.sink = a->sink;
   p.out = a->out, p.out_dtype = a->out_dtype;

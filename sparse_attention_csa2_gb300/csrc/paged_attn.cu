@@ -5,10 +5,10 @@
 //   o_i  = sum_j exp(z_ij) v_j / (sum_j exp(z_ij) + exp(sink))
 //
 // Bound by the codes' way from memory: 2 * dim bytes per cached token and head, each read once.  32 sequences of
-// 65,536 tokens, 8 heads of 8 rows (4.3 GB at dim 128): 652 us, 6.6 TB/s, 97% of a copy's rate; at dim 64 352 us,
-// 90%.  Many short tiles are bound by instructions instead (per 32 tokens at dim 64 a warp issues 352 for 8 rows,
-// 417 for 16) and by their beginnings and ends: 96 sequences of 5 tokens, 8 heads, window 1,024 (101 MB) 51 us, of
-// which 23 are steps; one sequence of 2,048 tokens 8.5 us, the chain of two launches, lengths, pages, codes.
+// 65,536 tokens, 8 heads of 8 rows (4.3 GB at dim 128): 637 to 650 us, 6.7 TB/s, 98% of a copy's rate; at dim 64
+// 355 us, 89%.  Many short tiles are bound by instructions instead and by their beginnings and ends: 96 sequences of
+// 5 tokens, 8 heads, window 1,024 (101 MB, 23.0 M warp instructions) 51 us, of which some 23 are steps; one sequence
+// of 2,048 tokens 8.1 us, the chain of two launches, lengths, pages, codes.
 // (Sending a tile's first copies out before the one before is joined gained nothing: the SM's other blocks work then.)
 //
 // Split.  A tile is up to 8 or 16 query rows (tokens x heads of the group) of one sequence and kv head;
@@ -32,9 +32,9 @@
 // at that time; 96 sequences of 5 drafted tokens each, window 1,024: 74 against 60 us.)  Weights are fp16 of
 // exp2(u - max + 11), u = z + log2(the page's V scale), where the row's maximum of u follows a larger one only when
 // that exceeds it by 2^4: weights are at most 2^15, those down to 2^-25 of the largest keep 11 bits, and the output is
-// rarely rescaled (paged_dev.cuh).  Maxima, sums and outputs are fp32.  For fp16 rows, whose outputs round as finely as the weights (2^-11), what the
-// weights' rounding leaves is multiplied too: the error against 64 bits falls from 2.7e-4 to the output's own
-// 2.1e-4, at 5% of the time.
+// rarely rescaled (paged_dev.cuh).  Maxima, sums and outputs are fp32.  For fp16 rows, whose outputs round as finely
+// as the weights (2^-11), what the weights' rounding leaves is multiplied too: the error against 64 bits falls from
+// 2.7e-4 to the output's own 2.1e-4, at 5% of the time.
 #include "common.cuh"
 #include "paged.h"
 #include "paged_dev.cuh"
@@ -72,7 +72,8 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t v) {
   return r;
 }
 // Stages of the ring: 64 KB a block, 48 KB where four blocks share an SM (dim 64 and 8 rows: 32 sequences of
-// 65,536 tokens with 8 heads 380 us with the fourth block, 414 without; with 16 rows its registers spill).
+// 65,536 tokens with 8 heads, when it was tried, 380 us with the fourth block, 414 without; with 16 rows its registers
+// spill).
 template <int D, int NB>
 constexpr int kStages = D == 128 ? 2 : NB == 1 ? 3 : 4;
 

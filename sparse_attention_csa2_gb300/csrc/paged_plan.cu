@@ -17,7 +17,7 @@ namespace {
 // then takes its share of the rows and pages, so that one launch does it all: a scan in a kernel of
 // its own would add a launch to a call that takes a few microseconds at the sizes of a decode step.
 // Bound by that latency below some 10^5 rows and by the 20 bytes written per row above: 256 decoding sequences
-// 4.5 us (a launch and three dependent loads), 260,000 rows of 48 prompts 5.3 us.
+// 4.7 us (a launch and three dependent loads), 260,000 rows of 48 prompts 5.4 us.
 constexpr int kPlanThreads = 512;
 constexpr int kPlanRows = 4;  // consecutive rows of a thread: one search, 16-byte stores
 
@@ -161,7 +161,7 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const PagePlanP
 // partners) and walks the heads with it, so that its angles' sines are formed once and stay in
 // registers.  Bound by memory: every element read and written once.  Half pairs of bf16, 336 MB in and out:
 // 58.2 us, 5.8 TB/s (85% of a copy's rate); adjacent pairs of fp32, 64 of 192 dims turned, 208 MB: 35.3 us, 87%;
-// a decode step's 1.2 MB: 2.9 us, a launch.
+// a decode step's 1.2 MB: 3.0 us, a launch.
 template <typename T>
 struct Vec;
 template <>

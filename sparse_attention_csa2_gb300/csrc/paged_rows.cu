@@ -3,7 +3,8 @@
 //
 // The same sums as the split attention (paged_attn.cu), which serves up to 8 rows at this dim: with 16 its
 // outputs and query rows leave registers for two blocks per SM only, which wait for memory more than they
-// read (4 sequences of 1M tokens, 209 us against 182 here; in fp16 232 against 183).  Here, per 128 tokens,
+// read (4 sequences of 1M tokens, when both were there: 209 us against 182; in fp16 232 against 183).  Here, per 128
+// tokens,
 //
 //   S^T [128 tokens x rows] = K Q^T      kind::f8f6f4, K's codes as they come from memory (no conversion),
 //                                        the query rows as E4M3 pieces added up in the accumulator
@@ -12,7 +13,7 @@
 //
 // with accumulators in tensor memory, so that a thread holds one token's few scores and no outputs.  Bound by
 // the codes' way from memory: 256 bytes per cached token and head.  4 sequences of 1M tokens, one head of 16
-// rows (1.08 GB): 182 us, 5.9 TB/s, 87% of a copy's rate (pages of 16 tokens; of 64 172 us, 93%).
+// rows (1.08 GB): 178 us, 6.0 TB/s, 89% of a copy's rate (pages of 16 tokens; of 64 172 us, 92%; fp16 180 us).
 //
 //   4 warps  weights (a token per thread), and at a tile's end its output (a dim per thread)
 //   4 warps  V to fp16, and the next tile's query pieces
@@ -30,7 +31,7 @@ namespace csa2 {
 namespace {
 
 constexpr int kTile = 128;              // tokens of a unit
-constexpr int kLead = 4;                // units that a tile's beginning and end take (see paged_attn.cu)
+constexpr int kLead = 4;                // units that a tile's beginning and end take (as in paged_attn.cu; not swept here)
 constexpr int kThreads = 10 * 32;       // warps: weights 0 .. 3, conversion 4 .. 7, copies 8, products 9
 constexpr int kInfos = 8;
 

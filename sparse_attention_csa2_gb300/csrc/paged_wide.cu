@@ -3,7 +3,7 @@
 //
 // The same sums as the split attention (paged_attn.cu).  Bound by the tensor cores: 4 * dim
 // operations per row, head and token, half of them scores (Q K^T) and half outputs (P V).  4,096 rows of 32 heads
-// over 8 of 128 dims, behind 32,768 tokens (2.34 TFLOP): 1.92 ms, 1.22 PFLOP/s, 64% of a bf16 product's rate.  A
+// over 8 of 128 dims, behind 32,768 tokens (2.34 TFLOP): 1.97 ms, 1.19 PFLOP/s, 63% of a bf16 product's rate.  A
 // score product (128 x 64 x 32 codes) takes 66 cycles, since both its operands come from shared memory (tensor memory
 // is full: two row tiles' scores and outputs); the products' cycles add up to three quarters of the time, the rest is
 // the chain from scores to weights.

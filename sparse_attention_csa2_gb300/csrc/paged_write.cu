@@ -15,8 +15,9 @@
 // pieces a thread; what a long page has beyond is read again from L2), reduced to the largest
 // magnitude, and written as codes; four blocks per SM (six where a thread holds one piece) keep the
 // loads of some in flight while others reduce and write.  Bound by memory: 2 (or 4) bytes read and one
-// written per value.  32,768 rows of 8 heads of 128, bf16 (202 MB): 34.6 us, 5.8 TB/s (86% of a copy's
-// rate); 512 rows that append to their pages: 8.3 us, the chain of lookups, rows, scale and older codes.
+// written per value.  32,768 rows of 8 heads of 128, bf16 (202 MB): 34.5 us, 5.8 TB/s (86% of a copy's
+// rate), fp32 (336 MB) 56.3 us, 6.0 TB/s; 512 rows that append to their pages: 6.4 to 8.3 us in either, the chain of
+// lookups, rows, scale and older codes.
 #include "common.cuh"
 #include "paged.h"
 
