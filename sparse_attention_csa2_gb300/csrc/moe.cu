@@ -25,7 +25,8 @@
 // bf16 weights multiply bf16: x as it is, h as two bf16 that add up to it to 2^-16 (its rounding to one would be as large
 // as that of the output).  E4M3 codes become fp16 (exact, an instruction for two; as bf16 they take seven for four, a batch
 // of 32 tokens 868 us) and multiply fp16: codes of x exactly, bf16 x and fp32 h times a power of two that brings the row's
-// largest to 2^14 .. 2^15, so that nothing is lost of x and h keeps 11 bits, 22 (in two parts) for fp32 outputs.
+// largest to 2^14 .. 2^15, so that nothing is lost of x, and h in two parts keeps 22 bits whatever the output's type (one part,
+// 11 bits, moves a tenth of the bf16 outputs to their neighbour).
 #include "moe_dev.cuh"
 
 namespace csa2 {
@@ -91,21 +92,25 @@ constexpr int kProducts = 1, kAtEnds = 2;  // barriers of the products' warps an
 __device__ __forceinline__ int lift_of(uint32_t top) { return top == 0 ? 0 : min(14 - ((int)(top >> 23) - 127), 100); }
 __device__ __forceinline__ float pow2(int e) { return __int_as_float((127 + e) << 23); }
 
+// Two fp16 of which a NaN becomes the lowest finite value: beside an infinity that what is left of it.
+__device__ __forceinline__ uint32_t above_lowest(uint32_t v) {
+  uint32_t r;
+  asm("max.f16x2 %0, %1, %2;\n" : "=r"(r) : "r"(v), "r"(0xfbfffbffu));
+  return r;
+}
+
 // The B operand of 8 tokens x 16 columns, row g of them at `at`, in the order in which the weights' operand has its
 // columns: their own for bf16, for codes four neighbours to a lane.  b[1]: what h's rounding leaves.
 template <class S, int KIND>
-__device__ __forceinline__ void load_b(const uint8_t* at, int t, float lift, bool both, uint32_t (&b)[2][2]) {
+__device__ __forceinline__ void load_b(const uint8_t* at, int t, float lift, uint32_t (&b)[2][2]) {
   if constexpr (S::W8 && KIND == 1) {
     const float4 v = *reinterpret_cast<const float4*>(at + 16 * t);
     const float f[4] = {v.x * lift, v.y * lift, v.z * lift, v.w * lift};
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       b[0][i] = pack_f16x2(f[2 * i], f[2 * i + 1]);
-      if (both) {
-        const float2 r = __half22float2(*reinterpret_cast<const __half2*>(&b[0][i]));
-        const float rest[2] = {f[2 * i] - r.x, f[2 * i + 1] - r.y};  // an infinity's is none
-        b[1][i] = pack_f16x2(rest[0] == rest[0] ? rest[0] : 0.f, rest[1] == rest[1] ? rest[1] : 0.f);
-      }
+      const float2 r = __half22float2(*reinterpret_cast<const __half2*>(&b[0][i]));
+      b[1][i] = above_lowest(pack_f16x2(f[2 * i] - r.x, f[2 * i + 1] - r.y));
     }
   } else if constexpr (S::W8 && S::X8) {
     f16_pairs(*reinterpret_cast<const uint32_t*>(at + 4 * t), b[0][0], b[0][1]);
@@ -128,8 +133,8 @@ __device__ __forceinline__ void load_b(const uint8_t* at, int t, float lift, boo
 
 // The products of a stage: KIND 0 with rows of x, 1 with rows of h.
 template <class S, int KIND>
-__device__ __forceinline__ void stage_products(const uint8_t* w, const uint8_t* x, int cols, const Tile& tile, bool both,
-                                               int warp, int lane, float (&acc)[kMT][4]) {
+__device__ __forceinline__ void stage_products(const uint8_t* w, const uint8_t* x, int cols, const Tile& tile, int warp, int lane,
+                                               float (&acc)[kMT][4]) {
   const int g = lane >> 2, t = lane & 3;
   const int k_first = warp % kKW * S::KWARP, row_first = warp / kKW * (kMT * 16);
   const int arow = row_first + (lane & 15), achunk = lane >> 4;
@@ -161,10 +166,9 @@ __device__ __forceinline__ void stage_products(const uint8_t* w, const uint8_t* 
         }
       }
       uint32_t b[2][2];
-      load_b<S, KIND>(x + g * ROW + (at + 16 * s) * SIZE, t, lift, both, b);
+      load_b<S, KIND>(x + g * ROW + (at + 16 * s) * SIZE, t, lift, b);
 #pragma unroll
       for (int i = 0; i < KIND + 1; ++i) {
-        if (S::W8 && i == 1 && !both) break;
 #pragma unroll
         for (int m = 0; m < kMT; ++m) {
           if constexpr (S::W8) mma_f16(acc[m], f[m][0], f[m][1], f[m][2], f[m][3], b[i][0], b[i][1]);
@@ -484,8 +488,8 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
         ok = moe_wait(&c.w_full[st], ph, &c.x_full[st], ph, p.wait_tries, dead);
         if (!ok) break;
         const uint8_t* w = ring + st * S::STAGE;
-        if (kind == 0) stage_products<S, 0>(w, w + S::W_BYTES, min(S::KST, cols - k), tile, false, warp, lane, acc);
-        else stage_products<S, 1>(w, w + S::W_BYTES, min(S::KST, cols - k), tile, p.out_dtype == CSA2_T_F32, warp, lane, acc);
+        if (kind == 0) stage_products<S, 0>(w, w + S::W_BYTES, min(S::KST, cols - k), tile, warp, lane, acc);
+        else stage_products<S, 1>(w, w + S::W_BYTES, min(S::KST, cols - k), tile, warp, lane, acc);
         __syncwarp();
         if (lane == 0) tc05::mbar_arrive(&c.free_[st]);
         if (++st == stages) st = 0, ph ^= 1;
