@@ -22,8 +22,8 @@
 // tcgen05 is not used here: at a few tokens per expert the tensor cores have little to win, and 8-bit weights have to be
 // converted in registers in front of them, from where mma.sync takes them as they are.
 //
-// bf16 weights multiply bf16: x as it is, h as two bf16 that add up to it to 2^-16 (its rounding to one would be as large
-// as that of the output).  E4M3 codes become fp16 (exact, an instruction for two; as bf16 they take seven for four, a batch
+// bf16 weights multiply bf16: x as it is, fp32 h as three bf16 that add up to it (two would leave 2^-17 of it, four times what
+// the sums are off by).  E4M3 codes become fp16 (exact, an instruction for two; as bf16 they take seven for four, a batch
 // of 32 tokens 868 us) and multiply fp16: codes of x exactly, bf16 x and fp32 h times a power of two that brings the row's
 // largest to 2^14 .. 2^15, so that nothing is lost of x, and h in two parts keeps 22 bits whatever the output's type (one part,
 // 11 bits, moves a tenth of the bf16 outputs to their neighbour).
@@ -60,10 +60,11 @@ struct Shape {
   static constexpr int BOXCOLS = W8 ? 128 : 64;
   // Rows of x and h beside the weights, apart so that a load meets no bank twice.
   static constexpr int PITCH = KST * 2 + (W8 ? 32 : 16);  // 16-bit values
-  __host__ __device__ static constexpr int value_bytes(int kind) { return kind == 0 ? (X8 ? 1 : 2) : W8 ? 4 : 2; }
-  __host__ __device__ static constexpr int row_bytes(int kind) { return kind == 0 ? (X8 ? KST + 16 : PITCH) : W8 ? KST * 4 + 64 : PITCH; }
+  __host__ __device__ static constexpr int value_bytes(int kind) { return kind == 0 ? (X8 ? 1 : 2) : 4; }
+  __host__ __device__ static constexpr int row_bytes(int kind) { return kind == 0 ? (X8 ? KST + 16 : PITCH) : KST * 4 + (W8 ? 64 : 32); }
   static constexpr int W_BYTES = kR * 128 * BOXES;
-  static constexpr int X_BYTES = kTok * (W8 ? KST * 4 + 64 : 2 * PITCH);
+  __host__ __device__ static constexpr int parts(int kind) { return kind == 0 ? 1 : W8 ? 2 : 3; }  // of the tokens' values
+  static constexpr int X_BYTES = kTok * row_bytes(1);
   static constexpr int STAGE = W_BYTES + (X_BYTES + 1023) / 1024 * 1024;
 };
 constexpr int kMaxStages = 8;
@@ -100,9 +101,9 @@ __device__ __forceinline__ uint32_t above_lowest(uint32_t v) {
 }
 
 // The B operand of 8 tokens x 16 columns, row g of them at `at`, in the order in which the weights' operand has its
-// columns: their own for bf16, for codes four neighbours to a lane.  b[1]: what h's rounding leaves.
+// columns: their own for bf16, for codes four neighbours to a lane.  b[1], b[2]: what h's roundings leave.
 template <class S, int KIND>
-__device__ __forceinline__ void load_b(const uint8_t* at, int t, float lift, uint32_t (&b)[2][2]) {
+__device__ __forceinline__ void load_b(const uint8_t* at, int t, float lift, uint32_t (&b)[3][2]) {
   if constexpr (S::W8 && KIND == 1) {
     const float4 v = *reinterpret_cast<const float4*>(at + 16 * t);
     const float f[4] = {v.x * lift, v.y * lift, v.z * lift, v.w * lift};
@@ -121,12 +122,19 @@ __device__ __forceinline__ void load_b(const uint8_t* at, int t, float lift, uin
   } else if constexpr (S::X8 && KIND == 0) {
     b[0][0] = e4m3x2_to_bf16x2(*reinterpret_cast<const uint16_t*>(at + 2 * t));
     b[0][1] = e4m3x2_to_bf16x2(*reinterpret_cast<const uint16_t*>(at + 2 * t + 8));
+  } else if constexpr (KIND == 0) {
+    b[0][0] = *reinterpret_cast<const uint32_t*>(at + 4 * t);
+    b[0][1] = *reinterpret_cast<const uint32_t*>(at + 4 * t + 16);
   } else {
 #pragma unroll
-    for (int i = 0; i < KIND + 1; ++i) {
-      const uint8_t* row = at + i * kTok * S::PITCH;
-      b[i][0] = *reinterpret_cast<const uint32_t*>(row + 4 * t);
-      b[i][1] = *reinterpret_cast<const uint32_t*>(row + 4 * t + 16);
+    for (int i = 0; i < 2; ++i) {
+      float2 v = *reinterpret_cast<const float2*>(at + 8 * t + 32 * i);
+#pragma unroll
+      for (int part = 0; part < 3; ++part) {  // 8 bits of 24 are cut off each
+        b[part][i] = __byte_perm(__float_as_uint(v.x), __float_as_uint(v.y), 0x7632);
+        v.x -= bf16_lo(b[part][i]), v.y -= bf16_hi(b[part][i]);
+        if (part == 0) v.x = v.x == v.x ? v.x : 0.f, v.y = v.y == v.y ? v.y : 0.f;  // an infinity leaves nothing
+      }
     }
   }
 }
@@ -165,10 +173,10 @@ __device__ __forceinline__ void stage_products(const uint8_t* w, const uint8_t* 
           for (int i = 0; i < 4; ++i) f[m][i] = a[m][i];
         }
       }
-      uint32_t b[2][2];
+      uint32_t b[3][2];
       load_b<S, KIND>(x + g * ROW + (at + 16 * s) * SIZE, t, lift, b);
 #pragma unroll
-      for (int i = 0; i < KIND + 1; ++i) {
+      for (int i = 0; i < S::parts(KIND); ++i) {
 #pragma unroll
         for (int m = 0; m < kMT; ++m) {
           if constexpr (S::W8) mma_f16(acc[m], f[m][0], f[m][1], f[m][2], f[m][3], b[i][0], b[i][1]);
@@ -309,22 +317,21 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
       if (!moe_wait(&c.tile_ready[ti], i / kTiles & 1, p.wait_tries, dead) || c.tile[ti].kind == 2) break;
       const Tile& tile = c.tile[ti];
       const bool up = tile.kind == 0;
-      const int n = tile.n, cols = up ? p.dim : p.inner, rows = up || S::W8 ? n : 2 * n;
+      const int n = tile.n, cols = up ? p.dim : p.inner;
       if (!up) asm volatile("fence.proxy.async;\n" ::: "memory");  // h was written by plain stores
       for (int k = 0; k < cols; k += S::KST) {
         if (sent >= (uint32_t)stages && !(ok = moe_wait(&c.free_[st], ph ^ 1, p.wait_tries, dead))) break;
         const uint32_t bytes = min(S::KST, cols - k) * (up ? S::value_bytes(0) : S::value_bytes(1));
-        if (lane == 0) tc05::mbar_expect_tx(&c.x_full[st], rows * bytes);
+        if (lane == 0) tc05::mbar_expect_tx(&c.x_full[st], n * bytes);
         __syncwarp();
         uint8_t* to = ring + st * S::STAGE + S::W_BYTES;
-        for (int j = lane; j < rows; j += 32) {
+        for (int j = lane; j < n; j += 32) {
           if (up) {
             const uint8_t* from = static_cast<const uint8_t*>(p.x) + ((long long)(tile.slot[j] / slots) * p.x_row + k) * S::value_bytes(0);
             copy_row(to + j * S::row_bytes(0), from, bytes, &c.x_full[st]);
-          } else {  // a slot of h: fp32, or the two parts
-            const int part = j >= n, of = j - part * n;
-            const uint8_t* from = p.h + ((long long)tile.slot[of] * 4 + part * 2) * p.inner + k * S::value_bytes(1);
-            copy_row(to + (part * kTok + of) * S::row_bytes(1), from, bytes, &c.x_full[st]);
+          } else {
+            const uint8_t* from = p.h + ((long long)tile.slot[j] * p.inner + k) * S::value_bytes(1);
+            copy_row(to + j * S::row_bytes(1), from, bytes, &c.x_full[st]);
           }
         }
         __syncwarp();
@@ -519,17 +526,11 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
             if constexpr (S::W8 || S::X8) gate *= tile.weight[col], up *= tile.weight[col];
             if constexpr (S::W8) gate *= tile.scale[r], up *= tile.scale[r + kR / 2];
             const float h = gated(gate, up, p.limit);
+            const bool in = f < p.inner;
+            if (in) reinterpret_cast<float*>(p.h)[(long long)slot * p.inner + f] = h;
             if constexpr (S::W8) {
-              const bool in = f < p.inner;
-              if (in) reinterpret_cast<float*>(p.h)[(long long)slot * p.inner + f] = h;
               const uint32_t top = __reduce_max_sync(0xffffffffu, in ? __float_as_uint(h) & 0x7fffffffu : 0u);
               if (lane == 0) atomicMax(p.h_top + slot, top);
-            } else if (f < p.inner) {
-              const __nv_bfloat16 hi = __float2bfloat16_rn(h);
-              const float rest = h - __bfloat162float(hi);
-              __nv_bfloat16* at = reinterpret_cast<__nv_bfloat16*>(p.h) + (long long)slot * 2 * p.inner + f;
-              at[0] = hi;
-              at[p.inner] = __float2bfloat16_rn(rest == rest ? rest : 0.f);  // an infinity's is none
             }
           }
         } else {

@@ -64,7 +64,7 @@ struct MoeParams {
   long long out_row;
   int out_dtype;
   // workspace; a slot is one of a token's k + shared experts
-  uint8_t* h;                   // [tokens, slots, inner] of 4 bytes: fp32 (codes as weights), or [.., 2, inner] bf16
+  uint8_t* h;                   // [tokens, slots, inner] fp32, or (the wide form) [2, tokens x slots, inner] bf16
   float* part;                  // [tokens, slots, dim]
   void* x_rows;                 // [tokens, slots, dim] bf16: x's rows by experts (the wide form, whose h and part go by those too)
   int* ticket;
