@@ -33,7 +33,11 @@ constexpr int kFirstEpi = 4, kEnds = 8, kFirstConv = 9;
 constexpr int kAtEpi = 1;                     // a barrier
 constexpr int kStep = 64;                     // columns of a step of the products
 constexpr int kABytes = kRows * 128, kXBytes = 2 * kTokens * 128;
-constexpr int kAccCols = 2 * kTokens;         // of an accumulator: a down tile's products with both parts of h
+// Tensor memory of a tile: four sums of an up tile, two of a down tile (whose products with both parts of h lie side by side),
+// which take the products of 16 columns by turns and are added as fp32: the tensor cores cut a sum off each time that they add
+// to it, always towards 0, by more the larger it has grown.  One sum of 8,192 positive products was 3.0e-5 too small, four
+// are 3e-6 and two 9e-6 (128 tokens of 8 experts take 166 us as a layer, with one sum 165).
+constexpr int kAccCols = 4 * kTokens;
 constexpr int kGather = 4;                    // rows that a ticket gathers
 constexpr int kMost = 8;                      // stages of a ring
 constexpr int kSumTokens = 16;                // of a piece of y
@@ -283,7 +287,8 @@ __global__ void __launch_bounds__(threads_of(W8), 1)
         if (elected()) {
 #pragma unroll
           for (int s = 0; s < 4; ++s)
-            mma_f16_ss(tmem + buf * kAccCols, ad + 2 * s, desc_hi(128), bd + 2 * s, desc_hi(128), idesc, k > 0 || s > 0);
+            mma_f16_ss(tmem + buf * kAccCols + (kind == kUp ? s : s % 2 * 2) * kTokens, ad + 2 * s, desc_hi(128), bd + 2 * s, desc_hi(128),
+                       idesc, k > 0 || (kind != kUp && s > 1));
           tc05::mma_commit(&a_free[a.st]);
           tc05::mma_commit(&c.x_free[x.st]);
         }
@@ -428,13 +433,28 @@ __global__ void __launch_bounds__(threads_of(W8), 1)
         };
         if (kind == kUp) {
           // warps 0, 1 hold gates, 2, 3 the up projection; each pair gives half of its tokens for half of the others'
-          uint32_t v[32];
-          tc05::tmem_ld32(acc + (half == 0 ? 32 : 0), v);
-          tc05::tmem_ld_wait();
+          float v[32];
+          auto add_up = [&](uint32_t at) {
 #pragma unroll
-          for (int j = 0; j < 32; ++j) c.exchange[half][r][j] = __uint_as_float(v[j]);
-          tc05::tmem_ld32(acc + (half == 0 ? 0 : 32), v);
-          tc05::tmem_ld_wait();
+            for (int j0 = 0; j0 < 32; j0 += 16) {
+              uint32_t u[2][16];
+#pragma unroll
+              for (int q = 0; q < 4; q += 2) {
+                tc05::tmem_ld16(at + q * kTokens + j0, u[0]);
+                tc05::tmem_ld16(at + (q + 1) * kTokens + j0, u[1]);
+                tc05::tmem_ld_wait();
+#pragma unroll
+                for (int j = 0; j < 16; ++j) {
+                  const float sum = __uint_as_float(u[0][j]) + __uint_as_float(u[1][j]);
+                  v[j0 + j] = q == 0 ? sum : v[j0 + j] + sum;
+                }
+              }
+            }
+          };
+          add_up(acc + (half == 0 ? 32 : 0));
+#pragma unroll
+          for (int j = 0; j < 32; ++j) c.exchange[half][r][j] = v[j];
+          add_up(acc + (half == 0 ? 0 : 32));
           taken();
           part_sync<kAtEpi, kEpi * 32>();
           const int f = tile.row + r;
@@ -445,7 +465,7 @@ __global__ void __launch_bounds__(threads_of(W8), 1)
 #pragma unroll
             for (int j = 0; j < 32; ++j) {
               if (half * 32 + j >= n) continue;
-              const float mine = __uint_as_float(v[j]), others = c.exchange[half ^ 1][r][j], xs = tile.weight[half * 32 + j];
+              const float mine = v[j], others = c.exchange[half ^ 1][r][j], xs = tile.weight[half * 32 + j];
               const float hv = gated((half == 0 ? mine : others) * xs * gate_scale, (half == 0 ? others : mine) * xs * up_scale, p.limit) *
                                (W8 ? kBack : 1.f);
               const __nv_bfloat16 up = __float2bfloat16_rn(hv);
@@ -462,15 +482,24 @@ __global__ void __launch_bounds__(threads_of(W8), 1)
           float* at = p.part + (long long)first * p.dim + d;
 #pragma unroll
           for (int j0 = 0; j0 < kTokens; j0 += 16) {
-            uint32_t v[16], rest[16];
-            tc05::tmem_ld16(acc + j0, v);
-            tc05::tmem_ld16(acc + kTokens + j0, rest);
-            tc05::tmem_ld_wait();
+            float v[16];
+            uint32_t u[2][16];
+#pragma unroll
+            for (int q = 1; q >= 0; --q) {  // the second parts of h first
+              tc05::tmem_ld16(acc + q * kTokens + j0, u[0]);
+              tc05::tmem_ld16(acc + (q + 2) * kTokens + j0, u[1]);
+              tc05::tmem_ld_wait();
+#pragma unroll
+              for (int j = 0; j < 16; ++j) {
+                const float sum = __uint_as_float(u[0][j]) + __uint_as_float(u[1][j]);
+                v[j] = q == 1 ? sum : v[j] + sum;
+              }
+            }
             if (j0 + 16 == kTokens) taken();
             if (ok && d < p.dim) {
 #pragma unroll
               for (int j = 0; j < 16; ++j)
-                if (j0 + j < n) at[(long long)(j0 + j) * p.dim] = (__uint_as_float(v[j]) + __uint_as_float(rest[j])) * scale * tile.weight[j0 + j];
+                if (j0 + j < n) at[(long long)(j0 + j) * p.dim] = v[j] * scale * tile.weight[j0 + j];
             }
           }
         }

@@ -53,3 +53,40 @@ def test_h_itself_to_its_bits(w_codes, T, form):
     # fp32, two fp16 leave 2^-22, two bf16 2^-17 (each takes 8 bits and a sign of what the last one left)
     eps = 2.0 ** -22 + 3 * 2.0 ** -24 + (2.0 ** -17 if form == "many" else 2.0 ** -22 if w_codes else 0)
     assert np.all(np.abs(got.double().cpu().numpy() - want) <= eps * np.abs(want))
+
+
+@pytest.mark.parametrize("form", ["few", "many"])
+@pytest.mark.parametrize("w_codes", [False, True])
+def test_sums_of_many_products_of_one_sign(w_codes, form):
+    """8,192 columns: both forms hold 2^-15 of what is added.  (Sums that a tensor core cuts off towards 0 each time that it adds
+    all err to one side; the up product's h is a sum itself, the down product's h have 15 bits and are exact.)"""
+    n, T, F = 8192, 40, 128
+    g = torch.Generator("cuda").manual_seed(35)
+    rand = lambda *s: (1 + torch.rand(*s, generator=g, device="cuda")).bfloat16()  # noqa: E731
+
+    def weights(up, down):
+        if not w_codes:
+            return S.ExpertWeights(up, down), up.double(), down.double()
+        codes = [m.to(torch.float8_e4m3fn) for m in (up, down)]
+        w = S.ExpertWeights(*(c.view(torch.uint8) for c in codes), torch.ones(up.shape[:2], device="cuda"), torch.ones(down.shape[:2], device="cuda"))
+        return w, *(c.double() for c in codes)
+
+    def outputs(x, w):
+        ids, ones = torch.zeros((T, 1), dtype=torch.int32, device="cuda"), torch.ones((T, 1), device="cuda")
+        return S.moe_experts(x, ids, ones, w, out_dtype=torch.float32, form=form).double()
+
+    up, down = torch.zeros((1, 2 * F, n), dtype=torch.bfloat16, device="cuda"), torch.zeros((1, n, F), dtype=torch.bfloat16, device="cuda")
+    up[0, :F], up[0, F:, 0], x = rand(F, n), 1, rand(T, n)
+    x[:, 0] = 1
+    down[0, torch.arange(F), torch.arange(F)] = 1
+    w, uv, _ = weights(up, down)
+    want = x.double() @ uv[0, :F].T              # silu of thousands is the same, times 1
+    assert torch.all((outputs(x, w)[:, :F] - want).abs() <= 2.0 ** -15 * want)
+
+    up, down = torch.zeros((1, 2 * n, 64), dtype=torch.bfloat16, device="cuda"), rand(1, 64, n)
+    up[0, :n, 0], up[0, n:, 1] = 96, 1
+    x = torch.zeros((T, 64), dtype=torch.bfloat16, device="cuda")
+    x[:, 0], x[:, 1] = 1, rand(T)
+    w, _, dv = weights(up, down)
+    want = 96 * x[:, 1].double()[:, None] * dv[0].sum(1)
+    assert torch.all((outputs(x, w) - want).abs() <= 2.0 ** -15 * want)
