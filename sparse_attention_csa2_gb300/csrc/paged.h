@@ -25,9 +25,10 @@ cudaError_t allow_smem(int bytes) {
 }
 
 // Launches a kernel behind the stream's work that may start before that is done: it calls prior_done() before
-// it reads or writes memory, and reads nothing by the non-coherent path, whose loads may move ahead of it.  Decode steps are made of kernels of a few microseconds, of which a launch takes
-// two.  These kernels give no early leave themselves: what follows them may read what they write.  (Leave from the
-// attention to its join, at its start or at a tile's end, measured no gain.)
+// it reads or writes memory, and reads nothing by the non-coherent path, whose loads may move ahead of it.  Decode steps
+// are made of kernels of a few microseconds, of which a launch takes two.  They give no early leave themselves (what follows
+// them may read what they write; from the attention to its join, at its start or at a tile's end, it measured no gain), but
+// for the router, once the work before it is done: what follows that waits for what it writes.
 template <typename... P, typename... A>
 cudaError_t launch_behind(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t stream, A&&... args) {
   cudaLaunchConfig_t cfg{};

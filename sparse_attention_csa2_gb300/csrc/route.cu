@@ -272,8 +272,8 @@ __global__ void __launch_bounds__(kWarps * 32) route_rows_kernel(const RoutePara
   extern __shared__ __align__(16) uint8_t smem[];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int e = blockIdx.x * kWarps + warp, t0 = blockIdx.y * TB, nt = min(TB, p.tokens - t0);
-  next_may_start();
   prior_done();
+  next_may_start();  // not before: what starts then may read at once what came before this kernel
   if (e < p.experts) {
     const TX* x = static_cast<const TX*>(p.x) + (long long)t0 * p.x_row;
     const TW* w = static_cast<const TW*>(p.w) + (long long)e * p.dim;
@@ -315,8 +315,8 @@ __global__ void __launch_bounds__(kTileWarps * 32) route_tiles_kernel(const Rout
   __shared__ float2 part[kTileWarps][16][9];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
   const int e0 = blockIdx.x * 16, t0 = blockIdx.y * kRouteTokens, nt = min(kRouteTokens, p.tokens - t0);
-  next_may_start();
   prior_done();
+  next_may_start();  // not before: what starts then may read at once what came before this kernel
   auto row = [&](const void* base, long long r, long long stride) { return static_cast<const T*>(base) + r * stride + t * 8; };
   const T* a_lo = row(p.w, min(e0 + g, p.experts - 1), p.dim);
   const T* a_hi = row(p.w, min(e0 + g + 8, p.experts - 1), p.dim);
