@@ -279,9 +279,10 @@ size_t attn_workspace(const csa2_attn_args* a, int n_split) {
          align_up((size_t)a->n_rows * n_split * CSA2_HEADS * 2 * 4) + align_up((size_t)a->n_rows * CSA2_ROPE_DIM * 4);
 }
 
-csa2_status run_attn(const csa2_attn_args* a, const int32_t* idx, uint8_t* ws, cudaStream_t s) {
+csa2_status run_attn(const csa2_attn_args* a, const int32_t* idx, bool query_waits, uint8_t* ws, cudaStream_t s) {
   const int n_split = attn_splits(a->n_rows, a->K, a->window);
   AttnParams p = attn_params(a, idx);
+  p.query_waits = query_waits;
   Carve c{ws};
   p.part_o = c.take<float>((size_t)a->n_rows * n_split * CSA2_HEADS * CSA2_HEAD_DIM);
   p.part_ml = c.take<float>((size_t)a->n_rows * n_split * CSA2_HEADS * 2);
@@ -514,7 +515,7 @@ csa2_status csa2_sparse_attn(const csa2_attn_args* a, void* stream) {
   if (st != CSA2_OK || a->n_rows == 0) return st;
   const size_t need = csa2_sparse_attn_workspace_size(a);
   if (need > 0 && (!a->workspace || a->workspace_bytes < need)) return CSA2_EWORKSPACE;
-  return run_attn(a, a->idx, static_cast<uint8_t*>(a->workspace), static_cast<cudaStream_t>(stream));
+  return run_attn(a, a->idx, true, static_cast<uint8_t*>(a->workspace), static_cast<cudaStream_t>(stream));
 }
 
 // ---------------------------------------------------------------------- fused decode layer
@@ -706,7 +707,7 @@ csa2_status csa2_fused_decode(const csa2_decode_args* a, void* stream) {
     }
   }
   mark(2);
-  st = run_attn(&at, a->idx, static_cast<uint8_t*>(a->workspace) + c.off, s);
+  st = run_attn(&at, a->idx, a->mode == CSA2_MODE_REUSE, static_cast<uint8_t*>(a->workspace) + c.off, s);
   mark(3);
   return st;
 }
@@ -1006,6 +1007,7 @@ csa2_status csa2_sparse_attn_partial(const csa2_partial_args* a, void* stream) {
   if (a->range_count < 0 || a->range_first < 0 || (a->range_count > 0 && a->range_count > a->attn.n_records))
     return CSA2_EINVAL;
   AttnParams p = attn_params(&a->attn, a->attn.idx);
+  p.query_waits = true;
   p.part_o = a->part_o;
   p.part_ml = a->part_ml;
   p.range_first = a->range_first;

@@ -252,6 +252,13 @@ __device__ __forceinline__ void gather_tile(const TileSrc& m, uint8_t* ks, const
   }
 }
 
+// Behind a kernel of another call the query may be what that one is writing (csa2_query_proj lets this one start at its
+// beginning), and the partials' room what it is reading: nothing of either is touched before it has ended.  Behind the
+// selection of the same call, which has waited itself, the query is older than the kernel before.
+__device__ __forceinline__ void wait_for_query(const AttnParams& p) {
+  if (p.query_waits) asm volatile("griddepcontrol.wait;\n" ::: "memory");
+}
+
 // Heads h0 .. h0+NH-1 of the row's query (NH x 512 dims) into `qs` (panel layout, NH rows per
 // 64-dim panel) by cp.async, one 16-byte chunk per copy (consecutive threads on consecutive
 // chunks); rotate_query then turns the rotary pairs (dims 448 + 2i, 448 + 2i + 1) in place once
@@ -397,11 +404,11 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_tc05_kernel(const AttnPa
   __syncthreads();
   tc05::fence_after();
   const uint32_t tmem = sh.tmem_base;
+  wait_for_query(p);
   // one block per row hands its rotary table to the merge
   if (p.rope_cs != nullptr && blockIdx.y == 0 && tid < kRopeDim) p.rope_cs[(size_t)row * kRopeDim + tid] = sh.cs[tid];
 
-  // the query is an input of the step, not of the previous kernel: it is copied and rotated
-  // before the wait below
+  // the query is copied and rotated before the wait below
   copy_query<NH>(p, row, h0, qs);
   cp_async_commit();
   cp_async_wait<0>();
@@ -660,7 +667,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_row_kernel(const AttnPar
   const uint32_t tmem = sh.tmem_base;
   const uint32_t qs_u = smem_u32(qs), ps_u = smem_u32(ps), ks_u = smem_u32(ks);
 
-  // the query is an input of the step: copied and rotated before any wait
+  // the query is copied and rotated before the wait for the indices
+  wait_for_query(p);
   copy_query<NH>(p, row, h0, qs);
   cp_async_commit();
   cp_async_wait<0>();
@@ -1029,7 +1037,8 @@ __global__ void __launch_bounds__(kPipeThreads, 1) attn_pipe_kernel(const AttnPa
   }
   asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
   __syncthreads();
-  // the query is an input of the step: copied and rotated before any wait
+  // the query is copied and rotated before the wait for the indices
+  wait_for_query(p);
   if (tid < kAttnThreads) copy_query<NH>(p, row, h0, qs);
   cp_async_commit();
   cp_async_wait<0>();

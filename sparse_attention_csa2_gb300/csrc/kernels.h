@@ -118,6 +118,7 @@ cudaError_t launch_lists_merge(const FeedParams& p, cudaStream_t stream);  // se
 cudaError_t launch_row_topk(const FeedParams& p, cudaStream_t stream);
 struct AttnParams {
   const void* q;
+  int query_waits;            // the kernel before is another call's
   const int64_t* q_pos;
   const int32_t* seq_of_row;
   int n_rows;

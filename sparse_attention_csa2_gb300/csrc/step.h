@@ -27,7 +27,7 @@ cudaError_t launch_add_norm(const AddNormParams& p, int x_dtype, int sum_dtype, 
 
 #ifdef __CUDACC__
 // Leave for a kernel launched behind (launch_behind) to take the SMs' room and wait there for this one's end.
-// Behind prior_done(): the CSA2 attention reads its query, which is older than the kernel before it, without a wait.
+// Behind prior_done(): what starts next need only wait for this kernel, not for those before it.
 __device__ __forceinline__ void next_may_start() { asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory"); }
 #endif
 

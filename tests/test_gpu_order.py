@@ -66,3 +66,39 @@ def in_a_row(layer, between, attention):
 def test_attention_behind_the_projection_and_the_router(T, window_only):
     layer = Layer(T, window_only)
     in_a_row(layer, (layer.route,), layer.attention)
+
+
+@pytest.mark.parametrize("T,window_only", [(1, False), (1, True), (32, False), (32, True), (320, False), (320, True)])
+def test_attention_directly_behind_the_projection(T, window_only):
+    layer = Layer(T, window_only)
+    in_a_row(layer, (), layer.attention)
+
+
+@pytest.mark.parametrize("T", [1, 32])
+def test_partial_and_fused_attention_behind_the_projection(T):
+    layer = Layer(T, False)
+    in_a_row(layer, (), lambda: S.sparse_attn_partial(*layer.args[:10], *layer.args[11:])[0])
+    q, q_pos, seq_of_row, lat, lat_scale, idx, swa, swa_scale, pos0, window, sink, theta, scale = layer.args
+    reuse = S.DecodeLayer("reuse", seq_of_row=seq_of_row, n_visible=None, q=q, q_pos=q_pos, latents=lat, lat_scale=lat_scale, swa=swa,
+                          swa_scale=swa_scale, swa_pos0=pos0, window=window, sink=sink, K=idx.shape[1], theta=theta, softmax_scale=scale, idx=idx)
+    in_a_row(layer, (), lambda: reuse().clone())
+
+
+@pytest.mark.parametrize("T", [1, 32])
+def test_attentions_behind_one_another_over_one_workspace(T):
+    """The second call's tiles over the window need nothing of the first's, whose partials are still being added up where
+    theirs go (the caching allocator gives both the same workspace)."""
+    layer = Layer(T, False)
+    qs = []
+    for x in layer.xs:
+        layer.x.copy_(x)
+        qs.append(layer.proj().clone())
+    one = lambda q: S.sparse_attn(q, *layer.args[1:])[0]  # noqa: E731
+    want = []
+    for q in qs:
+        torch.cuda.synchronize()
+        want.append(one(q))
+    torch.cuda.synchronize()
+    for _ in range(25):
+        got = [one(q) for q in qs]
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
