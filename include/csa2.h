@@ -788,8 +788,9 @@ typedef enum csa2_score { CSA2_SCORE_SOFTMAX = 0, CSA2_SCORE_SIGMOID = 1, CSA2_S
  *   weights = score of those (without the bias), over their sum where `normalize`, times `scale`
  * The choice is made as in exact arithmetic: where a bound of the products' errors leaves it open, those in question are
  * computed again to some 2^-45 of the sizes of what is added (with softmax and a bias, the sum under the scores keeps
- * its fp32 products).  Scores are compared as products z, which they grow with, where there is no bias.  Experts whose
- * score is NaN come last. */
+ * its fp32 products).  Scores are compared as products z, which they grow with, where there is no bias.  Products
+ * beyond fp32's range are infinite, and compared as that.  Experts whose score is NaN come last; weights that need one
+ * (softmax's all, or those over a sum with it) are NaN. */
 typedef struct {
   int32_t tokens;             /* 0 .. 16384 */
   int32_t dim;                /* multiple of 8 */

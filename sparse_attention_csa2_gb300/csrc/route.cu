@@ -103,11 +103,13 @@ __device__ __forceinline__ double2 exact_products(const TW* w0, const TW* w1, co
 __host__ __device__ constexpr int choice_bytes(int experts) { return (experts * 20 + 15) / 16 * 16; }
 
 // What an expert is chosen by, and how far that may be off: without a bias the product itself, as scores grow with it.
-// (Not softmax's score, which needs all.)
+// (Not softmax's score, which needs all.)  An infinite product is what it is.
 __device__ __forceinline__ float4 told(const RouteParams& p, int e, float z, float off) {
+  const bool infinite = fabsf(z) == INFINITY;
+  if (infinite) off = 0.f;
   if (p.bias == nullptr || p.score == CSA2_SCORE_SOFTMAX) return make_float4(z, off, z, 0.f);
   const float score = score_of(p.score, z, 0.f);
-  return make_float4(z, slack_of(p.score, z, off, score, p.bias[e]), score + p.bias[e], 0.f);
+  return make_float4(z, infinite ? 0.f : slack_of(p.score, z, off, score, p.bias[e]), score + p.bias[e], 0.f);
 }
 
 // The experts of token t, by a warp.
@@ -213,7 +215,9 @@ __device__ void choose(const RouteParams& p, uint8_t* smem, int lane, int t) {
     for (int i = 0; i < n; i += 2) {
       const int j = min(i + 1, n - 1);
       const double2 d = zero ? make_double2(0., 0.) : exact_products(w + (long long)key[i] * p.dim, w + (long long)key[j] * p.dim, x, p.dim, lane);
-      if (lane == 0) exact[i] = d.x, exact[j] = j > i ? d.y : d.x;
+      // a product beyond fp32 has no remainders to add up
+      const float first_i = product[key[i]].x, first_j = product[key[j]].x;
+      if (lane == 0) exact[i] = d.x == d.x ? d.x : first_i, exact[j] = j == i ? exact[i] : d.y == d.y ? d.y : first_j;
     }
     __syncwarp();
     double sum64 = 1.;

@@ -3,7 +3,8 @@ import numpy as np
 import pytest
 import torch
 
-from test_gpu_moe import layer, pick, rows
+import oracle.step as OS
+from test_gpu_moe import TYPES, layer, pick, rows
 
 pytestmark = pytest.mark.gpu
 
@@ -90,3 +91,53 @@ def test_sums_of_many_products_of_one_sign(w_codes, form):
     w, _, dv = weights(up, down)
     want = 96 * x[:, 1].double()[:, None] * dv[0].sum(1)
     assert torch.all((outputs(x, w) - want).abs() <= 2.0 ** -15 * want)
+
+
+@pytest.mark.parametrize("score", ["sigmoid", "sqrtsoftplus", "softmax"])
+@pytest.mark.parametrize("types", [("bf16", "bf16"), ("f16", "f16"), ("f32", "f32"), ("bf16", "f32")])
+@pytest.mark.parametrize("T", [1, 3, 9, 40])
+def test_route_by_products_that_are_infinite(types, score, T):
+    """An infinity in x makes every product infinite, by the weight's sign: scores of 1 (or infinity) and 0, of which the bias
+    says the order.  Beside it rows as they are, and (fp32) rows whose products overflow."""
+    D, E, k = 256, 48, 6
+    g = torch.Generator().manual_seed(36)
+    x = torch.randn(T, D, generator=g).to(TYPES[types[0]])
+    w = torch.randn(E, D, generator=g).to(TYPES[types[1]])
+    bias = torch.randperm(E, generator=g) / 100.0
+    w[:, 7] = torch.where(torch.arange(E) % 3 == 0, 1.0, -1.0).to(w.dtype)  # 16 of 48 above
+    x[0, 7] = float("inf")
+    if T > 2:
+        x[2, 7] = -float("inf")
+    if T > 1 and types[0] == "f32":
+        x[1] *= 2.0 ** 124                    # products are sums of some 2^128
+    with_bias = score != "softmax"            # (with a bias, softmax's scores beside an infinite product are NaN)
+    got = S.route_experts(x.cuda(), w.cuda(), k, bias=bias.cuda() if with_bias else None, score=score, normalize=False)
+    # products beyond fp32's range as infinities, as they are compared
+    z = x.double().numpy() @ w.double().numpy().T
+    z = np.where(np.abs(z) >= 2.0 ** 128, np.sign(z) * np.inf, z)
+    by = OS.score(z, score) + bias.double().numpy() if with_bias else z
+    sure = [t for t in range(T) if not (types[0] == "f32" and t == 1)]   # (of a sum near 2^128 the order of addition decides)
+    ids = np.stack([sorted(range(E), key=lambda e, r=r: (-r[e], e))[:k] for r in by])
+    assert np.array_equal(got.ids.cpu().numpy()[sure], ids[sure])
+    if with_bias:
+        weights = np.take_along_axis(OS.score(z, score), ids, 1)[sure]
+        mine = got.weights.double().cpu().numpy()[sure]
+        inf = np.isinf(weights)
+        # finite products as in test_gpu_moe.test_route: their rows are those without an infinity
+        rest = [t for t in sure if t not in (0, 2)]
+        dz = (D / 32 + 6) * 2.0 ** -24 * (np.abs(x.double().numpy()[rest]) @ np.abs(w.double().numpy()).T).max() if rest else 0.0
+        assert np.array_equal(np.isinf(mine), inf) and np.all(np.abs(mine - weights)[~inf] <= (2 * dz + 2.0 ** -21) * weights[~inf])
+    elif T > 3:
+        assert got.weights[0].isnan().all() and got.weights[3].isfinite().all()
+
+
+def test_route_weights_beside_a_nan():
+    D, E = 64, 32
+    x, w = torch.randn(5, D, device="cuda"), torch.randn(E, D, device="cuda")
+    w[7], x[2] = float("nan"), float("nan")
+    assert S.route_experts(x, w, 31).weights.isnan().all()       # of a softmax that holds one
+    for score in ("sigmoid", "sqrtsoftplus"):
+        got = S.route_experts(x, w, 31, score=score)
+        assert got.weights[2].isnan().all() and got.weights[[0, 1, 3, 4]].isfinite().all()
+        assert not (got.ids[[0, 1, 3, 4]] == 7).any()
+        assert S.route_experts(x, w, 32, score=score, normalize=False).weights.isnan().sum(1).tolist() == [1, 1, 32, 1, 1]
