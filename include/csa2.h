@@ -780,6 +780,12 @@ csa2_status csa2_add_norm(const csa2_add_norm_args* a, void* stream);
  * overlap on the GPU need workspaces of their own. */
 #define CSA2_COUNTER_BYTES 65536
 
+/* For callers that keep such a workspace: a number of the graph capture that `stream` is in (0: none), since zeros written
+ * within a capture are there for runs of that graph alone; and a wait on the host for a CUDA event (of work outside any
+ * capture), which may be called during one. */
+csa2_status csa2_capture_id(void* stream, uint64_t* id);
+csa2_status csa2_finish_event(void* event);
+
 typedef enum csa2_score { CSA2_SCORE_SOFTMAX = 0, CSA2_SCORE_SIGMOID = 1, CSA2_SCORE_SQRTSOFTPLUS = 2 } csa2_score;
 
 /* csa2_route - the experts of each token.

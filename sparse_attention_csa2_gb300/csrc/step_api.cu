@@ -194,6 +194,25 @@ csa2_status csa2_selftest_moe_waits(const csa2_moe_args* a, int32_t tries, void*
   return moe(a, (uint32_t)tries, stream);
 }
 
+csa2_status csa2_capture_id(void* stream, uint64_t* id) {
+  if (!id) return CSA2_EINVAL;
+  cudaStreamCaptureStatus status = cudaStreamCaptureStatusNone;
+  unsigned long long of = 0;
+  const cudaError_t e = cudaStreamGetCaptureInfo(static_cast<cudaStream_t>(stream), &status, &of);
+  *id = e == cudaSuccess && status != cudaStreamCaptureStatusNone ? of : 0;
+  return cuda_status(e);
+}
+
+csa2_status csa2_finish_event(void* event) {
+  if (!event) return CSA2_EINVAL;
+  cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;  // a wait for other work leaves this thread's captures as they are
+  cudaError_t e = cudaThreadExchangeStreamCaptureMode(&mode);
+  if (e != cudaSuccess) return cuda_status(e);
+  e = cudaEventSynchronize(static_cast<cudaEvent_t>(event));
+  const cudaError_t back = cudaThreadExchangeStreamCaptureMode(&mode);
+  return cuda_status(e != cudaSuccess ? e : back);
+}
+
 csa2_status csa2_sample(const csa2_sample_args* a, void* stream) {
   if (!a || a->n_rows < 0 || a->vocab < 1 || !type_ok(a->dtype)) return CSA2_EINVAL;
   if (a->vocab > kSampleMostVocab || a->n_rows > (1 << 26)) return CSA2_EUNSUPPORTED;

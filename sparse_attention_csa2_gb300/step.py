@@ -8,7 +8,8 @@ router and its experts, and the choice of a token from the logits.
 
 Each call exists as a class that binds its tensors once (as the paged cache's calls do) and is then run by
 calling the object, for decode loops and for capture into a CUDA graph.  Running one object on two streams at
-once races on its outputs and workspace.  One made within a capture belongs to that graph.  These calls record no autograd graph: tensors whose gradient torch
+once races on its outputs and workspace.  A router or experts object made within a capture belongs to that graph:
+calls outside it, or in another capture, are refused.  These calls record no autograd graph: tensors whose gradient torch
 would track are refused outside torch.no_grad().
 """
 from __future__ import annotations
@@ -58,6 +59,8 @@ _moe_ws = _sig("csa2_moe_workspace_size", [C.POINTER(MoEArgs)], _sz)
 _moe = _sig("csa2_moe", [C.POINTER(MoEArgs), _vp], C.c_int)
 _moe_waits = _sig("csa2_selftest_moe_waits", [C.POINTER(MoEArgs), _i32, _vp], C.c_int)
 _sample = _sig("csa2_sample", [C.POINTER(SampleArgs), _vp], C.c_int)
+_capture_id = _sig("csa2_capture_id", [_vp, C.POINTER(C.c_uint64)], C.c_int)
+_finish_event = _sig("csa2_finish_event", [_vp], C.c_int)
 
 
 # ------------------------------------------------------------------ checks
@@ -77,6 +80,13 @@ def _rows(t, name, device=None, shape=None):
     return _on(t, name, device), t.stride(0) if t.shape[0] > 1 else 0
 
 
+def _capture_of(stream) -> int:
+    """A number of the graph capture that a stream is in, 0 outside."""
+    of = C.c_uint64()
+    _check(_capture_id(stream, C.byref(of)), "csa2_capture_id")
+    return of.value
+
+
 class _Counted(_Prepared):
     """A prepared call whose workspace begins with counters that are zero between calls."""
 
@@ -84,20 +94,27 @@ class _Counted(_Prepared):
         self._wsp = torch.empty(max(int(nbytes), COUNTER_BYTES), dtype=torch.uint8, device=device)
         with torch.cuda.device(device):
             self._wsp[:COUNTER_BYTES].zero_()
-            # a call on another stream comes behind the zeros; in a capture they are the graph's
-            self._in_capture = torch.cuda.is_current_stream_capturing()
-            self._zeroed = None if self._in_capture else torch.cuda.current_stream().record_event()
+            # in a capture the zeros are the graph's; otherwise until they are known to be there, calls come behind them
+            self._capture = _capture_of(_raw_stream(device.index))
+            self._zeroed = None if self._capture else torch.cuda.current_stream().record_event()
         return self._wsp.data_ptr(), self._wsp.numel()
 
     def _launch(self):
-        if self._in_capture or _raw_stream(self._index) != self._made_on:
-            if torch.cuda.is_current_stream_capturing():
-                pass  # a graph's runs come behind what its capture came behind
-            elif self._in_capture:
-                raise RuntimeError(f"{self._name}: made within a graph capture, whose runs alone have its counters at zero")
-            else:
-                torch.cuda.current_stream().wait_event(self._zeroed)
+        if self._capture or self._zeroed is not None:
+            self._behind_zeros()
         super()._launch()
+
+    def _behind_zeros(self):
+        if self._capture:
+            if _capture_of(_raw_stream(self._index)) != self._capture:
+                raise RuntimeError(f"{self._name}: made within a graph capture, whose runs alone have its counters at zero")
+        elif torch.cuda.is_current_stream_capturing():  # a graph may run on any stream, behind nothing
+            _check(_finish_event(self._zeroed.cuda_event), self._name)
+            self._zeroed = None
+        elif self._zeroed.query():
+            self._zeroed = None
+        elif _raw_stream(self._index) != self._made_on:
+            torch.cuda.current_stream().wait_event(self._zeroed)
 
 
 # ------------------------------------------------------------------ norm
