@@ -19,6 +19,7 @@ import ctypes as C
 from typing import NamedTuple
 
 import torch
+from torch.autograd.forward_ad import unpack_dual
 
 from . import (_check, _f32, _i32, _i64, _lib, _sig, _sz, _vp, _ws)
 
@@ -85,6 +86,13 @@ def _on(t, name, device=None):
     if device is not None and t.device != device:
         raise ValueError(f"{name} is on {t.device}, expected {device}")
     return t.data_ptr()
+
+
+def _no_tangent(name, *tensors):
+    """Refuses dual tensors, whose tangents (forward-mode gradients) the call would drop; under torch.no_grad() too, which leaves
+    forward mode on."""
+    if any(t is not None and unpack_dual(t).tangent is not None for t in tensors):
+        raise ValueError(f"{name} computes no forward-mode gradient: call it with the primal (unpack_dual)")
 
 
 def _int(v, name):
@@ -198,6 +206,7 @@ class RopeAxes(_Prepared):
         if x.requires_grad and torch.is_grad_enabled():
             raise ValueError("x requires a gradient, which a prepared call or one with `out` does not record: call rope_axes "
                              "without `out`, or under torch.no_grad()")
+        _no_tangent("rope_axes", x)
         dev = x.device
         a = RopeAxesArgs()
         a.x, a.x_row, a.x_head = _heads(x, "x")

@@ -10,7 +10,7 @@ Each call exists as a class that binds its tensors once (as the paged cache's ca
 calling the object, for decode loops and for capture into a CUDA graph.  Running one object on two streams at
 once races on its outputs and workspace.  A router or experts object made within a capture belongs to that graph:
 calls outside it, or in another capture, are refused.  These calls record no autograd graph: tensors whose gradient torch
-would track are refused outside torch.no_grad().
+would track are refused outside torch.no_grad(), and forward mode's dual tensors everywhere.
 """
 from __future__ import annotations
 
@@ -20,7 +20,7 @@ from typing import NamedTuple, Optional
 import torch
 
 from . import _check, _f32, _i32, _i64, _sig, _sz, _vp
-from .paged import _TYPES, _Prepared, _dense, _int, _on, _raw_stream
+from .paged import _TYPES, _Prepared, _dense, _int, _no_tangent, _on, _raw_stream
 
 
 class AddNormArgs(C.Structure):
@@ -67,6 +67,7 @@ _finish_event = _sig("csa2_finish_event", [_vp], C.c_int)
 def _forward_only(name, *tensors):
     if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors):
         raise ValueError(f"{name} records no gradient: call it under torch.no_grad() or with detached tensors")
+    _no_tangent(name, *tensors)
 
 
 def _rows(t, name, device=None, shape=None):

@@ -77,3 +77,27 @@ def test_a_captured_call_has_its_zeros(monkeypatch):
 def test_the_two_helpers_refuse_null():
     assert P._capture_id(None, None) == 1 and P._finish_event(None) == 1
     assert P._capture_id.argtypes[1] is C.POINTER(C.c_uint64)
+
+
+def test_dual_tensors_are_refused():
+    """Forward mode sets no requires_grad, and is on under torch.no_grad()."""
+    fwd = torch.autograd.forward_ad
+    x, i32, f32 = torch.zeros(4, 64), torch.zeros((4, 2), dtype=torch.int32), torch.zeros(4, 2)
+    up, down = torch.zeros(3, 32, 64, dtype=torch.bfloat16), torch.zeros(3, 64, 16, dtype=torch.bfloat16)
+    with fwd.dual_level():
+        dual = lambda t: fwd.make_dual(t, torch.ones_like(t))  # noqa: E731
+        calls = [lambda: S.add_norm(dual(x)), lambda: S.add_norm(x, dual(x[0])), lambda: S.add_norm(x, residual=dual(x)),
+                 lambda: S.route_experts(x, dual(x), 2), lambda: S.route_experts(x, x, 2, bias=dual(torch.zeros(4))),
+                 lambda: S.moe_experts(dual(x.bfloat16()), i32, f32, S.ExpertWeights(up, down)),
+                 lambda: S.moe_experts(x.bfloat16(), i32, dual(f32), S.ExpertWeights(up, down)),
+                 lambda: S.moe_experts(x.bfloat16(), i32, f32, S.ExpertWeights(up, dual(down))),
+                 lambda: S.sample_tokens(dual(x), torch.zeros(4)), lambda: S.sample_tokens(x, torch.zeros(4), temperature=dual(torch.ones(4))),
+                 lambda: S.rope_axes(dual(x[:, None]), torch.zeros(4, dtype=torch.int64))]
+        for call in calls:
+            with pytest.raises(ValueError, match="forward-mode"):
+                call()
+            with torch.no_grad(), pytest.raises(ValueError, match="forward-mode"):
+                call()
+        for call in (lambda: S.add_norm(fwd.unpack_dual(dual(x)).primal), lambda: S.add_norm(x)):
+            with pytest.raises(ValueError, match="CUDA"):   # on to the next check
+                call()
