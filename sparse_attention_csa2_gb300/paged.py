@@ -20,6 +20,7 @@ from typing import NamedTuple
 
 import torch
 from torch.autograd.forward_ad import unpack_dual
+from torch.autograd.graph import increment_version
 
 from . import (_check, _f32, _i32, _i64, _lib, _sig, _sz, _vp, _ws)
 
@@ -120,10 +121,12 @@ class _Prepared:
     """A call with its tensors bound: runs on the current stream of its tensors' device."""
     _name = ""
 
-    def _bind(self, call, args, device, mine, keep):
+    def _bind(self, call, args, device, mine, keep, written=()):
+        """mine: outputs and workspace; written: what else the call writes."""
         self._call, self._args, self._device = call, args, device
         self._ref = C.byref(args)
         self._mine, self._keep = mine, keep
+        self._written = (*mine, *(t for t in written if t is not None))
         self._index = device.index
         self._made_on = _raw_stream(self._index)
         self._alone = torch.cuda.device_count() == 1
@@ -145,6 +148,7 @@ class _Prepared:
         status = self._call(self._ref, raw)
         if status:
             _check(status, self._name)
+        increment_version(self._written)  # torch sees no writes by address: what saved one for its backward pass is to be told
 
 
 # ------------------------------------------------------------------ page plan
@@ -178,7 +182,7 @@ class PagePlan(_Prepared):
         mine = (self.row_start, self.kv_len, self.n_taken, self.seq_of_row, self.pos, self.slot)
         a.row_start, a.kv_len, a.n_taken, a.seq_of_row, a.pos, a.slot = (t.data_ptr() for t in mine)
         a.dev_status = None if dev_status is None else _dense(dev_status, "dev_status", torch.int32, (1,), dev)
-        self._bind(_page_plan, a, dev, mine, (ctx_len, new_len, table, free_pages, dev_status))
+        self._bind(_page_plan, a, dev, mine, (ctx_len, new_len, table, free_pages, dev_status), (table, dev_status))
 
     def __call__(self):
         self._run()
@@ -327,7 +331,7 @@ class PageWriter(_Prepared):
         a.seq_of_row = _dense(seq_of_row, "seq_of_row", torch.int32, (k.shape[0],), dev)
         a.n_rows, a.dtype = k.shape[0], _TYPES[k.dtype]
         a.dev_status = None if dev_status is None else _dense(dev_status, "dev_status", torch.int32, (1,), dev)
-        self._bind(_write_pages, a, dev, (), (cache, k, v, row_start, kv_len, seq_of_row, table, dev_status))
+        self._bind(_write_pages, a, dev, (), (cache, k, v, row_start, kv_len, seq_of_row, table, dev_status), (*cache, dev_status))
 
     def __call__(self):
         self._run()
@@ -366,7 +370,7 @@ class PagedAttn(_Prepared):
         self._wsp, a.workspace_bytes = _ws(int(_paged_attn_ws(C.byref(a))), dev)
         a.workspace = None if self._wsp is None else self._wsp.data_ptr()
         mine = (out,) if self._wsp is None else (out, self._wsp)
-        self._bind(_paged_attn, a, dev, mine, (q, cache, row_start, kv_len, table, sink, dev_status))
+        self._bind(_paged_attn, a, dev, mine, (q, cache, row_start, kv_len, table, sink, dev_status), (dev_status,))
 
     def __call__(self):
         self._run()

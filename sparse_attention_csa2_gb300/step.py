@@ -172,7 +172,7 @@ class AddNorm(_Prepared):
             a.codes, a.scales = self.codes.data_ptr(), self.scales.data_ptr()
             mine += [self.codes, self.scales]
         self.out, self.residual_out = out, residual_out
-        self._bind(_add_norm, a, dev, tuple(mine), (x, weight, residual, residual_out, out))
+        self._bind(_add_norm, a, dev, tuple(mine), (x, weight, residual, residual_out, out), (residual_out, out))
 
     def __call__(self):
         self._run()
@@ -292,7 +292,7 @@ class MoEExperts(_Counted):
             raise ValueError('form is "few", "many" or None')
         a.form = FORMS[form]
         a.workspace, a.workspace_bytes = self._workspace(_moe_ws(C.byref(a)), dev)
-        self._bind(_moe, a, dev, (out, self._wsp), (x, ids, weights, experts, x_scale, dev_status))
+        self._bind(_moe, a, dev, (out, self._wsp), (x, ids, weights, experts, x_scale, dev_status), (dev_status,))
 
     def __call__(self):
         self._run()

@@ -75,3 +75,18 @@ def test_codes_of_more_rows_than_blocks(dtype, stream, n, dim, offset, group):
     assert torch.equal(got.scales.reshape(scale.shape), scale)
     q = (y.double() / scale.double()[..., None]).float().to(torch.float8_e4m3fn)
     assert torch.equal(got.codes.reshape(y.shape), q.view(torch.uint8))
+
+
+def test_a_sum_in_place_is_told_to_what_has_saved_it():
+    x, r, w = torch.randn(3, 64, device="cuda"), torch.randn(3, 64, device="cuda"), torch.ones(64, device="cuda", requires_grad=True)
+    y = (r * w).sum()
+    S.add_norm(x, residual=r)
+    with pytest.raises(RuntimeError, match="inplace"):
+        y.backward()
+    call = S.AddNorm(x)
+    y = (call().out * w).sum()
+    y.backward()
+    y = (call().out * w).sum()
+    call()
+    with pytest.raises(RuntimeError, match="inplace"):
+        y.backward()

@@ -101,3 +101,65 @@ def test_dual_tensors_are_refused():
         for call in (lambda: S.add_norm(fwd.unpack_dual(dual(x)).primal), lambda: S.add_norm(x)):
             with pytest.raises(ValueError, match="CUDA"):   # on to the next check
                 call()
+
+
+def test_what_a_call_writes_is_marked_as_changed(monkeypatch):
+    """An operator that has saved a tensor for its backward pass is told that a call wrote over it, as torch's own writes tell it."""
+    from sparse_attention_csa2_gb300 import paged
+    monkeypatch.setattr(paged, "_raw_stream", lambda index: 1)
+    status = [0]
+    call = paged._Prepared()
+    mine, theirs, kept = torch.ones(4), torch.ones(4), torch.ones(4)
+    call._bind(lambda ref, stream: status[0], C.c_int(), torch.device("cuda", 0), (mine,), (kept,), (theirs, None))
+    w = torch.ones(4, requires_grad=True)
+    products = [(t * w).sum() for t in (mine, theirs, kept)]
+    call._launch()
+    for p in products[:2]:
+        with pytest.raises(RuntimeError, match="inplace"):
+            p.backward()
+    products[2].backward()
+    with torch.inference_mode():
+        call._written = (torch.ones(4),)   # has no version
+        call._launch()
+    status[0] = 1
+    before = theirs._version
+    call._written = (theirs,)
+    with pytest.raises(S.CSA2Error):
+        call._launch()
+    assert theirs._version == before
+
+
+def test_every_call_that_writes_what_it_is_given_says_so(monkeypatch):
+    from sparse_attention_csa2_gb300 import paged
+    seen = {}
+
+    class Stop(Exception):
+        pass
+
+    def bind(self, call, args, device, mine, keep, written=()):
+        seen[type(self).__name__] = (*mine, *written)
+        raise Stop
+
+    monkeypatch.setattr(paged._Prepared, "_bind", bind)
+    for module in (paged, P):
+        monkeypatch.setattr(module, "_on", lambda t, name, device=None: 0)
+        monkeypatch.setattr(module, "_dense", lambda t, name, dtype, shape, device=None: 0)
+    monkeypatch.setattr(P._Counted, "_workspace", lambda self, n, device: setattr(self, "_wsp", None) or (0, 0))
+    i32 = lambda *n: torch.zeros(n, dtype=torch.int32)  # noqa: E731
+    x, r, to, out = (torch.zeros(4, 64) for _ in range(4))
+    table, q = i32(2, 3), torch.zeros((4, 2, 64), dtype=torch.bfloat16)
+    cache = paged.PageCache.empty(3, 2, 16, 64, device="cpu")
+    o16, q_out = torch.zeros((4, 64), dtype=torch.bfloat16), torch.zeros_like(q)
+    experts = S.ExpertWeights(torch.zeros(3, 32, 64, dtype=torch.bfloat16), torch.zeros(3, 64, 16, dtype=torch.bfloat16))
+    status = i32(1)
+    for name, make, written in (
+            ("AddNorm", lambda: S.AddNorm(x, residual=r), (r,)),
+            ("AddNorm", lambda: S.AddNorm(x, residual=r, residual_out=to, out=out), (to, out)),
+            ("MoEExperts", lambda: S.MoEExperts(o16, i32(4, 2), torch.zeros(4, 2), experts, out=out, dev_status=status), (out, status)),
+            ("PagePlan", lambda: S.PagePlan(i32(2), i32(2), table, i32(5), 16, 8), (table,)),
+            ("PageWriter", lambda: S.PageWriter(cache, q, q, i32(3), i32(2), i32(4), table), tuple(cache)),
+            ("RopeAxes", lambda: S.RopeAxes(q, torch.zeros(4, dtype=torch.int64), out=q_out), (q_out,)),
+            ("PagedAttn", lambda: S.PagedAttn(q, cache, i32(3), i32(2), table, 1.0, out=q_out), (q_out,))):
+        with pytest.raises(Stop):
+            make()
+        assert all(any(t is s for s in seen[name]) for t in written), name
