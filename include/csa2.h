@@ -860,7 +860,7 @@ typedef struct {
   int64_t out_row;
   void* workspace;            /* csa2_moe_workspace_size bytes, 256-byte aligned */
   size_t workspace_bytes;
-  int32_t* dev_status;        /* optional */
+  int32_t* dev_status;        /* optional: CSA2_EDEVICE_INDEX, or CSA2_ETIMEOUT where a wait ran out; all of `out` is then NaN */
   int32_t form;               /* csa2_moe_form */
 } csa2_moe_args;
 size_t csa2_moe_workspace_size(const csa2_moe_args* a);
@@ -935,7 +935,7 @@ csa2_status csa2_selftest_wait_timeout(int32_t* dev_status, int32_t tries, void*
  * wait, so that some or all give up while their copies are under way.  Where one does, dev_status
  * (required) reads CSA2_ETIMEOUT and `out` holds anything; the kernels end as usual otherwise. */
 csa2_status csa2_selftest_paged_waits(const csa2_paged_attn_args* a, int32_t tries, void* stream);
-/* And for those of csa2_moe. */
+/* And for those of csa2_moe, whose `out` is then NaN. */
 csa2_status csa2_selftest_moe_waits(const csa2_moe_args* a, int32_t tries, void* stream);
 
 #ifdef __cplusplus

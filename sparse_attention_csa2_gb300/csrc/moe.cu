@@ -269,8 +269,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
   volatile int* dead = &c.dead;
 
   if (n_jobs == 0) {  // no expert is asked for
-    for (long long i = (long long)blockIdx.x * kThreads + tid; i < (long long)p.tokens * p.dim; i += (long long)gridDim.x * kThreads)
-      put_out(p, i / p.dim, (int)(i % p.dim), 0.f);
+    fill_out<kThreads>(p, tid, blockIdx.x, gridDim.x, 0.f);
   } else if (warp == kWarps) {
     // ---- weights
     uint32_t sent = 0;
@@ -550,14 +549,11 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
     }
   }
   __syncthreads();
-  if (c.dead && tid == 0 && p.dev_status != nullptr) atomicExch(p.dev_status, (int)CSA2_ETIMEOUT);
-  // the block that leaves last leaves the counters as it found them
-  if (tid == 0) {
-    __threadfence();
-    c.last = atomicAdd(p.left, 1) == (int)gridDim.x - 1;
-  }
+  // the block that leaves last leaves the counters as it found them, and no output that could pass for one after a time-out
+  if (tid == 0) c.last = leave(p, c.dead);
   __syncthreads();
   if (c.last) {
+    if (c.last == 2) fill_out<kThreads>(p, tid, 0, 1, __int_as_float(0x7fc00000));
     for (int i = tid; i < n_jobs; i += kThreads) p.up_done[i] = 0;
     for (int i = tid; i < down_tiles; i += kThreads) p.down_done[i] = 0;
     if constexpr (S::W8)

@@ -181,6 +181,22 @@ __device__ __forceinline__ void add_parts(const MoeParams& p, int thread, int ro
   else add_parts_of<N, 4>(p, thread, row, rows, t0, nt, slots, row_of);
 }
 
+// The end of a block, by one thread: 0 while others are still at it; of the last one 1, or 2 where a wait ran out in one of them.
+__device__ __forceinline__ int leave(const MoeParams& p, bool dead) {
+  __threadfence();
+  if (dead && p.dev_status != nullptr) atomicExch(p.dev_status, (int)CSA2_ETIMEOUT);
+  const int left = atomicAdd(p.left, dead ? 1 << 16 | 1 : 1) + (dead ? 1 << 16 | 1 : 1);
+  return (left & 0xffff) != (int)gridDim.x ? 0 : left >> 16 ? 2 : 1;
+}
+// Rows of y from `first` on, every `step`-th, by N threads.
+template <int N>
+__device__ __forceinline__ void fill_out(const MoeParams& p, int thread, int first, int step, float v) {
+#pragma unroll 1
+  for (int t = first; t < p.tokens; t += step)
+#pragma unroll 1
+    for (int d = thread; d < p.dim; d += N) put_out(p, t, d, v);
+}
+
 struct MoeMaps {
   CUtensorMap up, down;
 };

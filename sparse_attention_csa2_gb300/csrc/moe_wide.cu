@@ -206,8 +206,7 @@ __global__ void __launch_bounds__(threads_of(W8), 1)
   auto next_tile = [&](uint32_t i, uint64_t* bar) { return moe_wait(&bar[i % kTiles], i / kTiles & 1, tries, dead) && c.tile[i % kTiles].kind != kEnd; };
 
   if (n_jobs == 0) {  // no expert is asked for
-    for (long long i = (long long)blockIdx.x * NT + tid; i < (long long)p.tokens * p.dim; i += (long long)gridDim.x * NT)
-      put_out(p, i / p.dim, (int)(i % p.dim), 0.f);
+    fill_out<NT>(p, tid, blockIdx.x, gridDim.x, 0.f);
   } else if (warp == 0) {
     // ---- weights
     constexpr int COLS = W8 ? 128 : kStep;
@@ -559,14 +558,11 @@ __global__ void __launch_bounds__(threads_of(W8), 1)
   __syncthreads();
   tc05::fence_after();
   if (warp == 0) tc05::tmem_dealloc(tmem, 2 * kAccCols);
-  if (c.dead && tid == 0 && p.dev_status != nullptr) atomicExch(p.dev_status, (int)CSA2_ETIMEOUT);
-  // the block that leaves last leaves the counters as it found them
-  if (tid == 0) {
-    __threadfence();
-    c.last = atomicAdd(p.left, 1) == (int)gridDim.x - 1;
-  }
+  // the block that leaves last leaves the counters as it found them, and no output that could pass for one after a time-out
+  if (tid == 0) c.last = leave(p, c.dead);
   __syncthreads();
   if (c.last) {
+    if (c.last == 2) fill_out<NT>(p, tid, 0, 1, __int_as_float(0x7fc00000));
     for (int i = tid; i < n_jobs; i += NT) p.up_done[i] = 0;
     for (int i = tid; i < down_tiles; i += NT) p.down_done[i] = 0;
     if (tid == 0) *p.ticket = 0, *p.left = 0, *p.gathered = 0;

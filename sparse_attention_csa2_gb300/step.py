@@ -242,7 +242,8 @@ class MoEExperts(_Counted):
     x_scale [T] fp32, as add_norm gives them; rows may be strided) through the experts ids [T, k] int32 (-1: none) with
     weights [T, k] fp32, and through the last `n_shared` of `experts` with weight 1.  `limit` clamps the gate from above
     and the up projection on both sides.  For up to 512 tokens (a decode step, drafts): the weights of the experts that
-    are met are what it reads.  `form` ("few", "many") overrides the choice by the tokens per expert, for tests and tuning."""
+    are met are what it reads.  `form` ("few", "many") overrides the choice by the tokens per expert, for tests and tuning.
+    dev_status [1] int32 tells of ids out of range, which are left out, and of waits that ran out, with which out is NaN."""
     _name = "csa2_moe"
 
     def __init__(self, x, ids, weights, experts: ExpertWeights, n_shared: int = 0, limit=None, x_scale=None, out_dtype=None,
@@ -307,7 +308,7 @@ def moe_experts(x, ids, weights, experts: ExpertWeights, n_shared: int = 0, limi
 
 def selftest_moe_waits(call: MoEExperts, tries: int) -> None:
     """Runs a prepared call (with a dev_status) whose waits give up after `tries` tries (csa2_selftest_moe_waits): its
-    status then reads ETIMEOUT and its output holds anything."""
+    status then reads ETIMEOUT and its output is NaN."""
     with torch.cuda.device(call._device):
         _check(_moe_waits(call._ref, int(tries), _raw_stream(call._index)), "csa2_selftest_moe_waits")
 

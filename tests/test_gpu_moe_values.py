@@ -141,3 +141,27 @@ def test_route_weights_beside_a_nan():
         assert got.weights[2].isnan().all() and got.weights[[0, 1, 3, 4]].isfinite().all()
         assert not (got.ids[[0, 1, 3, 4]] == 7).any()
         assert S.route_experts(x, w, 32, score=score, normalize=False).weights.isnan().sum(1).tolist() == [1, 1, 32, 1, 1]
+
+
+@pytest.mark.parametrize("form", ["few", "many"])
+@pytest.mark.parametrize("w_codes", [False, True])
+@pytest.mark.parametrize("out", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("T", [4, 100])
+def test_an_output_after_a_wait_that_ran_out_is_nan(w_codes, T, out, form):
+    E, k, D, F = 4, 2, 1024, 512
+    w, _, _ = layer(E, 1, D, F, w_codes, 37)
+    x, _, _ = rows(T, D, False, 38)
+    ids, weights = (torch.from_numpy(v).cuda() for v in pick(T, E, k, 39))
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    wide = torch.zeros((T + 1, D + 8), dtype=out, device="cuda")
+    call = S.MoEExperts(x, ids, weights, w, n_shared=1, dev_status=status, out=wide[:T, :D], form=form)
+    want = call().clone()
+    for tries in (0, 0, 1, 2, 3, 5, 8):
+        status.zero_()
+        S.selftest_moe_waits(call, tries)
+        if S.read_device_status(status) == S.ETIMEOUT:
+            assert call.out.isnan().all()
+        else:
+            assert tries and torch.equal(call.out, want)
+        assert not wide[T].any() and not wide[:, D:].any()
+        assert torch.equal(call(), want)
