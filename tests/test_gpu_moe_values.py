@@ -165,3 +165,57 @@ def test_an_output_after_a_wait_that_ran_out_is_nan(w_codes, T, out, form):
             assert tries and torch.equal(call.out, want)
         assert not wide[T].any() and not wide[:, D:].any()
         assert torch.equal(call(), want)
+
+
+def held_small(got, oracle, D, F, h_eps):
+    """test_gpu_moe.held for an fp32 output, with nothing absolute but what fp32 itself cannot hold: steps of 2^-149, of which
+    F products and their parts each leave one."""
+    want, inner, outer = oracle
+    step = lambda n: (n / 32 + 24) * 2.0 ** -23  # noqa: E731
+    bound = step(D) * inner + (step(F) + h_eps + 2.0 ** -18) * outer + 2.0 ** -24 * np.abs(want) + 4 * F * 2.0 ** -149
+    off = np.abs(got.double().cpu().numpy() - want)
+    assert np.all(off <= bound), f"{(off / bound).max():.3g} of the bound"
+
+
+@pytest.mark.parametrize("form,w_codes", [("few", False), ("few", True), ("many", False)])   # (many, codes: not below 2^-57)
+@pytest.mark.parametrize("factor", [1e-9, 1e-12, 1e-15, 1e-16])
+def test_small_values_as_good_as_others(form, w_codes, factor):
+    """x of these sizes gives h and outputs of their squares, down to 1e-33."""
+    E, k, D, F, T = 2, 1, 64, 32, 12
+    w, up, down = layer(E, 0, D, F, w_codes, 40)
+    x, _, _ = rows(T, D, False, 41)
+    ids, weights = pick(T, E, k, 42)
+    x = (x.float() * factor).bfloat16()
+    oracle = OS.moe(x.double().cpu().numpy(), ids, weights.astype(np.float64), up, down)
+    got = S.moe_experts(x, torch.from_numpy(ids).cuda(), torch.from_numpy(weights).cuda(), w, out_dtype=torch.float32, form=form)
+    held_small(got, oracle, D, F, 2.0 ** -16 if form == "many" else 2.0 ** -22)
+    # below what fp32 holds of h, 0 or the smallest values, and nothing that is not finite
+    tiny = S.moe_experts((x.float() * 1e-16).bfloat16(), torch.from_numpy(ids).cuda(), torch.from_numpy(weights).cuda(), w, out_dtype=torch.float32, form=form)
+    assert tiny.abs().max() <= 1e-36
+
+
+@pytest.mark.parametrize("w_codes", [False, True])
+def test_small_and_large_values_in_one_row(w_codes):
+    """A value of x or h 2^-30 of its row's largest, alone in a product, counts whole in the form for few tokens (with codes h
+    in two parts keeps 2^-39 of the largest: 2^-9 of such a value, bf16 x all its bits)."""
+    D, F = 64, 32
+    up, down = torch.zeros((1, 2 * F, D)), torch.zeros((1, D, F))
+    up[0, :F, 0], up[0, F:, 1] = 1, 1                # h_f = silu(x_0) x_1 ..
+    up[0, 1, 0], up[0, 1, 2] = 0, 1                  # .. but for h_1 = silu(x_2) x_1
+    down[0, 0, 0], down[0, 1, 1] = 1, 1
+    x = torch.zeros((3, D))
+    x[:, 0], x[:, 1], x[:, 2] = torch.tensor([30.0, 3.0, 100.0]), 1, 1.3125 * 2.0 ** -25
+    if w_codes:
+        code = lambda m: m.to(torch.float8_e4m3fn).view(torch.uint8).cuda()  # noqa: E731
+        w = S.ExpertWeights(code(up), code(down), torch.ones((1, 2 * F), device="cuda"), torch.ones((1, D), device="cuda"))
+    else:
+        w = S.ExpertWeights(up.bfloat16().cuda(), down.bfloat16().cuda())
+    got = S.moe_experts(x.bfloat16().cuda(), torch.zeros((3, 1), dtype=torch.int32, device="cuda"), torch.ones((3, 1), device="cuda"), w,
+                        out_dtype=torch.float32, form="few").double().cpu()
+    xv = x.bfloat16().double()
+    silu = lambda v: v / (1 + torch.exp(-v))  # noqa: E731
+    eps = 2.0 ** -22 + 4 * 2.0 ** -24
+    for i, g in ((0, xv[:, 0]), (1, xv[:, 2])):
+        want = silu(g) * xv[:, 1]
+        most = silu(xv[:, 0]) * xv[:, 1]
+        assert torch.all((got[:, i] - want).abs() <= eps * want + (2.0 ** -22 * want + 2.0 ** -39 * most if w_codes else 0))
