@@ -435,19 +435,14 @@ __global__ void __launch_bounds__(threads_of(W8), 1)
           float v[32];
           auto add_up = [&](uint32_t at) {
 #pragma unroll
-            for (int j0 = 0; j0 < 32; j0 += 16) {
-              uint32_t u[2][16];
+            for (int j0 = 0; j0 < 32; j0 += 8) {
+              uint32_t u[4][8];
 #pragma unroll
-              for (int q = 0; q < 4; q += 2) {
-                tc05::tmem_ld16(at + q * kTokens + j0, u[0]);
-                tc05::tmem_ld16(at + (q + 1) * kTokens + j0, u[1]);
-                tc05::tmem_ld_wait();
+              for (int q = 0; q < 4; ++q) tc05::tmem_ld8(at + q * kTokens + j0, u[q]);
+              tc05::tmem_ld_wait();
 #pragma unroll
-                for (int j = 0; j < 16; ++j) {
-                  const float sum = __uint_as_float(u[0][j]) + __uint_as_float(u[1][j]);
-                  v[j0 + j] = q == 0 ? sum : v[j0 + j] + sum;
-                }
-              }
+              for (int j = 0; j < 8; ++j)
+                v[j0 + j] = (__uint_as_float(u[0][j]) + __uint_as_float(u[1][j])) + (__uint_as_float(u[2][j]) + __uint_as_float(u[3][j]));
             }
           };
           add_up(acc + (half == 0 ? 32 : 0));
@@ -480,25 +475,18 @@ __global__ void __launch_bounds__(threads_of(W8), 1)
           if constexpr (W8) scale = tile.scale[quarter * 32 + lane] * kBack;
           float* at = p.part + (long long)first * p.dim + d;
 #pragma unroll
-          for (int j0 = 0; j0 < kTokens; j0 += 16) {
-            float v[16];
-            uint32_t u[2][16];
+          for (int j0 = 0; j0 < kTokens; j0 += 8) {
+            uint32_t u[4][8];
 #pragma unroll
-            for (int q = 1; q >= 0; --q) {  // the second parts of h first
-              tc05::tmem_ld16(acc + q * kTokens + j0, u[0]);
-              tc05::tmem_ld16(acc + (q + 2) * kTokens + j0, u[1]);
-              tc05::tmem_ld_wait();
-#pragma unroll
-              for (int j = 0; j < 16; ++j) {
-                const float sum = __uint_as_float(u[0][j]) + __uint_as_float(u[1][j]);
-                v[j] = q == 1 ? sum : v[j] + sum;
-              }
-            }
-            if (j0 + 16 == kTokens) taken();
+            for (int q = 0; q < 4; ++q) tc05::tmem_ld8(acc + q * kTokens + j0, u[q]);  // h's first parts, second, first, second
+            tc05::tmem_ld_wait();
+            if (j0 + 8 == kTokens) taken();
             if (ok && d < p.dim) {
 #pragma unroll
-              for (int j = 0; j < 16; ++j)
-                if (j0 + j < n) at[(long long)(j0 + j) * p.dim] = v[j] * scale * tile.weight[j0 + j];
+              for (int j = 0; j < 8; ++j) {
+                const float v = (__uint_as_float(u[1][j]) + __uint_as_float(u[3][j])) + (__uint_as_float(u[0][j]) + __uint_as_float(u[2][j]));
+                if (j0 + j < n) at[(long long)(j0 + j) * p.dim] = v * scale * tile.weight[j0 + j];
+              }
             }
           }
         }
