@@ -106,12 +106,13 @@ template <class S, int KIND>
 __device__ __forceinline__ void load_b(const uint8_t* at, int t, float lift, uint32_t (&b)[3][2]) {
   if constexpr (S::W8 && KIND == 1) {
     const float4 v = *reinterpret_cast<const float4*>(at + 16 * t);
-    const float f[4] = {v.x * lift, v.y * lift, v.z * lift, v.w * lift};
+    const float2 lifts = make_float2(lift, lift), less = make_float2(-1.f, -1.f);
+    const float2 f[2] = {mul2(make_float2(v.x, v.y), lifts), mul2(make_float2(v.z, v.w), lifts)};
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      b[0][i] = pack_f16x2(f[2 * i], f[2 * i + 1]);
-      const float2 r = __half22float2(*reinterpret_cast<const __half2*>(&b[0][i]));
-      b[1][i] = above_lowest(pack_f16x2(f[2 * i] - r.x, f[2 * i + 1] - r.y));
+      b[0][i] = pack_f16x2(f[i].x, f[i].y);
+      const float2 rest = fma2(__half22float2(*reinterpret_cast<const __half2*>(&b[0][i])), less, f[i]);
+      b[1][i] = above_lowest(pack_f16x2(rest.x, rest.y));
     }
   } else if constexpr (S::W8 && S::X8) {
     f16_pairs(*reinterpret_cast<const uint32_t*>(at + 4 * t), b[0][0], b[0][1]);
