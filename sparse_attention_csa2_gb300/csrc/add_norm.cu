@@ -292,8 +292,9 @@ cudaError_t launch(const AddNormParams& p, bool vectors, cudaStream_t stream) {
   int nt = ((pieces + want - 1) / want + 31) / 32 * 32;
   if (nt > 1024) nt = 1024;
   const int per = (pieces + nt - 1) / nt;
-  // as many blocks as there is room for, or a row each
-  const int most = device_sm_count() * (nt <= 1024 ? 2048 / nt : 1);
+  // a row each, or as many blocks as an SM has threads for.  (Some half of those are there at once: 61 to 64 registers, to
+  // which a block of 1,024 threads binds all, leave room for 1,024 threads.)
+  const int most = device_sm_count() * (2048 / nt);
   const dim3 grid((unsigned)(p.n_rows < most ? p.n_rows : most));
   if (vectors) {
     if (per <= 2) return launch_behind(add_norm_kernel<T, SUM, 8, 2>, grid, nt, 0, stream, p);

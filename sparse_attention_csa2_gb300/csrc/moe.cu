@@ -4,8 +4,8 @@
 //
 // over the routed experts of each token and the shared ones.  Bound by the weights of the experts that are met, which
 // are read once (per 8 tokens of an expert): of 4,096 x 2,048 in 8 bits, a token's 6 experts and the shared one, 176 MB, in
-// 40 us, of which some 12 are the launch's beginning, the first copies' way and the end; 32 tokens' 154 experts, 3.9 GB, in
-// 582 us or 6.7 TB/s.  The work is a list of tiles of weight rows: all tiles of gate and
+// 41 us, of which some 12 are the launch's beginning, the first copies' way and the end; 32 tokens' 154 experts, 3.9 GB, in
+// 604 us or 6.5 TB/s (582 with h in one part).  The work is a list of tiles of weight rows: all tiles of gate and
 // up rows, expert after expert, then all of down rows.  Blocks, one per SM, take tiles from a counter.  In a block
 //
 //   warp 16      copies weights (TMA, 128-byte swizzle) into a ring of stages
@@ -22,11 +22,11 @@
 // tcgen05 is not used here: at a few tokens per expert the tensor cores have little to win, and 8-bit weights have to be
 // converted in registers in front of them, from where mma.sync takes them as they are.
 //
-// bf16 weights multiply bf16: x as it is, fp32 h as three bf16 that add up to it (two would leave 2^-17 of it, four times what
-// the sums are off by).  E4M3 codes become fp16 (exact, an instruction for two; as bf16 they take seven for four, a batch
+// bf16 weights multiply bf16: x as it is, fp32 h as three bf16 that add up to it (two leave 2^-17 of it, six times what the sums of
+// 512 columns are off by; 5 tokens' layer of 60 experts 51.8 us, with three 53).  E4M3 codes become fp16 (exact, an instruction for two; as bf16 they take seven for four, a batch
 // of 32 tokens 868 us) and multiply fp16: codes of x exactly, bf16 x and fp32 h times a power of two that brings the row's
 // largest to 2^14 .. 2^15, so that nothing is lost of x, and h in two parts keeps 22 bits whatever the output's type (one part,
-// 11 bits, moves a tenth of the bf16 outputs to their neighbour).
+// 11 bits, moves a tenth of the bf16 outputs to their neighbour; a batch of 32 tokens as a layer 494 us with one part, 509 with two).
 #include "moe_dev.cuh"
 
 namespace csa2 {
@@ -344,7 +344,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
   } else if (warp == kWarps + 2) {
     // ---- tickets and what belongs to them, up to kTiles tiles ahead of the products
     // One warp's chain of instructions for every tile, some of which are of one stage: 158 tokens' 5 of 227 experts of
-    // 128 x 1,280, 214 MB, take 149 us (with 32 entries looked at in turn 247, with
+    // 128 x 1,280, 214 MB, take 150 us with the router (with 32 entries looked at in turn 247, with
     // sums over the lanes and whole divisions 161).
     uint32_t told = 0, done = 0;
     int done_from = 0;

@@ -3,8 +3,9 @@
 // cores, weights as A and tokens as B.
 //
 // The rows of the tokens, an expert's one after the other, are first brought together (16-bit x, so that they are boxes
-// of a tensor map like the weights); h is written in that order, as two bf16 that add up to it to 2^-16, of which both
-// are multiplied.  In a block
+// of a tensor map like the weights); h is written in that order, as two bf16 that add up to it to 2^-17, of which both
+// are multiplied (a third would be read from memory and multiplied like them; what the tensor cores cut off of the sums is as
+// much: h's rest 2.5e-6 of fp32 outputs in the mean, all 4.8e-6 at 4,096 x 4,096).  In a block
 //
 //   warp 0        copies weights (TMA, 128-byte swizzle)          warp 1       copies rows of x or h beside them
 //   warp 2        issues the products into two accumulators in tensor memory, by turns
@@ -15,7 +16,7 @@
 //                 small, met halfway by rows of x and h times 2^60
 //
 // Bound by the weights' bytes where an expert meets up to some 100 tokens: 128 tokens of two of 8 experts of 4,096 x 4,096
-// in bf16, 805 MB, in 153 us (5.2 TB/s; on the few tokens' kernel 425); in 8 bits, 403 MB, in 180, as the codes' way through
+// in bf16, 805 MB, in 155 us (5.2 TB/s; on the few tokens' kernel 445); in 8 bits, 403 MB, in 183, as the codes' way through
 // shared memory (16 KB converted, 16 KB read by the products for 8 KB of codes) is longer than theirs from memory.
 #include "moe_dev.cuh"
 #include "tc05.cuh"
@@ -36,7 +37,7 @@ constexpr int kABytes = kRows * 128, kXBytes = 2 * kTokens * 128;
 // Tensor memory of a tile: four sums of an up tile, two of a down tile (whose products with both parts of h lie side by side),
 // which take the products of 16 columns by turns and are added as fp32: the tensor cores cut a sum off each time that they add
 // to it, always towards 0, by more the larger it has grown.  One sum of 8,192 positive products was 3.0e-5 too small, four
-// are 3e-6 and two 9e-6 (128 tokens of 8 experts take 166 us as a layer, with one sum 165).
+// are 3e-6 and two 9e-6.  (128 tokens of 8 experts as a layer: 162.2 us, with one sum 162.0; in 8 bits 196 to 198 and 194.)
 constexpr int kAccCols = 4 * kTokens;
 constexpr int kGather = 4;                    // rows that a ticket gathers
 constexpr int kMost = 8;                      // stages of a ring
@@ -60,7 +61,7 @@ struct WideControl {
   float exchange[2][64][33];
   int warp_tmp[32];
   uint32_t tmem;
-  int dup, dead, last, rows;
+  int dup, dead, last;
 };
 struct WideMaps {
   MoeMaps w;

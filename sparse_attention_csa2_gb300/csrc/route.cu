@@ -6,7 +6,7 @@
 // One launch: blocks compute the products of some experts with some tokens, and the block that ends last of those of a
 // group of tokens chooses their experts, a warp per token.  Bound by latency for the few tokens of a decode step: W (some
 // MB) and x are read once, all loads set out early, the choice is k rounds of two warp reductions.  At 4,096
-// values and 384 experts, W 3 MB: one token 8.2 us, 32 tokens 13, 512 tokens 45.
+// values and 384 experts, W 3 MB: one token 8 us, 32 tokens 11 to 14, 512 tokens 43 to 47.
 //
 // Which expert comes next can hang on the last bits of near scores.  Every product comes with a bound of its error (sums
 // of the sizes of what was rounded on the way, so that it holds for large values that cancel, too).  Where two scores of
@@ -370,8 +370,8 @@ __global__ void __launch_bounds__(kTileWarps * 32) route_tiles_kernel(const Rout
 }
 
 // Up to four tokens: a row of W per warp and token (they end together, and W comes from L2 for the second token on), for
-// tensor cores' types while that is no more than two thirds of a block per SM (4,096 values: 4 tokens of 64 experts 6.3 us,
-// as tiles 6.9; 3 of 384 10.9 and 9.4, 2 of 384 9.4 both).  More: tiles of 16 experts and 8 tokens, or with fp32 weights, which
+// tensor cores' types while that is no more than two thirds of a block per SM (4,096 values: 4 tokens of 64 experts 6.1 us,
+// as tiles 7.0; 3 of 384 10.9 and 9.2 to 10.4, 2 of 384 8.3 to 9.4 both).  More: tiles of 16 experts and 8 tokens, or with fp32 weights, which
 // tensor cores would round, rows with 8 tokens.
 template <typename TX, typename TW>
 cudaError_t launch(const RouteParams& p, cudaStream_t stream) {

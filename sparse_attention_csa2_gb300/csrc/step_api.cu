@@ -38,11 +38,11 @@ MoePlan moe_plan(const csa2_moe_args* a) {
   // The few tokens' form reads (from L2) and converts the weights again for every 8 tokens of an expert, in tiles of 64 rows, the
   // other begins some 6 us later and has less room for 8-bit ones.  In us, that form and the other,
   // at t tokens per expert in the mean:
-  //   8 experts of 4,096 x 4,096, bf16:  t = 4  127  143,  8  160  149,  12  208  151,  24  353  156
-  //   the same in 8 bits:                t = 8   95  170,  16  155  175,  24  207  177
-  //   64 of 4,096 x 2,048, 8 bits:       t = 12  483  586,  18  678  602
-  // and at n tiles per SM of the few tokens' form, where t is large:
-  //   n = 1.0  15  21,  2.5  21  22,  3.4  21  26,  3.8  25  24,  4.4  33  23,  6.7  36  27,  8.2  74  27
+  //   8 experts of 4,096 x 4,096, bf16:  t = 4  124  142,  8  155  149,  12  202  151,  24  342  154
+  //   the same in 8 bits:                t = 8   96  183,  16  160  184,  24  215  184
+  //   64 of 4,096 x 2,048, 8 bits:       t = 12  514  609,  18  721  620
+  // and at n tiles per SM of the few tokens' form, where t is large (two experts of 1,024 x 512 in bf16, from 3.6 on):
+  //   n = 1.1  15  21,  2.7  21  26,  3.6  21  26,  4.0  23  27,  4.4  25  27,  5.3  27  27,  6.9  36  27,  21  159  37
   const long long met = pairs < a->experts ? pairs : a->experts;
   const double tiles = ((pairs + 4 * met) / 8.0 + a->n_shared * ((a->tokens + 7) / 8)) * ((a->inner + 31) / 32 + (a->dim + 63) / 64);
   pl.many = a->form != CSA2_MOE_AUTO ? a->form == CSA2_MOE_MANY : pairs > (a->w_codes ? 16LL : 6LL) * a->experts && tiles > 4.0 * device_sm_count();
