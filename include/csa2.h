@@ -828,11 +828,12 @@ typedef enum csa2_moe_form { CSA2_MOE_AUTO = 0, CSA2_MOE_FEW = 1, CSA2_MOE_MANY 
  * W_up [experts + n_shared, 2 inner, dim] holds the gate's rows, then the up projection's; W_down
  * [experts + n_shared, dim, inner].  Both bf16, or E4M3 codes with one fp32 scale per row (value =
  * code * scale; no NaN codes).  x: bf16, or E4M3 codes with one fp32 scale per token.  Sums are fp32.
- * There are two forms: for few tokens per expert (CSA2_MOE_FEW) and for many.  FEW holds h as fp32 (bf16 weights) or
- * to 2^-22 of its values, 2^-39 of its token's largest or 2^-125 (codes; bf16 x likewise).  MANY holds h to 2^-17; with codes, bf16 x, h and the weights' scales are to be below
- * 2^67, and values of bf16 x and h below 2^-57 may count as 0.  MANY is chosen where tokens * k exceeds 6 (bf16) or
- * 16 (codes) times `experts` and the weights' rows in tiles for every 8 tokens are more than four for each SM.  Its sums of
- * 8,192 columns are good to 2^-15 of the sizes of what is added, those of fewer columns better in proportion.
+ * There are two forms: for few tokens per expert (CSA2_MOE_FEW) and for many.  FEW holds h as fp32 (bf16
+ * weights) or to 2^-22 of its values, 2^-39 of its token's largest or 2^-125 (codes; bf16 x likewise).  MANY
+ * holds h to 2^-17; with codes, bf16 x, h and the weights' scales are to be below 2^67, and values of bf16 x
+ * and h below 2^-57 may count as 0.  Its sums of 8,192 columns are good to 2^-15 of the sizes of what is added,
+ * those of fewer columns better in proportion.  MANY is chosen where tokens * k exceeds 6 (bf16) or 16 (codes)
+ * times `experts` and the weights' rows in tiles for every 8 tokens are more than four for each SM.
  * An id of -1 is no expert; other ids outside [0, experts) are left out and reported as CSA2_EDEVICE_INDEX; an
  * expert that a token names twice counts with both weights.  A token without experts is 0.  `out` lies apart from
  * what is read. */
