@@ -477,6 +477,8 @@ csa2_status csa2_compress(const csa2_compress_args* a, void* stream);
  * "The query and output paths": low-rank query projection, grouped output projection;
  * "DeepSeek V4 Inside": query rank 1024, RMSNorm on the query head, 64 heads in 8 output
  * groups).  RMSNorm(v) = v / sqrt(mean(v^2) + eps) over the last axis.
+ * Weights are read while a projection or an attention before the call may still be running on the stream (the
+ * inputs behind it): they are not to be an output of such a call that has not ended.  csa2_linear's likewise.
  *
  * csa2_query_proj - the attention query of hidden states x:
  *   c   = W_DQ x                          (hidden -> q_rank)
