@@ -783,10 +783,11 @@ csa2_status csa2_add_norm(const csa2_add_norm_args* a, void* stream);
 #define CSA2_COUNTER_BYTES 65536
 
 /* For callers that keep such a workspace: a number of the graph capture that `stream` is in (0: none), since zeros written
- * within a capture are there for runs of that graph alone; and a wait on the host for a CUDA event (of work outside any
- * capture), which may be called during one. */
+ * within a capture are there for runs of that graph alone; and whether the work before a CUDA event (recorded outside any
+ * capture) has ended, after a wait on the host where `wait` is not 0, which may be asked while this or another thread
+ * captures. */
 csa2_status csa2_capture_id(void* stream, uint64_t* id);
-csa2_status csa2_finish_event(void* event);
+csa2_status csa2_event_done(void* event, int32_t wait, int32_t* done);
 
 typedef enum csa2_score { CSA2_SCORE_SOFTMAX = 0, CSA2_SCORE_SIGMOID = 1, CSA2_SCORE_SQRTSOFTPLUS = 2 } csa2_score;
 

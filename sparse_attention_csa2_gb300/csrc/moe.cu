@@ -22,11 +22,12 @@
 // tcgen05 is not used here: at a few tokens per expert the tensor cores have little to win, and 8-bit weights have to be
 // converted in registers in front of them, from where mma.sync takes them as they are.
 //
-// bf16 weights multiply bf16: x as it is, fp32 h as three bf16 that add up to it (two leave 2^-17 of it, six times what the sums of
-// 512 columns are off by; 5 tokens' layer of 60 experts 51.8 us, with three 53).  E4M3 codes become fp16 (exact, an instruction for two; as bf16 they take seven for four, a batch
-// of 32 tokens 868 us) and multiply fp16: codes of x exactly, bf16 x and fp32 h times a power of two that brings the row's
-// largest to 2^14 .. 2^15, so that nothing is lost of x, and h in two parts keeps 22 bits whatever the output's type (one part,
-// 11 bits, moves a tenth of the bf16 outputs to their neighbour; a batch of 32 tokens as a layer 494 us with one part, 509 with two).
+// bf16 weights multiply bf16: x as it is, fp32 h as three bf16 that add up to it (two leave 2^-17 of it, six times what the
+// sums of 512 columns are off by; 5 tokens' layer of 60 experts 51.8 us, with three 53).  E4M3 codes become fp16 (exact, an
+// instruction for two; as bf16 they take seven for four) and multiply fp16: codes of x exactly, bf16 x and fp32 h times a
+// power of two that brings the row's largest to 2^14 .. 2^15, so that nothing is lost of x, and h in two parts keeps 22 bits
+// whatever the output's type (one part, 11 bits, moves a tenth of the bf16 outputs to their neighbour; 32 tokens' layer of 384
+// experts 494 us with one part, 509 with two).
 #include "moe_dev.cuh"
 
 namespace csa2 {

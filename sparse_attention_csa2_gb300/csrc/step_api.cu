@@ -203,14 +203,15 @@ csa2_status csa2_capture_id(void* stream, uint64_t* id) {
   return cuda_status(e);
 }
 
-csa2_status csa2_finish_event(void* event) {
-  if (!event) return CSA2_EINVAL;
-  cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;  // a wait for other work leaves this thread's captures as they are
+csa2_status csa2_event_done(void* event, int32_t wait, int32_t* done) {
+  if (!event || !done) return CSA2_EINVAL;
+  cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;  // other work's event is no matter of a capture, which stays valid
   cudaError_t e = cudaThreadExchangeStreamCaptureMode(&mode);
   if (e != cudaSuccess) return cuda_status(e);
-  e = cudaEventSynchronize(static_cast<cudaEvent_t>(event));
+  e = wait ? cudaEventSynchronize(static_cast<cudaEvent_t>(event)) : cudaEventQuery(static_cast<cudaEvent_t>(event));
   const cudaError_t back = cudaThreadExchangeStreamCaptureMode(&mode);
-  return cuda_status(e != cudaSuccess ? e : back);
+  *done = e == cudaSuccess;
+  return cuda_status(e != cudaSuccess && e != cudaErrorNotReady ? e : back);
 }
 
 csa2_status csa2_sample(const csa2_sample_args* a, void* stream) {

@@ -60,7 +60,7 @@ _moe = _sig("csa2_moe", [C.POINTER(MoEArgs), _vp], C.c_int)
 _moe_waits = _sig("csa2_selftest_moe_waits", [C.POINTER(MoEArgs), _i32, _vp], C.c_int)
 _sample = _sig("csa2_sample", [C.POINTER(SampleArgs), _vp], C.c_int)
 _capture_id = _sig("csa2_capture_id", [_vp, C.POINTER(C.c_uint64)], C.c_int)
-_finish_event = _sig("csa2_finish_event", [_vp], C.c_int)
+_event_done = _sig("csa2_event_done", [_vp, _i32, C.POINTER(_i32)], C.c_int)
 
 
 # ------------------------------------------------------------------ checks
@@ -88,6 +88,13 @@ def _capture_of(stream) -> int:
     return of.value
 
 
+def _done(event, wait: bool) -> bool:
+    """Whether an event's work has ended, on wish after a wait; unlike event.query() also while any thread captures a graph."""
+    done = _i32()
+    _check(_event_done(event.cuda_event, wait, C.byref(done)), "csa2_event_done")
+    return bool(done.value)
+
+
 class _Counted(_Prepared):
     """A prepared call whose workspace begins with counters that are zero between calls."""
 
@@ -96,8 +103,9 @@ class _Counted(_Prepared):
         with torch.cuda.device(device):
             self._wsp[:COUNTER_BYTES].zero_()
             # in a capture the zeros are the graph's; otherwise until they are known to be there, calls come behind them
-            self._capture = _capture_of(_raw_stream(device.index))
+            self._capture = _capture_of(_raw_stream(device.index)) if torch.cuda.is_current_stream_capturing() else 0
             self._zeroed = None if self._capture else torch.cuda.current_stream().record_event()
+            self._first = True
         return self._wsp.data_ptr(), self._wsp.numel()
 
     def _launch(self):
@@ -109,12 +117,14 @@ class _Counted(_Prepared):
         if self._capture:
             if _capture_of(_raw_stream(self._index)) != self._capture:
                 raise RuntimeError(f"{self._name}: made within a graph capture, whose runs alone have its counters at zero")
-        elif torch.cuda.is_current_stream_capturing():  # a graph may run on any stream, behind nothing
-            _check(_finish_event(self._zeroed.cuda_event), self._name)
+            return
+        first, self._first = self._first, False
+        capturing, elsewhere = torch.cuda.is_current_stream_capturing(), _raw_stream(self._index) != self._made_on
+        if first and not capturing and not elsewhere:
+            return  # the usual way of an object that is run once
+        if _done(self._zeroed, capturing):  # a graph may run on any stream, behind nothing
             self._zeroed = None
-        elif self._zeroed.query():
-            self._zeroed = None
-        elif _raw_stream(self._index) != self._made_on:
+        elif elsewhere:
             torch.cuda.current_stream().wait_event(self._zeroed)
 
 

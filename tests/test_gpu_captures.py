@@ -70,3 +70,41 @@ def test_one_made_before_a_capture_without_a_synchronisation():
         del call, graph
         junk = torch.full((1 << 22,), 77, dtype=torch.uint8, device="cuda")
         torch.cuda.synchronize()
+
+
+def test_calls_while_another_thread_captures():
+    """What a call asks about its zeros leaves a capture of another thread valid."""
+    import threading
+    x, ids, weights, w = inputs()
+    want = S.moe_experts(x, ids, weights, w)
+    call = S.MoEExperts(x, ids, weights, w)
+    graph, begun, go_on, failed = torch.cuda.CUDAGraph(), threading.Event(), threading.Event(), []
+    y = torch.zeros(8, device="cuda")
+    one, two = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+
+    def capture():
+        try:
+            with torch.cuda.stream(one):
+                graph.capture_begin()
+                y.add_(1)
+                begun.set()
+                go_on.wait(60)
+                y.add_(1)
+                graph.capture_end()
+        except Exception as e:  # noqa: BLE001
+            failed.append(e)
+            begun.set()
+
+    thread = threading.Thread(target=capture)
+    thread.start()
+    assert begun.wait(60)
+    with torch.cuda.stream(two):
+        for _ in range(3):
+            call()
+    go_on.set()
+    thread.join()
+    torch.cuda.synchronize()
+    assert not failed, failed
+    graph.replay()
+    assert torch.equal(call.out, want) and (y == 2).all()

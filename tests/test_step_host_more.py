@@ -17,21 +17,21 @@ class Machine:
         monkeypatch.setattr(P, "_capture_of", lambda stream: self.captures.get(stream, 0))
         monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: bool(self.captures.get(self.stream)))
         monkeypatch.setattr(torch.cuda, "current_stream", lambda: self)
-        monkeypatch.setattr(P, "_finish_event", lambda e: self.log.append(("finish", e)) or 0)
+        monkeypatch.setattr(P, "_done", self.done)
         monkeypatch.setattr(P._Prepared, "_launch", lambda call: self.log.append(("launch", self.stream)))
-        self.cuda_event = 7
 
     def wait_event(self, event):
         self.log.append(("wait", self.stream))
 
-    def query(self):
-        assert not self.captures.get(self.stream), "an event is not asked during a capture"
-        return self.ready
+    def done(self, event, wait):
+        if wait:
+            self.log.append(("finish", self.stream))
+        return wait or self.ready
 
     def call(self, capture=0):
         c = P._Counted.__new__(P._Counted)
         c._name, c._index, c._made_on = "call", 0, self.stream
-        c._capture, c._zeroed = capture, None if capture else self
+        c._capture, c._zeroed, c._first = capture, None if capture else self, True
         return c
 
 
@@ -58,7 +58,7 @@ def test_a_call_comes_behind_its_zeros(monkeypatch):
     call._launch()
     m.ready = True
     call._launch()
-    m.ready = None                       # is not asked again
+    m.ready = False                      # is not asked again
     call._launch()
     assert m.log == [("launch", 1), ("wait", 2), ("launch", 2), ("launch", 2), ("launch", 2)]
 
@@ -71,11 +71,11 @@ def test_a_captured_call_has_its_zeros(monkeypatch):
         m.stream, m.captures = 2, {2: 9}
         call._launch()
         call._launch()
-        assert m.log == [("finish", 7), ("launch", 2), ("launch", 2)]
+        assert m.log == [("finish", 2), ("launch", 2), ("launch", 2)]
 
 
 def test_the_two_helpers_refuse_null():
-    assert P._capture_id(None, None) == 1 and P._finish_event(None) == 1
+    assert P._capture_id(None, None) == 1 and P._event_done(None, 0, None) == 1 and P._event_done(1, 1, None) == 1
     assert P._capture_id.argtypes[1] is C.POINTER(C.c_uint64)
 
 
